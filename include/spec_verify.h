@@ -489,6 +489,151 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
                    int path_stride, int N, const int32_t* accept_len, int32_t* out_len, void* hip_stream);
 
 /*
+ * ---- A key/value cache held in four bits ----
+ *
+ * The target's forward pass over a draft reads the whole cache once a step, so
+ * at long contexts the cache's bytes are the step's time.  These calls keep it
+ * in four bits, around the verification: append the draft's rows, attend to
+ * cache and draft, verify, commit the accepted path (spec_kv_commit on the
+ * four arrays), score the cached rows, evict.
+ *
+ * A cached K or V row of head_dim = D elements (D = 64, 128 or 256) is D/2
+ * bytes of E2M1 codes (element 2i in the low half of byte i; magnitudes 0, .5,
+ * 1, 1.5, 2, 3, 4, 6 for codes 0..7, bit 3 the sign) and D/32 scale bytes, one
+ * for each 32 elements: the OCP microscaling layout.  Byte s in 1..254 stands
+ * for 2^(s-127), byte 0 comes with an all-zero block, byte 255 means NaN.
+ *
+ * Every batch row b has `prefix[b]` committed rows, slots 0 .. prefix[b]-1 of
+ * each of its heads, and `counts[b]` new ones (counts NULL: N) in the slots
+ * behind them.  A batch row with prefix[b] < 0, counts[b] outside [0, N] or
+ * prefix[b] + counts[b] > capacity is an error row: nothing of its cache,
+ * scores or positions is read or written, and its outputs are the ones named at
+ * each call.  A negative prefix (what spec_kv_commit reports for an error row)
+ * so marks a row of the batch as unused.
+ */
+
+/* One layer's cache.  Row (b, h, slot): codes at b*code_batch + h*code_head +
+ * slot*code_pos bytes from k_codes / v_codes, scales likewise.  Codes: base and
+ * strides multiples of 16 bytes; scales: of D/32 bytes.  No two rows may share
+ * bytes (zero strides where B, heads or capacity exceed 1 are SPEC_EINVAL).
+ * code_pos and scale_pos at most 2^24. */
+typedef struct {
+    void* k_codes;
+    void* k_scales;
+    void* v_codes;
+    void* v_scales;
+    int32_t B, heads, capacity, head_dim;
+    int64_t code_batch, code_head, code_pos;
+    int64_t scale_batch, scale_head, scale_pos;
+} spec_kvq_cache_t;
+
+/* Rows of D elements, (b, n, head) at data + b*batch + n*pos + head*head
+ * elements; base and strides multiples of 16 bytes, D contiguous. */
+typedef struct {
+    const void* data;
+    int64_t batch, pos, head;
+} spec_kvq_rows_t;
+
+/*
+ * spec_kvq_append -- quantise new K and V rows into slots prefix[b] ..
+ * prefix[b] + counts[b] - 1.  A block of 32 gets the smallest scale 2^e, e >=
+ * -96, with max|x| <= 7 * 2^e (so the largest element is off by at most half a
+ * step, as the others are) and its elements round to nearest, ties to the even
+ * code.  A block holding a NaN or an infinity is stored as NaN (scale 255),
+ * and so is the first block of the slot's K row, whichever of the two rows held
+ * it: every query that sees the slot answers NaN, and no other.
+ *   k, v      rows of (b, n, head), SPEC_F32 or SPEC_BF16, n < N
+ *   prefix    [B] int32 device; counts [B] int32 device or NULL
+ */
+int spec_kvq_append(const spec_kvq_cache_t* cache, const spec_kvq_rows_t* k, const spec_kvq_rows_t* v,
+                    spec_dtype_t dtype, int N, const int32_t* prefix, const int32_t* counts, void* hip_stream);
+
+/*
+ * spec_kvq_read -- the values that slots prefix[b] .. prefix[b] + counts[b] - 1
+ * stand for (exact in either type): out_k, out_v [B][N][heads][D] contiguous,
+ * 16-byte aligned.  Rows past counts[b] and error rows are zeros.
+ */
+int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, const int32_t* prefix,
+                  const int32_t* counts, void* out_k, void* out_v, void* hip_stream);
+
+/*
+ * spec_kvq_attention -- softmax attention of N new tokens' queries.  Query
+ * (b, n, hq) reads head hq / (q_heads / heads) of the cache: o = sum_s p_s V_s,
+ * p = softmax over its visible slots of scale * (q . K_s).  It sees every
+ * committed slot and, of the new ones prefix[b] + m (m < counts[b]), those with
+ * m <= n (mask NULL: a chain or a prompt) or with mask[b][n][m] != 0 (a tree's
+ * ancestor mask, as spec_tree_rerank writes it).
+ *   q        rows of (b, n, hq), SPEC_F32 or SPEC_BF16
+ *   mask     [B][N][N] uint8 device, batch rows mask_batch bytes apart (0: one
+ *            mask for all), or NULL
+ *   scale    finite, above 0
+ *   out      [B][N][q_heads][D], of q's type, contiguous, 16-byte aligned
+ *   out_lse  [B][N][q_heads] float32: log sum_s exp(scale * (q . K_s)); or NULL
+ * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros
+ * and an out_lse of -inf.  K and V enter exactly (E2M1 times a power of two is a
+ * bfloat16), products and sums are float32; the probabilities round to bfloat16
+ * before they meet V (SPEC_F32: to a sum of two bfloat16, 16 bits).
+ * q_heads a multiple of heads; N <= 65536 (with a mask: N <= SPEC_MAX_NODES).
+ * workspace: spec_kvq_attention_workspace_bytes(...) bytes (may be 0), any
+ * contents; left as scratch.
+ */
+size_t spec_kvq_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim, int capacity,
+                                          spec_dtype_t dtype);
+int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, int N,
+                       const spec_kvq_cache_t* cache, const int32_t* prefix, const int32_t* counts,
+                       const uint8_t* mask, int64_t mask_batch, float scale, void* out, float* out_lse,
+                       void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * spec_kvq_score -- accumulated attention weight, after the accepted path was
+ * committed.  The accepted queries are tokens path[b][0..d], d = accept_len[b]
+ * (path NULL: tokens 0..d), of which the t-th sees slots 0 .. prefix[b] + t.
+ * With w_s = sum over them and over the queries hq of a cache head of
+ * exp(scale * (q . K_s) - lse), scores[b][h][s] += w_s for committed slots, and
+ * the slots the commit added, prefix[b] .. prefix[b] + d, start at w_s; their
+ * positions[b][h][s] become seen[b] + (s - prefix[b]).  Sums are float32 in a
+ * fixed order.
+ *   q, lse       what spec_kvq_attention took and gave ([B][N][q_heads])
+ *   prefix       the committed rows before this step; path [B][path_stride]
+ *   scores       [B][heads][capacity] float32, positions [B][heads][capacity]
+ *                int32, read and written; seen [B] int32: tokens the sequence
+ *                had before this step (evicted ones too)
+ * A query whose lse is -inf adds nothing.  Error rows here: accept_len < 0 (or
+ * >= path_stride, or >= N), a path that is not token 0 followed by increasing
+ * tokens below N, prefix < 0, or prefix + d + 1 > capacity; they are left as
+ * they were.  path_stride <= SPEC_MAX_NODES where path is given.
+ */
+int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, int N, const float* lse,
+                   const spec_kvq_cache_t* cache, const int32_t* prefix, const int32_t* path, int path_stride,
+                   const int32_t* accept_len, float scale, float* scores, int32_t* positions, const int32_t* seen,
+                   void* hip_stream);
+
+/*
+ * spec_kvq_evict -- cut every head of a batch row down to `keep` rows, in
+ * place.  Of slots 0 .. lengths[b]-1 the kept ones are first those with
+ * positions < sink or >= seen[b] - recent, then the others by score, larger
+ * first (NaN after all numbers), the lower slot first among equals.  A kept row
+ * below slot keep stays where it is; the i-th kept row at or above it moves
+ * into the i-th gap below it (both counted upwards), so only those rows move.
+ * Slots past the new length are left as they were.
+ *   scores, positions          [B][heads][capacity], read
+ *   out_scores, out_positions  the same, written up to the new length: either
+ *                              the arrays read, or others that do not overlap
+ *   lengths, seen              [B] int32
+ *   out_len     [B] int32: min(lengths[b], keep); error rows (lengths[b] < 0 or
+ *               above capacity): -1, and nothing of them moves
+ *   out_source  [B][heads][keep] int32: the slot each kept row came from, -1
+ *               past the new length
+ *   1 <= keep <= capacity; sink, recent >= 0
+ * workspace: spec_kvq_evict_workspace_bytes(...) bytes, any contents.
+ */
+size_t spec_kvq_evict_workspace_bytes(int B, int heads, int capacity, int keep);
+int spec_kvq_evict(const spec_kvq_cache_t* cache, const float* scores, const int32_t* positions,
+                   const int32_t* lengths, const int32_t* seen, int keep, int sink, int recent, float* out_scores,
+                   int32_t* out_positions, int32_t* out_len, int32_t* out_source, void* workspace,
+                   size_t workspace_bytes, void* hip_stream);
+
+/*
  * spec_accept_rate -- "064 · 投机解码", section 二: the chance that one drafted
  * token is accepted is the overlap of the two distributions,
  * alpha[b][k] = sum_i min(p'_k(i), q'_k(i)) for k < K, with

@@ -87,6 +87,20 @@ def lib() -> ctypes.CDLL:
         L.spec_kv_commit.restype = I
         L.spec_accept_rate.argtypes = [P, I, P, I, I, I, F, I, P, P, Z, P]
         L.spec_accept_rate.restype = I
+        L.spec_kvq_append.argtypes = [P, P, P, I, I, P, P, P]
+        L.spec_kvq_append.restype = I
+        L.spec_kvq_read.argtypes = [P, I, I, P, P, P, P, P]
+        L.spec_kvq_read.restype = I
+        L.spec_kvq_attention_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+        L.spec_kvq_attention_workspace_bytes.restype = Z
+        L.spec_kvq_attention.argtypes = [P, I, I, I, P, P, P, P, LL, F, P, P, P, Z, P]
+        L.spec_kvq_attention.restype = I
+        L.spec_kvq_score.argtypes = [P, I, I, I, P, P, P, P, I, P, F, P, P, P, P]
+        L.spec_kvq_score.restype = I
+        L.spec_kvq_evict_workspace_bytes.argtypes = [I, I, I, I]
+        L.spec_kvq_evict_workspace_bytes.restype = Z
+        L.spec_kvq_evict.argtypes = [P, P, P, P, P, I, I, I, P, P, P, P, P, Z, P]
+        L.spec_kvq_evict.restype = I
         L.spec_profile_events.argtypes = [P, P]
         L.spec_profile_events.restype = I
         L.spec_workspace_init.argtypes = [P, Z, P]
@@ -543,3 +557,7 @@ def read_probe(src: torch.Tensor, sink: torch.Tensor) -> None:
     """Read-only streaming kernel over src (achievable HBM read bandwidth)."""
     n = src.numel() * src.element_size()
     _check(lib().spec_read_probe(_dev(src, "src"), n, _dev(sink, "sink"), _stream(src.device)), "spec_read_probe")
+
+
+from .kvq import (KVQCache, kvq_append, kvq_attention, kvq_attention_workspace_bytes, kvq_commit, kvq_evict,  # noqa: E402,F401
+                  kvq_evict_workspace_bytes, kvq_read, kvq_score, new_kvq_cache)

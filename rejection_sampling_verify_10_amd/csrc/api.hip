@@ -11,6 +11,7 @@
 #include "../../include/spec_verify.h"
 #include "common.hpp"
 #include "internal.hpp"
+#include "kvq.hpp"
 
 using namespace sv;
 
@@ -339,6 +340,64 @@ struct ScratchSlot {
     std::atomic<bool> zeroed{false};   // no call other than a top-k chain has written it since it was zeroed
 };
 ScratchSlot g_scratch[kScratchDevices];
+
+// ---- four-bit cache: argument blocks from the caller's structs ----
+
+bool kvq_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
+
+// Element and grid indices of a call over B*H heads, n tokens or slots each and G query heads fit 31 bits.
+bool kvq_count_ok(int B, int H, int n, int G) {
+    return static_cast<double>(B) * H * n * G < 2147483648.0;
+}
+bool kvq_sizes_ok(int B, int H, int N, int G) { return N <= 65536 && kvq_count_ok(B, H, N, G); }
+
+int take_cache(const spec_kvq_cache_t* c, KvqCache& o) {
+    if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return SPEC_EINVAL;
+    if (c->B < 1 || c->heads < 1 || c->capacity < 1 || c->head_dim < 1) return SPEC_EINVAL;
+    if (!kvq_dim_ok(c->head_dim) || c->B > 65535 || c->heads > 65535) return SPEC_EUNSUPPORTED;
+    const int64_t codes = c->head_dim / 2, scales = c->head_dim / kQBlock;
+    const auto strides_ok = [c](int64_t batch, int64_t head, int64_t pos, int64_t row, int64_t unit) {
+        if (batch < 0 || head < 0 || pos < 0 || batch % unit || head % unit || pos % unit) return false;
+        return (c->B == 1 || batch >= row) && (c->heads == 1 || head >= row) && (c->capacity == 1 || pos >= row);
+    };
+    if (!strides_ok(c->code_batch, c->code_head, c->code_pos, codes, 16) ||
+        !strides_ok(c->scale_batch, c->scale_head, c->scale_pos, scales, scales))
+        return SPEC_EINVAL;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, scales) ||
+        !aligned(c->v_scales, scales))
+        return SPEC_EINVAL;
+    if (c->code_pos > (1 << 24) || c->scale_pos > (1 << 24)) return SPEC_EUNSUPPORTED;
+    o.kc = static_cast<uint8_t*>(c->k_codes);
+    o.ks = static_cast<uint8_t*>(c->k_scales);
+    o.vc = static_cast<uint8_t*>(c->v_codes);
+    o.vs = static_cast<uint8_t*>(c->v_scales);
+    o.cb = c->code_batch, o.ch = c->code_head, o.cp = c->code_pos;
+    o.sb = c->scale_batch, o.sh = c->scale_head, o.sp = c->scale_pos;
+    o.B = c->B, o.H = c->heads, o.capacity = c->capacity, o.D = c->head_dim;
+    return SPEC_OK;
+}
+
+int take_rows(const spec_kvq_rows_t* r, int dtype, KvqRows& o) {
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_EINVAL;
+    const int64_t unit = 16 / esz_of(dtype);
+    if (!r || !r->data || !aligned(r->data, 16) || r->batch % unit || r->pos % unit || r->head % unit)
+        return SPEC_EINVAL;
+    o.data = r->data;
+    o.batch = r->batch, o.pos = r->pos, o.head = r->head;
+    return SPEC_OK;
+}
+
+void carve_kvq_parts(Carver& c, KvqAttnArgs& a) {
+    if (a.splits < 2) return;
+    const size_t rows = static_cast<size_t>(a.c.B) * a.c.H * a.splits * a.M;
+    a.part_o = c.take<float>(rows * a.c.D);
+    a.part_ml = c.take<float>(rows * 2);
+}
+
+void carve_kvq_gaps(Carver& c, KvqEvictArgs& a) {
+    a.gap_stride = a.keep < a.c.capacity - a.keep ? a.keep : a.c.capacity - a.keep;
+    a.gaps = c.take<int32_t>(static_cast<size_t>(a.c.B) * a.c.H * a.gap_stride);
+}
 
 #define SV_TRY(expr)                                  \
     do {                                              \
@@ -997,6 +1056,189 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
     ka.new_len = out_len;
     ProfileScope prof;
     SV_TRY(launch_kv_commit(ka, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+// ---- the four-bit key/value cache ----
+
+size_t spec_kvq_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim, int capacity,
+                                          spec_dtype_t dtype) {
+    if (B < 1 || N < 1 || heads < 1 || q_heads < 1 || q_heads % heads != 0 || capacity < 1) return 0;
+    if (!kvq_dim_ok(head_dim) || (dtype != SPEC_F32 && dtype != SPEC_BF16)) return 0;
+    if (!kvq_sizes_ok(B, heads, N, q_heads / heads)) return 0;
+    KvqAttnArgs a{};
+    a.c.B = B;
+    a.c.H = heads;
+    a.c.D = head_dim;
+    a.c.capacity = capacity;
+    a.dtype = dtype;
+    a.M = N * (q_heads / heads);
+    kvq_attention_plan(a);
+    Carver c(nullptr);
+    carve_kvq_parts(c, a);
+    return c.off;
+}
+
+int spec_kvq_append(const spec_kvq_cache_t* cache, const spec_kvq_rows_t* k, const spec_kvq_rows_t* v,
+                    spec_dtype_t dtype, int N, const int32_t* prefix, const int32_t* counts, void* hip_stream) {
+    KvqAppendArgs a{};
+    int rc = take_cache(cache, a.c);
+    if (rc) return rc;
+    rc = take_rows(k, dtype, a.k);
+    if (rc) return rc;
+    rc = take_rows(v, dtype, a.v);
+    if (rc) return rc;
+    if (N < 1 || !prefix || !aligned(prefix, 4) || !aligned(counts, 4)) return SPEC_EINVAL;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, 1)) return SPEC_EUNSUPPORTED;
+    a.dtype = dtype;
+    a.N = N;
+    a.prefix = prefix;
+    a.counts = counts;
+    ProfileScope prof;
+    SV_TRY(launch_kvq_append(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, const int32_t* prefix,
+                  const int32_t* counts, void* out_k, void* out_v, void* hip_stream) {
+    KvqReadArgs a{};
+    int rc = take_cache(cache, a.c);
+    if (rc) return rc;
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_EINVAL;
+    if (N < 1 || !prefix || !out_k || !out_v || !aligned(prefix, 4) || !aligned(counts, 4) || !aligned(out_k, 16) ||
+        !aligned(out_v, 16))
+        return SPEC_EINVAL;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, 1)) return SPEC_EUNSUPPORTED;
+    a.dtype = dtype;
+    a.N = N;
+    a.prefix = prefix;
+    a.counts = counts;
+    a.out_k = out_k;
+    a.out_v = out_v;
+    ProfileScope prof;
+    SV_TRY(launch_kvq_read(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, int N,
+                       const spec_kvq_cache_t* cache, const int32_t* prefix, const int32_t* counts,
+                       const uint8_t* mask, int64_t mask_batch, float scale, void* out, float* out_lse,
+                       void* workspace, size_t workspace_bytes, void* hip_stream) {
+    KvqAttnArgs a{};
+    int rc = take_cache(cache, a.c);
+    if (rc) return rc;
+    rc = take_rows(q, dtype, a.q);
+    if (rc) return rc;
+    if (N < 1 || q_heads < 1 || q_heads % a.c.H != 0 || !prefix || !out || !aligned(prefix, 4) ||
+        !aligned(counts, 4) || !aligned(out, 16) || !aligned(out_lse, 4) || mask_batch < 0)
+        return SPEC_EINVAL;
+    if (!(scale > 0.f) || !isfinite(scale)) return SPEC_EINVAL;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (mask && N > SPEC_MAX_NODES)) return SPEC_EUNSUPPORTED;
+    a.dtype = dtype;
+    a.Hq = q_heads;
+    a.G = q_heads / a.c.H;
+    a.N = N;
+    a.M = N * a.G;
+    a.prefix = prefix;
+    a.counts = counts;
+    a.mask = mask;
+    a.mask_batch = mask_batch;
+    a.cexp = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.out = out;
+    a.out_lse = out_lse;
+    kvq_attention_plan(a);
+    Carver size(nullptr);
+    carve_kvq_parts(size, a);
+    rc = check_workspace(workspace, workspace_bytes, size.off);
+    if (rc) return rc;
+    Carver c(workspace);
+    carve_kvq_parts(c, a);
+    ProfileScope prof;
+    SV_TRY(launch_kvq_attention(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, int N, const float* lse,
+                   const spec_kvq_cache_t* cache, const int32_t* prefix, const int32_t* path, int path_stride,
+                   const int32_t* accept_len, float scale, float* scores, int32_t* positions, const int32_t* seen,
+                   void* hip_stream) {
+    KvqScoreArgs a{};
+    int rc = take_cache(cache, a.c);
+    if (rc) return rc;
+    rc = take_rows(q, dtype, a.q);
+    if (rc) return rc;
+    if (N < 1 || q_heads < 1 || q_heads % a.c.H != 0 || !lse || !prefix || !accept_len || !scores || !positions ||
+        !seen || (path && path_stride < 1))
+        return SPEC_EINVAL;
+    if (!aligned(lse, 4) || !aligned(prefix, 4) || !aligned(path, 4) || !aligned(accept_len, 4) ||
+        !aligned(scores, 4) || !aligned(positions, 4) || !aligned(seen, 4))
+        return SPEC_EINVAL;
+    if (!(scale > 0.f) || !isfinite(scale)) return SPEC_EINVAL;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (path && path_stride > SPEC_MAX_NODES))
+        return SPEC_EUNSUPPORTED;
+    a.dtype = dtype;
+    a.Hq = q_heads;
+    a.G = q_heads / a.c.H;
+    a.N = N;
+    a.lse = lse;
+    a.prefix = prefix;
+    a.path = path;
+    a.path_stride = path ? path_stride : N;
+    a.accept_len = accept_len;
+    a.cexp = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.scores = scores;
+    a.positions = positions;
+    a.seen = seen;
+    ProfileScope prof;
+    SV_TRY(launch_kvq_score(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+size_t spec_kvq_evict_workspace_bytes(int B, int heads, int capacity, int keep) {
+    if (B < 1 || heads < 1 || capacity < 1 || keep < 1 || keep > capacity || !kvq_count_ok(B, heads, keep, 1)) return 0;
+    KvqEvictArgs a{};
+    a.c.B = B;
+    a.c.H = heads;
+    a.c.capacity = capacity;
+    a.keep = keep;
+    Carver c(nullptr);
+    carve_kvq_gaps(c, a);
+    return c.off;
+}
+
+int spec_kvq_evict(const spec_kvq_cache_t* cache, const float* scores, const int32_t* positions,
+                   const int32_t* lengths, const int32_t* seen, int keep, int sink, int recent, float* out_scores,
+                   int32_t* out_positions, int32_t* out_len, int32_t* out_source, void* workspace,
+                   size_t workspace_bytes, void* hip_stream) {
+    KvqEvictArgs a{};
+    int rc = take_cache(cache, a.c);
+    if (rc) return rc;
+    if (!scores || !positions || !lengths || !seen || !out_scores || !out_positions || !out_len || !out_source)
+        return SPEC_EINVAL;
+    if (!aligned(scores, 4) || !aligned(positions, 4) || !aligned(lengths, 4) || !aligned(seen, 4) ||
+        !aligned(out_scores, 4) || !aligned(out_positions, 4) || !aligned(out_len, 4) || !aligned(out_source, 4))
+        return SPEC_EINVAL;
+    if (keep < 1 || keep > a.c.capacity || sink < 0 || recent < 0) return SPEC_EINVAL;
+    if (!kvq_count_ok(a.c.B, a.c.H, keep, 1)) return SPEC_EUNSUPPORTED;
+    a.scores = scores;
+    a.positions = positions;
+    a.lengths = lengths;
+    a.seen = seen;
+    a.keep = keep;
+    a.sink = sink;
+    a.recent = recent;
+    a.out_scores = out_scores;
+    a.out_positions = out_positions;
+    a.out_len = out_len;
+    a.out_source = out_source;
+    Carver size(nullptr);
+    carve_kvq_gaps(size, a);
+    rc = check_workspace(workspace, workspace_bytes, size.off);
+    if (rc) return rc;
+    Carver c(workspace);
+    carve_kvq_gaps(c, a);
+    ProfileScope prof;
+    SV_TRY(launch_kvq_evict(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
     return SPEC_OK;
 }
 

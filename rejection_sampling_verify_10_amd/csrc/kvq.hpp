@@ -1,0 +1,125 @@
+// The four-bit key/value cache: argument blocks of its kernels, the rows' layout
+// and the conversions between E2M1 codes and bfloat16 (gfx950 has both as
+// instructions that take the block's scale).
+#pragma once
+
+#include "common.hpp"
+#include "internal.hpp"
+
+namespace sv {
+
+constexpr int kQBlock = 32;            // elements that share a scale byte
+constexpr int kQScaleMin = -96 + 127;  // smallest scale byte of a block that is not all zero
+constexpr int kQScaleNaN = 255;
+
+// Row (b, h, slot) of the codes at kc/vc + b*cb + h*ch + slot*cp, of the scales at ks/vs + b*sb + h*sh + slot*sp.
+struct KvqCache {
+    uint8_t *kc, *ks, *vc, *vs;
+    long long cb, ch, cp, sb, sh, sp;
+    int B, H, capacity, D;
+};
+// Rows (b, n, head) of D elements, strides in elements.
+struct KvqRows {
+    const void* data;
+    long long batch, pos, head;
+};
+
+struct KvqAppendArgs {
+    KvqCache c;
+    KvqRows k, v;
+    int dtype, N;
+    const int32_t* prefix;
+    const int32_t* counts;
+};
+struct KvqReadArgs {
+    KvqCache c;
+    int dtype, N;
+    const int32_t* prefix;
+    const int32_t* counts;
+    void *out_k, *out_v;
+};
+struct KvqAttnArgs {
+    KvqCache c;
+    KvqRows q;
+    int dtype, Hq, G, N, M;             // G query heads a cache head, M = N*G rows of a (b, h)
+    const int32_t* prefix;
+    const int32_t* counts;
+    const uint8_t* mask;
+    long long mask_batch;
+    float cexp;                         // scale * log2(e): scores in base 2
+    void* out;
+    float* out_lse;
+    int splits, row_tiles;
+    float* part_o;                      // [B*H][splits][M][D] (splits > 1)
+    float* part_ml;                     // [B*H][splits][M][2]
+};
+struct KvqScoreArgs {
+    KvqCache c;
+    KvqRows q;
+    int dtype, Hq, G, N;
+    const float* lse;
+    const int32_t* prefix;
+    const int32_t* path;
+    int path_stride;
+    const int32_t* accept_len;
+    float cexp;
+    float* scores;
+    int32_t* positions;
+    const int32_t* seen;
+};
+struct KvqEvictArgs {
+    KvqCache c;
+    const float* scores;
+    const int32_t* positions;
+    const int32_t* lengths;
+    const int32_t* seen;
+    int keep, sink, recent;
+    float* out_scores;
+    int32_t* out_positions;
+    int32_t* out_len;
+    int32_t* out_source;
+    int32_t* gaps;                      // [B*H][min(keep, capacity - keep)] slots to fill
+    int gap_stride;
+};
+
+hipError_t launch_kvq_append(const KvqAppendArgs& a, hipStream_t s, Timing t = {});
+hipError_t launch_kvq_read(const KvqReadArgs& a, hipStream_t s, Timing t = {});
+// Splits of the key axis and query row tiles of an attention call; fills a.splits and a.row_tiles.
+void kvq_attention_plan(KvqAttnArgs& a);
+hipError_t launch_kvq_attention(const KvqAttnArgs& a, hipStream_t s, Timing t = {});
+hipError_t launch_kvq_score(const KvqScoreArgs& a, hipStream_t s, Timing t = {});
+hipError_t launch_kvq_evict(const KvqEvictArgs& a, hipStream_t s, Timing t = {});
+
+#ifdef __HIP_DEVICE_COMPILE__
+#define SV_KVQ_DEVICE 1
+#else
+#define SV_KVQ_DEVICE 0
+#endif
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Byte `sel` of w (two E2M1 codes, the lower element first) times scale, as a pair of bfloat16: exact.
+template <int SEL> __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale) {
+#if SV_KVQ_DEVICE
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+#else
+    return 0;
+#endif
+}
+__device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale, int sel) {
+    return sel == 0 ? fp4_pair<0>(w, scale) : sel == 1 ? fp4_pair<1>(w, scale) : sel == 2 ? fp4_pair<2>(w, scale)
+                                                                                          : fp4_pair<3>(w, scale);
+}
+
+// Slots of a batch row: committed ones and new ones; false for an error row.
+__device__ __forceinline__ bool kvq_row_ok(int pre, int cnt, int N, int capacity) {
+    return pre >= 0 && cnt >= 0 && cnt <= N && static_cast<long>(pre) + cnt <= capacity;
+}
+
+}  // namespace sv

@@ -1,0 +1,199 @@
+"""The four-bit cache's calls refuse bad arguments before anything is launched (no GPU needed), and the 64-bit
+reference of its tests agrees with hand-made values."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import kvq_ref as ref
+
+EINVAL, EWORKSPACE, EUNSUPPORTED = -1, -2, -4
+FAKE = 0x7F0000000000   # never dereferenced: every call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def R():
+    import rejection_sampling_verify_10_amd as R
+    R.lib()
+    return R
+
+
+def cache(R, **kw):
+    D = kw.pop("head_dim", 128)
+    B, H, S = kw.pop("B", 2), kw.pop("heads", 4), kw.pop("capacity", 64)
+    a = dict(k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, B=B, heads=H, capacity=S, head_dim=D,
+             code_batch=H * S * D // 2, code_head=S * D // 2, code_pos=D // 2,
+             scale_batch=H * S * D // 32, scale_head=S * D // 32, scale_pos=D // 32)
+    a.update(kw)
+    from rejection_sampling_verify_10_amd.kvq import _CacheArgs
+    return _CacheArgs(**a)
+
+
+def rows(data=FAKE, batch=4096, pos=1024, head=128):
+    from rejection_sampling_verify_10_amd.kvq import _Rows
+    return _Rows(data, batch, pos, head)
+
+
+def ref_of(s):
+    return ctypes.byref(s) if s is not None else None
+
+
+BAD_CACHES = [
+    (dict(k_codes=None), EINVAL), (dict(v_scales=None), EINVAL), (dict(B=0), EINVAL), (dict(heads=0), EINVAL),
+    (dict(capacity=0), EINVAL), (dict(head_dim=0), EINVAL), (dict(k_codes=FAKE + 8), EINVAL),
+    (dict(k_scales=FAKE + 2), EINVAL), (dict(code_pos=72), EINVAL), (dict(code_pos=48), EINVAL),
+    (dict(code_pos=0), EINVAL), (dict(code_head=0), EINVAL), (dict(code_batch=0), EINVAL),
+    (dict(scale_pos=2), EINVAL), (dict(scale_pos=0), EINVAL), (dict(scale_head=-4), EINVAL),
+    (dict(head_dim=96, code_pos=64), EUNSUPPORTED), (dict(code_pos=1 << 25), EUNSUPPORTED),
+    (dict(B=65536), EUNSUPPORTED), (dict(heads=65536), EUNSUPPORTED),
+]
+
+
+def append(R, c, k=rows(), v=rows(), dtype=1, N=4, prefix=FAKE, counts=None):
+    return R.lib().spec_kvq_append(ref_of(c), ref_of(k), ref_of(v), dtype, N, prefix, counts, None)
+
+
+def read(R, c, dtype=1, N=4, prefix=FAKE, counts=None, k=FAKE, v=FAKE):
+    return R.lib().spec_kvq_read(ref_of(c), dtype, N, prefix, counts, k, v, None)
+
+
+def attend(R, c, q=rows(), dtype=1, Hq=16, N=4, prefix=FAKE, counts=None, mask=None, mb=0, scale=0.1, out=FAKE,
+           lse=FAKE, ws=FAKE, wsb=1 << 40):
+    return R.lib().spec_kvq_attention(ref_of(q), dtype, Hq, N, ref_of(c), prefix, counts, mask, mb, scale, out, lse,
+                                      ws, wsb, None)
+
+
+def score(R, c, q=rows(), dtype=1, Hq=16, N=4, lse=FAKE, prefix=FAKE, path=FAKE, stride=4, alen=FAKE, scale=0.1,
+          scores=FAKE, positions=FAKE, seen=FAKE):
+    return R.lib().spec_kvq_score(ref_of(q), dtype, Hq, N, lse, ref_of(c), prefix, path, stride, alen, scale, scores,
+                                  positions, seen, None)
+
+
+def evict(R, c, keep=32, sink=0, recent=0, ws=FAKE, wsb=1 << 40, **kw):
+    a = dict(scores=FAKE, positions=FAKE, lengths=FAKE, seen=FAKE, out_scores=FAKE, out_positions=FAKE, out_len=FAKE,
+             out_source=FAKE)
+    a.update(kw)
+    return R.lib().spec_kvq_evict(ref_of(c), a["scores"], a["positions"], a["lengths"], a["seen"], keep, sink, recent,
+                                  a["out_scores"], a["out_positions"], a["out_len"], a["out_source"], ws, wsb, None)
+
+
+@pytest.mark.parametrize("bad,code", BAD_CACHES)
+def test_every_call_checks_the_cache(R, bad, code):
+    c = cache(R, **bad)
+    for call in (append, read, attend, score, evict):
+        assert call(R, c) == code, call.__name__
+
+
+def test_no_cache(R):
+    for call in (append, read, attend, score, evict):
+        assert call(R, None) == EINVAL, call.__name__
+
+
+def test_rows_and_pointers(R):
+    c = cache(R)
+    for call, names in ((append, ("k", "v")), (attend, ("q",)), (score, ("q",))):
+        for name in names:
+            assert call(R, c, **{name: None}) == EINVAL
+            assert call(R, c, **{name: rows(data=None)}) == EINVAL
+            assert call(R, c, **{name: rows(data=FAKE + 2)}) == EINVAL      # 16-byte vectors
+            assert call(R, c, **{name: rows(pos=1028)}) == EINVAL           # 8 bytes off
+            assert call(R, c, **{name: rows(batch=1)}) == EINVAL
+    assert append(R, c, dtype=2) == EINVAL
+    assert read(R, c, dtype=-1) == EINVAL
+    assert attend(R, c, dtype=2) == EINVAL
+    assert score(R, c, dtype=2) == EINVAL
+    for call, names in ((append, ("prefix",)), (read, ("prefix", "k", "v")), (attend, ("prefix", "out")),
+                        (score, ("lse", "prefix", "alen", "scores", "positions", "seen")),
+                        (evict, ("scores", "positions", "lengths", "seen", "out_scores", "out_positions", "out_len",
+                                 "out_source"))):
+        for name in names:
+            assert call(R, c, **{name: None}) == EINVAL, (call.__name__, name)
+            assert call(R, c, **{name: FAKE + 1}) == EINVAL, (call.__name__, name)
+
+
+def test_sizes(R):
+    c = cache(R)
+    assert append(R, c, N=0) == EINVAL
+    assert append(R, c, N=65537) == EUNSUPPORTED
+    assert read(R, c, N=0) == EINVAL
+    assert attend(R, c, N=0) == EINVAL
+    assert attend(R, c, Hq=0) == EINVAL
+    assert attend(R, c, Hq=6) == EINVAL                     # not a multiple of the cache's heads
+    assert attend(R, c, N=65, mask=FAKE) == EUNSUPPORTED    # a tree has at most 64 nodes
+    assert attend(R, c, mask=FAKE, mb=-1) == EINVAL
+    assert attend(R, c, N=65537) == EUNSUPPORTED
+    assert attend(R, c, N=65536, Hq=4 << 14) == EUNSUPPORTED
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert attend(R, c, scale=bad) == EINVAL
+        assert score(R, c, scale=bad) == EINVAL
+    assert score(R, c, Hq=6) == EINVAL
+    assert score(R, c, stride=0) == EINVAL
+    assert score(R, c, stride=65) == EUNSUPPORTED
+    assert evict(R, c, keep=0) == EINVAL
+    assert evict(R, c, keep=65) == EINVAL
+    assert evict(R, c, sink=-1) == EINVAL
+    assert evict(R, c, recent=-1) == EINVAL
+
+
+def test_workspaces(R):
+    c = cache(R, capacity=4096)
+    L = R.lib()
+    need = L.spec_kvq_attention_workspace_bytes(2, 4, 16, 4, 128, 4096, 1)
+    assert need > 0
+    for bad in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 64)):
+        assert attend(R, c, **bad) == EWORKSPACE
+    need = L.spec_kvq_evict_workspace_bytes(2, 4, 4096, 32)
+    assert need >= 2 * 4 * 32 * 4
+    for bad in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 64)):
+        assert evict(R, c, **bad) == EWORKSPACE
+    assert L.spec_kvq_attention_workspace_bytes(0, 4, 16, 4, 128, 4096, 1) == 0
+    assert L.spec_kvq_attention_workspace_bytes(2, 4, 15, 4, 128, 4096, 1) == 0
+    assert L.spec_kvq_attention_workspace_bytes(2, 4, 16, 4, 96, 4096, 1) == 0
+    assert L.spec_kvq_attention_workspace_bytes(2, 4, 16, 4, 128, 4096, 2) == 0
+    assert L.spec_kvq_evict_workspace_bytes(2, 4, 16, 17) == 0
+
+
+def test_declared_calls_are_exported(R):
+    for name in ("append", "read", "attention", "attention_workspace_bytes", "score", "evict",
+                 "evict_workspace_bytes"):
+        assert hasattr(R.lib(), "spec_kvq_" + name)
+
+
+def test_binding_refuses_cpu_tensors_and_bad_shapes(R):
+    import torch
+    u = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    with pytest.raises(ValueError, match="GPU"):
+        R.KVQCache(u(1, 2, 8, 64), u(1, 2, 8, 4), u(1, 2, 8, 64), u(1, 2, 8, 4))
+    with pytest.raises(ValueError, match="head_dim"):
+        R.KVQCache(u(1, 2, 8, 48), u(1, 2, 8, 3), u(1, 2, 8, 48), u(1, 2, 8, 3))
+    with pytest.raises(ValueError):
+        R.KVQCache(u(2, 8, 64), u(2, 8, 4), u(2, 8, 64), u(2, 8, 4))
+    with pytest.raises(ValueError, match="head_dim"):
+        R.new_kvq_cache(1, 1, 8, 80, "cpu")
+
+
+def test_reference_decodes_and_quantises_by_hand():
+    codes = np.array([[0x10, 0x32, 0x54, 0x76, 0x98, 0xBA, 0xDC, 0xFE] + [0] * 8], np.uint8)
+    v = ref.decode(codes, np.array([[128]], np.uint8))[0, :16]
+    want = 2.0 * np.array([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6])
+    assert np.array_equal(v, want)
+    # ties go to the even code; 7 is the largest value a scale of 1 holds
+    x = np.zeros(32)
+    x[:10] = [7, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -5.0001, -.2]
+    v, s = ref.quantise(x[None])
+    assert s[0, 0] == 127 and v[0, :10].tolist() == [6, 0, 1, 1, 2, 2, 4, 4, -6, 0]
+    x[0] = 7.0001
+    v, s = ref.quantise(x[None])
+    assert s[0, 0] == 128 and v[0, 0] == 8
+
+
+def test_reference_eviction_by_hand():
+    scores = np.array([[[5, 1, 4, 1, 9, np.nan, 3, 0]]], np.float32)
+    pos = np.arange(8, dtype=np.int32).reshape(1, 1, 8)
+    n, src = ref.evict(scores, pos, [8], [8], 4, 0, 0)
+    assert n[0] == 4 and src[0, 0].tolist() == [0, 4, 2, 6]          # 9, 5, 4, 3 stay; 1 and 1 give way
+    n, src = ref.evict(scores, pos, [8], [8], 4, 2, 1)
+    assert src[0, 0].tolist() == [0, 1, 4, 7]                        # 0, 1 and the latest are kept, then 9
+    n, src = ref.evict(scores, pos, [3], [8], 4, 0, 0)
+    assert n[0] == 3 and src[0, 0].tolist() == [0, 1, 2, -1]
