@@ -388,8 +388,8 @@ int take_rows(const spec_kvq_rows_t* r, int dtype, KvqRows& o) {
 }
 
 void carve_kvq_parts(Carver& c, KvqAttnArgs& a) {
-    if (a.splits < 2) return;
-    const size_t rows = static_cast<size_t>(a.c.B) * a.c.H * a.splits * a.M;
+    if (!a.units) return;
+    const size_t rows = static_cast<size_t>(a.units) * a.c.H * a.M;
     a.part_o = c.take<float>(rows * a.c.D);
     a.part_ml = c.take<float>(rows * 2);
 }

@@ -49,9 +49,10 @@ struct KvqAttnArgs {
     float cexp;                         // scale * log2(e): scores in base 2
     void* out;
     float* out_lse;
-    int splits, row_tiles;
-    float* part_o;                      // [B*H][splits][M][D] (splits > 1)
-    float* part_ml;                     // [B*H][splits][M][2]
+    int q_tiles, row_tiles, waves;      // 16-row tiles of a workgroup, workgroups a unit, waves a workgroup
+    int units, min_per;                 // parts of the batch's key axis and their least chunks; 0: one a batch row
+    float* part_o;                      // [units][H][M][D] (units > 0)
+    float* part_ml;                     // [units][H][M][2]
 };
 struct KvqScoreArgs {
     KvqCache c;
@@ -84,7 +85,7 @@ struct KvqEvictArgs {
 
 hipError_t launch_kvq_append(const KvqAppendArgs& a, hipStream_t s, Timing t = {});
 hipError_t launch_kvq_read(const KvqReadArgs& a, hipStream_t s, Timing t = {});
-// Splits of the key axis and query row tiles of an attention call; fills a.splits and a.row_tiles.
+// How an attention call is cut up: fills a.q_tiles .. a.min_per.
 void kvq_attention_plan(KvqAttnArgs& a);
 hipError_t launch_kvq_attention(const KvqAttnArgs& a, hipStream_t s, Timing t = {});
 hipError_t launch_kvq_score(const KvqScoreArgs& a, hipStream_t s, Timing t = {});

@@ -20,16 +20,17 @@
 //
 // float32 queries enter as three bf16 parts (exact) and P as two.
 
+#include <stdlib.h>
+
 #include "kvq.hpp"
 
 namespace sv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kStep = 32;                               // keys a wave takes at a time
-constexpr int kRound = kStep * kWaves;                  // keys a workgroup takes at a time
+constexpr int kChunk = 128;                             // units of the key axis' split
+constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
 #if SV_KVQ_DEVICE
@@ -54,50 +55,137 @@ template <int D> struct Raw {
     uint32_t v[8][kVW], vs[8];
 };
 
+#if SV_KVQ_DEVICE
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
+}
+#endif
+
+// Reads keys through buffer descriptors that end at the last visible slot: what
+// lies past it comes back as zeros (code 0, scale 0) and costs no traffic, so
+// every step, the last and the one prefetched past the end too, is the same
+// straight run of loads and the wait for a step never includes the next one's.
 template <int D> struct Loader {
     const uint8_t *kc, *ks, *vc, *vs;                   // of the (b, h)
     long cp, sp;
-    int c, g;
-    // keys kb .. kb+31, those at or past `lim` replaced by key lim - 1
-    __device__ __forceinline__ void load(Raw<D>& r, long kb, long lim) const {
-        const int last = static_cast<int>(min(lim - kb, 32l)) - 1;
-        const uint8_t* kcb = kc + kb * cp;
-        const uint8_t* ksb = ks + kb * sp;
-        const uint8_t* vcb = vc + kb * cp;
-        const uint8_t* vsb = vs + kb * sp;
-        const uint32_t cp32 = static_cast<uint32_t>(cp), sp32 = static_cast<uint32_t>(sp);
+    uint32_t ko, kso, vo, vso;                          // the lane's offsets
+    __device__ __forceinline__ Loader(const KvqCache& c, int b, int h, int lane) {
+        const int col = lane & 15, g = lane >> 4;
+        kc = c.kc + b * c.cb + h * c.ch;
+        vc = c.vc + b * c.cb + h * c.ch;
+        ks = c.ks + b * c.sb + h * c.sh;
+        vs = c.vs + b * c.sb + h * c.sh;
+        cp = c.cp;
+        sp = c.sp;
+        ko = static_cast<uint32_t>(col * cp) + g * (D / 8);
+        kso = static_cast<uint32_t>(col * sp) + g * D / 128;
+        vo = static_cast<uint32_t>(4 * g * cp) + col * (D / 32);
+        vso = static_cast<uint32_t>(4 * g * sp) + col * (D / 16) / kQBlock;
+    }
+    // keys kb .. kb+31 of those below lim
+    __device__ __forceinline__ void load_k(Raw<D>& r, long kb, long lim) const {
+#if SV_KVQ_DEVICE
+        const int n = static_cast<int>(max(min(lim - kb, static_cast<long>(kStep)), 0l));
+        const int cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
+        const auto rk = rsrc(kc + kb * cp, n * cp32), rks = rsrc(ks + kb * sp, n * sp32);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t key = min(16 * t + c, last);
-            const uint8_t* p = kcb + (key * cp32 + static_cast<uint32_t>(g * (D / 8)));
             if (D == 64) {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rk, ko, 16 * t * cp32, 0);
                 r.k[t][0] = w[0], r.k[t][1] = w[1];
             } else {
 #pragma unroll
                 for (int x = 0; x < D / 128; ++x) {
-                    const u32x4 w = reinterpret_cast<const u32x4*>(p)[x];
+                    const auto w = __builtin_amdgcn_raw_buffer_load_b128(rk, ko + 16 * x, 16 * t * cp32, 0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) r.k[t][(4 * x + e) % Raw<D>::kKW] = w[e];
                 }
             }
-            const uint8_t* s = ksb + (key * sp32 + static_cast<uint32_t>(g * D / 128));
-            r.ks[t] = D == 256 ? *reinterpret_cast<const uint16_t*>(s) : *s;
+            r.ks[t] = D == 256 ? __builtin_amdgcn_raw_buffer_load_b16(rks, kso, 16 * t * sp32, 0)
+                               : __builtin_amdgcn_raw_buffer_load_b8(rks, kso, 16 * t * sp32, 0);
         }
+#endif
+    }
+    __device__ __forceinline__ void load_v(Raw<D>& r, long kb, long lim) const {
+#if SV_KVQ_DEVICE
+        const int n = static_cast<int>(max(min(lim - kb, static_cast<long>(kStep)), 0l));
+        const int cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
+        const auto rv = rsrc(vc + kb * cp, n * cp32), rvs = rsrc(vs + kb * sp, n * sp32);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t key = min(16 * (j / 4) + 4 * g + j % 4, last);
-            const uint8_t* p = vcb + (key * cp32 + static_cast<uint32_t>(c * (D / 32)));
-            if (D == 64) r.v[j][0] = *reinterpret_cast<const uint16_t*>(p);
-            else if (D == 128) r.v[j][0] = *reinterpret_cast<const uint32_t*>(p);
+            const int key = 16 * (j / 4) + j % 4;       // and 4g more, in the lane's offset
+            if (D == 64) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rv, vo, key * cp32, 0);
+            else if (D == 128) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, vo, key * cp32, 0);
             else {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rv, vo, key * cp32, 0);
                 r.v[j][0] = w[0], r.v[j][Raw<D>::kVW - 1] = w[1];
             }
-            r.vs[j] = vsb[key * sp32 + static_cast<uint32_t>(c * (D / 16) / kQBlock)];
+            r.vs[j] = __builtin_amdgcn_raw_buffer_load_b8(rvs, vso, key * sp32, 0);
         }
+#endif
     }
 };
+
+// A call's split of the key axis.  Batch rows hold pre + cnt slots each, in whole
+// chunks; a unit is `per` chunks of one batch row, and the units are numbered
+// through the batch, so that a long row gets many and a short one few and all
+// of them cost the same.  Every workgroup finds its own from the lengths (the
+// host does not know them): units_of(b) = ceil(chunks(b) / per), with the
+// smallest `per` that keeps their number within a.units.
+__device__ __forceinline__ int kvq_chunks(const KvqAttnArgs& a, int b) {
+    const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
+    return kvq_row_ok(pre, cnt, a.N, a.c.capacity) ? static_cast<int>((static_cast<long>(pre) + cnt + kChunk - 1) / kChunk)
+                                                   : 0;
+}
+__device__ __forceinline__ int wave_scan_int(int v) {   // inclusive
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int t = __shfl_up(v, o, kWave);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+// Chunks a unit holds.
+__device__ __forceinline__ int kvq_per(const KvqAttnArgs& a) {
+    const int lane = threadIdx.x & (kWave - 1);
+    long total = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += kWave) total += wave_sum(b0 + lane < a.c.B ? kvq_chunks(a, b0 + lane) : 0);
+    const long room = a.units - a.c.B;
+    const int per = static_cast<int>(max((total + room - 1) / room, static_cast<long>(a.min_per)));
+    return __builtin_amdgcn_readfirstlane(per);         // the same in every lane, kept in a scalar register
+}
+// Batch row and place in it of unit u; false past the last unit.
+__device__ __forceinline__ bool kvq_unit(const KvqAttnArgs& a, int u, int per, int& b, int& split) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int base = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
+        const int n = b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0;
+        const int incl = wave_scan_int(n);
+        const unsigned long long past = __ballot(base + incl > u);   // (u, base and per are scalars, and so b and split)
+        if (past) {
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(past)) - 1);
+            b = b0 + l;
+            split = u - base - (bcast(incl, l) - bcast(n, l));
+            return true;
+        }
+        base += bcast(incl, kWave - 1);
+    }
+    return false;
+}
+// First unit of batch row b, and how many it has.
+__device__ __forceinline__ int kvq_first_unit(const KvqAttnArgs& a, int b, int per, int& mine) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int first = 0;
+    mine = 0;
+    for (int b0 = 0; b0 <= b; b0 += kWave) {
+        const int r = b0 + lane;
+        const int n = r < a.c.B ? (kvq_chunks(a, r) + per - 1) / per : 0;
+        first += __builtin_amdgcn_readfirstlane(wave_sum(r < b ? n : 0));
+        if (b < b0 + kWave) mine = bcast(n, b - b0);
+    }
+    return first;
+}
 
 // Query rows as the B operand of S^T: lane (c, g) holds elements g*D/4 .. of row c.  bf16 rows are one part, float32
 // rows three whose sum is the value.
@@ -132,22 +220,48 @@ __device__ __forceinline__ void load_query(const KvqRows& q, long off, bool live
     }
 }
 
-template <int D, int DT, int QT>
-__global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) {
+// Waves a SIMD to fit the registers of one variant to.
+constexpr int attend_occupancy(int D, int DT, int QT) {
+#ifdef OCC2
+    if (D == 128 && QT == 2 && DT == 1) return OCC2;
+#endif
+    const int size = (D / 64) * QT * (DT == 1 ? 2 : 3);     // of the sums and the queries
+    return size <= 4 ? 3 : size <= 16 ? 2 : 1;
+}
+
+// Keeps the instructions on either side apart, so that operands are not formed long before their use.
+template <bool ON> __device__ __forceinline__ void fence() {
+#if SV_KVQ_DEVICE
+    if (ON) __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// Query operands kept in registers up to this many, in LDS beyond.
+constexpr bool queries_in_lds(int D, int DT, int QT) { return QT * (DT == 1 ? 1 : 3) * (D / 8) > 48; }
+constexpr int max2(int a, int b) { return a > b ? a : b; }
+
+template <int D, int DT, int QT, int WAVES>
+__global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq_attention_kernel(KvqAttnArgs a) {
     constexpr int NQ = DT == 1 ? 1 : 3, NP = DT == 1 ? 1 : 2;
     constexpr int kNT = D / 16;                         // 16-row tiles of O^T
     constexpr int kRows = 16 * QT;
-    // units (b, h, split) of one residue mod 8 with all their row tiles: neighbours in time on one XCD, whose L2 serves
+    constexpr int kRound = kStep * WAVES;               // keys a workgroup takes at a time
+    // (unit, head) pairs of one residue mod 8 with all their row tiles: neighbours in time on one XCD, whose L2 serves
     // the row tiles that read the same keys
     const int RT = a.row_tiles;
     const int x = blockIdx.x % 8, y = blockIdx.x / 8;
-    const int rt = y % RT, unit = (y / RT) * 8 + x;
-    const int split = unit % a.splits, bh = unit / a.splits;
-    if (bh >= a.c.B * a.c.H) return;
-    const int h = bh % a.c.H, b = bh / a.c.H;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
+    const int rt = y % RT, uh = (y / RT) * 8 + x;
+    const int h = uh % a.c.H, unit = uh / a.c.H;
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
     const int c = lane & 15, g = lane >> 4;
 
+    int b = unit, split = 0, per = 0;
+    if (a.units) {
+        per = kvq_per(a);
+        if (!kvq_unit(a, unit, per, b, split)) return;
+    } else if (b >= a.c.B) {
+        return;
+    }
     const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
     const bool ok = kvq_row_ok(pre, cnt, a.N, a.c.capacity);
     const int row0 = rt * kRows;
@@ -155,14 +269,19 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
     const int tok_end = ok ? min(cnt, (min(row0 + kRows, a.M) - 1) / a.G + 1) : 0;
     const bool any = ok && row0 / a.G < tok_end;
     const long lim = any ? static_cast<long>(pre) + (a.mask ? cnt : tok_end) : 0;
-    const long all = ok ? static_cast<long>(pre) + cnt : 0;
-    // equal chunks of whole rounds over the row's own slots
-    const long rounds = (all + kRound - 1) / kRound;
-    const long chunk = (rounds + a.splits - 1) / a.splits * kRound;
-    const long k0 = split * chunk, k1 = min(k0 + chunk, lim);
+    const long k0 = a.units ? static_cast<long>(split) * per * kChunk : 0;
+    const long k1 = a.units ? min(k0 + static_cast<long>(per) * kChunk, lim) : lim;
+
+    // LDS: the queries during the loop, the waves' sums after it
+    constexpr bool kQL = queries_in_lds(D, DT, QT);
+    constexpr int kQWords = kQL ? QT * NQ * (D / 32) * kWave : 0, kJoinWords = WAVES / 2 * kRows * D / 4;
+    __shared__ u32x4 shared[max2(kQWords, kJoinWords)];
+    u32x4* const sh_q = shared + lane;
+    f32x4* const sh_o = reinterpret_cast<f32x4*>(shared);
+    __shared__ float sh_ml[WAVES / 2][kRows][2];
 
     // this lane's query (one a tile): its row, token, and whether it exists
-    u32x4 Q[QT][NQ][D / 32];
+    u32x4 Q[kQL ? 1 : QT][NQ][D / 32];
     int tok[QT];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
@@ -170,8 +289,40 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
         tok[qt] = r / a.G;
         const bool live = r < a.M && tok[qt] < (ok ? cnt : 0);
         const int hq = h * a.G + r % a.G;
-        load_query<D, NQ, DT>(a.q, b * a.q.batch + tok[qt] * a.q.pos + hq * a.q.head, live, g, Q[qt]);
+        const long off = b * a.q.batch + tok[qt] * a.q.pos + hq * a.q.head;
+        if (!kQL) {
+            load_query<D, NQ, DT>(a.q, off, live, g, Q[kQL ? 0 : qt]);
+        } else if (qt % WAVES == wave) {
+            load_query<D, NQ, DT>(a.q, off, live, g, Q[0]);
+#pragma unroll
+            for (int p = 0; p < NQ; ++p)
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) sh_q[((qt * NQ + p) * (D / 32) + x) * kWave] = Q[0][p][x];
+        }
         if (!live) tok[qt] = -1;
+    }
+    if (kQL) __syncthreads();
+
+    // a tree's mask rows as bits: the new tokens m < cnt this lane's queries see
+    unsigned long long tree[QT];
+    if (a.mask && k1 > pre) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            const uint8_t* row = a.mask + b * a.mask_batch + static_cast<long>(max(tok[qt], 0)) * a.N;
+            unsigned bits = 0;                          // tokens 16g .. 16g+15, the other three groups' follow
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int node = 16 * g + e;
+                bits |= static_cast<unsigned>((row[min(node, a.N - 1)] != 0) & (node < cnt)) << e;
+            }
+            const unsigned lo = bits << (16 * (g & 1)), hi = lo;
+            unsigned w0 = g < 2 ? lo : 0u, w1 = g < 2 ? 0u : hi;
+            w0 |= xshfl(w0, 16);
+            w0 |= xshfl(w0, 32);
+            w1 |= xshfl(w1, 16);
+            w1 |= xshfl(w1, 32);
+            tree[qt] = (static_cast<unsigned long long>(w1) << 32) | w0;
+        }
     }
 
     f32x4 O[QT][kNT];
@@ -184,54 +335,66 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
         for (int n = 0; n < kNT; ++n) O[qt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    Loader<D> ld;
-    ld.kc = a.c.kc + b * a.c.cb + h * a.c.ch;
-    ld.vc = a.c.vc + b * a.c.cb + h * a.c.ch;
-    ld.ks = a.c.ks + b * a.c.sb + h * a.c.sh;
-    ld.vs = a.c.vs + b * a.c.sb + h * a.c.sh;
-    ld.cp = a.c.cp;
-    ld.sp = a.c.sp;
-    ld.c = c;
-    ld.g = g;
-
-    Raw<D> cur, nxt;
+    const Loader<D> ld(a.c, b, h, lane);
+    // m follows the true maximum within a factor of 2^8 of the probabilities: sums stay exact in float32, a bf16
+    // keeps its eight bits at any size, and a step whose scores stay below needs no exchange between the lanes
+    const float slack = fminf(8.f / a.cexp, 1e30f);
+    Raw<D> cur;
     long kb = k0 + kStep * wave;
-    if (kb < k1) ld.load(cur, kb, lim);
+    if (kb < k1) {
+        ld.load_k(cur, kb, k1);
+        ld.load_v(cur, kb, k1);
+    }
     for (; kb < k1; kb += kRound) {
-        if (kb + kRound < k1) ld.load(nxt, kb + kRound, lim);
-
         // S^T = K Q^T
         f32x4 S[QT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) S[qt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (kQL) asm volatile("" ::: "memory");         // queries are read again every step, not kept in registers
 #pragma unroll
-            for (int s = 0; s < D / 32; ++s) {
-                const float sc = scale_value(D == 256 && s >= 4 ? cur.ks[t] >> 8 : cur.ks[t] & 255u);
+        for (int s = 0; s < D / 32; ++s) {
+            u32x4 A[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float sc = scale_value(D == 256 && s >= 4 ? cur.ks[t] >> 8 : cur.ks[t]);
                 const uint32_t w = cur.k[t][s];
-                const u32x4 A = {fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
-#pragma unroll
-                for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-                    for (int p = 0; p < NQ; ++p) S[qt][t] = mfma(A, Q[qt][p][s], S[qt][t]);
+                A[t] = u32x4{fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
             }
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+#pragma unroll
+                for (int p = 0; p < NQ; ++p) {
+                    const u32x4 q = kQL ? sh_q[((qt * NQ + p) * (D / 32) + s) * kWave] : Q[kQL ? 0 : qt][p][s];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) S[qt][t] = mfma(A[t], q, S[qt][t]);
+                }
+            }
+            fence<kQL>();
         }
+        ld.load_k(cur, kb + kRound, k1);
         const bool edge = kb + kStep > pre;             // some of the 32 slots are new ones, or past the end
         if (edge) {
             // selects, not branches: a lane's eight slots may fall on either side of every limit
             const int node0 = static_cast<int>(kb - pre) + 4 * g;
+            if (a.mask) {
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-                const uint8_t* mrow = a.mask + b * a.mask_batch + static_cast<long>(max(tok[qt], 0)) * a.N;
+                for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int node = node0 + 16 * (j / 4) + j % 4;
-                    int sees = a.mask ? mrow[min(max(node, 0), a.N - 1)] : node <= tok[qt];
-                    sees = (sees != 0) & (node < cnt);
-                    const float x = S[qt][j / 4][j % 4];
-                    S[qt][j / 4][j % 4] = (node < 0) | sees ? x : -INFINITY;
+                    for (int j = 0; j < 8; ++j) {
+                        const int node = node0 + 16 * (j / 4) + j % 4;
+                        const bool sees = (node < 0) | ((node < 64) & static_cast<int>((tree[qt] >> (node & 63)) & 1u));
+                        S[qt][j / 4][j % 4] = sees ? S[qt][j / 4][j % 4] : -INFINITY;
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        S[qt][j / 4][j % 4] =
+                            node0 + 16 * (j / 4) + j % 4 <= tok[qt] ? S[qt][j / 4][j % 4] : -INFINITY;
             }
         }
 
@@ -242,10 +405,10 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
             float mx = S[qt][0][0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) mx = fmaxf(mx, S[qt][j / 4][j % 4]);
-            mx = fmaxf(mx, xshfl(mx, 16));
-            mx = fmaxf(mx, xshfl(mx, 32));
-            const float mn = fmaxf(m[qt], mx);
-            if (__ballot(mn > m[qt]) != 0ull) {
+            if (__ballot(mx > m[qt] + slack) != 0ull) {
+                mx = fmaxf(mx, xshfl(mx, 16));
+                mx = fmaxf(mx, xshfl(mx, 32));
+                const float mn = fmaxf(m[qt], mx);
                 const float al = m[qt] == -INFINITY ? 0.f : exp2_fast((m[qt] - mn) * a.cexp);
                 l[qt] *= al;
 #pragma unroll
@@ -274,11 +437,8 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
         float vsc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // a slot past the end holds anything; its P is 0, its V has to be finite
-            const bool past = kb + 16 * (j / 4) + 4 * g + j % 4 >= lim;
-            vsc[j] = past ? 0.f : scale_value(min(cur.vs[j], 254u));
-#pragma unroll
-            for (int x = 0; x < Raw<D>::kVW; ++x) cur.v[j][x] = past ? 0u : cur.v[j][x];
+            // a block stored as NaN has zero codes: its V is finite, and its K row says NaN
+            vsc[j] = scale_value(min(cur.vs[j], 254u));
         }
 #pragma unroll
         for (int pr = 0; pr < kNT / 2; ++pr) {
@@ -299,13 +459,12 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
                     O[qt][2 * pr + 1] = mfma(hi, P[qt][x], O[qt][2 * pr + 1]);
                 }
             }
+            fence<kQL>();
         }
-        cur = nxt;
+        ld.load_v(cur, kb + kRound, k1);
     }
 
-    // join the waves: the sums of a lane's four g-groups, then the four waves, two at a time through LDS
-    __shared__ float sh_o[2][kRows * D];
-    __shared__ float sh_ml[2][kRows][2];
+    // join the waves: the sums of a lane's four g-groups, then the waves, half of them at a time through LDS
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
         l[qt] += xshfl(l[qt], 16);
@@ -318,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
         }
     }
 #pragma unroll
-    for (int half = 2; half >= 1; half >>= 1) {
+    for (int half = WAVES / 2; half >= 1; half >>= 1) {
         __syncthreads();
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
@@ -326,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
                 // element (row, d) of O^T in the lane's own order: one 16-byte run per (qt, n)
 #pragma unroll
                 for (int n = 0; n < kNT; ++n)
-                    *reinterpret_cast<f32x4*>(&sh_o[wave - half][((qt * kNT + n) * kWave + lane) * 4]) = O[qt][n];
+                    sh_o[((wave - half) * QT + qt) * kNT * kWave + n * kWave + lane] = O[qt][n];
                 if (g == 0) {
                     sh_ml[wave - half][qt * 16 + c][0] = m[qt];
                     sh_ml[wave - half][qt * 16 + c][1] = l[qt];
@@ -346,8 +505,7 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
                 l[qt] = l[qt] * wa + ol * wb;
 #pragma unroll
                 for (int n = 0; n < kNT; ++n)
-                    O[qt][n] = O[qt][n] * wa +
-                               *reinterpret_cast<const f32x4*>(&sh_o[wave][((qt * kNT + n) * kWave + lane) * 4]) * wb;
+                    O[qt][n] = O[qt][n] * wa + sh_o[(wave * QT + qt) * kNT * kWave + n * kWave + lane] * wb;
             }
         }
     }
@@ -358,8 +516,8 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
     for (int qt = 0; qt < QT; ++qt) {
         const int r = row0 + qt * 16 + c;
         if (r >= a.M) continue;
-        if (a.splits > 1) {
-            const long at = (static_cast<long>(bh) * a.splits + split) * a.M + r;
+        if (a.units) {
+            const long at = static_cast<long>(uh) * a.M + r;
             if (g == 0) {
                 a.part_ml[2 * at] = m[qt];
                 a.part_ml[2 * at + 1] = l[qt];
@@ -396,31 +554,74 @@ __global__ __launch_bounds__(kThreads) void kvq_attention_kernel(KvqAttnArgs a) 
     }
 }
 
-// Joins the splits: four elements a thread, D/4 neighbouring threads a row.
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads) void kvq_join_kernel(KvqAttnArgs a) {
-    const long row = (static_cast<long>(blockIdx.x) * kThreads + threadIdx.x) / (D / 4);
-    const int d = static_cast<int>(threadIdx.x % (D / 4)) * 4;
-    if (row >= static_cast<long>(a.c.B) * a.c.H * a.M) return;
-    const int r = static_cast<int>(row % a.M), bh = static_cast<int>(row / a.M);
+// Joins the units of each query row: D/4 neighbouring threads a row, four elements each, and S such groups that
+// share the row's units and add up through LDS.
+template <int D, int DT, int S>
+__global__ __launch_bounds__(kJoinThreads) void kvq_join_kernel(KvqAttnArgs a) {
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kRowsWg = kGroups / S;
+    const int d = static_cast<int>(threadIdx.x % kLanes) * 4;
+    const int grp = threadIdx.x / kLanes, sub = grp % S, rw = grp / S;
+    // rows of one (b, h) a workgroup, so that the units are found once
+    const int tiles = (a.M + kRowsWg - 1) / kRowsWg;
+    const int r = static_cast<int>(blockIdx.x % tiles) * kRowsWg + rw, bh = blockIdx.x / tiles;
     const int h = bh % a.c.H, b = bh / a.c.H;
-    const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
-    const long all = kvq_row_ok(pre, cnt, a.N, a.c.capacity) ? static_cast<long>(pre) + cnt : 0;
-    const long rounds = (all + kRound - 1) / kRound;
-    const long per = (rounds + a.splits - 1) / a.splits;
-    const int used = per ? static_cast<int>((rounds + per - 1) / per) : 0;   // splits that hold keys
-    const long at0 = static_cast<long>(bh) * a.splits * a.M + r;
-    float m = -INFINITY;
-    for (int s = 0; s < used; ++s) m = fmaxf(m, a.part_ml[2 * (at0 + static_cast<long>(s) * a.M)]);
-    float l = 0.f;
+    const int per = kvq_per(a);
+    int used;
+    const int first = kvq_first_unit(a, b, per, used);
+    const bool live = r < a.M;
+    const long step = static_cast<long>(a.c.H) * a.M;
+    const long at0 = (static_cast<long>(first) * a.c.H + h) * a.M + (live ? r : 0);
+    float m = -INFINITY, l = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < used; ++s) {
-        const long at = at0 + static_cast<long>(s) * a.M;
-        const float ms = a.part_ml[2 * at], ls = a.part_ml[2 * at + 1];
-        const float w = ms == -INFINITY ? 0.f : exp2_fast((ms - m) * a.cexp);
-        l += ls * w;
-        o += *reinterpret_cast<const f32x4*>(a.part_o + at * D + d) * w;
+    for (int s0 = sub; s0 < used; s0 += 4 * S) {
+        // four units at a time: their loads are independent
+        float ms[4], ls[4];
+        f32x4 os[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int s = min(s0 + e * S, used - 1);
+            const long at = at0 + s * step;
+            ms[e] = a.part_ml[2 * at];
+            ls[e] = a.part_ml[2 * at + 1];
+            os[e] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + d);
+        }
+        float mn = m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mn = fmaxf(mn, ms[e]);
+        const float w = m == -INFINITY ? 0.f : exp2_fast((m - mn) * a.cexp);
+        l *= w;
+        o *= w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float we = ms[e] == -INFINITY || s0 + e * S >= used ? 0.f : exp2_fast((ms[e] - mn) * a.cexp);
+            l += s0 + e * S < used ? ls[e] * we : 0.f;
+            o += os[e] * we;
+        }
+        m = mn;
     }
+    if (S > 1) {
+        __shared__ float sh[kGroups][kLanes][4];
+        __shared__ float sml[kGroups][2];
+        *reinterpret_cast<f32x4*>(sh[grp][threadIdx.x % kLanes]) = o;
+        if (d == 0) sml[grp][0] = m, sml[grp][1] = l;
+        __syncthreads();
+        if (sub != 0) return;
+        float mn = m;
+#pragma unroll
+        for (int e = 1; e < S; ++e) mn = fmaxf(mn, sml[grp + e][0]);
+        const float w = m == -INFINITY ? 0.f : exp2_fast((m - mn) * a.cexp);
+        l *= w;
+        o *= w;
+#pragma unroll
+        for (int e = 1; e < S; ++e) {
+            const float me = sml[grp + e][0];
+            const float we = me == -INFINITY ? 0.f : exp2_fast((me - mn) * a.cexp);
+            l += sml[grp + e][1] * we;
+            o += *reinterpret_cast<const f32x4*>(sh[grp + e][threadIdx.x % kLanes]) * we;
+        }
+        m = mn;
+    }
+    if (!live) return;
     const bool empty = l == 0.f;
     const float inv = empty ? 0.f : 1.f / l;
     const long at = (static_cast<long>(b) * a.N + r / a.G) * a.Hq + h * a.G + r % a.G;
@@ -434,39 +635,56 @@ __global__ __launch_bounds__(kThreads) void kvq_join_kernel(KvqAttnArgs a) {
         *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at * D + d) = o;
 }
 
-int query_tiles(int D, int dtype, int M) {
-    const int most = (D == 256 || dtype == 0) ? 2 : 4;
-    const int t = (M + 15) / 16;
-    return t >= most ? most : (t == 3 ? 4 : t);
+template <int D, int DT, int S> void join(const KvqAttnArgs& a, hipStream_t s) {
+    constexpr int rows = kJoinThreads / (D / 4) / S;
+    const unsigned grid = static_cast<unsigned>(a.c.B) * a.c.H * ((a.M + rows - 1) / rows);
+    kvq_join_kernel<D, DT, S><<<dim3(grid), kJoinThreads, 0, s>>>(a);
 }
 
-template <int D, int DT, int QT> void attend(const KvqAttnArgs& a, hipStream_t s, Timing t) {
-    const long units = static_cast<long>(a.c.B) * a.c.H * a.splits;
-    const dim3 grid(static_cast<unsigned>((units + 7) / 8 * 8 * a.row_tiles));
-    launch_timed(t, kvq_attention_kernel<D, DT, QT>, grid, dim3(kThreads), 0, s, a);
+template <int D, int DT, int QT, int WAVES> void attend(const KvqAttnArgs& a, hipStream_t s, Timing t) {
+    const long uh = static_cast<long>(a.units ? a.units : a.c.B) * a.c.H;
+    const dim3 grid(static_cast<unsigned>((uh + 7) / 8 * 8 * a.row_tiles));
+    launch_timed(t, kvq_attention_kernel<D, DT, QT, WAVES>, grid, dim3(WAVES * kWave), 0, s, a);
 }
+// 16-row tiles of a workgroup's queries: two share each key's conversion where the registers allow two waves a SIMD
+// (16 wide with bf16, D = 128: 27 nodes x 4 heads at 4096 keys 110 us, 32 wide 78, 64 wide 107).
+constexpr int most_tiles(int D, int DT) { return DT == 1 || D == 64 ? 2 : 1; }
+int query_tiles(int D, int dtype, int M) { return M > 16 ? most_tiles(D, dtype) : 1; }
+
 template <int D, int DT> void attend(const KvqAttnArgs& a, hipStream_t s, Timing t) {
-    switch (query_tiles(D, DT, a.M)) {
-        case 1: attend<D, DT, 1>(a, s, t); break;
-        case 2: attend<D, DT, 2>(a, s, t); break;
-        default:
-            if constexpr (D != 256 && DT == 1) attend<D, DT, 4>(a, s, t);
+    if (a.q_tiles == 2) {
+        if constexpr (most_tiles(D, DT) == 2) attend<D, DT, 2, 4>(a, s, t);
+    } else if (a.waves == 8) {
+        attend<D, DT, 1, 8>(a, s, t);
+    } else {
+        attend<D, DT, 1, 4>(a, s, t);
     }
-    if (a.splits > 1) {
-        const long threads = static_cast<long>(a.c.B) * a.c.H * a.M * (D / 4);
-        kvq_join_kernel<D, DT><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), kThreads, 0, s>>>(a);
-    }
+    if (!a.units) return;
+    if (a.units >= 4 * a.c.B) join<D, DT, 4>(a, s);     // many units a row
+    else join<D, DT, 1>(a, s);
 }
 
 }  // namespace
 
 void kvq_attention_plan(KvqAttnArgs& a) {
-    const int rows = 16 * query_tiles(a.c.D, a.dtype, a.M);
+    static const char* e1 = getenv("KVQ_TARGET");
+    static const char* e3 = getenv("KVQ_DIRECT");
+    const int target = e1 ? atoi(e1) : 512;
+    a.q_tiles = query_tiles(a.c.D, a.dtype, a.M);
+    const int rows = 16 * a.q_tiles;
     a.row_tiles = (a.M + rows - 1) / rows;
     const long items = static_cast<long>(a.c.B) * a.c.H * a.row_tiles;
-    const long most = (static_cast<long>(a.c.capacity) + kRound - 1) / kRound;
-    long n = (1024 + items - 1) / items;
-    a.splits = static_cast<int>(n < most ? n : most);
+    a.units = 0;
+    a.min_per = 2;
+    a.waves = 4;
+    const int direct = e3 ? atoi(e3) : 1024;
+    if (items < target && a.c.capacity > direct) {
+        a.units = static_cast<int>(target / (static_cast<long>(a.c.H) * a.row_tiles)) + a.c.B;
+        const long chunks = (static_cast<long>(a.c.capacity) + kChunk - 1) / kChunk * a.c.B + a.c.B;
+        if (a.units > chunks) a.units = static_cast<int>(chunks);
+    } else if (items < target && a.q_tiles == 1) {
+        a.waves = 8;
+    }
 }
 
 hipError_t launch_kvq_attention(const KvqAttnArgs& a, hipStream_t s, Timing t) {
