@@ -392,11 +392,13 @@ void carve_kvq_parts(Carver& c, KvqAttnArgs& a) {
     const size_t rows = static_cast<size_t>(a.units) * a.c.H * a.M;
     a.part_o = c.take<float>(rows * a.c.D);
     a.part_ml = c.take<float>(rows * 2);
+    a.first_unit = c.take<int32_t>(static_cast<size_t>(a.c.B) + 1);
 }
 
-void carve_kvq_gaps(Carver& c, KvqEvictArgs& a) {
+void carve_kvq_plan(Carver& c, KvqEvictArgs& a) {
     a.gap_stride = a.keep < a.c.capacity - a.keep ? a.keep : a.c.capacity - a.keep;
-    a.gaps = c.take<int32_t>(static_cast<size_t>(a.c.B) * a.c.H * a.gap_stride);
+    a.plan = c.take<int32_t>(static_cast<size_t>(a.c.B) * a.c.H * a.gap_stride * 2);
+    a.moves = c.take<int32_t>(static_cast<size_t>(a.c.B) * a.c.H);
 }
 
 #define SV_TRY(expr)                                  \
@@ -1180,6 +1182,8 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
     a.Hq = q_heads;
     a.G = q_heads / a.c.H;
     a.N = N;
+    // exact while row * G < 2^32: rows are below 65536 * G
+    a.magic = a.G > 1 && a.G < 256 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0;
     a.lse = lse;
     a.prefix = prefix;
     a.path = path;
@@ -1202,7 +1206,7 @@ size_t spec_kvq_evict_workspace_bytes(int B, int heads, int capacity, int keep) 
     a.c.capacity = capacity;
     a.keep = keep;
     Carver c(nullptr);
-    carve_kvq_gaps(c, a);
+    carve_kvq_plan(c, a);
     return c.off;
 }
 
@@ -1232,11 +1236,11 @@ int spec_kvq_evict(const spec_kvq_cache_t* cache, const float* scores, const int
     a.out_len = out_len;
     a.out_source = out_source;
     Carver size(nullptr);
-    carve_kvq_gaps(size, a);
+    carve_kvq_plan(size, a);
     rc = check_workspace(workspace, workspace_bytes, size.off);
     if (rc) return rc;
     Carver c(workspace);
-    carve_kvq_gaps(c, a);
+    carve_kvq_plan(c, a);
     ProfileScope prof;
     SV_TRY(launch_kvq_evict(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
     return SPEC_OK;

@@ -49,15 +49,17 @@ struct KvqAttnArgs {
     float cexp;                         // scale * log2(e): scores in base 2
     void* out;
     float* out_lse;
-    int q_tiles, row_tiles, waves;      // 16-row tiles of a workgroup, workgroups a unit, waves a workgroup
+    int q_tiles, row_tiles, waves;      // 16-row tiles of a wave's queries, workgroups a unit, waves a workgroup
     int units, min_per;                 // parts of the batch's key axis and their least chunks; 0: one a batch row
     float* part_o;                      // [units][H][M][D] (units > 0)
     float* part_ml;                     // [units][H][M][2]
+    int32_t* first_unit;                // [B + 1]
 };
 struct KvqScoreArgs {
     KvqCache c;
     KvqRows q;
     int dtype, Hq, G, N;
+    uint32_t magic;                     // ceil(2^32 / G): row / G = high word of row * magic (1 < G < 256), or 0
     const float* lse;
     const int32_t* prefix;
     const int32_t* path;
@@ -79,8 +81,9 @@ struct KvqEvictArgs {
     int32_t* out_positions;
     int32_t* out_len;
     int32_t* out_source;
-    int32_t* gaps;                      // [B*H][min(keep, capacity - keep)] slots to fill
-    int gap_stride;
+    int32_t* plan;                      // [B*H][gap_stride][2]: the slot to fill, and the one it is filled from
+    int32_t* moves;                     // [B*H] entries of the plan
+    int gap_stride;                     // min(keep, capacity - keep), the most moves there can be
 };
 
 hipError_t launch_kvq_append(const KvqAppendArgs& a, hipStream_t s, Timing t = {});

@@ -2,8 +2,8 @@
 //
 // For a cache head, the M = N*G query rows (N tokens, G query heads sharing the
 // head) meet keys s in one pass with a running maximum and sum: S = q . K_s,
-// P = exp2(c*(S - m)), O += P V_s, where c = scale*log2(e) and m is the largest
-// S so far.  Workgroups split the key axis; their (m, l, O) join at the end.
+// P = exp2(c*(S - m)), O += P V_s, where c = scale*log2(e) and m follows the
+// largest S so far.  Parts of the key axis join at the end.
 //
 // A wave takes 32 keys a step and 16*QT query rows, on 16x16x32 bf16 MFMAs in the
 // transposed form, S^T = K Q^T and O^T = V^T P^T, so that nothing crosses lanes
@@ -19,8 +19,11 @@
 // key where the product wants two keys of one element: one byte permute each.
 //
 // float32 queries enter as three bf16 parts (exact) and P as two.
-
-#include <stdlib.h>
+//
+// Where the rows are few the cache's bytes bound it, so the key axis is what is
+// spread: the waves of a workgroup take 32 keys each in turn and join through
+// LDS, and workgroups take units of the batch's whole key axis, alike whatever
+// the lengths, which a second kernel joins.
 
 #include "kvq.hpp"
 
@@ -28,9 +31,8 @@ namespace sv {
 
 namespace {
 
-constexpr int kStep = 32;                               // keys a wave takes at a time
+constexpr int kStep = 32;                               // keys of one step
 constexpr int kChunk = 128;                             // units of the key axis' split
-constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
 #if SV_KVQ_DEVICE
@@ -47,6 +49,325 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, p);
 }
 
+#if SV_KVQ_DEVICE
+// A buffer descriptor: loads past `bytes` give zeros and touch nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
+}
+#endif
+
+// A call's split of the key axis.  Batch rows hold pre + cnt slots each, in whole
+// chunks; a unit is `per` chunks of one batch row, and the units are numbered
+// through the batch, so that a long row gets many and a short one few and all
+// of them cost the same.  Every workgroup finds its own from the lengths (the
+// host does not know them): row b has ceil(chunks(b) / per) units.
+__device__ __forceinline__ int kvq_chunks(const KvqAttnArgs& a, int b) {
+    const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
+    return kvq_row_ok(pre, cnt, a.N, a.c.capacity) ? static_cast<int>((static_cast<long>(pre) + cnt + kChunk - 1) / kChunk)
+                                                   : 0;
+}
+__device__ __forceinline__ int wave_scan_int(int v) {   // inclusive
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int t = __shfl_up(v, o, kWave);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+// Chunks a unit holds: the fewest for which the batch has no more than a.units units.
+__device__ __forceinline__ int kvq_per(const KvqAttnArgs& a) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const auto units = [&](int per) {
+        int n = 0;
+        for (int b0 = 0; b0 < a.c.B; b0 += kWave)
+            n += wave_sum(b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0);
+        return __builtin_amdgcn_readfirstlane(n);       // the same in every lane, kept in a scalar register
+    };
+    int most = 1;
+    for (int b0 = 0; b0 < a.c.B; b0 += kWave) most = max(most, b0 + lane < a.c.B ? kvq_chunks(a, b0 + lane) : 0);
+    int lo = a.min_per, hi = max(__builtin_amdgcn_readfirstlane(wave_max_int(most)), lo);
+    while (lo < hi) {                                   // one a batch row, at hi = the longest, always fits
+        const int mid = (lo + hi) / 2;
+        if (units(mid) <= a.units) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+// Batch row and place in it of unit u, and how many units the row has; false past the last unit.
+__device__ __forceinline__ bool kvq_unit(const KvqAttnArgs& a, int u, int per, int& b, int& split, int& mine) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int base = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
+        const int n = b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0;
+        const int incl = wave_scan_int(n);
+        const unsigned long long past = __ballot(base + incl > u);   // (u, base and per are scalars, and so b and split)
+        if (past) {
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(past)) - 1);
+            b = b0 + l;
+            mine = bcast(n, l);
+            split = u - base - (bcast(incl, l) - mine);
+            return true;
+        }
+        base += bcast(incl, kWave - 1);
+    }
+    return false;
+}
+// The units' first numbers by batch row (and their count at the end), for the kernel that joins them.
+__device__ __forceinline__ void kvq_note_units(const KvqAttnArgs& a, int per) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int base = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
+        const int n = b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0;
+        const int incl = wave_scan_int(n);
+        if (b0 + lane < a.c.B) a.first_unit[b0 + lane] = base + incl - n;
+        base += bcast(incl, kWave - 1);
+    }
+    if (lane == 0) a.first_unit[a.c.B] = base;
+}
+
+// Query rows as the B operand of S^T: lane (c, g) holds elements g*D/4 .. of row c.  bf16 rows are one part, float32
+// rows three whose sum is the value.
+template <int D, int NQ, int DT>
+__device__ __forceinline__ void load_query(const KvqRows& q, long off, bool live, int g, u32x4 (&out)[NQ][D / 32]) {
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        const long i = off + g * (D / 4) + 8 * s;
+        if (DT == 1) {
+            const u32x4 z = {0, 0, 0, 0};
+            out[0][s] = live ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(q.data) + i) : z;
+        } else {
+            float x[8] = {};
+            if (live) {
+                const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(q.data) + i);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(q.data) + i + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = a[e], x[4 + e] = b[e];
+            }
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                    x[2 * e] -= bf16_lo(w[e]);
+                    x[2 * e + 1] -= bf16_hi(w[e]);
+                }
+                out[p][s] = w;
+            }
+        }
+    }
+}
+
+// The queries of a wave: row, token (-1: no query here) and, for a tree, the new
+// tokens each sees as bits (the four lanes of a query read 16 mask bytes each).
+template <int QT> struct Queries {
+    int tok[QT];
+    unsigned long long tree[QT];
+    __device__ __forceinline__ void place(const KvqAttnArgs& a, int row0, int cnt, int c) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            const int r = row0 + qt * 16 + c;
+            tok[qt] = r < a.M && r / a.G < cnt ? r / a.G : -1;
+        }
+    }
+    // Whether some of slots first .. first+31 are hidden from some query of rows row0 .. (or lie past the end).
+    __device__ static __forceinline__ bool edge(const KvqAttnArgs& a, long first, long pre, int row0) {
+        return first + kStep > pre + (a.mask ? 0 : row0 / a.G + 1);
+    }
+    __device__ __forceinline__ void read_mask(const KvqAttnArgs& a, int b, int cnt, int g) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            const uint8_t* row = a.mask + b * a.mask_batch + static_cast<long>(max(tok[qt], 0)) * a.N;
+            unsigned bits = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int node = 16 * g + e;
+                bits |= static_cast<unsigned>((row[min(node, a.N - 1)] != 0) & (node < cnt)) << e;
+            }
+            const unsigned half = bits << (16 * (g & 1));
+            unsigned w0 = g < 2 ? half : 0u, w1 = g < 2 ? 0u : half;
+            w0 |= xshfl(w0, 16);
+            w0 |= xshfl(w0, 32);
+            w1 |= xshfl(w1, 16);
+            w1 |= xshfl(w1, 32);
+            tree[qt] = (static_cast<unsigned long long>(w1) << 32) | w0;
+        }
+    }
+    // Scores of slots the query does not see become -inf; node0: the new token that the lane's first slot holds
+    // (negative: a committed slot, which every query sees).  Selects, not branches: a lane's eight slots may fall on
+    // either side of every limit.
+    __device__ __forceinline__ void hide(f32x4 (&S)[QT][2], int node0, bool masked) const {
+        if (masked) {
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int node = node0 + 16 * (j / 4) + j % 4;
+                    const bool sees = (node < 0) | ((node < 64) & static_cast<int>((tree[qt] >> (node & 63)) & 1u));
+                    S[qt][j / 4][j % 4] = sees ? S[qt][j / 4][j % 4] : -INFINITY;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    S[qt][j / 4][j % 4] = node0 + 16 * (j / 4) + j % 4 <= tok[qt] ? S[qt][j / 4][j % 4] : -INFINITY;
+        }
+    }
+};
+
+// Running maximum, sum and output of a wave's queries.  m follows the true
+// maximum within a factor of 2^8 of the probabilities (slack): sums stay as exact
+// in float32, a bf16 keeps its eight bits at any size, and a step whose scores
+// stay below needs no exchange between the lanes and no rescaling.
+template <int D, int QT, int NP> struct Softmax {
+    static constexpr int kNT = D / 16;                  // 16-row tiles of O^T
+    f32x4 O[QT][kNT];
+    float m[QT], l[QT];
+    __device__ __forceinline__ Softmax() {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            m[qt] = -INFINITY;
+            l[qt] = 0.f;
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) O[qt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+    __device__ static __forceinline__ float slack(float cexp) { return fminf(8.f / cexp, 1e30f); }
+    __device__ __forceinline__ void weigh(const f32x4 (&S)[QT][2], u32x4 (&P)[QT][NP], float cexp, float slack) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            float mx = S[qt][0][0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) mx = fmaxf(mx, S[qt][j / 4][j % 4]);
+            if (__ballot(mx > m[qt] + slack) != 0ull) {
+                mx = fmaxf(mx, xshfl(mx, 16));
+                mx = fmaxf(mx, xshfl(mx, 32));
+                const float mn = fmaxf(m[qt], mx);
+                const float al = m[qt] == -INFINITY ? 0.f : exp2_fast((m[qt] - mn) * cexp);
+                l[qt] *= al;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) O[qt][n] *= al;
+                m[qt] = mn;
+            }
+            const float mc = m[qt] == -INFINITY ? 0.f : m[qt] * cexp;
+            float p[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p[j] = exp2_fast(fmaf(S[qt][j / 4][j % 4], cexp, -mc));
+                l[qt] += p[j];
+            }
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    P[qt][x][e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+                    p[2 * e] -= bf16_lo(P[qt][x][e]);
+                    p[2 * e + 1] -= bf16_hi(P[qt][x][e]);
+                }
+            }
+        }
+    }
+    // The sums over the keys of all four g-groups; queries that are not there give nothing.
+    __device__ __forceinline__ void finish(const int (&tok)[QT]) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            l[qt] += xshfl(l[qt], 16);
+            l[qt] += xshfl(l[qt], 32);
+            if (tok[qt] < 0) {
+                m[qt] = -INFINITY;
+                l[qt] = 0.f;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) O[qt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+    }
+    // Rows row0 .. of (unit, h) `uh` as a part to be joined, or as the call's output.  O^T tile n, register i is
+    // element (D/16)*(4g + i) + n of query c.
+    template <int DT>
+    __device__ __forceinline__ void write(const KvqAttnArgs& a, int row0, int b, int h, long uh, bool part, int c,
+                                          int g) const {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            const int r = row0 + qt * 16 + c;
+            if (r >= a.M) continue;
+            if (part) {
+                const long at = uh * a.M + r;
+                if (g == 0) {
+                    a.part_ml[2 * at] = m[qt];
+                    a.part_ml[2 * at + 1] = l[qt];
+                }
+                float* o = a.part_o + at * D + (D / 4) * g;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < kNT; n += 4)
+                        *reinterpret_cast<f32x4*>(o + (D / 16) * i + n) =
+                            f32x4{O[qt][n][i], O[qt][n + 1][i], O[qt][n + 2][i], O[qt][n + 3][i]};
+            } else {
+                const long at = (static_cast<long>(b) * a.N + r / a.G) * a.Hq + h * a.G + r % a.G;
+                const bool empty = l[qt] == 0.f;
+                const float inv = empty ? 0.f : 1.f / l[qt];
+                if (g == 0 && a.out_lse)
+                    a.out_lse[at] = empty ? -INFINITY : (m[qt] * a.cexp + __builtin_amdgcn_logf(l[qt])) * 0.69314718056f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const long d = at * D + (D / 4) * g + (D / 16) * i;
+#pragma unroll
+                    for (int n = 0; n < kNT; n += 4) {
+                        const float o0 = O[qt][n][i] * inv, o1 = O[qt][n + 1][i] * inv, o2 = O[qt][n + 2][i] * inv,
+                                    o3 = O[qt][n + 3][i] * inv;
+                        if (DT == 1)
+                            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + d + n) =
+                                u32x2{pack_bf16(o0, o1), pack_bf16(o2, o3)};
+                        else
+                            *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + d + n) = f32x4{o0, o1, o2, o3};
+                    }
+                }
+            }
+        }
+    }
+};
+
+// What a workgroup works on: batch row, head and a part of its key axis.
+struct Place {
+    int b, h, cnt;
+    long uh;                // (unit, head) index of its part
+    bool ok, part;          // the batch row is valid; its units are to be joined
+    long pre, k0, k1;       // committed slots; first key and the end of the unit (the row's slots may end before)
+};
+__device__ __forceinline__ bool kvq_place(const KvqAttnArgs& a, int uh, Place& p) {
+    p.uh = uh;
+    p.h = uh % a.c.H;
+    const int unit = uh / a.c.H;
+    int b = unit, split = 0, per = 0, mine = 1;
+    if (a.units) {
+        per = kvq_per(a);
+        if (blockIdx.x == 0 && wave_id() == 0) kvq_note_units(a, per);
+        if (!kvq_unit(a, unit, per, b, split, mine)) return false;
+    } else if (b >= a.c.B) {
+        return false;
+    }
+    p.b = b;
+    p.part = mine > 1;
+    p.pre = a.prefix[b];
+    p.cnt = a.counts ? a.counts[b] : a.N;
+    p.ok = kvq_row_ok(static_cast<int>(p.pre), p.cnt, a.N, a.c.capacity);
+    p.k0 = static_cast<long>(split) * per * kChunk;
+    p.k1 = a.units ? p.k0 + static_cast<long>(per) * kChunk : a.c.capacity;
+    if (!p.ok) p.pre = p.cnt = 0;
+    return true;
+}
+// End of the slots that rows row0 .. row0 + rows - 1 see (0: no query there).
+__device__ __forceinline__ long kvq_limit(const KvqAttnArgs& a, const Place& p, int row0, int rows) {
+    const int end = min(p.cnt, (min(row0 + rows, a.M) - 1) / a.G + 1);
+    return row0 < a.M && row0 / a.G < end ? p.pre + (a.mask ? p.cnt : end) : 0;
+}
+
+constexpr int kJoinThreads = 256;
+
 // The lane's codes and scales of one step, as loaded.
 template <int D> struct Raw {
     static constexpr int kKW = D / 32;                  // words of a quarter K row
@@ -54,12 +375,6 @@ template <int D> struct Raw {
     uint32_t k[2][kKW], ks[2];
     uint32_t v[8][kVW], vs[8];
 };
-
-#if SV_KVQ_DEVICE
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
-}
-#endif
 
 // Reads keys through buffer descriptors that end at the last visible slot: what
 // lies past it comes back as zeros (code 0, scale 0) and costs no traffic, so
@@ -126,219 +441,64 @@ template <int D> struct Loader {
     }
 };
 
-// A call's split of the key axis.  Batch rows hold pre + cnt slots each, in whole
-// chunks; a unit is `per` chunks of one batch row, and the units are numbered
-// through the batch, so that a long row gets many and a short one few and all
-// of them cost the same.  Every workgroup finds its own from the lengths (the
-// host does not know them): units_of(b) = ceil(chunks(b) / per), with the
-// smallest `per` that keeps their number within a.units.
-__device__ __forceinline__ int kvq_chunks(const KvqAttnArgs& a, int b) {
-    const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
-    return kvq_row_ok(pre, cnt, a.N, a.c.capacity) ? static_cast<int>((static_cast<long>(pre) + cnt + kChunk - 1) / kChunk)
-                                                   : 0;
-}
-__device__ __forceinline__ int wave_scan_int(int v) {   // inclusive
-    const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const int t = __shfl_up(v, o, kWave);
-        if (lane >= o) v += t;
-    }
-    return v;
-}
-// Chunks a unit holds.
-__device__ __forceinline__ int kvq_per(const KvqAttnArgs& a) {
-    const int lane = threadIdx.x & (kWave - 1);
-    long total = 0;
-    for (int b0 = 0; b0 < a.c.B; b0 += kWave) total += wave_sum(b0 + lane < a.c.B ? kvq_chunks(a, b0 + lane) : 0);
-    const long room = a.units - a.c.B;
-    const int per = static_cast<int>(max((total + room - 1) / room, static_cast<long>(a.min_per)));
-    return __builtin_amdgcn_readfirstlane(per);         // the same in every lane, kept in a scalar register
-}
-// Batch row and place in it of unit u; false past the last unit.
-__device__ __forceinline__ bool kvq_unit(const KvqAttnArgs& a, int u, int per, int& b, int& split) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int base = 0;
-    for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
-        const int n = b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0;
-        const int incl = wave_scan_int(n);
-        const unsigned long long past = __ballot(base + incl > u);   // (u, base and per are scalars, and so b and split)
-        if (past) {
-            const int l = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(past)) - 1);
-            b = b0 + l;
-            split = u - base - (bcast(incl, l) - bcast(n, l));
-            return true;
-        }
-        base += bcast(incl, kWave - 1);
-    }
-    return false;
-}
-// First unit of batch row b, and how many it has.
-__device__ __forceinline__ int kvq_first_unit(const KvqAttnArgs& a, int b, int per, int& mine) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int first = 0;
-    mine = 0;
-    for (int b0 = 0; b0 <= b; b0 += kWave) {
-        const int r = b0 + lane;
-        const int n = r < a.c.B ? (kvq_chunks(a, r) + per - 1) / per : 0;
-        first += __builtin_amdgcn_readfirstlane(wave_sum(r < b ? n : 0));
-        if (b < b0 + kWave) mine = bcast(n, b - b0);
-    }
-    return first;
-}
-
-// Query rows as the B operand of S^T: lane (c, g) holds elements g*D/4 .. of row c.  bf16 rows are one part, float32
-// rows three whose sum is the value.
-template <int D, int NQ, int DT>
-__device__ __forceinline__ void load_query(const KvqRows& q, long off, bool live, int g, u32x4 (&out)[NQ][D / 32]) {
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-        const long i = off + g * (D / 4) + 8 * s;
-        if (DT == 1) {
-            const u32x4 z = {0, 0, 0, 0};
-            out[0][s] = live ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(q.data) + i) : z;
-        } else {
-            float x[8] = {};
-            if (live) {
-                const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(q.data) + i);
-                const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(q.data) + i + 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = a[e], x[4 + e] = b[e];
-            }
-#pragma unroll
-            for (int p = 0; p < NQ; ++p) {
-                u32x4 w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-                    x[2 * e] -= bf16_lo(w[e]);
-                    x[2 * e + 1] -= bf16_hi(w[e]);
-                }
-                out[p][s] = w;
-            }
-        }
-    }
-}
-
 // Waves a SIMD to fit the registers of one variant to.
 constexpr int attend_occupancy(int D, int DT, int QT) {
-#ifdef OCC2
-    if (D == 128 && QT == 2 && DT == 1) return OCC2;
-#endif
     const int size = (D / 64) * QT * (DT == 1 ? 2 : 3);     // of the sums and the queries
-    return size <= 4 ? 3 : size <= 16 ? 2 : 1;
+    return size <= 4 ? 3 : 2;
 }
-
-// Keeps the instructions on either side apart, so that operands are not formed long before their use.
-template <bool ON> __device__ __forceinline__ void fence() {
+// Queries stay in registers where that leaves room for two waves a SIMD, and are read from LDS every step where it
+// does not (D = 256, 32 rows: 27 nodes x 4 heads, 16 batch rows at 4096 keys, 94 us against 68).
+constexpr bool queries_in_lds(int D, int DT, int QT) { return D == 256 && QT == 2; }
+template <bool ON> __device__ __forceinline__ void fence() {        // keeps operands from being formed early
 #if SV_KVQ_DEVICE
     if (ON) __builtin_amdgcn_sched_barrier(0);
 #endif
 }
-
-// Query operands kept in registers up to this many, in LDS beyond.
-constexpr bool queries_in_lds(int D, int DT, int QT) { return QT * (DT == 1 ? 1 : 3) * (D / 8) > 48; }
-constexpr int max2(int a, int b) { return a > b ? a : b; }
+constexpr int larger(int a, int b) { return a > b ? a : b; }
 
 template <int D, int DT, int QT, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq_attention_kernel(KvqAttnArgs a) {
     constexpr int NQ = DT == 1 ? 1 : 3, NP = DT == 1 ? 1 : 2;
-    constexpr int kNT = D / 16;                         // 16-row tiles of O^T
-    constexpr int kRows = 16 * QT;
+    constexpr int kNT = D / 16, kRows = 16 * QT;
     constexpr int kRound = kStep * WAVES;               // keys a workgroup takes at a time
     // (unit, head) pairs of one residue mod 8 with all their row tiles: neighbours in time on one XCD, whose L2 serves
     // the row tiles that read the same keys
-    const int RT = a.row_tiles;
     const int x = blockIdx.x % 8, y = blockIdx.x / 8;
-    const int rt = y % RT, uh = (y / RT) * 8 + x;
-    const int h = uh % a.c.H, unit = uh / a.c.H;
+    const int row0 = y % a.row_tiles * kRows;
+    Place pl;
+    if (!kvq_place(a, y / a.row_tiles * 8 + x, pl)) return;
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
     const int c = lane & 15, g = lane >> 4;
+    const long lim = kvq_limit(a, pl, row0, kRows);
+    const long k0 = pl.k0, k1 = min(pl.k1, lim);
 
-    int b = unit, split = 0, per = 0;
-    if (a.units) {
-        per = kvq_per(a);
-        if (!kvq_unit(a, unit, per, b, split)) return;
-    } else if (b >= a.c.B) {
-        return;
-    }
-    const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
-    const bool ok = kvq_row_ok(pre, cnt, a.N, a.c.capacity);
-    const int row0 = rt * kRows;
-    // tokens of this tile that exist, and the slots any of them may see
-    const int tok_end = ok ? min(cnt, (min(row0 + kRows, a.M) - 1) / a.G + 1) : 0;
-    const bool any = ok && row0 / a.G < tok_end;
-    const long lim = any ? static_cast<long>(pre) + (a.mask ? cnt : tok_end) : 0;
-    const long k0 = a.units ? static_cast<long>(split) * per * kChunk : 0;
-    const long k1 = a.units ? min(k0 + static_cast<long>(per) * kChunk, lim) : lim;
-
-    // LDS: the queries during the loop, the waves' sums after it
+    Queries<QT> qs;
+    qs.place(a, row0, pl.cnt, c);
+    // LDS: the queries during the loop (if they are there), the waves' sums after it
     constexpr bool kQL = queries_in_lds(D, DT, QT);
-    constexpr int kQWords = kQL ? QT * NQ * (D / 32) * kWave : 0, kJoinWords = WAVES / 2 * kRows * D / 4;
-    __shared__ u32x4 shared[max2(kQWords, kJoinWords)];
-    u32x4* const sh_q = shared + lane;
-    f32x4* const sh_o = reinterpret_cast<f32x4*>(shared);
+    constexpr int kQOps = kQL ? QT * NQ * (D / 32) : 0, kSumOps = WAVES / 2 * QT * kNT;
+    __shared__ u32x4 shared[larger(kQOps, kSumOps)][kWave];
     __shared__ float sh_ml[WAVES / 2][kRows][2];
-
-    // this lane's query (one a tile): its row, token, and whether it exists
     u32x4 Q[kQL ? 1 : QT][NQ][D / 32];
-    int tok[QT];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
+        if (kQL && qt % WAVES != wave) continue;
         const int r = row0 + qt * 16 + c;
-        tok[qt] = r / a.G;
-        const bool live = r < a.M && tok[qt] < (ok ? cnt : 0);
-        const int hq = h * a.G + r % a.G;
-        const long off = b * a.q.batch + tok[qt] * a.q.pos + hq * a.q.head;
-        if (!kQL) {
-            load_query<D, NQ, DT>(a.q, off, live, g, Q[kQL ? 0 : qt]);
-        } else if (qt % WAVES == wave) {
-            load_query<D, NQ, DT>(a.q, off, live, g, Q[0]);
+        const long off = pl.b * a.q.batch + max(qs.tok[qt], 0) * a.q.pos + (pl.h * a.G + r % a.G) * a.q.head;
+        load_query<D, NQ, DT>(a.q, off, qs.tok[qt] >= 0, g, Q[kQL ? 0 : qt]);
+        if (kQL) {
 #pragma unroll
             for (int p = 0; p < NQ; ++p)
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) sh_q[((qt * NQ + p) * (D / 32) + x) * kWave] = Q[0][p][x];
+                for (int s = 0; s < D / 32; ++s) shared[(qt * NQ + p) * (D / 32) + s][lane] = Q[0][p][s];
         }
-        if (!live) tok[qt] = -1;
     }
     if (kQL) __syncthreads();
+    if (a.mask && k1 > pl.pre) qs.read_mask(a, pl.b, pl.cnt, g);
 
-    // a tree's mask rows as bits: the new tokens m < cnt this lane's queries see
-    unsigned long long tree[QT];
-    if (a.mask && k1 > pre) {
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-            const uint8_t* row = a.mask + b * a.mask_batch + static_cast<long>(max(tok[qt], 0)) * a.N;
-            unsigned bits = 0;                          // tokens 16g .. 16g+15, the other three groups' follow
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int node = 16 * g + e;
-                bits |= static_cast<unsigned>((row[min(node, a.N - 1)] != 0) & (node < cnt)) << e;
-            }
-            const unsigned lo = bits << (16 * (g & 1)), hi = lo;
-            unsigned w0 = g < 2 ? lo : 0u, w1 = g < 2 ? 0u : hi;
-            w0 |= xshfl(w0, 16);
-            w0 |= xshfl(w0, 32);
-            w1 |= xshfl(w1, 16);
-            w1 |= xshfl(w1, 32);
-            tree[qt] = (static_cast<unsigned long long>(w1) << 32) | w0;
-        }
-    }
-
-    f32x4 O[QT][kNT];
-    float m[QT], l[QT];
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        m[qt] = -INFINITY;
-        l[qt] = 0.f;
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) O[qt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-
-    const Loader<D> ld(a.c, b, h, lane);
-    // m follows the true maximum within a factor of 2^8 of the probabilities: sums stay exact in float32, a bf16
-    // keeps its eight bits at any size, and a step whose scores stay below needs no exchange between the lanes
-    const float slack = fminf(8.f / a.cexp, 1e30f);
+    const Loader<D> ld(a.c, pl.b, pl.h, lane);
+    Softmax<D, QT, NP> sm;
+    const float slack = sm.slack(a.cexp);
     Raw<D> cur;
     long kb = k0 + kStep * wave;
     if (kb < k1) {
@@ -352,7 +512,7 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) S[qt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (kQL) asm volatile("" ::: "memory");         // queries are read again every step, not kept in registers
+        if (kQL) asm volatile("" ::: "memory");         // read again every step, not kept
 #pragma unroll
         for (int s = 0; s < D / 32; ++s) {
             u32x4 A[2];
@@ -366,7 +526,7 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
             for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
                 for (int p = 0; p < NQ; ++p) {
-                    const u32x4 q = kQL ? sh_q[((qt * NQ + p) * (D / 32) + s) * kWave] : Q[kQL ? 0 : qt][p][s];
+                    const u32x4 q = kQL ? shared[(qt * NQ + p) * (D / 32) + s][lane] : Q[kQL ? 0 : qt][p][s];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) S[qt][t] = mfma(A[t], q, S[qt][t]);
                 }
@@ -374,64 +534,9 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
             fence<kQL>();
         }
         ld.load_k(cur, kb + kRound, k1);
-        const bool edge = kb + kStep > pre;             // some of the 32 slots are new ones, or past the end
-        if (edge) {
-            // selects, not branches: a lane's eight slots may fall on either side of every limit
-            const int node0 = static_cast<int>(kb - pre) + 4 * g;
-            if (a.mask) {
-#pragma unroll
-                for (int qt = 0; qt < QT; ++qt) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int node = node0 + 16 * (j / 4) + j % 4;
-                        const bool sees = (node < 0) | ((node < 64) & static_cast<int>((tree[qt] >> (node & 63)) & 1u));
-                        S[qt][j / 4][j % 4] = sees ? S[qt][j / 4][j % 4] : -INFINITY;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        S[qt][j / 4][j % 4] =
-                            node0 + 16 * (j / 4) + j % 4 <= tok[qt] ? S[qt][j / 4][j % 4] : -INFINITY;
-            }
-        }
-
-        // running maximum and sum; P rounded to bf16 parts
+        if (qs.edge(a, kb, pl.pre, row0)) qs.hide(S, static_cast<int>(kb - pl.pre) + 4 * g, a.mask != nullptr);
         u32x4 P[QT][NP];
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-            float mx = S[qt][0][0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) mx = fmaxf(mx, S[qt][j / 4][j % 4]);
-            if (__ballot(mx > m[qt] + slack) != 0ull) {
-                mx = fmaxf(mx, xshfl(mx, 16));
-                mx = fmaxf(mx, xshfl(mx, 32));
-                const float mn = fmaxf(m[qt], mx);
-                const float al = m[qt] == -INFINITY ? 0.f : exp2_fast((m[qt] - mn) * a.cexp);
-                l[qt] *= al;
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) O[qt][n] *= al;
-                m[qt] = mn;
-            }
-            const float mc = m[qt] == -INFINITY ? 0.f : m[qt] * a.cexp;
-            float p[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                p[j] = exp2_fast(fmaf(S[qt][j / 4][j % 4], a.cexp, -mc));
-                l[qt] += p[j];
-            }
-#pragma unroll
-            for (int x = 0; x < NP; ++x) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    P[qt][x][e] = pack_bf16(p[2 * e], p[2 * e + 1]);
-                    p[2 * e] -= bf16_lo(P[qt][x][e]);
-                    p[2 * e + 1] -= bf16_hi(P[qt][x][e]);
-                }
-            }
-        }
+        sm.weigh(S, P, a.cexp, slack);
 
         // O^T += V^T P^T
         float vsc[8];
@@ -454,9 +559,9 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
-                for (int x = 0; x < NP; ++x) {
-                    O[qt][2 * pr] = mfma(lo, P[qt][x], O[qt][2 * pr]);
-                    O[qt][2 * pr + 1] = mfma(hi, P[qt][x], O[qt][2 * pr + 1]);
+                for (int p = 0; p < NP; ++p) {
+                    sm.O[qt][2 * pr] = mfma(lo, P[qt][p], sm.O[qt][2 * pr]);
+                    sm.O[qt][2 * pr + 1] = mfma(hi, P[qt][p], sm.O[qt][2 * pr + 1]);
                 }
             }
             fence<kQL>();
@@ -464,31 +569,20 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
         ld.load_v(cur, kb + kRound, k1);
     }
 
-    // join the waves: the sums of a lane's four g-groups, then the waves, half of them at a time through LDS
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        l[qt] += xshfl(l[qt], 16);
-        l[qt] += xshfl(l[qt], 32);
-        if (tok[qt] < 0) {                              // no query here (a padded token, or the tile's end)
-            m[qt] = -INFINITY;
-            l[qt] = 0.f;
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) O[qt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-    }
+    // join the waves, half of them at a time through LDS
+    f32x4(*const sh_o)[kWave] = reinterpret_cast<f32x4(*)[kWave]>(shared);
+    sm.finish(qs.tok);
 #pragma unroll
     for (int half = WAVES / 2; half >= 1; half >>= 1) {
         __syncthreads();
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
-                // element (row, d) of O^T in the lane's own order: one 16-byte run per (qt, n)
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-                    sh_o[((wave - half) * QT + qt) * kNT * kWave + n * kWave + lane] = O[qt][n];
+                for (int n = 0; n < kNT; ++n) sh_o[((wave - half) * QT + qt) * kNT + n][lane] = sm.O[qt][n];
                 if (g == 0) {
-                    sh_ml[wave - half][qt * 16 + c][0] = m[qt];
-                    sh_ml[wave - half][qt * 16 + c][1] = l[qt];
+                    sh_ml[wave - half][qt * 16 + c][0] = sm.m[qt];
+                    sh_ml[wave - half][qt * 16 + c][1] = sm.l[qt];
                 }
             }
         }
@@ -497,61 +591,18 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
                 const float om = sh_ml[wave][qt * 16 + c][0], ol = sh_ml[wave][qt * 16 + c][1];
-                const float mn = fmaxf(m[qt], om);
-                const float wa = m[qt] == -INFINITY ? 0.f : exp2_fast((m[qt] - mn) * a.cexp);
+                const float mn = fmaxf(sm.m[qt], om);
+                const float wa = sm.m[qt] == -INFINITY ? 0.f : exp2_fast((sm.m[qt] - mn) * a.cexp);
                 const float wb = om == -INFINITY ? 0.f : exp2_fast((om - mn) * a.cexp);
-                m[qt] = mn;
+                sm.m[qt] = mn;
                 // a sum that is NaN stays NaN whatever its maximum
-                l[qt] = l[qt] * wa + ol * wb;
+                sm.l[qt] = sm.l[qt] * wa + ol * wb;
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-                    O[qt][n] = O[qt][n] * wa + sh_o[(wave * QT + qt) * kNT * kWave + n * kWave + lane] * wb;
+                for (int n = 0; n < kNT; ++n) sm.O[qt][n] = sm.O[qt][n] * wa + sh_o[(wave * QT + qt) * kNT + n][lane] * wb;
             }
         }
     }
-    if (wave != 0) return;
-
-    // O^T tile n, register i is element (D/16)*(4g + i) + n of query c
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        const int r = row0 + qt * 16 + c;
-        if (r >= a.M) continue;
-        if (a.units) {
-            const long at = static_cast<long>(uh) * a.M + r;
-            if (g == 0) {
-                a.part_ml[2 * at] = m[qt];
-                a.part_ml[2 * at + 1] = l[qt];
-            }
-            float* o = a.part_o + at * D + (D / 4) * g;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int n = 0; n < kNT; n += 4)
-                    *reinterpret_cast<f32x4*>(o + (D / 16) * i + n) =
-                        f32x4{O[qt][n][i], O[qt][n + 1][i], O[qt][n + 2][i], O[qt][n + 3][i]};
-        } else {
-            const int tk = r / a.G, hq = h * a.G + r % a.G;
-            const long at = (static_cast<long>(b) * a.N + tk) * a.Hq + hq;
-            const bool empty = l[qt] == 0.f;
-            const float inv = empty ? 0.f : 1.f / l[qt];
-            if (g == 0 && a.out_lse)
-                a.out_lse[at] = empty ? -INFINITY : (m[qt] * a.cexp + __builtin_amdgcn_logf(l[qt])) * 0.69314718056f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const long d = at * D + (D / 4) * g + (D / 16) * i;
-#pragma unroll
-                for (int n = 0; n < kNT; n += 4) {
-                    const float o0 = O[qt][n][i] * inv, o1 = O[qt][n + 1][i] * inv, o2 = O[qt][n + 2][i] * inv,
-                                o3 = O[qt][n + 3][i] * inv;
-                    if (DT == 1)
-                        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + d + n) =
-                            u32x2{pack_bf16(o0, o1), pack_bf16(o2, o3)};
-                    else
-                        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + d + n) = f32x4{o0, o1, o2, o3};
-                }
-            }
-        }
-    }
+    if (wave == 0) sm.template write<DT>(a, row0, pl.b, pl.h, pl.uh, pl.part, c, g);
 }
 
 // Joins the units of each query row: D/4 neighbouring threads a row, four elements each, and S such groups that
@@ -565,9 +616,8 @@ __global__ __launch_bounds__(kJoinThreads) void kvq_join_kernel(KvqAttnArgs a) {
     const int tiles = (a.M + kRowsWg - 1) / kRowsWg;
     const int r = static_cast<int>(blockIdx.x % tiles) * kRowsWg + rw, bh = blockIdx.x / tiles;
     const int h = bh % a.c.H, b = bh / a.c.H;
-    const int per = kvq_per(a);
-    int used;
-    const int first = kvq_first_unit(a, b, per, used);
+    const int first = a.first_unit[b], used = a.first_unit[b + 1] - first;
+    if (used == 1) return;                              // written by its one unit
     const bool live = r < a.M;
     const long step = static_cast<long>(a.c.H) * a.M;
     const long at0 = (static_cast<long>(first) * a.c.H + h) * a.M + (live ? r : 0);
@@ -647,9 +697,8 @@ template <int D, int DT, int QT, int WAVES> void attend(const KvqAttnArgs& a, hi
     launch_timed(t, kvq_attention_kernel<D, DT, QT, WAVES>, grid, dim3(WAVES * kWave), 0, s, a);
 }
 // 16-row tiles of a workgroup's queries: two share each key's conversion where the registers allow two waves a SIMD
-// (16 wide with bf16, D = 128: 27 nodes x 4 heads at 4096 keys 110 us, 32 wide 78, 64 wide 107).
+// (float32 at D = 128 and 256 does not: 27 nodes x 4 heads, 16 batch rows at 4096 keys, 69 us against 61 with one).
 constexpr int most_tiles(int D, int DT) { return DT == 1 || D == 64 ? 2 : 1; }
-int query_tiles(int D, int dtype, int M) { return M > 16 ? most_tiles(D, dtype) : 1; }
 
 template <int D, int DT> void attend(const KvqAttnArgs& a, hipStream_t s, Timing t) {
     if (a.q_tiles == 2) {
@@ -666,23 +715,24 @@ template <int D, int DT> void attend(const KvqAttnArgs& a, hipStream_t s, Timing
 
 }  // namespace
 
+// The key axis is split so that a launch has about 512 workgroups (two a compute unit: 131071 keys, 8 heads, 32 rows
+// each: 39 + 5 us; 1024 workgroups 51 + 12, 256 41 + 5), into units of 256 keys at least.  A cache of up to 1024 slots
+// is not: its one launch beats two (1000 keys, 8 heads, one token: 9.6 us against 8 + 3.5 and a second launch), with
+// eight waves where the rows fit one tile.
 void kvq_attention_plan(KvqAttnArgs& a) {
-    static const char* e1 = getenv("KVQ_TARGET");
-    static const char* e3 = getenv("KVQ_DIRECT");
-    const int target = e1 ? atoi(e1) : 512;
-    a.q_tiles = query_tiles(a.c.D, a.dtype, a.M);
+    a.q_tiles = a.M > 16 ? most_tiles(a.c.D, a.dtype) : 1;
     const int rows = 16 * a.q_tiles;
     a.row_tiles = (a.M + rows - 1) / rows;
-    const long items = static_cast<long>(a.c.B) * a.c.H * a.row_tiles;
+    const long target = 512, items = static_cast<long>(a.c.B) * a.c.H * a.row_tiles;
     a.units = 0;
     a.min_per = 2;
     a.waves = 4;
-    const int direct = e3 ? atoi(e3) : 1024;
-    if (items < target && a.c.capacity > direct) {
-        a.units = static_cast<int>(target / (static_cast<long>(a.c.H) * a.row_tiles)) + a.c.B;
-        const long chunks = (static_cast<long>(a.c.capacity) + kChunk - 1) / kChunk * a.c.B + a.c.B;
-        if (a.units > chunks) a.units = static_cast<int>(chunks);
-    } else if (items < target && a.q_tiles == 1) {
+    if (items >= target) return;
+    if (a.c.capacity > 1024) {
+        const long units = target / (static_cast<long>(a.c.H) * a.row_tiles);
+        const long chunks = (static_cast<long>(a.c.capacity) + kChunk - 1) / kChunk * a.c.B;
+        a.units = static_cast<int>(units < chunks ? units : chunks);
+    } else if (a.q_tiles == 1) {
         a.waves = 8;
     }
 }

@@ -22,6 +22,8 @@ import torch
 from . import SPEC_BF16, SPEC_F32, SpecError, _check, _stream, lib
 
 _DIMS = (64, 128, 256)
+# the handle of a device's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
 _CODES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
 
 
@@ -73,6 +75,13 @@ class KVQCache:
         self._args = _CacheArgs(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                                 B, H, S, D, *k_codes.stride()[:3], *k_scales.stride()[:3])
         self._ref = ctypes.addressof(self._args)
+        self._needs = {}                # workspace bytes of the calls made so far, by their sizes
+
+    def _need(self, fn, *sizes) -> int:
+        n = self._needs.get(sizes)
+        if n is None:
+            n = self._needs[sizes] = int(fn())
+        return n
 
 
 def _overlaps(t: torch.Tensor) -> bool:
@@ -96,15 +105,15 @@ def new_kvq_cache(B: int, heads: int, capacity: int, head_dim: int, device) -> K
 
 def _tensor(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """Checks a contiguous tensor of the call and returns its address."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.get_device() == device.index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _optional(t: Optional[torch.Tensor], name: str, dtype, shape, device):
@@ -113,27 +122,27 @@ def _optional(t: Optional[torch.Tensor], name: str, dtype, shape, device):
 
 def _rows(t: torch.Tensor, name: str, cache: KVQCache) -> _Rows:
     """The strided rows [B, N, heads, D] of a call."""
-    if t.dim() != 4 or t.shape[0] != cache.B or t.shape[3] != cache.head_dim or t.shape[1] < 1 or t.shape[2] < 1:
-        raise ValueError(f"{name} must be [{cache.B}, N, heads, {cache.head_dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.head_dim or shape[1] < 1 or shape[2] < 1:
+        raise ValueError(f"{name} must be [{cache.B}, N, heads, {cache.head_dim}], got {tuple(shape)}")
     if t.dtype not in _CODES:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.device != cache.device:
+    if t.get_device() != cache.device.index:
         raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
     s = t.stride()
     if s[3] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # the stride of a dimension of one element never counts
-    return _Rows(t.data_ptr(), s[0] if t.shape[0] > 1 else 0, s[1] if t.shape[1] > 1 else 0,
-                 s[2] if t.shape[2] > 1 else 0)
+    return _Rows(t.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
 
 
 def _call(fn, what: str, device: torch.device, *args) -> None:
     """One library call on the device's current stream, with that device current."""
     if torch.cuda.current_device() == device.index:
-        rc = fn(*args, _stream(device))
+        rc = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream(device))
+            rc = fn(*args, _raw_stream(device.index))
     if rc:
         _check(rc, what)
 
@@ -217,7 +226,7 @@ def kvq_attention(q: torch.Tensor, cache: KVQCache, prefix: torch.Tensor, *, mas
         _tensor(o, "out", q.dtype, (B, N, Hq, D), dev)
         _tensor(lse, "out lse", torch.float32, (B, N, Hq), dev)
     code = _CODES[q.dtype]
-    need = lib().spec_kvq_attention_workspace_bytes(B, N, Hq, cache.heads, D, cache.capacity, code)
+    need = cache._need(lambda: kvq_attention_workspace_bytes(cache, N, Hq, q.dtype), N, Hq, code)
     wp, _ws = _scratch(need, dev, workspace)
     _call(lib().spec_kvq_attention, "spec_kvq_attention", dev, ctypes.addressof(rq), code, Hq, N, cache._ref,
           _tensor(prefix, "prefix", torch.int32, row, dev), _optional(counts, "counts", torch.int32, row, dev),
@@ -289,7 +298,7 @@ def kvq_evict(cache: KVQCache, scores: torch.Tensor, positions: torch.Tensor, le
     out_positions = positions if out_positions is None else out_positions
     new_len = torch.empty(row, dtype=torch.int32, device=dev)
     source = torch.empty((cache.B, cache.heads, keep), dtype=torch.int32, device=dev)
-    need = lib().spec_kvq_evict_workspace_bytes(cache.B, cache.heads, cache.capacity, keep)
+    need = cache._need(lambda: kvq_evict_workspace_bytes(cache, keep), keep)
     wp, _ws = _scratch(need, dev, workspace)
     _call(lib().spec_kvq_evict, "spec_kvq_evict", dev, cache._ref,
           _tensor(scores, "scores", torch.float32, slots, dev),
