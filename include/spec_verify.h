@@ -516,7 +516,8 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
  * slot*code_pos bytes from k_codes / v_codes, scales likewise.  Codes: base and
  * strides multiples of 16 bytes; scales: of D/32 bytes.  No two rows may share
  * bytes (zero strides where B, heads or capacity exceed 1 are SPEC_EINVAL).
- * code_pos and scale_pos at most 2^24. */
+ * B and heads at most 65535, capacity at most 2^30, code_pos and scale_pos at
+ * most 2^24. */
 typedef struct {
     void* k_codes;
     void* k_scales;

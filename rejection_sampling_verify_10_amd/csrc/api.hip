@@ -354,7 +354,8 @@ bool kvq_sizes_ok(int B, int H, int N, int G) { return N <= 65536 && kvq_count_o
 int take_cache(const spec_kvq_cache_t* c, KvqCache& o) {
     if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return SPEC_EINVAL;
     if (c->B < 1 || c->heads < 1 || c->capacity < 1 || c->head_dim < 1) return SPEC_EINVAL;
-    if (!kvq_dim_ok(c->head_dim) || c->B > 65535 || c->heads > 65535) return SPEC_EUNSUPPORTED;
+    if (!kvq_dim_ok(c->head_dim) || c->B > 65535 || c->heads > 65535 || c->capacity > (1 << 30))
+        return SPEC_EUNSUPPORTED;
     const int64_t codes = c->head_dim / 2, scales = c->head_dim / kQBlock;
     const auto strides_ok = [c](int64_t batch, int64_t head, int64_t pos, int64_t row, int64_t unit) {
         if (batch < 0 || head < 0 || pos < 0 || batch % unit || head % unit || pos % unit) return false;

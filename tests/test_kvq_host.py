@@ -46,7 +46,7 @@ BAD_CACHES = [
     (dict(code_pos=0), EINVAL), (dict(code_head=0), EINVAL), (dict(code_batch=0), EINVAL),
     (dict(scale_pos=2), EINVAL), (dict(scale_pos=0), EINVAL), (dict(scale_head=-4), EINVAL),
     (dict(head_dim=96, code_pos=64), EUNSUPPORTED), (dict(code_pos=1 << 25), EUNSUPPORTED),
-    (dict(B=65536), EUNSUPPORTED), (dict(heads=65536), EUNSUPPORTED),
+    (dict(capacity=(1 << 30) + 1), EUNSUPPORTED), (dict(B=65536), EUNSUPPORTED), (dict(heads=65536), EUNSUPPORTED),
 ]
 
 
