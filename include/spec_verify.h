@@ -603,11 +603,15 @@ int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads
  * >= path_stride, or >= N), a path that is not token 0 followed by increasing
  * tokens below N, prefix < 0, or prefix + d + 1 > capacity; they are left as
  * they were.  path_stride <= SPEC_MAX_NODES where path is given.
+ * workspace: spec_kvq_score_workspace_bytes(...) bytes (path_stride 0: no path;
+ * may be 0), any contents; left as scratch.
  */
+size_t spec_kvq_score_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim, int capacity,
+                                      int path_stride, spec_dtype_t dtype);
 int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, int N, const float* lse,
                    const spec_kvq_cache_t* cache, const int32_t* prefix, const int32_t* path, int path_stride,
                    const int32_t* accept_len, float scale, float* scores, int32_t* positions, const int32_t* seen,
-                   void* hip_stream);
+                   void* workspace, size_t workspace_bytes, void* hip_stream);
 
 /*
  * spec_kvq_evict -- cut every head of a batch row down to `keep` rows, in

@@ -95,7 +95,9 @@ def lib() -> ctypes.CDLL:
         L.spec_kvq_attention_workspace_bytes.restype = Z
         L.spec_kvq_attention.argtypes = [P, I, I, I, P, P, P, P, LL, F, P, P, P, Z, P]
         L.spec_kvq_attention.restype = I
-        L.spec_kvq_score.argtypes = [P, I, I, I, P, P, P, P, I, P, F, P, P, P, P]
+        L.spec_kvq_score_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
+        L.spec_kvq_score_workspace_bytes.restype = Z
+        L.spec_kvq_score.argtypes = [P, I, I, I, P, P, P, P, I, P, F, P, P, P, P, Z, P]
         L.spec_kvq_score.restype = I
         L.spec_kvq_evict_workspace_bytes.argtypes = [I, I, I, I]
         L.spec_kvq_evict_workspace_bytes.restype = Z
@@ -560,4 +562,4 @@ def read_probe(src: torch.Tensor, sink: torch.Tensor) -> None:
 
 
 from .kvq import (KVQCache, kvq_append, kvq_attention, kvq_attention_workspace_bytes, kvq_commit, kvq_evict,  # noqa: E402,F401
-                  kvq_evict_workspace_bytes, kvq_read, kvq_score, new_kvq_cache)
+                  kvq_evict_workspace_bytes, kvq_read, kvq_score, kvq_score_workspace_bytes, new_kvq_cache)

@@ -396,6 +396,10 @@ void carve_kvq_parts(Carver& c, KvqAttnArgs& a) {
     a.first_unit = c.take<int32_t>(static_cast<size_t>(a.c.B) + 1);
 }
 
+void carve_kvq_sums(Carver& c, KvqScoreArgs& a) {
+    if (a.segs > 1) a.part = c.take<float>(static_cast<size_t>(a.segs) * a.c.B * a.c.H * a.c.capacity);
+}
+
 void carve_kvq_plan(Carver& c, KvqEvictArgs& a) {
     a.gap_stride = a.keep < a.c.capacity - a.keep ? a.keep : a.c.capacity - a.keep;
     a.plan = c.take<int32_t>(static_cast<size_t>(a.c.B) * a.c.H * a.gap_stride * 2);
@@ -1161,10 +1165,32 @@ int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads
     return SPEC_OK;
 }
 
+size_t spec_kvq_score_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim, int capacity,
+                                      int path_stride, spec_dtype_t dtype) {
+    if (B < 1 || N < 1 || heads < 1 || q_heads < 1 || q_heads % heads != 0 || capacity < 1 || path_stride < 0) return 0;
+    if (!kvq_dim_ok(head_dim) || (dtype != SPEC_F32 && dtype != SPEC_BF16)) return 0;
+    if (!kvq_sizes_ok(B, heads, N, q_heads / heads)) return 0;
+    static const int32_t a_path = 0;
+    KvqScoreArgs a{};
+    a.c.B = B;
+    a.c.H = heads;
+    a.c.D = head_dim;
+    a.c.capacity = capacity;
+    a.dtype = dtype;
+    a.N = N;
+    a.G = q_heads / heads;
+    a.path = path_stride ? &a_path : nullptr;           // only whether there is one counts
+    a.path_stride = path_stride ? path_stride : N;
+    kvq_score_plan(a);
+    Carver c(nullptr);
+    carve_kvq_sums(c, a);
+    return c.off;
+}
+
 int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, int N, const float* lse,
                    const spec_kvq_cache_t* cache, const int32_t* prefix, const int32_t* path, int path_stride,
                    const int32_t* accept_len, float scale, float* scores, int32_t* positions, const int32_t* seen,
-                   void* hip_stream) {
+                   void* workspace, size_t workspace_bytes, void* hip_stream) {
     KvqScoreArgs a{};
     int rc = take_cache(cache, a.c);
     if (rc) return rc;
@@ -1183,8 +1209,6 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
     a.Hq = q_heads;
     a.G = q_heads / a.c.H;
     a.N = N;
-    // exact while row * G < 2^32: rows are below 65536 * G
-    a.magic = a.G > 1 && a.G < 256 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0;
     a.lse = lse;
     a.prefix = prefix;
     a.path = path;
@@ -1194,6 +1218,13 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
     a.scores = scores;
     a.positions = positions;
     a.seen = seen;
+    kvq_score_plan(a);
+    Carver size(nullptr);
+    carve_kvq_sums(size, a);
+    rc = check_workspace(workspace, workspace_bytes, size.off);
+    if (rc) return rc;
+    Carver c(workspace);
+    carve_kvq_sums(c, a);
     ProfileScope prof;
     SV_TRY(launch_kvq_score(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
     return SPEC_OK;

@@ -59,7 +59,6 @@ struct KvqScoreArgs {
     KvqCache c;
     KvqRows q;
     int dtype, Hq, G, N;
-    uint32_t magic;                     // ceil(2^32 / G): row / G = high word of row * magic (1 < G < 256), or 0
     const float* lse;
     const int32_t* prefix;
     const int32_t* path;
@@ -69,6 +68,9 @@ struct KvqScoreArgs {
     float* scores;
     int32_t* positions;
     const int32_t* seen;
+    int q_tiles;                        // 16-row tiles kept in registers; 0: rows in LDS
+    int key_wgs, segs;                  // workgroups along the keys of a head, and along its rows
+    float* part;                        // [segs][B*H][capacity] (segs > 1)
 };
 struct KvqEvictArgs {
     KvqCache c;
@@ -91,6 +93,7 @@ hipError_t launch_kvq_read(const KvqReadArgs& a, hipStream_t s, Timing t = {});
 // How an attention call is cut up: fills a.q_tiles .. a.min_per.
 void kvq_attention_plan(KvqAttnArgs& a);
 hipError_t launch_kvq_attention(const KvqAttnArgs& a, hipStream_t s, Timing t = {});
+void kvq_score_plan(KvqScoreArgs& a);    // fills q_tiles, key_wgs and segs
 hipError_t launch_kvq_score(const KvqScoreArgs& a, hipStream_t s, Timing t = {});
 hipError_t launch_kvq_evict(const KvqEvictArgs& a, hipStream_t s, Timing t = {});
 

@@ -7,14 +7,13 @@
 // no atomics and the same bits every time.  Operands are laid out as in attention
 // (16x16x32 bf16 MFMAs, lane (c, g) with c = lane % 16, g = lane / 16).
 //
-// A tree's path has a handful of rows: bound by the K codes.  A wave keeps all the
-// queries (16*QT rows) and streams keys, S = Q K^T, 32 a step: lane (c, g) gets
-// rows 4g + i against key c, so a key's sum is over registers and two exchanges.
-//
-// A prompt has thousands: bound by the exponentials.  The waves of a workgroup
-// hold the same 16*KT keys, converted once, and walk every WAVES-th tile of 16
-// rows, S^T = K Q^T: lane (c, g) adds up query c for keys 4g + i, and lanes and
-// waves are summed at the end.
+// A wave streams keys, S = Q K^T, 32 a step, against query rows 16 a tile: lane
+// (c, g) gets rows 4g + i against key c, so a key's sum is over registers and two
+// exchanges.  A tree's path has a handful of rows, kept in registers: bound by the
+// K codes.  More rows are kept in LDS, a lot of them at a time, for the eight
+// waves of a workgroup.  A prompt has thousands, bound by the exponentials, and
+// too few keys to fill the GPU: there the rows are split over workgroups as well,
+// whose sums meet in the workspace.
 
 #include "kvq.hpp"
 
@@ -66,265 +65,136 @@ __device__ __forceinline__ void put_weight(const KvqScoreArgs& a, int b, int h, 
     if (slot >= pre) a.positions[at] = a.seen[b] + (slot - pre);
 }
 
-// 16 query rows as loaded: lane (c, g) has elements 32s + 8g .. of row c, and its lse in base 2.
-template <int D, int DT> struct RowTile {
-    static constexpr int kVecs = D / 32 * (DT == 1 ? 1 : 2);
-    u32x4 w[kVecs];
-    float lse;
-    int tok;                                            // which accepted token; -1: no row
-};
-
-template <int D, int DT, int KT, int WAVES>
-__global__ __launch_bounds__(WAVES* kWave) void kvq_score_rows_kernel(KvqScoreArgs a) {
-    constexpr int NQ = DT == 1 ? 1 : 3;
-    constexpr int kKeys = 16 * KT, kVecs = RowTile<D, DT>::kVecs;
-    // heads side by side in the grid, so that one XCD (every eighth workgroup) has one head's queries in its L2
-    const int bhs = a.c.B * a.c.H, blocks = static_cast<int>(gridDim.x) / bhs;
-    const int bh = blockIdx.x % bhs, turn = blockIdx.x / bhs;
-    const int h = bh % a.c.H, b = bh / a.c.H;
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
-    const int c = lane & 15, g = lane >> 4;
-    const int pre = a.prefix[b], d = a.accept_len[b];
-    if (d < 0 || d >= a.N || d >= a.path_stride || pre < 0 || static_cast<long>(pre) + d + 1 > a.c.capacity) return;
-    const int all = pre + d + 1;                        // slots after the commit
-    // later keys have fewer rows: every other eight heads take them from the other end
-    const int blk = (bh / 8) & 1 ? blocks - 1 - turn : turn;
-    const int kb = blk * kKeys;
-    if (kb >= all) return;
-
-    // K rows of the wave's keys.  Elements are numbered 32s + 8g + j here, not 32g + 8s + j: a load of query rows, of
-    // which there are many, then takes 64 bytes of each row instead of every fourth 16
-    uint32_t raw[KT][D / 32], rs[KT][D == 256 ? 2 : 1];
-    const uint8_t* kc = a.c.kc + b * a.c.cb + h * a.c.ch;
-    const uint8_t* ks = a.c.ks + b * a.c.sb + h * a.c.sh;
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-        const long key = min(kb + 16 * t + c, all - 1);
-        const uint8_t* sp = ks + key * a.c.sp;
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s)
-            raw[t][s] = *reinterpret_cast<const uint32_t*>(kc + key * a.c.cp + 16 * s + 4 * g);
-        if (D == 64) rs[t][0] = *reinterpret_cast<const uint16_t*>(sp);
-        else rs[t][0] = *reinterpret_cast<const uint32_t*>(sp);
-        if (D == 256) rs[t][D == 256 ? 1 : 0] = *reinterpret_cast<const uint32_t*>(sp + 4);
+// What a wave that streams keys works with: two tiles of 16 keys a step, read ahead through buffer descriptors that
+// end at the last slot, and the scores its lanes add to.
+template <int D> struct KeyStream {
+    const uint8_t *kc, *ks;
+    float* scores;
+    long cp, sp;
+    uint32_t ko, kso;
+    int all, mine;                                      // slots; this lane's slot of a step's 32 (lanes of g < 2 write)
+    uint32_t k[2][D / 32], s[2];
+    float old;
+    __device__ __forceinline__ KeyStream(const KvqScoreArgs& a, int b, int h, int all, int lane) : all(all) {
+        const int c = lane & 15, g = lane >> 4;
+        kc = a.c.kc + b * a.c.cb + h * a.c.ch;
+        ks = a.c.ks + b * a.c.sb + h * a.c.sh;
+        scores = a.scores + (static_cast<long>(b) * a.c.H + h) * a.c.capacity;
+        cp = a.c.cp;
+        sp = a.c.sp;
+        ko = static_cast<uint32_t>(c * cp) + g * (D / 8);
+        kso = static_cast<uint32_t>(c * sp) + g * D / 128;
+        mine = (g & 1) * 16 + c;
     }
-
-    int node = lane;                                    // lane t holds path[t] of a tree
-    if (a.path) {
-        node = lane < a.path_stride ? a.path[static_cast<long>(b) * a.path_stride + lane] : 0;
-        const int before = __shfl_up(node, 1, kWave);
-        if (__ballot(lane <= d && (lane == 0 ? node != 0 : (node <= before || node >= a.N))) != 0ull) return;
-    }
-    const int rows = (d + 1) * a.G;
-    const auto load = [&](RowTile<D, DT>& r, int r0) {
-        const int row = r0 + c;
-        const bool live = row < rows;
-        const unsigned at = live ? row : 0;
-        const int t = a.G == 1 ? at : a.magic ? __umulhi(at, a.magic) : at / a.G;
-        const int tk = a.path ? __shfl(node, t, kWave) : t;
-        const int hq = h * a.G + (static_cast<int>(at) - t * a.G);
-        const long off = b * a.q.batch + tk * a.q.pos + hq * a.q.head + 8 * g;
-        const float lse = a.lse[(static_cast<long>(b) * a.N + tk) * a.Hq + hq] * 1.44269504089f;
-        // a query that saw nothing, or a row past the last, weighs nothing
-        r.lse = live && lse != -INFINITY ? lse : INFINITY;
-        r.tok = live ? t : -1;
-        const char* q = static_cast<const char*>(a.q.data) + off * (DT == 1 ? 2 : 4);
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) {
-            if (DT == 1) {
-                r.w[s] = *reinterpret_cast<const u32x4*>(q + 64 * s);
-            } else {
-                r.w[(2 * s) % kVecs] = *reinterpret_cast<const u32x4*>(q + 128 * s);
-                r.w[(2 * s + 1) % kVecs] = *reinterpret_cast<const u32x4*>(q + 128 * s + 16);
-            }
-        }
-    };
-
-    constexpr int step = 16 * WAVES;
-    // the first tile whose tokens see the keys
-    int r0 = (kb > pre ? (kb - pre) * a.G / 16 * 16 : 0) + 16 * wave;
-    RowTile<D, DT> ta, tb;
-    load(ta, r0);                                       // (past the last row: row 0, weighing nothing)
-
-    u32x4 A[KT][D / 32];
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) {
-            const float sc = scale_value(rs[t][D == 256 ? s / 4 : 0] >> (8 * (s % 4)) & 255u);
-            const uint32_t w = raw[t][s];
-            A[t][s] = u32x4{fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
-        }
-
-    float w[KT][4];
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[t][i] = 0.f;
-
-    const auto weigh = [&](const RowTile<D, DT>& cur, int r0) {
-        f32x4 S[KT];
-#pragma unroll
-        for (int k = 0; k < KT; ++k) S[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) {
-            u32x4 q[NQ];
-            if (DT == 1) {
-                q[0] = cur.w[s];
-            } else {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[e] = __uint_as_float(cur.w[(2 * s + e / 4) % kVecs][e % 4]);
-                bf16_parts<NQ>(x, [&](int p, const u32x4& w) { q[p] = w; });
-            }
-#pragma unroll
-            for (int p = 0; p < NQ; ++p)
-#pragma unroll
-                for (int k = 0; k < KT; ++k) S[k] = mfma(A[k][s], q[p], S[k]);
-        }
-        const bool part = kb + 16 * KT - 1 - pre > r0 / a.G;    // some key is newer than the tile's first token
-        const int node0 = kb - pre + 4 * g;
-#pragma unroll
-        for (int k = 0; k < KT; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float p = __builtin_amdgcn_exp2f(fmaf(S[k][i], a.cexp, -cur.lse));
-                if (part) p = node0 + 16 * k + i <= cur.tok ? p : 0.f;
-                w[k][i] += p;
-            }
-        }
-    };
-    // two tiles in turn: one is on its way while the other is weighed
-    for (; r0 < rows; r0 += 2 * step) {
-        load(tb, r0 + step);
-        weigh(ta, r0);
-        load(ta, r0 + 2 * step);
-        if (r0 + step < rows) weigh(tb, r0 + step);
-    }
-
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x = w[k][i];
-            x += xshfl(x, 1);
-            x += xshfl(x, 2);
-            x += xshfl(x, 4);
-            x += xshfl(x, 8);
-            w[k][i] = x;
-        }
-    }
-    __shared__ float sh[WAVES][kKeys];
-    if (c == 0) {
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sh[wave][16 * k + 4 * g + i] = w[k][i];
-    }
-    __syncthreads();
-    if (threadIdx.x < kKeys && kb + static_cast<int>(threadIdx.x) < all) {
-        float x = 0.f;
-#pragma unroll
-        for (int v = 0; v < WAVES; ++v) x += sh[v][threadIdx.x];
-        const int slot = kb + threadIdx.x;
-        const float old = a.scores[(static_cast<long>(b) * a.c.H + h) * a.c.capacity + slot];
-        put_weight(a, b, h, pre, slot, x, old);
-    }
-}
-
-// Few rows: the queries stay, the keys stream.
-template <int D, int DT, int QT>
-__global__ __launch_bounds__(kKeyWaves* kWave) void kvq_score_kernel(KvqScoreArgs a) {
-    constexpr int NQ = DT == 1 ? 1 : 3;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
-    const int c = lane & 15, g = lane >> 4;
-    const int pre = a.prefix[b], d = a.accept_len[b];
-    if (d < 0 || d >= a.N || d >= a.path_stride || pre < 0 || static_cast<long>(pre) + d + 1 > a.c.capacity) return;
-    const int all = pre + d + 1;                        // slots after the commit
-    const int stride = static_cast<int>(gridDim.x) * kKeyWaves * 32;
-    int kb = (static_cast<int>(blockIdx.x) * kKeyWaves + wave) * 32;
-    if (kb >= all) return;
-
-    // two tiles of 16 keys: codes and scales; past the last slot zeros
-    struct Raw {
-        uint32_t k[2][D / 32], s[2];
-        float old;                                      // the score this lane adds to
-    };
-    float* const scores = a.scores + (static_cast<long>(b) * a.c.H + h) * a.c.capacity;
-    const int mine = (g & 1) * 16 + c;                  // its slot of a step's 32 (lanes of g < 2 write)
-    [[maybe_unused]] const uint8_t* kc = a.c.kc + b * a.c.cb + h * a.c.ch;
-    [[maybe_unused]] const uint8_t* ks = a.c.ks + b * a.c.sb + h * a.c.sh;
-    [[maybe_unused]] const uint32_t ko = static_cast<uint32_t>(c * a.c.cp) + g * (D / 8);
-    [[maybe_unused]] const uint32_t kso = static_cast<uint32_t>(c * a.c.sp) + g * D / 128;
-    const auto load_k = [&](Raw& r, int kb) {
+    __device__ __forceinline__ void load(int kb) {
 #if SV_KVQ_DEVICE
-        r.old = scores[min(kb + mine, all - 1)];
-        const int n = max(min(all - kb, 32), 0), cp32 = static_cast<int>(a.c.cp), sp32 = static_cast<int>(a.c.sp);
-        const auto rk = rsrc(kc + kb * a.c.cp, n * cp32), rks = rsrc(ks + kb * a.c.sp, n * sp32);
+        old = scores[min(kb + mine, all - 1)];
+        const int n = max(min(all - kb, 32), 0), cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
+        const auto rk = rsrc(kc + kb * cp, n * cp32), rks = rsrc(ks + kb * sp, n * sp32);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (D == 64) {
                 const auto w = __builtin_amdgcn_raw_buffer_load_b64(rk, ko, 16 * t * cp32, 0);
-                r.k[t][0] = w[0], r.k[t][1] = w[1];
+                k[t][0] = w[0], k[t][1] = w[1];
             } else {
 #pragma unroll
                 for (int x = 0; x < D / 128; ++x) {
                     const auto w = __builtin_amdgcn_raw_buffer_load_b128(rk, ko + 16 * x, 16 * t * cp32, 0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r.k[t][(4 * x + e) % (D / 32)] = w[e];
+                    for (int e = 0; e < 4; ++e) k[t][(4 * x + e) % (D / 32)] = w[e];
                 }
             }
-            r.s[t] = D == 256 ? __builtin_amdgcn_raw_buffer_load_b16(rks, kso, 16 * t * sp32, 0)
-                              : __builtin_amdgcn_raw_buffer_load_b8(rks, kso, 16 * t * sp32, 0);
+            s[t] = D == 256 ? __builtin_amdgcn_raw_buffer_load_b16(rks, kso, 16 * t * sp32, 0)
+                            : __builtin_amdgcn_raw_buffer_load_b8(rks, kso, 16 * t * sp32, 0);
         }
 #endif
-    };
-    Raw cur;
-    load_k(cur, kb);
+    }
+    __device__ __forceinline__ u32x4 operand(int t, int x) const {
+        const float sc = scale_value(D == 256 && x >= 4 ? s[t] >> 8 : s[t]);
+        const uint32_t w = k[t][x];
+        return u32x4{fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
+    }
+};
 
-    int node = lane;                                    // lane t holds path[t] of a tree
-    if (a.path) {
+// The accepted tokens of a batch row.
+struct Accepted {
+    int pre, d, all, node;                              // node: lane t holds path[t] of a tree
+    __device__ __forceinline__ bool read(const KvqScoreArgs& a, int b) {
+        const int lane = threadIdx.x & (kWave - 1);
+        pre = a.prefix[b];
+        d = a.accept_len[b];
+        all = pre + d + 1;                              // slots after the commit
+        return !(d < 0 || d >= a.N || d >= a.path_stride || pre < 0 || static_cast<long>(pre) + d + 1 > a.c.capacity) &&
+               (node = lane, true);
+    }
+    __device__ __forceinline__ bool read_path(const KvqScoreArgs& a, int b) {
+        if (!a.path) return true;
+        const int lane = threadIdx.x & (kWave - 1);
         node = lane < a.path_stride ? a.path[static_cast<long>(b) * a.path_stride + lane] : 0;
         const int before = __shfl_up(node, 1, kWave);
-        if (__ballot(lane <= d && (lane == 0 ? node != 0 : (node <= before || node >= a.N))) != 0ull) return;
+        return __ballot(lane <= d && (lane == 0 ? node != 0 : (node <= before || node >= a.N))) == 0ull;
     }
-    const int rows = (d + 1) * a.G;
+};
+
+// One query row as loaded for an operand (elements 32g' .. of its lane's quarter) with its lse in base 2 and token.
+template <int D, int DT, int NQ>
+__device__ __forceinline__ void load_row(const KvqScoreArgs& a, const Accepted& ac, int b, int h, int row, int rows,
+                                         int g, u32x4 (&q)[NQ][D / 32], float& lse, int& tok) {
+    const int r = row < rows ? row : 0;
+    const int t = r / a.G;
+    const int tk = a.path ? __shfl(ac.node, t, kWave) : t;
+    const int hq = h * a.G + (r - t * a.G);
+    const char* p = static_cast<const char*>(a.q.data) +
+                    (b * a.q.batch + tk * a.q.pos + hq * a.q.head + g * (D / 4)) * (DT == 1 ? 2 : 4);
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        if (DT == 1) {
+            q[0][s] = reinterpret_cast<const u32x4*>(p)[s];
+        } else {
+            const f32x4 lo = reinterpret_cast<const f32x4*>(p)[2 * s], hi = reinterpret_cast<const f32x4*>(p)[2 * s + 1];
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
+            bf16_parts<NQ>(x, [&](int part, const u32x4& w) { q[part][s] = w; });
+        }
+    }
+    const float lse2 = a.lse[(static_cast<long>(b) * a.N + tk) * a.Hq + hq] * 1.44269504089f;
+    // a query that saw nothing, or a row past the last, weighs nothing
+    lse = row < rows && lse2 != -INFINITY ? lse2 : INFINITY;
+    tok = row < rows ? t : -1;
+}
+
+// Few rows: the queries stay in registers, the keys stream.
+template <int D, int DT, int QT>
+__global__ __launch_bounds__(kKeyWaves* kWave) void kvq_score_kernel(KvqScoreArgs a) {
+    constexpr int NQ = DT == 1 ? 1 : 3;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int lane = threadIdx.x & (kWave - 1), c = lane & 15, g = lane >> 4;
+    Accepted ac;
+    if (!ac.read(a, b)) return;
+    const int pre = ac.pre, all = ac.all;
+    const int stride = static_cast<int>(gridDim.x) * kKeyWaves * 32;
+    int kb = (static_cast<int>(blockIdx.x) * kKeyWaves + wave_id()) * 32;
+    if (kb >= all) return;
+    KeyStream<D> cur(a, b, h, all, lane);
+    cur.load(kb);
+    if (!ac.read_path(a, b)) return;
+    const int rows = (ac.d + 1) * a.G;
     u32x4 Q[QT][NQ][D / 32];
     float lse[QT][4];
     int tok[QT][4];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
         // lane (c, g) loads a quarter of row 16*qt + c, and keeps the lse and tokens of rows 16*qt + 4g + i
-        const int row = 16 * qt + c < rows ? 16 * qt + c : 0;
-        const int t = row / a.G;
-        const int tk = a.path ? __shfl(node, t, kWave) : t;
-        const int hq = h * a.G + (row - t * a.G);
-        const char* q = static_cast<const char*>(a.q.data) +
-                        (b * a.q.batch + tk * a.q.pos + hq * a.q.head + g * (D / 4)) * (DT == 1 ? 2 : 4);
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) {
-            if (DT == 1) {
-                Q[qt][0][s] = reinterpret_cast<const u32x4*>(q)[s];
-            } else {
-                const f32x4 lo = reinterpret_cast<const f32x4*>(q)[2 * s], hi = reinterpret_cast<const f32x4*>(q)[2 * s + 1];
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
-                bf16_parts<NQ>(x, [&](int p, const u32x4& w) { Q[qt][p][s] = w; });
-            }
-        }
-        const float lse2 = a.lse[(static_cast<long>(b) * a.N + tk) * a.Hq + hq] * 1.44269504089f;
-        // a query that saw nothing, or a row past the last, weighs nothing
-        const float l = 16 * qt + c < rows && lse2 != -INFINITY ? lse2 : INFINITY;
+        float l;
+        int t;
+        load_row<D, DT, NQ>(a, ac, b, h, 16 * qt + c, rows, g, Q[qt], l, t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             lse[qt][i] = lane_gather(l, 4 * g + i);
-            tok[qt][i] = 16 * qt + 4 * g + i < rows ? static_cast<int>(lane_gather(static_cast<uint32_t>(t), 4 * g + i)) : -1;
+            tok[qt][i] = static_cast<int>(lane_gather(static_cast<uint32_t>(t), 4 * g + i));
         }
     }
-
     for (; kb < all; kb += stride) {
         f32x4 S[2][QT];
 #pragma unroll
@@ -335,9 +205,7 @@ __global__ __launch_bounds__(kKeyWaves* kWave) void kvq_score_kernel(KvqScoreArg
         for (int s = 0; s < D / 32; ++s) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const float sc = scale_value(D == 256 && s >= 4 ? cur.s[t] >> 8 : cur.s[t]);
-                const uint32_t w = cur.k[t][s];
-                const u32x4 K = {fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
+                const u32x4 K = cur.operand(t, s);
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
@@ -345,7 +213,7 @@ __global__ __launch_bounds__(kKeyWaves* kWave) void kvq_score_kernel(KvqScoreArg
             }
         }
         const float old = cur.old;
-        load_k(cur, kb + stride);
+        cur.load(kb + stride);
         const bool part = kb + 31 > pre;                // some key is newer than the first token
         float x[2] = {0.f, 0.f};
 #pragma unroll
@@ -363,41 +231,172 @@ __global__ __launch_bounds__(kKeyWaves* kWave) void kvq_score_kernel(KvqScoreArg
             x[t] += xshfl(x[t], 16);
             x[t] += xshfl(x[t], 32);
         }
-        const int slot = kb + mine;
+        const int slot = kb + cur.mine;
         if (g < 2 && slot < all) put_weight(a, b, h, pre, slot, g ? x[1] : x[0], old);
     }
 }
 
-#ifndef SKT
-#define SKT 4
-#define SW 8
-#endif
-#ifndef SCORE_WGS
-#define SCORE_WGS 1024
-#endif
+// More rows: they stay in LDS, a lot of kRows at a time, and the keys stream once for each lot.
+constexpr int kLdsWaves = 8;
+constexpr int lds_rows(int D, int DT) { return 65536 / (2 * D * (DT == 1 ? 1 : 3)) / 16 * 16; }
+
+template <int D, int DT>
+__global__ __launch_bounds__(kLdsWaves* kWave) void kvq_score_lds_kernel(KvqScoreArgs a) {
+    constexpr int NQ = DT == 1 ? 1 : 3, kRows = lds_rows(D, DT), kTiles = kRows / 16;
+    __shared__ u32x4 sh_q[kTiles][NQ * (D / 32)][kWave];
+    __shared__ f32x4 sh_lse[kRows / 4];
+    __shared__ int sh_tok[kRows];
+    // heads side by side in the grid, so that one XCD (every eighth workgroup) has one head's queries in its L2
+    const int bhs = a.c.B * a.c.H, bh = blockIdx.x % bhs, turn = blockIdx.x / bhs;
+    const int seg = turn / a.key_wgs, block = turn % a.key_wgs;
+    const int h = bh % a.c.H, b = bh / a.c.H;
+    const int lane = threadIdx.x & (kWave - 1), c = lane & 15, g = lane >> 4, wave = wave_id();
+    Accepted ac;
+    if (!ac.read(a, b)) return;
+    const int pre = ac.pre, all = ac.all;
+    const int stride = a.key_wgs * kLdsWaves * 32, first = block * kLdsWaves * 32;
+    if (first >= all || !ac.read_path(a, b)) return;
+    const int rows = (ac.d + 1) * a.G;
+    // this segment's lots, as many for each segment as the row count needs
+    const int lots = (rows + kRows - 1) / kRows, per = (lots + a.segs - 1) / a.segs;
+    const int row0 = seg * per * kRows, row1 = min(row0 + per * kRows, rows);
+    float* const part = a.part ? a.part + (static_cast<long>(seg) * bhs + bh) * a.c.capacity : nullptr;
+    KeyStream<D> cur(a, b, h, all, lane);
+    bool again = false;                                 // the keys' sums of an earlier lot are there already
+    for (int lot = row0; lot < row1; lot += kRows) {
+        if (first - pre > (min(lot + kRows, row1) - 1) / a.G) continue;     // all its tokens are older than the keys
+        const int tiles = (min(row1 - lot, kRows) + 15) / 16;
+        __syncthreads();
+        for (int i = wave; i < tiles; i += kLdsWaves) {
+            u32x4 q[NQ][D / 32];
+            float l;
+            int t;
+            load_row<D, DT, NQ>(a, ac, b, h, lot + 16 * i + c, rows, g, q, l, t);
+#pragma unroll
+            for (int p = 0; p < NQ; ++p)
+#pragma unroll
+                for (int s = 0; s < D / 32; ++s) sh_q[i][p * (D / 32) + s][lane] = q[p][s];
+            if (g == 0) {
+                reinterpret_cast<float*>(sh_lse)[16 * i + c] = l;
+                sh_tok[16 * i + c] = t;
+            }
+        }
+        __syncthreads();
+        int kb = first + wave * 32;
+        if (kb < all) cur.load(kb);
+        for (; kb < all; kb += stride) {
+            u32x4 K[2][D / 32];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int s = 0; s < D / 32; ++s) K[t][s] = cur.operand(t, s);
+            const int slot = kb + cur.mine;
+            float old = cur.old;
+            if (part) old = again && slot < all ? part[slot] : 0.f;
+            cur.load(kb + stride);
+            float x[2] = {0.f, 0.f};
+            // from the first tile of the lot whose tokens see the keys
+            const int from = kb > pre ? max(((kb - pre) * a.G - lot) / 16, 0) : 0;
+            for (int i = from; i < tiles; ++i) {
+                f32x4 S[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int s = 0; s < D / 32; ++s)
+#pragma unroll
+                    for (int p = 0; p < NQ; ++p) {
+                        const u32x4 q = sh_q[i][p * (D / 32) + s][lane];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) S[t] = mfma(q, K[t][s], S[t]);
+                    }
+                const f32x4 lse = sh_lse[4 * i + g];
+                // whether some key is newer than the tile's first token
+                const bool edge = kb + 31 - pre > __builtin_amdgcn_readfirstlane(sh_tok[16 * i]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int key = kb + 16 * t + c - pre;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float p = __builtin_amdgcn_exp2f(fmaf(S[t][e], a.cexp, -lse[e]));
+                        if (edge) p = key <= sh_tok[16 * i + 4 * g + e] ? p : 0.f;
+                        x[t] += p;
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                x[t] += xshfl(x[t], 16);
+                x[t] += xshfl(x[t], 32);
+            }
+            if (g < 2 && slot < all) {
+                const float w = g ? x[1] : x[0];
+                if (part) part[slot] = old + w;
+                else if (again) cur.scores[slot] = old + w;
+                else put_weight(a, b, h, pre, slot, w, old);
+            }
+        }
+        again = true;
+    }
+    if (!part || again) return;
+    for (int kb = first; kb < all; kb += stride)        // every lot was older
+        for (int slot = kb + static_cast<int>(threadIdx.x); slot < min(kb + kLdsWaves * 32, all); slot += kLdsWaves * kWave)
+            part[slot] = 0.f;
+}
+
+// Adds up the segments' sums, in their order.
+__global__ __launch_bounds__(256) void kvq_score_sum_kernel(KvqScoreArgs a, int lot_rows) {
+    const int blocks = (a.c.capacity + 255) / 256;
+    const int slot = static_cast<int>(blockIdx.x % blocks) * 256 + threadIdx.x, bh = blockIdx.x / blocks;
+    const int h = bh % a.c.H, b = bh / a.c.H;
+    Accepted ac;
+    if (!ac.read(a, b) || !ac.read_path(a, b) || slot >= ac.all) return;
+    const int lots = ((ac.d + 1) * a.G + lot_rows - 1) / lot_rows, per = (lots + a.segs - 1) / a.segs;
+    const int used = (lots + per - 1) / per;            // segments that hold rows
+    const long bhs = static_cast<long>(a.c.B) * a.c.H;
+    float x = 0.f;
+    for (int s = 0; s < used; ++s) x += a.part[(s * bhs + bh) * a.c.capacity + slot];
+    put_weight(a, b, h, ac.pre, slot, x, a.scores[bh * static_cast<long>(a.c.capacity) + slot]);
+}
+
 template <int D, int DT, int QT> void stream_keys(const KvqScoreArgs& a, hipStream_t s, Timing t) {
-    const int keys = kKeyWaves * 32, bh = a.c.B * a.c.H;
-    const int blocks = (a.c.capacity + keys - 1) / keys, most = (SCORE_WGS + bh - 1) / bh;
-    launch_timed(t, kvq_score_kernel<D, DT, QT>, dim3(blocks < most ? blocks : most, a.c.H, a.c.B),
-                 dim3(kKeyWaves * kWave), 0, s, a);
+    launch_timed(t, kvq_score_kernel<D, DT, QT>, dim3(a.key_wgs, a.c.H, a.c.B), dim3(kKeyWaves * kWave), 0, s, a);
 }
 template <int D, int DT> void score(const KvqScoreArgs& a, hipStream_t s, Timing t) {
-    // the most rows there can be (the host knows no lengths)
-    const long rows = static_cast<long>(a.path && a.path_stride < a.N ? a.path_stride : a.N) * a.G;
-    if (rows <= 16) {
+    if (a.q_tiles == 1) {
         stream_keys<D, DT, 1>(a, s, t);
-    } else if (rows <= 32) {
+    } else if (a.q_tiles == 2) {
         stream_keys<D, DT, 2>(a, s, t);
-    } else if (DT == 1 && D <= 128 && rows <= 64) {
-        stream_keys<DT == 1 && D <= 128 ? D : 64, DT, DT == 1 && D <= 128 ? 4 : 1>(a, s, t);
     } else {
-        constexpr int KT = SKT, W = SW;
-        const unsigned blocks = (a.c.capacity + 16 * KT - 1) / (16 * KT);
-        launch_timed(t, kvq_score_rows_kernel<D, DT, KT, W>, dim3(blocks * a.c.H * a.c.B), dim3(W * kWave), 0, s, a);
+        const unsigned bhs = static_cast<unsigned>(a.c.B) * a.c.H;
+        launch_timed(t, kvq_score_lds_kernel<D, DT>, dim3(bhs * a.key_wgs * a.segs), dim3(kLdsWaves * kWave), 0, s, a);
+        if (a.segs > 1)
+            kvq_score_sum_kernel<<<dim3(bhs * ((a.c.capacity + 255) / 256)), 256, 0, s>>>(a, lds_rows(D, DT));
     }
 }
 
 }  // namespace
+
+// Workgroups: four a compute unit for rows in registers (27-node trees, 32 batch rows at 4096 keys: 21 us; half as many
+// 27, twice as many 24), two where the rows fill LDS (32 tokens x 4 heads, 8 batch rows at 30000 keys: 74 us; half as
+// many 92), and with the rows split as well four (2048 tokens x 4 heads on their own 2048 keys: 53 + 6 us; two 65 + 5).
+void kvq_score_plan(KvqScoreArgs& a) {
+    // the most rows there can be (the host knows no lengths)
+    const long rows = static_cast<long>(a.path && a.path_stride < a.N ? a.path_stride : a.N) * a.G;
+    const long bhs = static_cast<long>(a.c.B) * a.c.H;
+    a.q_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+    a.segs = 1;
+    const auto wgs = [&](int waves, long target) {      // workgroups along the keys, each with one step a wave at least
+        const long blocks = (static_cast<long>(a.c.capacity) + 32 * waves - 1) / (32 * waves);
+        const long most = (target + bhs - 1) / bhs;
+        return static_cast<int>(blocks < most ? blocks : most);
+    };
+    if (a.q_tiles) {
+        a.key_wgs = wgs(kKeyWaves, 1024);
+        return;
+    }
+    a.key_wgs = wgs(kLdsWaves, 512);
+    const int lot = lds_rows(a.c.D, a.dtype);
+    const long lots = (rows + lot - 1) / lot, most = 1024 / (bhs * a.key_wgs);
+    if (most > 1 && lots > 1) a.segs = static_cast<int>(lots < most ? lots : most);
+}
 
 hipError_t launch_kvq_score(const KvqScoreArgs& a, hipStream_t s, Timing t) {
     if (a.dtype == 1) {

@@ -244,9 +244,17 @@ def kvq_commit(cache: KVQCache, prefix: torch.Tensor, path: torch.Tensor, accept
     return out
 
 
+def kvq_score_workspace_bytes(cache: KVQCache, N: int, q_heads: int, path_len: int = 0,
+                              dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of :func:`kvq_score`'s workspace (give a tensor of 256 more); path_len: path.shape[1], 0 without one."""
+    return int(lib().spec_kvq_score_workspace_bytes(cache.B, N, q_heads, cache.heads, cache.head_dim, cache.capacity,
+                                                    path_len, _CODES[dtype]))
+
+
 def kvq_score(q: torch.Tensor, lse: torch.Tensor, cache: KVQCache, prefix: torch.Tensor, accept_len: torch.Tensor,
               scores: torch.Tensor, positions: torch.Tensor, seen: torch.Tensor, *,
-              path: Optional[torch.Tensor] = None, scale: Optional[float] = None) -> None:
+              path: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+              workspace: Optional[torch.Tensor] = None) -> None:
     """Add the accepted queries' attention weights onto ``scores``, in place (``spec_kvq_score``).
 
     After :func:`kvq_commit`: q and lse [B, N, q_heads] as :func:`kvq_attention` took and gave them, prefix [B] the
@@ -265,12 +273,15 @@ def kvq_score(q: torch.Tensor, lse: torch.Tensor, cache: KVQCache, prefix: torch
             raise ValueError("path must be [B, D+1]")
         stride = path.shape[1]
         pp = _tensor(path, "path", torch.int32, (B, stride), dev)
+    width = 0 if path is None else stride
+    need = cache._need(lambda: kvq_score_workspace_bytes(cache, N, Hq, width, q.dtype), N, Hq, width, q.dtype)
+    wp, _ws = _scratch(need, dev, workspace)
     _call(lib().spec_kvq_score, "spec_kvq_score", dev, ctypes.addressof(rq), _CODES[q.dtype], Hq, N,
           _tensor(lse, "lse", torch.float32, (B, N, Hq), dev), cache._ref,
           _tensor(prefix, "prefix", torch.int32, row, dev), pp, stride,
           _tensor(accept_len, "accept_len", torch.int32, row, dev),
           1.0 / math.sqrt(D) if scale is None else float(scale), _tensor(scores, "scores", torch.float32, slots, dev),
-          _tensor(positions, "positions", torch.int32, slots, dev), _tensor(seen, "seen", torch.int32, row, dev))
+          _tensor(positions, "positions", torch.int32, slots, dev), _tensor(seen, "seen", torch.int32, row, dev), wp, need)
 
 
 def kvq_evict_workspace_bytes(cache: KVQCache, keep: int) -> int:

@@ -380,6 +380,54 @@ def test_score_prompt(R, D, G, N, prefix, alen):
     assert (ds2 == ds).all()                             # the same bits
 
 
+@pytest.mark.parametrize("B,H,G,D,N,prefix,dtype", [
+    (8, 8, 4, 64, 2400, 0, "bf16"),      # rows in two segments, several key blocks a workgroup, lots older than all keys
+    (1, 2, 4, 128, 700, 1500, "bf16"), (1, 1, 3, 256, 300, 90, "f32"), (2, 2, 2, 128, 150, 40, "f32"),
+    (1, 16, 16, 64, 40, 3000, "bf16"), (16, 4, 8, 128, 9, 9000, "bf16")])
+def test_score_many_rows(R, B, H, G, D, N, prefix, dtype):
+    """Prompts and long chains against the definition in 64 bits (torch on the GPU, one head at a time)."""
+    import torch
+    rng = np.random.default_rng(N)
+    S = prefix + N + 3
+    cache = make_cache(R, rng, B, H, S, D)
+    q = queries(rng, B, N, H * G, D, dtype, size=0.5)
+    lse = torch.from_numpy((4 + rng.standard_normal((B, N, H * G))).astype(np.float32)).cuda()
+    pre = [prefix] * B
+    alen = [N - 1 - b for b in range(B)]
+    scores = torch.from_numpy(rng.random((B, H, S)).astype(np.float32)).cuda()
+    pos = torch.zeros((B, H, S), dtype=torch.int32, device="cuda")
+    before = scores.double()
+    R.kvq_score(q, lse, cache, ints(*pre), ints(*alen), scores, pos, ints(*pre))
+    table = torch.tensor(list(ref.GRID) + [-v for v in ref.GRID], dtype=torch.float64, device="cuda")
+    slot = torch.arange(S, device="cuda")
+    u = 2.0 ** -24
+    for b in range(B):
+        T = alen[b] + 1
+        if T < 1:                                        # an error row: left as it was
+            assert torch.equal(scores[b].double(), before[b]) and (pos[b] == 0).all()
+            continue
+        sees = slot <= prefix + torch.arange(T, device="cuda").view(-1, 1)
+        for h in range(H):
+            c = cache.k_codes[b, h].long()
+            K = table[torch.stack((c & 15, c >> 4), -1).flatten(-2)]
+            K = K * torch.exp2(cache.k_scales[b, h].double() - 127).repeat_interleave(32, -1)
+            w = torch.zeros(S, dtype=torch.float64, device="cuda")
+            err = torch.zeros_like(w)
+            for g in range(G):
+                x, z = q[b, :T, h * G + g].double(), lse[b, :T, h * G + g].double().view(-1, 1)
+                s = (x @ K.T) * D ** -0.5
+                e = torch.where(sees, torch.exp(s - z), 0.0)
+                w += e.sum(0)
+                # as in kvq_ref.score: D products, a rounded exponent, exp2
+                err += (e * (D * (x.abs() @ K.abs().T) * D ** -0.5 + 8 * s.abs() + 8 * z.abs() + 8)).sum(0) * u
+            err += w * (T * G + 24) * u                  # the sums, over at most T*G terms and a few segments
+            want = torch.where(slot < prefix, before[b, h] + w, torch.where(slot < prefix + T, w, before[b, h]))
+            off = (scores[b, h].double() - want).abs()
+            assert (off <= err + 2 * u * want.abs()).all(), (b, h, off.max())
+        assert (pos[b, :, prefix:prefix + T] == prefix + torch.arange(T, device="cuda")).all()
+        assert (pos[b, :, :prefix] == 0).all() and (pos[b, :, prefix + T:] == 0).all()
+
+
 def test_scores_of_attention_sum_to_the_queries(R):
     """With attention's own lse the weights of a query sum to one: the new scores hold (d + 1) * G in total."""
     import torch

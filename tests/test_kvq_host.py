@@ -65,9 +65,9 @@ def attend(R, c, q=rows(), dtype=1, Hq=16, N=4, prefix=FAKE, counts=None, mask=N
 
 
 def score(R, c, q=rows(), dtype=1, Hq=16, N=4, lse=FAKE, prefix=FAKE, path=FAKE, stride=4, alen=FAKE, scale=0.1,
-          scores=FAKE, positions=FAKE, seen=FAKE):
+          scores=FAKE, positions=FAKE, seen=FAKE, ws=FAKE, wsb=1 << 40):
     return R.lib().spec_kvq_score(ref_of(q), dtype, Hq, N, lse, ref_of(c), prefix, path, stride, alen, scale, scores,
-                                  positions, seen, None)
+                                  positions, seen, ws, wsb, None)
 
 
 def evict(R, c, keep=32, sink=0, recent=0, ws=FAKE, wsb=1 << 40, **kw):
@@ -143,6 +143,12 @@ def test_workspaces(R):
     assert need > 0
     for bad in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 64)):
         assert attend(R, c, **bad) == EWORKSPACE
+    need = L.spec_kvq_score_workspace_bytes(2, 2048, 16, 4, 128, 4096, 0, 1)
+    assert need > 0
+    for bad in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 64)):
+        assert score(R, c, N=2048, path=None, stride=0, **bad) == EWORKSPACE
+    assert L.spec_kvq_score_workspace_bytes(2, 4, 16, 4, 128, 4096, 4, 1) == 0      # few rows need none
+    assert L.spec_kvq_score_workspace_bytes(2, 2048, 15, 4, 128, 4096, 0, 1) == 0
     need = L.spec_kvq_evict_workspace_bytes(2, 4, 4096, 32)
     assert need >= 2 * 4 * 32 * 4
     for bad in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 64)):
@@ -155,8 +161,8 @@ def test_workspaces(R):
 
 
 def test_declared_calls_are_exported(R):
-    for name in ("append", "read", "attention", "attention_workspace_bytes", "score", "evict",
-                 "evict_workspace_bytes"):
+    for name in ("append", "read", "attention", "attention_workspace_bytes", "score", "score_workspace_bytes",
+                 "evict", "evict_workspace_bytes"):
         assert hasattr(R.lib(), "spec_kvq_" + name)
 
 
