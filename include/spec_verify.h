@@ -572,8 +572,8 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
  *   out_lse  [B][N][q_heads] float32: log sum_s exp(scale * (q . K_s)); or NULL
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros
  * and an out_lse of -inf.  K and V enter exactly (E2M1 times a power of two is a
- * bfloat16), products and sums are float32; the probabilities round to bfloat16
- * before they meet V (SPEC_F32: to a sum of two bfloat16, 16 bits).
+ * bfloat16), products and sums are float32; with bfloat16 queries the
+ * probabilities round to bfloat16 before they meet V.
  * q_heads a multiple of heads; N <= 65536 (with a mask: N <= SPEC_MAX_NODES).
  * workspace: spec_kvq_attention_workspace_bytes(...) bytes (may be 0), any
  * contents; left as scratch.

@@ -18,7 +18,7 @@
 // instruction, exactly (E2M1 times a power of two).  V pairs two elements of one
 // key where the product wants two keys of one element: one byte permute each.
 //
-// float32 queries enter as three bf16 parts (exact) and P as two.
+// float32 queries enter as three bf16 parts, and so does P: exact both.
 //
 // Where the rows are few the cache's bytes bound it, so the key axis is what is
 // spread: the waves of a workgroup take 32 keys each in turn and join through
@@ -331,6 +331,19 @@ template <int D, int QT, int NP> struct Softmax {
     }
 };
 
+// The batch row with the turn-th most slots (a batch of at most 64): long rows start first, so that the short ones fill
+// the end of the launch.
+__device__ __forceinline__ int kvq_by_length(const KvqAttnArgs& a, int turn) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int mine = lane < a.c.B ? kvq_chunks(a, lane) : -1;
+    int before = 0;                                     // rows that come before this lane's
+    for (int r = 0; r < a.c.B; ++r) {
+        const int n = bcast(mine, r);
+        before += n > mine || (n == mine && r < lane) ? 1 : 0;
+    }
+    return __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(__ballot(before == turn))) - 1);
+}
+
 // What a workgroup works on: batch row, head and a part of its key axis.
 struct Place {
     int b, h, cnt;
@@ -349,6 +362,8 @@ __device__ __forceinline__ bool kvq_place(const KvqAttnArgs& a, int uh, Place& p
         if (!kvq_unit(a, unit, per, b, split, mine)) return false;
     } else if (b >= a.c.B) {
         return false;
+    } else if (a.c.B > 1 && a.c.B <= kWave) {
+        b = kvq_by_length(a, b);
     }
     p.b = b;
     p.part = mine > 1;
@@ -458,13 +473,13 @@ constexpr int larger(int a, int b) { return a > b ? a : b; }
 
 template <int D, int DT, int QT, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq_attention_kernel(KvqAttnArgs a) {
-    constexpr int NQ = DT == 1 ? 1 : 3, NP = DT == 1 ? 1 : 2;
+    constexpr int NQ = DT == 1 ? 1 : 3, NP = NQ;
     constexpr int kNT = D / 16, kRows = 16 * QT;
     constexpr int kRound = kStep * WAVES;               // keys a workgroup takes at a time
     // (unit, head) pairs of one residue mod 8 with all their row tiles: neighbours in time on one XCD, whose L2 serves
     // the row tiles that read the same keys
     const int x = blockIdx.x % 8, y = blockIdx.x / 8;
-    const int row0 = y % a.row_tiles * kRows;
+    const int row0 = (a.row_tiles - 1 - y % a.row_tiles) * kRows;      // a prompt's last rows see the most keys
     Place pl;
     if (!kvq_place(a, y / a.row_tiles * 8 + x, pl)) return;
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id();

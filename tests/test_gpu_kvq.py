@@ -83,9 +83,8 @@ def check_attention(out, lse, q, cache, prefix, counts, mask, scale):
     counts = [N] * B if counts is None else counts
     want, wlse, tol, ltol = ref.attend(f64(q), K, V, prefix, counts, mask, scale)
     size = ref.attend_abs(f64(q), K, V, prefix, counts, mask, scale)
-    # a probability rounds to bf16 (2^-8), or to two bf16 (2^-16); both the sum of products and, through the rounding
-    # of the output, the value itself
-    p_round, o_round = (2.0 ** -8, 2.0 ** -8) if q.dtype == torch.bfloat16 else (2.0 ** -16, U)
+    # with bf16 queries a probability rounds to bf16 before it meets V (2^-8), and so does the output
+    p_round, o_round = (2.0 ** -8, 2.0 ** -8) if q.dtype == torch.bfloat16 else (U, U)
     tol = tol + p_round * size + o_round * np.abs(want) * 1.01
     got, glse = f64(out), f64(lse)
     bad = np.abs(got - want) > tol + 1e-37
