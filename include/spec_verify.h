@@ -571,7 +571,9 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
  *   out      [B][N][q_heads][D], of q's type, contiguous, 16-byte aligned
  *   out_lse  [B][N][q_heads] float32: log sum_s exp(scale * (q . K_s)); or NULL
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros
- * and an out_lse of -inf.  K and V enter exactly (E2M1 times a power of two is a
+ * and an out_lse of -inf.  What a query does not see never reaches it, whatever
+ * its bytes; a NaN reaches it through a K row alone (spec_kvq_append marks the K
+ * row of either).  Queries that are not finite give unspecified rows.  K and V enter exactly (E2M1 times a power of two is a
  * bfloat16), products and sums are float32; with bfloat16 queries the
  * probabilities round to bfloat16 before they meet V.
  * q_heads a multiple of heads; N <= 65536 (with a mask: N <= SPEC_MAX_NODES).
@@ -622,8 +624,8 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
  * into the i-th gap below it (both counted upwards), so only those rows move.
  * Slots past the new length are left as they were.
  *   scores, positions          [B][heads][capacity], read
- *   out_scores, out_positions  the same, written up to the new length: either
- *                              the arrays read, or others that do not overlap
+ *   out_scores, out_positions  the same, written up to the new length: each
+ *                              either the array read, or one that overlaps neither
  *   lengths, seen              [B] int32
  *   out_len     [B] int32: min(lengths[b], keep); error rows (lengths[b] < 0 or
  *               above capacity): -1, and nothing of them moves

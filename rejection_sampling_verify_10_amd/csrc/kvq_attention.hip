@@ -459,11 +459,12 @@ template <int D> struct Loader {
 // Waves a SIMD to fit the registers of one variant to.
 constexpr int attend_occupancy(int D, int DT, int QT) {
     const int size = (D / 64) * QT * (DT == 1 ? 2 : 3);     // of the sums and the queries
-    return size <= 4 ? 3 : 2;
+    return size <= 4 || (D == 128 && DT == 1) ? 3 : 2;
 }
-// Queries stay in registers where that leaves room for two waves a SIMD, and are read from LDS every step where it
-// does not (D = 256, 32 rows: 27 nodes x 4 heads, 16 batch rows at 4096 keys, 94 us against 68).
-constexpr bool queries_in_lds(int D, int DT, int QT) { return D == 256 && QT == 2; }
+// 32 bf16 queries of D = 128 and 256 are read from LDS every step: their registers make room for a third wave a SIMD
+// (prompts of 1023 tokens x 4 heads 74 -> 69 us), and for a second (27 nodes x 4 heads, 16 batch rows at 4096 keys,
+// D = 256: 94 -> 68 us).
+constexpr bool queries_in_lds(int D, int DT, int QT) { return D >= 128 && DT == 1 && QT == 2; }
 template <bool ON> __device__ __forceinline__ void fence() {        // keeps operands from being formed early
 #if SV_KVQ_DEVICE
     if (ON) __builtin_amdgcn_sched_barrier(0);
@@ -546,7 +547,7 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
                     for (int t = 0; t < 2; ++t) S[qt][t] = mfma(A[t], q, S[qt][t]);
                 }
             }
-            fence<kQL>();
+            fence<D == 256>();
         }
         ld.load_k(cur, kb + kRound, k1);
         if (qs.edge(a, kb, pl.pre, row0)) qs.hide(S, static_cast<int>(kb - pl.pre) + 4 * g, a.mask != nullptr);
@@ -579,7 +580,7 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
                     sm.O[qt][2 * pr + 1] = mfma(hi, P[qt][p], sm.O[qt][2 * pr + 1]);
                 }
             }
-            fence<kQL>();
+            fence<D == 256>();
         }
         ld.load_v(cur, kb + kRound, k1);
     }

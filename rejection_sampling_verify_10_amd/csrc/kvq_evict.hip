@@ -13,6 +13,8 @@
 // written, so the rows move in one parallel pass with no order between them; a
 // handful is moved by the selecting workgroup itself.
 
+#include <type_traits>
+
 #include "kvq.hpp"
 
 namespace sv {
@@ -49,29 +51,29 @@ __device__ __forceinline__ int lanes_before(unsigned long long m) {
                                      __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(m), 0));
 }
 
-// A head's plan carried out: D/32 lanes a row of K and as many of V, 16 bytes of codes and one scale byte each; the
-// first of them moves the row's score, position and source too.
+// A head's plan carried out: D/32 lanes a row of K and as many of V, 16 bytes of codes each; one of them moves the
+// scales, another the row's score, position and source.
 template <int D>
 __device__ __forceinline__ void move_rows(const KvqEvictArgs& a, int bh, int moves, int thread, int threads) {
     constexpr int kParts = D / 32;
+    using Scales = std::conditional_t<D == 64, uint16_t, std::conditional_t<D == 128, uint32_t, u32x2>>;
     const int h = bh % a.c.H, b = bh / a.c.H;
     const int part = thread % kParts;
     const bool is_v = (thread / kParts) & 1;
     uint8_t* codes = (is_v ? a.c.vc : a.c.kc) + b * a.c.cb + h * a.c.ch + part * 16;
-    uint8_t* scales = (is_v ? a.c.vs : a.c.ks) + b * a.c.sb + h * a.c.sh + part;
+    uint8_t* scales = (is_v ? a.c.vs : a.c.ks) + b * a.c.sb + h * a.c.sh;
     const int32_t* plan = a.plan + static_cast<long>(bh) * a.gap_stride * 2;
     const long at = static_cast<long>(bh) * a.c.capacity;
     for (int i = thread / (2 * kParts); i < moves; i += threads / (2 * kParts)) {
         const long to = plan[2 * i], from = plan[2 * i + 1];
-        if (!is_v && part == 0) {
+        *reinterpret_cast<u32x4*>(codes + to * a.c.cp) = *reinterpret_cast<const u32x4*>(codes + from * a.c.cp);
+        if (part == 0)
+            *reinterpret_cast<Scales*>(scales + to * a.c.sp) = *reinterpret_cast<const Scales*>(scales + from * a.c.sp);
+        if (part == 1 && !is_v) {
             a.out_source[static_cast<long>(bh) * a.keep + to] = static_cast<int32_t>(from);
             a.out_scores[at + to] = a.scores[at + from];
             a.out_positions[at + to] = a.positions[at + from];
         }
-        const u32x4 w = *reinterpret_cast<const u32x4*>(codes + from * a.c.cp);
-        const uint8_t s = scales[from * a.c.sp];
-        *reinterpret_cast<u32x4*>(codes + to * a.c.cp) = w;
-        scales[to * a.c.sp] = s;
     }
 }
 
@@ -95,7 +97,7 @@ __global__ __launch_bounds__(T) void kvq_select_kernel(KvqEvictArgs a) {
     float* osc = a.out_scores + at;
     int32_t* opos = a.out_positions + at;
     // every kept slot as if nothing moved; the gaps are written over at the end
-    const bool apart = osc != sc;
+    const bool apart = osc != sc || opos != pos;
     for (int j0 = tid; j0 < kept; j0 += 4 * T) {
         float x[4];
         int p[4];

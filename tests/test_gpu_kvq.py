@@ -507,7 +507,98 @@ def test_evict_more_protected_than_kept_and_none(R):
     run_evict(R, cache, scores, pos, [300, 299], [300, -2 ** 31], 20, 0, 2 ** 31 - 1, True)
 
 
+@pytest.mark.parametrize("S,keep", [(60, 20), (3000, 1000)])
+def test_evict_one_array_in_place(R, S, keep):
+    """The scores in place and the positions elsewhere, and the other way round."""
+    import torch
+    rng = np.random.default_rng(S)
+    for which in range(2):
+        cache = make_cache(R, rng, 2, 2, S, 64)
+        scores = rng.random((2, 2, S)).astype(np.float32)
+        pos = np.tile(np.arange(S, dtype=np.int32), (2, 2, 1))
+        ds, dp = dev(scores), dev(pos)
+        other = torch.full_like(dp if which else ds, -7)
+        n, src = R.kvq_evict(cache, ds, dp, ints(S, S - 1), ints(S, S), keep, sink=1, recent=3,
+                             **{"out_positions" if which else "out_scores": other})
+        wn, wsrc = ref.evict(scores, pos, [S, S - 1], [S, S], keep, 1, 3)
+        assert np.array_equal(src.cpu().numpy(), wsrc)
+        ms, mp = ref.move(scores, wsrc, wn), ref.move(pos, wsrc, wn)
+        gs, gp = (ds, other) if which else (other, dp)
+        assert np.array_equal(gs.cpu().numpy()[..., :keep], ms[..., :keep])
+        assert np.array_equal(gp.cpu().numpy()[..., :keep], mp[..., :keep])
+
+
+@pytest.mark.parametrize("n,keep", [(60000, 20000), (50001, 50000), (4097, 2000), (49152, 48000)])
+def test_evict_long_heads(R, n, keep):
+    """Heads whose keys fit the registers of sixteen waves, just do, and do not."""
+    rng = np.random.default_rng(n)
+    S = n + 5
+    cache = make_cache(R, rng, 1, 2, S, 64)
+    scores = np.exp(2 * rng.standard_normal((1, 2, S))).astype(np.float32)
+    scores[0, 1] = np.round(scores[0, 1])                            # great ties, across waves
+    pos = np.tile(np.arange(S, dtype=np.int32), (1, 2, 1))
+    run_evict(R, cache, scores, pos, [n], [n], keep, 4, 30, False)
+
+
 # ---- together ----
+
+@pytest.mark.parametrize("layout", ["heads", "rows", "slots"])
+def test_commit_moves_every_part(R, layout):
+    rng = np.random.default_rng(50)
+    B, H, S, D, N = 3, 2, 40, 128, 9
+    cache = make_cache(R, rng, B, H, S, D, layout)
+    old = arrays(cache)
+    path = np.array([[0, 2, 5, 8], [0, 1, -1, -1], [0, 4, 7, -1]], np.int32)
+    alen, prefix = [3, 1, -1], [10, 0, 5]
+    n = R.kvq_commit(cache, ints(*prefix), dev(path), ints(*alen), N)
+    assert n.tolist() == [14, 2, -1]
+    for x0, x1 in zip(old, arrays(cache)):
+        for b in range(2):
+            p = path[b, :alen[b] + 1]
+            x0[b][:, prefix[b]:prefix[b] + len(p)] = x0[b][:, prefix[b] + p].copy()
+        assert np.array_equal(x0, x1)
+
+
+def test_calls_on_two_streams_at_once(R):
+    """Two caches attended and scored on two streams, each with its own workspace from the allocator: the bits of the
+    calls made one after the other."""
+    import torch
+    rng = np.random.default_rng(51)
+    jobs = []
+    for i in range(2):
+        cache = make_cache(R, rng, 2, 2, 6000, 128)
+        q = queries(rng, 2, 40, 8, 128, "bf16")
+        jobs.append((cache, q, ints(5000, 700 + i), torch.zeros((2, 2, 6000), device="cuda"),
+                     torch.zeros((2, 2, 6000), dtype=torch.int32, device="cuda")))
+
+    def work(cache, q, prefix, scores, pos):
+        out, lse = R.kvq_attention(q, cache, prefix)
+        scores.zero_()
+        R.kvq_score(q, lse, cache, prefix, ints(39, 39), scores, pos, prefix)
+        return out, lse, scores.clone()
+
+    want = [work(*j) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, j in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(work(*j))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_one_query_for_all(R):
+    """Queries broadcast over the batch and the tokens (strides of zero)."""
+    rng = np.random.default_rng(52)
+    cache = make_cache(R, rng, 3, 2, 200, 64)
+    one = queries(rng, 1, 1, 4, 64, "bf16")
+    q = one.expand(3, 5, 4, 64)
+    out, lse = R.kvq_attention(q, cache, ints(100, 7, 190))
+    check_attention(out, lse, q, cache, [100, 7, 190], None, None, 0.125)
+
 
 def test_speculative_steps(R):
     """Three steps as a serving loop makes them: rerank a draft tree, append its rows, attend under its mask, verify
