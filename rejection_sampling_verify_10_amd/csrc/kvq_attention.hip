@@ -75,56 +75,71 @@ __device__ __forceinline__ int wave_scan_int(int v) {   // inclusive
     }
     return v;
 }
-// Chunks a unit holds: the fewest for which the batch has no more than a.units units.
-__device__ __forceinline__ int kvq_per(const KvqAttnArgs& a) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const auto units = [&](int per) {
-        int n = 0;
-        for (int b0 = 0; b0 < a.c.B; b0 += kWave)
-            n += wave_sum(b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0);
-        return __builtin_amdgcn_readfirstlane(n);       // the same in every lane, kept in a scalar register
-    };
-    int most = 1;
-    for (int b0 = 0; b0 < a.c.B; b0 += kWave) most = max(most, b0 + lane < a.c.B ? kvq_chunks(a, b0 + lane) : 0);
-    int lo = a.min_per, hi = max(__builtin_amdgcn_readfirstlane(wave_max_int(most)), lo);
-    while (lo < hi) {                                   // one a batch row, at hi = the longest, always fits
-        const int mid = (lo + hi) / 2;
-        if (units(mid) <= a.units) hi = mid;
-        else lo = mid + 1;
+// The batch's chunks, 64 batch rows at a time: lane i has rows i, i + 64, ..; the first 64 are read once.
+struct Lengths {
+    const KvqAttnArgs& a;
+    int lane, own;
+    __device__ __forceinline__ explicit Lengths(const KvqAttnArgs& a) : a(a), lane(threadIdx.x & (kWave - 1)) {
+        own = lane < a.c.B ? kvq_chunks(a, lane) : 0;
     }
-    return lo;
-}
-// Batch row and place in it of unit u, and how many units the row has; false past the last unit.
-__device__ __forceinline__ bool kvq_unit(const KvqAttnArgs& a, int u, int per, int& b, int& split, int& mine) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int base = 0;
-    for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
-        const int n = b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0;
-        const int incl = wave_scan_int(n);
-        const unsigned long long past = __ballot(base + incl > u);   // (u, base and per are scalars, and so b and split)
-        if (past) {
-            const int l = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(past)) - 1);
-            b = b0 + l;
-            mine = bcast(n, l);
-            split = u - base - (bcast(incl, l) - mine);
-            return true;
+    __device__ __forceinline__ int chunks(int b0) const {
+        return b0 == 0 ? own : b0 + lane < a.c.B ? kvq_chunks(a, b0 + lane) : 0;
+    }
+    __device__ __forceinline__ int units(int b0, int per) const { return (chunks(b0) + per - 1) / per; }
+    // Chunks a unit holds: the fewest for which the batch has no more than a.units units.  (The same in every lane, and
+    // kept in scalar registers, as everything derived from it.)
+    __device__ __forceinline__ int per() const {
+        int most = 1;
+        for (int b0 = 0; b0 < a.c.B; b0 += kWave) most = max(most, chunks(b0));
+        int lo = a.min_per, hi = max(__builtin_amdgcn_readfirstlane(wave_max_int(most)), lo);
+        while (lo < hi) {                               // one a batch row, at hi = the longest, always fits
+            const int mid = (lo + hi) / 2;
+            int n = 0;
+            for (int b0 = 0; b0 < a.c.B; b0 += kWave) n += __builtin_amdgcn_readfirstlane(wave_sum(units(b0, mid)));
+            if (n <= a.units) hi = mid;
+            else lo = mid + 1;
         }
-        base += bcast(incl, kWave - 1);
+        return lo;
     }
-    return false;
-}
-// The units' first numbers by batch row (and their count at the end), for the kernel that joins them.
-__device__ __forceinline__ void kvq_note_units(const KvqAttnArgs& a, int per) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int base = 0;
-    for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
-        const int n = b0 + lane < a.c.B ? (kvq_chunks(a, b0 + lane) + per - 1) / per : 0;
-        const int incl = wave_scan_int(n);
-        if (b0 + lane < a.c.B) a.first_unit[b0 + lane] = base + incl - n;
-        base += bcast(incl, kWave - 1);
+    // Batch row and place in it of unit u, and how many units the row has; false past the last unit.
+    __device__ __forceinline__ bool find(int u, int per, int& b, int& split, int& mine) const {
+        int base = 0;
+        for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
+            const int n = units(b0, per), incl = wave_scan_int(n);
+            const unsigned long long past = __ballot(base + incl > u);
+            if (past) {
+                const int l = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(past)) - 1);
+                b = b0 + l;
+                mine = bcast(n, l);
+                split = u - base - (bcast(incl, l) - mine);
+                return true;
+            }
+            base += bcast(incl, kWave - 1);
+        }
+        return false;
     }
-    if (lane == 0) a.first_unit[a.c.B] = base;
-}
+    // The units' first numbers by batch row (and their count at the end), for the kernel that joins them.
+    __device__ __forceinline__ void note(int per) const {
+        int base = 0;
+        for (int b0 = 0; b0 < a.c.B; b0 += kWave) {
+            const int n = units(b0, per), incl = wave_scan_int(n);
+            if (b0 + lane < a.c.B) a.first_unit[b0 + lane] = base + incl - n;
+            base += bcast(incl, kWave - 1);
+        }
+        if (lane == 0) a.first_unit[a.c.B] = base;
+    }
+    // The batch row with the turn-th most slots (a batch of at most 64): long rows start first, so that the short ones
+    // fill the end of the launch.
+    __device__ __forceinline__ int by_length(int turn) const {
+        const int mine = lane < a.c.B ? own : -1;
+        int before = 0;                                 // rows that come before this lane's
+        for (int r = 0; r < a.c.B; ++r) {
+            const int n = bcast(mine, r);
+            before += n > mine || (n == mine && r < lane) ? 1 : 0;
+        }
+        return __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(__ballot(before == turn))) - 1);
+    }
+};
 
 // Query rows as the B operand of S^T: lane (c, g) holds elements g*D/4 .. of row c.  bf16 rows are one part, float32
 // rows three whose sum is the value.
@@ -331,19 +346,6 @@ template <int D, int QT, int NP> struct Softmax {
     }
 };
 
-// The batch row with the turn-th most slots (a batch of at most 64): long rows start first, so that the short ones fill
-// the end of the launch.
-__device__ __forceinline__ int kvq_by_length(const KvqAttnArgs& a, int turn) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int mine = lane < a.c.B ? kvq_chunks(a, lane) : -1;
-    int before = 0;                                     // rows that come before this lane's
-    for (int r = 0; r < a.c.B; ++r) {
-        const int n = bcast(mine, r);
-        before += n > mine || (n == mine && r < lane) ? 1 : 0;
-    }
-    return __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(__ballot(before == turn))) - 1);
-}
-
 // What a workgroup works on: batch row, head and a part of its key axis.
 struct Place {
     int b, h, cnt;
@@ -357,13 +359,14 @@ __device__ __forceinline__ bool kvq_place(const KvqAttnArgs& a, int uh, Place& p
     const int unit = uh / a.c.H;
     int b = unit, split = 0, per = 0, mine = 1;
     if (a.units) {
-        per = kvq_per(a);
-        if (blockIdx.x == 0 && wave_id() == 0) kvq_note_units(a, per);
-        if (!kvq_unit(a, unit, per, b, split, mine)) return false;
+        const Lengths len(a);
+        per = len.per();
+        if (blockIdx.x == 0 && wave_id() == 0) len.note(per);
+        if (!len.find(unit, per, b, split, mine)) return false;
     } else if (b >= a.c.B) {
         return false;
     } else if (a.c.B > 1 && a.c.B <= kWave) {
-        b = kvq_by_length(a, b);
+        b = Lengths(a).by_length(b);
     }
     p.b = b;
     p.part = mine > 1;
