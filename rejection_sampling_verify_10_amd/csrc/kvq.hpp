@@ -124,6 +124,36 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale, int sel) {
                                                                                           : fp4_pair<3>(w, scale);
 }
 
+__device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
+#if SV_KVQ_DEVICE
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+#else
+    return c;
+#endif
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2 p = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, p);
+}
+
+#if SV_KVQ_DEVICE
+// A buffer descriptor: loads past `bytes` give zeros and touch nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
+}
+#endif
+
+__device__ __forceinline__ int wave_scan_int(int v) {   // sum over the lanes up to this one
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int t = __shfl_up(v, o, kWave);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
 // Slots of a batch row: committed ones and new ones; false for an error row.
 __device__ __forceinline__ bool kvq_row_ok(int pre, int cnt, int N, int capacity) {
     return pre >= 0 && cnt >= 0 && cnt <= N && static_cast<long>(pre) + cnt <= capacity;

@@ -34,27 +34,7 @@ namespace {
 constexpr int kStep = 32;                               // keys of one step
 constexpr int kChunk = 128;                             // units of the key axis' split
 
-__device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
-#if SV_KVQ_DEVICE
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                   0, 0, 0);
-#else
-    return c;
-#endif
-}
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const bf16x2 p = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
-    return __builtin_bit_cast(uint32_t, p);
-}
-
-#if SV_KVQ_DEVICE
-// A buffer descriptor: loads past `bytes` give zeros and touch nothing.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
-}
-#endif
 
 // A call's split of the key axis.  Batch rows hold pre + cnt slots each, in whole
 // chunks; a unit is `per` chunks of one batch row, and the units are numbered
@@ -65,15 +45,6 @@ __device__ __forceinline__ int kvq_chunks(const KvqAttnArgs& a, int b) {
     const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
     return kvq_row_ok(pre, cnt, a.N, a.c.capacity) ? static_cast<int>((static_cast<long>(pre) + cnt + kChunk - 1) / kChunk)
                                                    : 0;
-}
-__device__ __forceinline__ int wave_scan_int(int v) {   // inclusive
-    const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const int t = __shfl_up(v, o, kWave);
-        if (lane >= o) v += t;
-    }
-    return v;
 }
 // The batch's chunks, 64 batch rows at a time: lane i has rows i, i + 64, ..; the first 64 are read once.
 struct Lengths {

@@ -21,26 +21,6 @@ namespace sv {
 
 namespace {
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const bf16x2 p = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
-    return __builtin_bit_cast(uint32_t, p);
-}
-__device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
-#if SV_KVQ_DEVICE
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                   0, 0, 0);
-#else
-    return c;
-#endif
-}
-
-#if SV_KVQ_DEVICE
-// A buffer descriptor: loads past `bytes` give zeros and touch nothing.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
-}
-#endif
-
 // Eight float32 values as NQ bf16 operands whose sum they are.
 template <int NQ, typename F> __device__ __forceinline__ void bf16_parts(float (&x)[8], F&& put) {
 #pragma unroll

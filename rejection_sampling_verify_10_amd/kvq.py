@@ -185,7 +185,8 @@ def kvq_read(cache: KVQCache, prefix: torch.Tensor, N: int, *, counts: Optional[
         raise ValueError(f"N must be at least 1, got {N}")
     dev, row = cache.device, (cache.B,)
     shape = (cache.B, int(N), cache.heads, cache.head_dim)
-    k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    k = torch.empty(shape, dtype=dtype, device=dev)
+    v = torch.empty_like(k)
     _call(lib().spec_kvq_read, "spec_kvq_read", dev, cache._ref, _CODES[dtype], int(N),
           _tensor(prefix, "prefix", torch.int32, row, dev), _optional(counts, "counts", torch.int32, row, dev),
           k.data_ptr(), v.data_ptr())
@@ -219,7 +220,7 @@ def kvq_attention(q: torch.Tensor, cache: KVQCache, prefix: torch.Tensor, *, mas
         rows = mask.dim() == 3
         mp, mb = _tensor(mask, "mask", torch.uint8, (B, N, N) if rows else (N, N), dev), N * N if rows else 0
     if out is None:
-        o = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
     else:
         o, lse = out
