@@ -10,7 +10,9 @@
 // Both kernels are bound by the wide side's bytes: eight elements a lane (one or
 // two 16-byte vectors), D/8 neighbouring lanes a row, four of them a block, so
 // the block's maximum is two lane exchanges and the row's codes leave as one
-// run of D/2 bytes.  A lane handles the same elements of K and of V, because a
+// run of D/2 bytes.  A prompt's 4 x 2047 float32 rows of 8 heads: 13.6 us for
+// 76 MB, 5.6 TB/s (and 9.2 us to read 8.4 million values of each back as bf16);
+// a tree's 32 x 27 rows are a launch and one load's latency, 4 us each way.  A lane handles the same elements of K and of V, because a
 // value that is not finite in either poisons the slot's K row.
 
 #include "kvq.hpp"

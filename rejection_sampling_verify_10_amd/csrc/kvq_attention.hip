@@ -24,6 +24,16 @@
 // spread: the waves of a workgroup take 32 keys each in turn and join through
 // LDS, and workgroups take units of the batch's whole key axis, alike whatever
 // the lengths, which a second kernel joins.
+//
+// Measured (8 cache heads, D = 128, bf16): 64 sequences of one token and 8 query
+// heads a cache head, ragged lengths to 8192: 74-78 us for 359 MB, 4.7 TB/s, the
+// bytes.  8 tokens x 4 heads at 131071 keys: 38 + 5 us for 143 MB, conversions
+// and bytes alike.  27-node trees x 4 heads, 32 sequences to 4096: 63-70 us for
+// 36 GFLOP, 550 TFLOP/s: of the cycles, the vector units are busy 58% (the
+// conversions of K and V, half rate, are nearly half of that) and the matrix
+// units 25%, and a wave does one or the other.  A prompt of 2 x 1023 tokens:
+// 56-68 us for 39 GFLOP, the same.  One token at 1000 keys: 8 us, the chain of
+// load, product, exponential, product, join.
 
 #include "kvq.hpp"
 

@@ -14,6 +14,12 @@
 // waves of a workgroup.  A prompt has thousands, bound by the exponentials, and
 // too few keys to fill the GPU: there the rows are split over workgroups as well,
 // whose sums meet in the workspace.
+//
+// 32 batch rows of 8 heads at ragged lengths to 4096 (27-node trees, paths of up
+// to 6 nodes): 18 us a call for 52 MB, 2.9 TB/s; a workgroup's few steps hardly
+// cover the latency of its first loads.  2048 tokens x 4 heads against their own
+// 2048 keys, 8 heads: 46 us for 17 GFLOP, 374 TFLOP/s, where an exponential a
+// score (135 million) alone is 14 us of the transcendental units.
 
 #include "kvq.hpp"
 
@@ -356,7 +362,8 @@ template <int D, int DT> void score(const KvqScoreArgs& a, hipStream_t s, Timing
 
 // Workgroups: four a compute unit for rows in registers (27-node trees, 32 batch rows at 4096 keys: 21 us; half as many
 // 27, twice as many 24), two where the rows fill LDS (32 tokens x 4 heads, 8 batch rows at 30000 keys: 74 us; half as
-// many 92), and with the rows split as well four (2048 tokens x 4 heads on their own 2048 keys: 53 + 6 us; two 65 + 5).
+// many 92), and with the rows split as well four (2048 tokens x 4 heads on their own 2048 keys: 44 + 6 us; two 65 + 5,
+// eight 49 + 7).
 void kvq_score_plan(KvqScoreArgs& a) {
     // the most rows there can be (the host knows no lengths)
     const long rows = static_cast<long>(a.path && a.path_stride < a.N ? a.path_stride : a.N) * a.G;
