@@ -500,8 +500,9 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
  * A cached K or V row of head_dim = D elements (D = 64, 128 or 256) is D/2
  * bytes of E2M1 codes (element 2i in the low half of byte i; magnitudes 0, .5,
  * 1, 1.5, 2, 3, 4, 6 for codes 0..7, bit 3 the sign) and D/32 scale bytes, one
- * for each 32 elements: the OCP microscaling layout.  Byte s in 1..254 stands
- * for 2^(s-127), byte 0 comes with an all-zero block, byte 255 means NaN.
+ * for each 32 elements: the OCP microscaling layout.  Byte s in 1..252 stands
+ * for 2^(s-127), byte 0 comes with an all-zero block, byte 255 means NaN (253
+ * and 254, whose values need not be float32 numbers, are not written).
  *
  * Every batch row b has `prefix[b]` committed rows, slots 0 .. prefix[b]-1 of
  * each of its heads, and `counts[b]` new ones (counts NULL: N) in the slots
@@ -515,7 +516,8 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
 /* One layer's cache.  Row (b, h, slot): codes at b*code_batch + h*code_head +
  * slot*code_pos bytes from k_codes / v_codes, scales likewise.  Codes: base and
  * strides multiples of 16 bytes; scales: of D/32 bytes.  No two rows may share
- * bytes (zero strides where B, heads or capacity exceed 1 are SPEC_EINVAL).
+ * bytes (zero strides where B, heads or capacity exceed 1 are SPEC_EINVAL; the
+ * stride of a dimension of one element does not count).
  * B and heads at most 65535, capacity at most 2^30, code_pos and scale_pos at
  * most 2^24. */
 typedef struct {
@@ -540,7 +542,7 @@ typedef struct {
  * prefix[b] + counts[b] - 1.  A block of 32 gets the smallest scale 2^e, e >=
  * -96, with max|x| <= 7 * 2^e (so the largest element is off by at most half a
  * step, as the others are) and its elements round to nearest, ties to the even
- * code.  A block holding a NaN or an infinity is stored as NaN (scale 255),
+ * code.  e ends at 125: larger elements than 7 * 2^125 become 6 * 2^125.  A block holding a NaN or an infinity is stored as NaN (scale 255),
  * and so is the first block of the slot's K row, whichever of the two rows held
  * it: every query that sees the slot answers NaN, and no other.
  *   k, v      rows of (b, n, head), SPEC_F32 or SPEC_BF16, n < N
@@ -573,9 +575,11 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros
  * and an out_lse of -inf.  What a query does not see never reaches it, whatever
  * its bytes; a NaN reaches it through a K row alone (spec_kvq_append marks the K
- * row of either).  Queries that are not finite give unspecified rows.  K and V enter exactly (E2M1 times a power of two is a
- * bfloat16), products and sums are float32; with bfloat16 queries the
- * probabilities round to bfloat16 before they meet V.
+ * row of either).  Queries that are not finite give unspecified rows.  K and V
+ * enter exactly (E2M1 times a power of two is a bfloat16), products and sums are
+ * float32 (V of 2^90 and more may overflow in them: they are divided by the
+ * probabilities' sum at the end); with bfloat16 queries the probabilities round
+ * to bfloat16 before they meet V.
  * q_heads a multiple of heads; N <= 65536 (with a mask: N <= SPEC_MAX_NODES).
  * workspace: spec_kvq_attention_workspace_bytes(...) bytes (may be 0), any
  * contents; left as scratch.

@@ -357,23 +357,23 @@ int take_cache(const spec_kvq_cache_t* c, KvqCache& o) {
     if (!kvq_dim_ok(c->head_dim) || c->B > 65535 || c->heads > 65535 || c->capacity > (1 << 30))
         return SPEC_EUNSUPPORTED;
     const int64_t codes = c->head_dim / 2, scales = c->head_dim / kQBlock;
+    // the stride of a dimension of one element never counts (the kernels read whole steps of slots, so slots keep one)
+    o.cb = c->B == 1 ? 0 : c->code_batch, o.sb = c->B == 1 ? 0 : c->scale_batch;
+    o.ch = c->heads == 1 ? 0 : c->code_head, o.sh = c->heads == 1 ? 0 : c->scale_head;
+    o.cp = c->capacity == 1 ? codes : c->code_pos, o.sp = c->capacity == 1 ? scales : c->scale_pos;
     const auto strides_ok = [c](int64_t batch, int64_t head, int64_t pos, int64_t row, int64_t unit) {
         if (batch < 0 || head < 0 || pos < 0 || batch % unit || head % unit || pos % unit) return false;
-        return (c->B == 1 || batch >= row) && (c->heads == 1 || head >= row) && (c->capacity == 1 || pos >= row);
+        return (c->B == 1 || batch >= row) && (c->heads == 1 || head >= row) && pos >= row;
     };
-    if (!strides_ok(c->code_batch, c->code_head, c->code_pos, codes, 16) ||
-        !strides_ok(c->scale_batch, c->scale_head, c->scale_pos, scales, scales))
-        return SPEC_EINVAL;
+    if (!strides_ok(o.cb, o.ch, o.cp, codes, 16) || !strides_ok(o.sb, o.sh, o.sp, scales, scales)) return SPEC_EINVAL;
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, scales) ||
         !aligned(c->v_scales, scales))
         return SPEC_EINVAL;
-    if (c->code_pos > (1 << 24) || c->scale_pos > (1 << 24)) return SPEC_EUNSUPPORTED;
+    if (o.cp > (1 << 24) || o.sp > (1 << 24)) return SPEC_EUNSUPPORTED;
     o.kc = static_cast<uint8_t*>(c->k_codes);
     o.ks = static_cast<uint8_t*>(c->k_scales);
     o.vc = static_cast<uint8_t*>(c->v_codes);
     o.vs = static_cast<uint8_t*>(c->v_scales);
-    o.cb = c->code_batch, o.ch = c->code_head, o.cp = c->code_pos;
-    o.sb = c->scale_batch, o.sh = c->scale_head, o.sp = c->scale_pos;
     o.B = c->B, o.H = c->heads, o.capacity = c->capacity, o.D = c->head_dim;
     return SPEC_OK;
 }

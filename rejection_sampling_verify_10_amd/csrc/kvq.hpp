@@ -10,6 +10,7 @@ namespace sv {
 
 constexpr int kQBlock = 32;            // elements that share a scale byte
 constexpr int kQScaleMin = -96 + 127;  // smallest scale byte of a block that is not all zero
+constexpr int kQScaleMax = 125 + 127;  // largest: 6 * 2^125 is the largest value that is a float32
 constexpr int kQScaleNaN = 255;
 
 // Row (b, h, slot) of the codes at kc/vc + b*cb + h*ch + slot*cp, of the scales at ks/vs + b*sb + h*sh + slot*sp.

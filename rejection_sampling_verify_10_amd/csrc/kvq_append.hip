@@ -45,11 +45,15 @@ __device__ __forceinline__ uint32_t block_scale(const float x[8]) {
     top = fmaxf(top, xshfl(top, 2));
     // 7 * 2^e = 1.75 * 2^(e+2): a mantissa above 1.75 takes the next exponent
     const int byte = static_cast<int>((__float_as_uint(top) + 0x1fffffu) >> 23) - 2;
-    return top == 0.f ? 0u : static_cast<uint32_t>(max(byte, kQScaleMin));
+    return top == 0.f ? 0u : static_cast<uint32_t>(min(max(byte, kQScaleMin), kQScaleMax));
 }
 
-__device__ __forceinline__ uint32_t pack8(const float x[8], uint32_t byte) {
+__device__ __forceinline__ uint32_t pack8(float x[8], uint32_t byte) {
     uint32_t w = 0;
+    if (byte == kQScaleMax) {                           // past 7 * 2^125 a block has no larger scale to go to
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -0x1.8p127f), 0x1.8p127f);
+    }
 #if SV_KVQ_DEVICE
     const float s = scale_value(byte == 0 ? 127u : byte);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], s, 0);

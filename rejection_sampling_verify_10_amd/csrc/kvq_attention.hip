@@ -542,8 +542,9 @@ __global__ __launch_bounds__(WAVES* kWave, attend_occupancy(D, DT, QT)) void kvq
         float vsc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // a block stored as NaN has zero codes: its V is finite, and its K row says NaN
-            vsc[j] = scale_value(min(cur.vs[j], 254u));
+            // a block stored as NaN has zero codes: its V is finite, and its K row says NaN.  Nor may bytes that append
+            // does not write give an infinity, which would reach queries that give the slot no weight.
+            vsc[j] = scale_value(min(cur.vs[j], static_cast<uint32_t>(kQScaleMax)));
         }
 #pragma unroll
         for (int pr = 0; pr < kNT / 2; ++pr) {

@@ -163,6 +163,63 @@ def test_append_rows_that_are_not_finite(R, dtype):
     assert np.array_equal(f64(rk)[0, [0, 3, 5]], fine)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_next_to_the_largest(R, dtype):
+    """Elements past 7 * 2^125 have no larger scale to go to: they become the largest value, never an infinity, and a
+    query that does not see them is what it is without them."""
+    import torch
+    rng = np.random.default_rng(31)
+    top = 6 * 2.0 ** 125
+    x = np.zeros((1, 3, 2, 1, 64), np.float32)
+    x[0, 0, :, 0, :4] = [3.38e38, -3.0e38, 7 * 2.0 ** 125, 2.0 ** 123]       # one step is 2^124 near zero: a tie, to zero
+    x[0, 1, :, 0, 40] = -3.38e38
+    x[0, 2] = rng.standard_normal((2, 1, 64))
+    kv = torch.from_numpy(x).cuda()
+    kv = kv.bfloat16() if dtype == "bf16" else kv
+    cache = make_cache(R, rng, 1, 1, 24, 64)
+    R.kvq_append(cache, kv[:, :, 0], kv[:, :, 1], ints(20))
+    for t in R.kvq_read(cache, ints(20), 3, dtype=torch.float32):
+        got = f64(t)[0, :, 0]
+        assert np.array_equal(got[0, :4], [top, -top, top, 0]) and (got[0, 4:] == 0).all()
+        assert got[1, 40] == -top and (np.delete(got[1], 40) == 0).all()
+    mask = np.array([[1, 0, 0], [0, 1, 0], [0, 0, 1]], np.uint8)
+    q = queries(rng, 1, 3, 2, 64, dtype)
+    out, lse = R.kvq_attention(q, cache, ints(20), mask=dev(mask))
+    assert torch.isfinite(out[0, 2]).all() and torch.isfinite(lse[0, 2]).all()
+    K, V = values(cache)
+    K, V = K.copy(), V.copy()
+    K[:, :, 20:22], V[:, :, 20:22] = 0, 0
+    want, wlse, tol, ltol = ref.attend(f64(q), K, V, [20], [3], mask[None], 64 ** -0.5)
+    size = ref.attend_abs(f64(q), K, V, [20], [3], mask[None], 64 ** -0.5)
+    tol = tol + ((2.0 ** -8) * (size + 1.01 * np.abs(want)) if dtype == "bf16" else U * (size + 1.01 * np.abs(want)))
+    assert (np.abs(f64(out) - want)[0, 2] <= tol[0, 2] + 1e-37).all()
+    assert (np.abs(f64(lse) - wlse)[0, 2] <= ltol[0, 2]).all()
+
+
+def test_one_slot_whatever_its_stride(R):
+    """A cache of one slot: the stride of a dimension of one element never counts."""
+    import torch
+    rng = np.random.default_rng(32)
+    D = 128
+    cache = R.new_kvq_cache(2, 2, 1, D, "cuda")
+    k, v = (torch.from_numpy(rng.standard_normal((2, 1, 2, D)).astype(np.float32)).cuda() for _ in range(2))
+    R.kvq_append(cache, k, v, ints(0, 0))
+    q = queries(rng, 2, 1, 4, D, "f32")
+    want, wlse = R.kvq_attention(q, cache, ints(0, 0))
+    assert wlse.isfinite().all() and (want != 0).any()
+    for step in (0, 16, 1 << 25):
+        odd = R.KVQCache(*(t.as_strided(t.shape, (t.stride(0), t.stride(1), step, 1))
+                           for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)))
+        got, lse = R.kvq_attention(q, odd, ints(0, 0))
+        assert (got == want).all() and (lse == wlse).all()
+        assert all((x == y).all() for x, y in zip(R.kvq_read(odd, ints(0, 0), 1), R.kvq_read(cache, ints(0, 0), 1)))
+        sums = [torch.zeros((2, 2, 1), device="cuda") for _ in range(2)]
+        for c, s in zip((cache, odd), sums):
+            R.kvq_score(q, wlse, c, ints(0, 0), ints(0, 0), s, torch.zeros((2, 2, 1), dtype=torch.int32, device="cuda"),
+                        ints(0, 0))
+        assert (sums[0] == sums[1]).all() and (sums[0] > 0).all()
+
+
 # ---- attention ----
 
 ATTEND = [
