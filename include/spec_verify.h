@@ -519,7 +519,9 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
  * bytes (zero strides where B, heads or capacity exceed 1 are SPEC_EINVAL; the
  * stride of a dimension of one element does not count).
  * B and heads at most 65535, capacity at most 2^30, code_pos and scale_pos at
- * most 2^24. */
+ * most 2^24.  Calls of 2^31 query rows, of 2^32 threads (rows of B, tokens and
+ * heads times D/8 in append and read, about 2^27 query rows in attention, 2^22
+ * heads of the batch in evict) and more are SPEC_EUNSUPPORTED. */
 typedef struct {
     void* k_codes;
     void* k_scales;
@@ -605,10 +607,11 @@ int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads
  *   scores       [B][heads][capacity] float32, positions [B][heads][capacity]
  *                int32, read and written; seen [B] int32: tokens the sequence
  *                had before this step (evicted ones too)
- * A query whose lse is -inf adds nothing.  Error rows here: accept_len < 0 (or
- * >= path_stride, or >= N), a path that is not token 0 followed by increasing
- * tokens below N, prefix < 0, or prefix + d + 1 > capacity; they are left as
- * they were.  path_stride <= SPEC_MAX_NODES where path is given.
+ * A query whose lse is -inf adds nothing (to a slot whose K is a number).
+ * Error rows here: accept_len < 0 (or >= path_stride, or >= N), a path that is
+ * not token 0 followed by increasing tokens below N, prefix < 0, or prefix + d
+ * + 1 > capacity; they are left as they were.  path_stride <= SPEC_MAX_NODES
+ * where path is given.
  * workspace: spec_kvq_score_workspace_bytes(...) bytes (path_stride 0: no path;
  * may be 0), any contents; left as scratch.
  */

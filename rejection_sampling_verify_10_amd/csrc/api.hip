@@ -350,6 +350,8 @@ bool kvq_count_ok(int B, int H, int n, int G) {
     return static_cast<double>(B) * H * n * G < 2147483648.0;
 }
 bool kvq_sizes_ok(int B, int H, int N, int G) { return N <= 65536 && kvq_count_ok(B, H, N, G); }
+// A launch has fewer than 2^32 threads.
+bool kvq_threads_ok(double workgroups, int threads) { return workgroups * threads < 4294967296.0; }
 
 int take_cache(const spec_kvq_cache_t* c, KvqCache& o) {
     if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return SPEC_EINVAL;
@@ -1096,7 +1098,8 @@ int spec_kvq_append(const spec_kvq_cache_t* cache, const spec_kvq_rows_t* k, con
     rc = take_rows(v, dtype, a.v);
     if (rc) return rc;
     if (N < 1 || !prefix || !aligned(prefix, 4) || !aligned(counts, 4)) return SPEC_EINVAL;
-    if (!kvq_sizes_ok(a.c.B, a.c.H, N, 1)) return SPEC_EUNSUPPORTED;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, 1) || !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H * N + 256, a.c.D / 8))
+        return SPEC_EUNSUPPORTED;
     a.dtype = dtype;
     a.N = N;
     a.prefix = prefix;
@@ -1115,7 +1118,8 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
     if (N < 1 || !prefix || !out_k || !out_v || !aligned(prefix, 4) || !aligned(counts, 4) || !aligned(out_k, 16) ||
         !aligned(out_v, 16))
         return SPEC_EINVAL;
-    if (!kvq_sizes_ok(a.c.B, a.c.H, N, 1)) return SPEC_EUNSUPPORTED;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, 1) || !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H * N + 256, a.c.D / 8))
+        return SPEC_EUNSUPPORTED;
     a.dtype = dtype;
     a.N = N;
     a.prefix = prefix;
@@ -1140,7 +1144,9 @@ int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads
         !aligned(counts, 4) || !aligned(out, 16) || !aligned(out_lse, 4) || mask_batch < 0)
         return SPEC_EINVAL;
     if (!(scale > 0.f) || !isfinite(scale)) return SPEC_EINVAL;
-    if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (mask && N > SPEC_MAX_NODES)) return SPEC_EUNSUPPORTED;
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (mask && N > SPEC_MAX_NODES) ||
+        !kvq_threads_ok((static_cast<double>(a.c.B) * a.c.H + 8) * ((N * (q_heads / a.c.H) + 15) / 16), 512))
+        return SPEC_EUNSUPPORTED;
     a.dtype = dtype;
     a.Hq = q_heads;
     a.G = q_heads / a.c.H;
@@ -1203,7 +1209,9 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
         !aligned(scores, 4) || !aligned(positions, 4) || !aligned(seen, 4))
         return SPEC_EINVAL;
     if (!(scale > 0.f) || !isfinite(scale)) return SPEC_EINVAL;
-    if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (path && path_stride > SPEC_MAX_NODES))
+    if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (path && path_stride > SPEC_MAX_NODES) ||
+        !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H + 1024, 512) ||
+        !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H * ((a.c.capacity + 255) / 256), 256))
         return SPEC_EUNSUPPORTED;
     a.dtype = dtype;
     a.Hq = q_heads;
@@ -1255,7 +1263,8 @@ int spec_kvq_evict(const spec_kvq_cache_t* cache, const float* scores, const int
         !aligned(out_scores, 4) || !aligned(out_positions, 4) || !aligned(out_len, 4) || !aligned(out_source, 4))
         return SPEC_EINVAL;
     if (keep < 1 || keep > a.c.capacity || sink < 0 || recent < 0) return SPEC_EINVAL;
-    if (!kvq_count_ok(a.c.B, a.c.H, keep, 1)) return SPEC_EUNSUPPORTED;
+    if (!kvq_count_ok(a.c.B, a.c.H, keep, 1) || !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H, 1024))
+        return SPEC_EUNSUPPORTED;
     a.scores = scores;
     a.positions = positions;
     a.lengths = lengths;

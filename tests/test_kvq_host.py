@@ -136,6 +136,18 @@ def test_sizes(R):
     assert evict(R, c, recent=-1) == EINVAL
 
 
+def test_launches_of_too_many_threads(R):
+    """Sizes whose indices fit but whose grids would not."""
+    big = cache(R, B=1 << 11, heads=1 << 8, capacity=1 << 9, head_dim=256)
+    assert append(R, big, N=256) == EUNSUPPORTED            # 2^27 rows of 32 lanes
+    assert read(R, big, N=256) == EUNSUPPORTED
+    assert attend(R, big, N=256, Hq=1 << 8) == EUNSUPPORTED
+    many = cache(R, B=1 << 12, heads=1 << 12, capacity=64)
+    assert attend(R, many, N=1, Hq=1 << 12) == EUNSUPPORTED  # 2^24 heads, a workgroup each
+    assert score(R, many, N=1, stride=1, Hq=1 << 12) == EUNSUPPORTED
+    assert evict(R, many, keep=1) == EUNSUPPORTED
+
+
 def test_workspaces(R):
     c = cache(R, capacity=4096)
     L = R.lib()
