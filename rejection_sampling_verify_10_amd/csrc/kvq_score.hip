@@ -223,6 +223,7 @@ __global__ __launch_bounds__(kKeyWaves* kWave) void kvq_score_kernel(KvqScoreArg
 }
 
 // More rows: they stay in LDS, a lot of kRows at a time, and the keys stream once for each lot.
+// (2048 tokens x 4 heads: 44 us; lots of half the rows 48, four or sixteen waves 50 and 45, 64 keys a wave and step 70.)
 constexpr int kLdsWaves = 8;
 constexpr int lds_rows(int D, int DT) { return 65536 / (2 * D * (DT == 1 ? 1 : 3)) / 16 * 16; }
 
