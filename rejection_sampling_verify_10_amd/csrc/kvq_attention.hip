@@ -51,20 +51,30 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // through the batch, so that a long row gets many and a short one few and all
 // of them cost the same.  Every workgroup finds its own from the lengths (the
 // host does not know them): row b has ceil(chunks(b) / per) units.
-__device__ __forceinline__ int kvq_chunks(const KvqAttnArgs& a, int b) {
-    const int pre = a.prefix[b], cnt = a.counts ? a.counts[b] : a.N;
+__device__ __forceinline__ int kvq_chunks(const KvqAttnArgs& a, int pre, int cnt) {
     return kvq_row_ok(pre, cnt, a.N, a.c.capacity) ? static_cast<int>((static_cast<long>(pre) + cnt + kChunk - 1) / kChunk)
                                                    : 0;
 }
 // The batch's chunks, 64 batch rows at a time: lane i has rows i, i + 64, ..; the first 64 are read once.
 struct Lengths {
     const KvqAttnArgs& a;
-    int lane, own;
+    int lane, pre, cnt, own;
     __device__ __forceinline__ explicit Lengths(const KvqAttnArgs& a) : a(a), lane(threadIdx.x & (kWave - 1)) {
-        own = lane < a.c.B ? kvq_chunks(a, lane) : 0;
+        const int b = min(lane, a.c.B - 1);
+        pre = a.prefix[b];
+        cnt = a.counts ? a.counts[b] : a.N;
+        own = lane < a.c.B ? kvq_chunks(a, pre, cnt) : 0;
     }
     __device__ __forceinline__ int chunks(int b0) const {
-        return b0 == 0 ? own : b0 + lane < a.c.B ? kvq_chunks(a, b0 + lane) : 0;
+        if (b0 == 0) return own;
+        const int b = b0 + lane;
+        return b < a.c.B ? kvq_chunks(a, a.prefix[b], a.counts ? a.counts[b] : a.N) : 0;
+    }
+    // Committed and new slots of batch row b.
+    __device__ __forceinline__ void row(int b, int& p, int& n) const {
+        const bool read = b < kWave;
+        p = read ? bcast(pre, b) : a.prefix[b];
+        n = read ? bcast(cnt, b) : a.counts ? a.counts[b] : a.N;
     }
     __device__ __forceinline__ int units(int b0, int per) const { return (chunks(b0) + per - 1) / per; }
     // Chunks a unit holds: the fewest for which the batch has no more than a.units units.  (The same in every lane, and
@@ -338,21 +348,26 @@ __device__ __forceinline__ bool kvq_place(const KvqAttnArgs& a, int uh, Place& p
     p.uh = uh;
     p.h = uh % a.c.H;
     const int unit = uh / a.c.H;
-    int b = unit, split = 0, per = 0, mine = 1;
+    int b = unit, split = 0, per = 0, mine = 1, pre;
     if (a.units) {
         const Lengths len(a);
         per = len.per();
         if (blockIdx.x == 0 && wave_id() == 0) len.note(per);
         if (!len.find(unit, per, b, split, mine)) return false;
+        len.row(b, pre, p.cnt);
     } else if (b >= a.c.B) {
         return false;
     } else if (a.c.B > 1 && a.c.B <= kWave) {
-        b = Lengths(a).by_length(b);
+        const Lengths len(a);
+        b = len.by_length(b);
+        len.row(b, pre, p.cnt);
+    } else {
+        pre = a.prefix[b];
+        p.cnt = a.counts ? a.counts[b] : a.N;
     }
     p.b = b;
     p.part = mine > 1;
-    p.pre = a.prefix[b];
-    p.cnt = a.counts ? a.counts[b] : a.N;
+    p.pre = pre;
     p.ok = kvq_row_ok(static_cast<int>(p.pre), p.cnt, a.N, a.c.capacity);
     p.k0 = static_cast<long>(split) * per * kChunk;
     p.k1 = a.units ? p.k0 + static_cast<long>(per) * kChunk : a.c.capacity;
