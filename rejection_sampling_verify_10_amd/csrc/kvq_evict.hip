@@ -128,7 +128,11 @@ __global__ __launch_bounds__(T) void kvq_select_kernel(KvqEvictArgs a) {
     const int bh = blockIdx.x, b = bh / a.c.H;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
     constexpr int kWaves = T / kWave;
-    const int len = a.lengths[b];
+    const int len = a.lengths[b], seen = a.seen[b];
+    __shared__ int hist[kBins];
+    if (K > 0) {
+        for (int i = tid; i < kBins; i += T) hist[i] = 0;
+    }
     int32_t* source = a.out_source + static_cast<long>(bh) * a.keep;
     const bool ok = len >= 0 && len <= a.c.capacity;
     const int kept = ok ? min(len, a.keep) : 0;
@@ -166,10 +170,9 @@ __global__ __launch_bounds__(T) void kvq_select_kernel(KvqEvictArgs a) {
         }
     }
     if (len == kept) return;                            // nothing to evict
-    const long from = static_cast<long>(a.seen[b]) - a.recent;
+    const long from = static_cast<long>(seen) - a.recent;
     int32_t* plan = a.plan + static_cast<long>(bh) * a.gap_stride * 2;
 
-    __shared__ int hist[kBins];
     __shared__ int sh[kWaves];
     __shared__ long sh_both[kWaves];
     __shared__ int sh_bin, sh_need, sh_count;
@@ -208,7 +211,6 @@ __global__ __launch_bounds__(T) void kvq_select_kernel(KvqEvictArgs a) {
     static_assert(K % 4 == 0 && K <= kWave, "held slots are read four at a time, and what stays of them is a lane's row each");
     __shared__ uint32_t held[K > 0 ? K * T : 1];
     if (K > 0) {                                        // their first digits are counted as they come
-        for (int i = tid; i < kBins; i += T) hist[i] = 0;
         __syncthreads();
         stream(0, ne, [&](int at, const float (&x)[kBatch], const int32_t (&p)[kBatch], const uint32_t (&k)[kBatch]) {
 #pragma unroll
