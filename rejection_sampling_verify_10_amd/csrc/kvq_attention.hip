@@ -27,7 +27,7 @@
 //
 // Measured (8 cache heads, D = 128, bf16): 64 sequences of one token and 8 query
 // heads a cache head, ragged lengths to 8192: 74-78 us for 359 MB, 4.7 TB/s, the
-// bytes.  8 tokens x 4 heads at 131071 keys: 38 + 5 us for 143 MB, conversions
+// bytes.  8 tokens x 4 heads at 131071 keys: 37 + 5 us for 143 MB, conversions
 // and bytes alike.  27-node trees x 4 heads, 32 sequences to 4096: 63-70 us for
 // 36 GFLOP, 550 TFLOP/s: of the cycles, the vector units are busy 58% (the
 // conversions of K and V, half rate, are nearly half of that) and the matrix

@@ -18,8 +18,9 @@
 // 32 batch rows of 8 heads at ragged lengths to 4096 (27-node trees, paths of up
 // to 6 nodes): 18 us a call for 52 MB, 2.9 TB/s; a workgroup's few steps hardly
 // cover the latency of its first loads.  2048 tokens x 4 heads against their own
-// 2048 keys, 8 heads: 46 us for 17 GFLOP, 374 TFLOP/s, where an exponential a
-// score (135 million) alone is 14 us of the transcendental units.
+// 2048 keys, 8 heads: 46 us for 17 GFLOP, 374 TFLOP/s: the vector units are busy
+// 32% of the cycles and the matrix units 15%, the rest waits between short steps
+// that each need the one before (LDS, product, exponential).
 
 #include "kvq.hpp"
 

@@ -286,6 +286,23 @@ def test_attention_ragged_batch_and_error_rows(R, splits_up):
     assert not (lse[0] == -np.inf).any() and (lse[1:4] == -np.inf).all()
 
 
+@pytest.mark.parametrize("B,H,N,S,dtype", [(65, 1, 1, 1300, "bf16"), (130, 1, 3, 1300, "f32"), (129, 2, 1, 1100, "bf16"),
+                                           (130, 2, 2, 300, "bf16")])
+def test_attention_batches_past_64(R, B, H, N, S, dtype):
+    """More batch rows than a wave has lanes: a few long ones, many short ones, unused ones at both ends."""
+    rng = np.random.default_rng(B + S)
+    prefix = rng.integers(0, 60, B)
+    prefix[rng.choice(B, 12, replace=False)] = rng.integers(S - 200, S - N, 12)
+    prefix[[0, 63, B - 2]] = [S - N, S - N - 1, S - N]
+    prefix[[1, 62, B - 1]] = [-1, S - N + 1, -7]
+    counts = rng.integers(0, N + 1, B)
+    counts[[0, 63, B - 2]] = N
+    cache = make_cache(R, rng, B, H, S, 64)
+    q = queries(rng, B, N, 3 * H, 64, dtype)
+    out, lse = R.kvq_attention(q, cache, ints(*prefix), counts=ints(*counts))
+    check_attention(out, lse, q, cache, prefix.tolist(), counts.tolist(), None, 0.125)
+
+
 def test_attention_masks_that_leave_a_row_empty(R):
     rng = np.random.default_rng(9)
     B, N, G, H, D = 2, 6, 2, 2, 64
