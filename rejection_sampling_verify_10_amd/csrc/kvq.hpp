@@ -5,6 +5,7 @@
 
 #include "common.hpp"
 #include "internal.hpp"
+#include "kvq_window.hpp"
 
 namespace sv {
 
@@ -139,11 +140,39 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 #if SV_KVQ_DEVICE
-// A buffer descriptor: loads past `bytes` give zeros and touch nothing.
+// A buffer descriptor: loads whose vector offset is not below `bytes` give zeros and touch nothing.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
 }
+// That of the tile at slot `first`, for those of its slots that lie below `end`.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const uint8_t* head, long pos, long first, long end) {
+    return rsrc(head + first * pos, tile_slots(first, end) * static_cast<int>(pos));
+}
 #endif
+// Codes and scales of slots first .. first+31 of those below `end`, as the lane of offsets ko, kso holds them; zeros for the
+// others.
+template <int D>
+__device__ __forceinline__ void load_k_step(const uint8_t* codes, const uint8_t* scales, long cp, long sp, long first, long end,
+                                            uint32_t ko, uint32_t kso, uint32_t (&k)[2][D / 32], uint32_t (&ks)[2]) {
+#if SV_KVQ_DEVICE
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const auto rk = tile_rsrc(codes, cp, first + kTile * t, end), rks = tile_rsrc(scales, sp, first + kTile * t, end);
+        if (D == 64) {
+            const auto w = __builtin_amdgcn_raw_buffer_load_b64(rk, ko, 0, 0);
+            k[t][0] = w[0], k[t][1] = w[1];
+        } else {
+#pragma unroll
+            for (int x = 0; x < D / 128; ++x) {
+                const auto w = __builtin_amdgcn_raw_buffer_load_b128(rk, ko + 16 * x, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) k[t][(4 * x + e) % (D / 32)] = w[e];
+            }
+        }
+        ks[t] = D == 256 ? __builtin_amdgcn_raw_buffer_load_b16(rks, kso, 0, 0) : __builtin_amdgcn_raw_buffer_load_b8(rks, kso, 0, 0);
+    }
+#endif
+}
 
 __device__ __forceinline__ int wave_scan_int(int v) {   // sum over the lanes up to this one
     const int lane = threadIdx.x & (kWave - 1);

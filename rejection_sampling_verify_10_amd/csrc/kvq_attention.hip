@@ -41,7 +41,6 @@ namespace sv {
 
 namespace {
 
-constexpr int kStep = 32;                               // keys of one step
 constexpr int kChunk = 128;                             // units of the key axis' split
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -394,6 +393,8 @@ template <int D> struct Raw {
 // lies past it comes back as zeros (code 0, scale 0) and costs no traffic, so
 // every step, the last and the one prefetched past the end too, is the same
 // straight run of loads and the wait for a step never includes the next one's.
+// A descriptor is one tile of 16 slots, and the loads' offsets are vector offsets
+// (kvq_window.hpp says why).
 template <int D> struct Loader {
     const uint8_t *kc, *ks, *vc, *vs;                   // of the (b, h)
     long cp, sp;
@@ -406,50 +407,30 @@ template <int D> struct Loader {
         vs = c.vs + b * c.sb + h * c.sh;
         cp = c.cp;
         sp = c.sp;
-        ko = static_cast<uint32_t>(col * cp) + g * (D / 8);
-        kso = static_cast<uint32_t>(col * sp) + g * D / 128;
-        vo = static_cast<uint32_t>(4 * g * cp) + col * (D / 32);
-        vso = static_cast<uint32_t>(4 * g * sp) + col * (D / 16) / kQBlock;
+        ko = k_offset(D, col, g, static_cast<int>(cp));
+        kso = k_scale_offset(D, col, g, static_cast<int>(sp));
+        vo = v_offset(D, col, g, static_cast<int>(cp));
+        vso = v_scale_offset(D, col, g, static_cast<int>(sp));
     }
     // keys kb .. kb+31 of those below lim
     __device__ __forceinline__ void load_k(Raw<D>& r, long kb, long lim) const {
-#if SV_KVQ_DEVICE
-        const int n = static_cast<int>(max(min(lim - kb, static_cast<long>(kStep)), 0l));
-        const int cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
-        const auto rk = rsrc(kc + kb * cp, n * cp32), rks = rsrc(ks + kb * sp, n * sp32);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if (D == 64) {
-                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rk, ko, 16 * t * cp32, 0);
-                r.k[t][0] = w[0], r.k[t][1] = w[1];
-            } else {
-#pragma unroll
-                for (int x = 0; x < D / 128; ++x) {
-                    const auto w = __builtin_amdgcn_raw_buffer_load_b128(rk, ko + 16 * x, 16 * t * cp32, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) r.k[t][(4 * x + e) % Raw<D>::kKW] = w[e];
-                }
-            }
-            r.ks[t] = D == 256 ? __builtin_amdgcn_raw_buffer_load_b16(rks, kso, 16 * t * sp32, 0)
-                               : __builtin_amdgcn_raw_buffer_load_b8(rks, kso, 16 * t * sp32, 0);
-        }
-#endif
+        load_k_step<D>(kc, ks, cp, sp, kb, lim, ko, kso, r.k, r.ks);
     }
     __device__ __forceinline__ void load_v(Raw<D>& r, long kb, long lim) const {
 #if SV_KVQ_DEVICE
-        const int n = static_cast<int>(max(min(lim - kb, static_cast<long>(kStep)), 0l));
-        const int cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
-        const auto rv = rsrc(vc + kb * cp, n * cp32), rvs = rsrc(vs + kb * sp, n * sp32);
+        uint32_t o = vo, so = vso;
+        asm volatile("" : "+v"(o), "+v"(so));           // the four offsets are formed every step, not kept
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int key = 16 * (j / 4) + j % 4;       // and 4g more, in the lane's offset
-            if (D == 64) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rv, vo, key * cp32, 0);
-            else if (D == 128) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, vo, key * cp32, 0);
+            const auto rv = tile_rsrc(vc, cp, kb + kTile * (j / 4), lim), rvs = tile_rsrc(vs, sp, kb + kTile * (j / 4), lim);
+            const uint32_t at = o + j % 4 * static_cast<int>(cp), sat = so + j % 4 * static_cast<int>(sp);
+            if (D == 64) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rv, at, 0, 0);
+            else if (D == 128) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, at, 0, 0);
             else {
-                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rv, vo, key * cp32, 0);
+                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rv, at, 0, 0);
                 r.v[j][0] = w[0], r.v[j][Raw<D>::kVW - 1] = w[1];
             }
-            r.vs[j] = __builtin_amdgcn_raw_buffer_load_b8(rvs, vso, key * sp32, 0);
+            r.vs[j] = __builtin_amdgcn_raw_buffer_load_b8(rvs, sat, 0, 0);
         }
 #endif
     }

@@ -69,32 +69,13 @@ template <int D> struct KeyStream {
         scores = a.scores + (static_cast<long>(b) * a.c.H + h) * a.c.capacity;
         cp = a.c.cp;
         sp = a.c.sp;
-        ko = static_cast<uint32_t>(c * cp) + g * (D / 8);
-        kso = static_cast<uint32_t>(c * sp) + g * D / 128;
+        ko = k_offset(D, c, g, static_cast<int>(cp));
+        kso = k_scale_offset(D, c, g, static_cast<int>(sp));
         mine = (g & 1) * 16 + c;
     }
     __device__ __forceinline__ void load(int kb) {
-#if SV_KVQ_DEVICE
         old = scores[min(kb + mine, all - 1)];
-        const int n = max(min(all - kb, 32), 0), cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
-        const auto rk = rsrc(kc + kb * cp, n * cp32), rks = rsrc(ks + kb * sp, n * sp32);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if (D == 64) {
-                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rk, ko, 16 * t * cp32, 0);
-                k[t][0] = w[0], k[t][1] = w[1];
-            } else {
-#pragma unroll
-                for (int x = 0; x < D / 128; ++x) {
-                    const auto w = __builtin_amdgcn_raw_buffer_load_b128(rk, ko + 16 * x, 16 * t * cp32, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) k[t][(4 * x + e) % (D / 32)] = w[e];
-                }
-            }
-            s[t] = D == 256 ? __builtin_amdgcn_raw_buffer_load_b16(rks, kso, 16 * t * sp32, 0)
-                            : __builtin_amdgcn_raw_buffer_load_b8(rks, kso, 16 * t * sp32, 0);
-        }
-#endif
+        load_k_step<D>(kc, ks, cp, sp, kb, all, ko, kso, k, s);
     }
     __device__ __forceinline__ u32x4 operand(int t, int x) const {
         const float sc = scale_value(D == 256 && x >= 4 ? s[t] >> 8 : s[t]);
