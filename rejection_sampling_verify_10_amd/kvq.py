@@ -237,12 +237,20 @@ def kvq_attention(q: torch.Tensor, cache: KVQCache, prefix: torch.Tensor, *, mas
 
 def kvq_commit(cache: KVQCache, prefix: torch.Tensor, path: torch.Tensor, accept_len: torch.Tensor,
                N: int) -> torch.Tensor:
-    """:func:`kv_commit` of the accepted paths on the cache's four arrays; returns the new lengths [B] int32."""
-    from . import kv_commit
-    out = None
+    """The accepted paths' rows into place in the cache's four arrays (``spec_kv_commit`` on each); returns the new
+    lengths [B] int32, -1 for malformed rows.  prefix and accept_len [B], path [B, D+1] int32."""
+    dev, row = cache.device, (cache.B,)
+    if path.dim() != 2:
+        raise ValueError("path must be [B, D+1]")
+    lists = (_tensor(prefix, "prefix", torch.int32, row, dev),
+             _tensor(path, "path", torch.int32, (cache.B, path.shape[1]), dev), path.shape[1], int(N),
+             _tensor(accept_len, "accept_len", torch.int32, row, dev))
+    new_len = torch.empty(row, dtype=torch.int32, device=dev)
     for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
-        out = kv_commit(t.transpose(0, 1), prefix, path, accept_len, N, out_len=out)
-    return out
+        batch, head, pos = t.stride()[:3]
+        _call(lib().spec_kv_commit, "spec_kv_commit", dev, t.data_ptr(), cache.heads, head, cache.B, batch, pos,
+              t.shape[3], cache.capacity, *lists, new_len.data_ptr())
+    return new_len
 
 
 def kvq_score_workspace_bytes(cache: KVQCache, N: int, q_heads: int, path_len: int = 0,

@@ -1,0 +1,89 @@
+"""What the four-bit cache's commit passes to the library, on which device and stream (no GPU: the library's call and
+torch's device are stood in for)."""
+
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from rejection_sampling_verify_10_amd import kvq
+import rejection_sampling_verify_10_amd as R
+
+
+class Machine:
+    """A machine whose current device is 0, and what was called on it."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.calls = 0, []
+        machine = self
+
+        class On:
+            def __init__(self, device):
+                self.index = device.index
+
+            def __enter__(self):
+                self.before, machine.current = machine.current, self.index
+
+            def __exit__(self, *a):
+                machine.current = self.before
+
+        def commit(*args):
+            self.calls.append((self.current, args))
+            return 0
+
+        library = SimpleNamespace(spec_kv_commit=commit)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
+        monkeypatch.setattr(torch.cuda, "device", On)
+        monkeypatch.setattr(kvq, "lib", lambda: library)
+        monkeypatch.setattr(R, "lib", lambda: library)
+        monkeypatch.setattr(kvq, "_raw_stream", lambda index: 1000 + index)
+        monkeypatch.setattr(R, "_stream", lambda device: 1000 + self.index_of(device))
+        self.index = -1
+
+    def index_of(self, device):
+        return self.index
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on a GPU."""
+    index = 0
+    is_cuda = True
+
+    def get_device(self):
+        return OnGpu.index
+
+
+def gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+def make(monkeypatch, index, B=2, H=3, S=8, D=64, pos=None):
+    monkeypatch.setattr(OnGpu, "index", index)
+    machine = Machine(monkeypatch)
+    machine.index = index
+    cache = kvq.KVQCache.__new__(kvq.KVQCache)
+    for name, last in (("k_codes", D // 2), ("k_scales", D // 32), ("v_codes", D // 2), ("v_scales", D // 32)):
+        t = torch.zeros((B, H, S, last), dtype=torch.uint8)
+        if pos is not None:
+            t = t.as_strided(t.shape, (t.stride(0), t.stride(1), pos, 1))
+        setattr(cache, name, gpu(t))
+    cache.B, cache.heads, cache.capacity, cache.head_dim = B, H, S, D
+    cache.device = SimpleNamespace(index=index)
+    real_empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: gpu(real_empty(*a, **kw)))
+    ints = lambda *s: gpu(torch.zeros(*s, dtype=torch.int32))  # noqa: E731
+    return machine, cache, ints
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_every_array_moves_on_the_caches_device(monkeypatch, index):
+    machine, cache, ints = make(monkeypatch, index)
+    kvq.kvq_commit(cache, ints(2), ints(2, 4), ints(2), 5)
+    arrays = [cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales]
+    assert [a[0] for _, a in machine.calls] == [t.data_ptr() for t in arrays]
+    for (current, args), t in zip(machine.calls, arrays):
+        assert current == index                              # kernels start on the current device
+        assert args[-1] == 1000 + index                      # and its stream
+        row = t.shape[3]
+        assert args[1:8] == (3, 8 * row, 2, 24 * row, row, row, 8)       # heads, their stride, batch, .., capacity
+    assert machine.current == 0
