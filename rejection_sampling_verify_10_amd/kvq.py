@@ -248,6 +248,8 @@ def kvq_commit(cache: KVQCache, prefix: torch.Tensor, path: torch.Tensor, accept
     new_len = torch.empty(row, dtype=torch.int32, device=dev)
     for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
         batch, head, pos = t.stride()[:3]
+        if cache.capacity == 1:                              # the stride of a dimension of one element never counts
+            pos = t.shape[3]
         _call(lib().spec_kv_commit, "spec_kv_commit", dev, t.data_ptr(), cache.heads, head, cache.B, batch, pos,
               t.shape[3], cache.capacity, *lists, new_len.data_ptr())
     return new_len

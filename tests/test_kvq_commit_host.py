@@ -87,3 +87,12 @@ def test_every_array_moves_on_the_caches_device(monkeypatch, index):
         row = t.shape[3]
         assert args[1:8] == (3, 8 * row, 2, 24 * row, row, row, 8)       # heads, their stride, batch, .., capacity
     assert machine.current == 0
+
+
+@pytest.mark.parametrize("pos", [0, 16, 1 << 25])
+def test_one_slot_has_no_stride(monkeypatch, pos):
+    """A cache of one slot may have any slot stride: the library gets one that it takes (at least a row)."""
+    machine, cache, ints = make(monkeypatch, 0, S=1, pos=pos)
+    kvq.kvq_commit(cache, ints(2), ints(2, 1), ints(2), 1)
+    for (_, args), t in zip(machine.calls, (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)):
+        assert args[5] == args[6] == t.shape[3]
