@@ -633,7 +633,9 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
  *   scores, positions          [B][heads][capacity], read
  *   out_scores, out_positions  the same, written up to the new length: each
  *                              either the array read, or one that overlaps neither
- *   lengths, seen              [B] int32
+ *   lengths, seen              [B] int32: the rows in the cache, and the tokens the sequence
+ *                              has had, this step's among them (spec_kvq_score's seen[b] +
+ *                              accept_len[b] + 1)
  *   out_len     [B] int32: min(lengths[b], keep); error rows (lengths[b] < 0 or
  *               above capacity): -1, and nothing of them moves
  *   out_source  [B][heads][keep] int32: the slot each kept row came from, -1

@@ -5,10 +5,15 @@ every argument means).  One :class:`KVQCache` is one layer's cache; a speculativ
 
     kvq_append(cache, k, v, prefix)                          # the draft's N rows
     out, lse = kvq_attention(q, cache, prefix, mask=mask)    # in every layer
-    ...                                                      # LM head, verify_tree_* / verify_chain
-    new_len = kvq_commit(cache, prefix, path, accept_len, N)
+    ...                                                      # LM head, verify_tree_*: path, accept_len
+    lengths = kvq_commit(cache, prefix, path, accept_len, N)
     kvq_score(q, lse, cache, prefix, accept_len, scores, positions, seen, path=path)
-    new_len, _ = kvq_evict(cache, scores, positions, new_len, seen, keep, sink=4, recent=64)
+    seen = seen + accept_len + 1                             # once a step; a malformed row (accept_len -1) adds none
+    prefix, _ = kvq_evict(cache, scores, positions, lengths, seen, keep, sink=4, recent=64)
+
+``prefix`` holds the rows in the cache, ``seen`` the tokens that the sequences have had, evicted ones too: score
+numbers the step's rows from ``seen`` as it was before the step, evict counts ``recent`` back from it after the step.
+A chain's accepted rows (verify_chain) are in place already: no commit and no path, lengths = prefix + accept_len + 1.
 """
 
 from __future__ import annotations
@@ -271,7 +276,8 @@ def kvq_score(q: torch.Tensor, lse: torch.Tensor, cache: KVQCache, prefix: torch
     After :func:`kvq_commit`: q and lse [B, N, q_heads] as :func:`kvq_attention` took and gave them, prefix [B] the
     lengths BEFORE the step, path [B, D+1] and accept_len [B] the verification's (path None: tokens 0 ..
     accept_len[b]).  scores [B, heads, capacity] f32 and positions [B, heads, capacity] int32: the slots the step
-    added start at their weight and at position seen[b] + i; seen [B] int32 counts the sequence's tokens so far.
+    added start at their weight and at position seen[b] + i; seen [B] int32 counts the sequence's tokens before the
+    step and is left as it is (add accept_len + 1 before :func:`kvq_evict` and the next step).
     """
     rq = _rows(q, "q", cache)
     B, N, Hq, D = q.shape
@@ -307,7 +313,7 @@ def kvq_evict(cache: KVQCache, scores: torch.Tensor, positions: torch.Tensor, le
     """Cut every head to its ``keep`` best rows, in place (``spec_kvq_evict``).
 
     Kept first are rows with positions below ``sink`` or at seen[b] - recent and later, then those of largest
-    score.  scores, positions [B, heads, capacity] are moved along in place, or written to ``out_scores`` and
+    score; seen [B] int32 counts the sequence's tokens with this step's.  scores, positions [B, heads, capacity] are moved along in place, or written to ``out_scores`` and
     ``out_positions``.  Returns (new lengths [B], the slot each kept row came from [B, heads, keep]) int32.
     """
     dev, row, slots = cache.device, (cache.B,), (cache.B, cache.heads, cache.capacity)
