@@ -245,7 +245,7 @@ def kvq_commit(cache: KVQCache, prefix: torch.Tensor, path: torch.Tensor, accept
     """The accepted paths' rows into place in the cache's four arrays (``spec_kv_commit`` on each); returns the new
     lengths [B] int32, -1 for malformed rows.  prefix and accept_len [B], path [B, D+1] int32."""
     dev, row = cache.device, (cache.B,)
-    if path.dim() != 2:
+    if path.dim() != 2 or path.shape[1] < 1:
         raise ValueError("path must be [B, D+1]")
     lists = (_tensor(prefix, "prefix", torch.int32, row, dev),
              _tensor(path, "path", torch.int32, (cache.B, path.shape[1]), dev), path.shape[1], int(N),
@@ -286,7 +286,7 @@ def kvq_score(q: torch.Tensor, lse: torch.Tensor, cache: KVQCache, prefix: torch
     dev, row, slots = cache.device, (B,), (B, cache.heads, cache.capacity)
     pp, stride = None, N
     if path is not None:
-        if path.dim() != 2:
+        if path.dim() != 2 or path.shape[1] < 1:
             raise ValueError("path must be [B, D+1]")
         stride = path.shape[1]
         pp = _tensor(path, "path", torch.int32, (B, stride), dev)
