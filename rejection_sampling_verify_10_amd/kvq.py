@@ -320,8 +320,9 @@ def kvq_evict(cache: KVQCache, scores: torch.Tensor, positions: torch.Tensor, le
     keep = int(keep)
     if not 1 <= keep <= cache.capacity:
         raise ValueError(f"keep must lie in [1, {cache.capacity}]")
-    if sink < 0 or recent < 0:
-        raise ValueError("sink and recent must not be negative")
+    for n, name in ((sink, "sink"), (recent, "recent")):
+        if not 0 <= n < 2 ** 31:
+            raise ValueError(f"{name} must lie in [0, 2^31)")
     out_scores = scores if out_scores is None else out_scores
     out_positions = positions if out_positions is None else out_positions
     new_len = torch.empty(row, dtype=torch.int32, device=dev)

@@ -38,3 +38,17 @@ def test_a_path_of_no_nodes_is_not_a_missing_path(monkeypatch, width):
             with pytest.raises(ValueError, match="path"):
                 call()
     assert bool(called) == bool(width)
+
+
+@pytest.mark.parametrize("name", ["sink", "recent"])
+@pytest.mark.parametrize("value", [0, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, -1])
+def test_counts_past_31_bits_do_not_wrap(monkeypatch, name, value):
+    cache, ints, called = stand_in(monkeypatch)
+    call = lambda: kvq.kvq_evict(cache, gpu(torch.zeros(2, 3, 8)), ints(2, 3, 8), ints(2), ints(2), 4, **{name: value})  # noqa: E731
+    if 0 <= value < 2 ** 31:
+        call()
+        assert called[0][6 if name == "sink" else 7] == value
+    else:
+        with pytest.raises(ValueError, match=name):
+            call()
+        assert not called
