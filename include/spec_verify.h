@@ -571,7 +571,7 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
  *   q        rows of (b, n, hq), SPEC_F32 or SPEC_BF16
  *   mask     [B][N][N] uint8 device, batch rows mask_batch bytes apart (0: one
  *            mask for all), or NULL
- *   scale    finite, above 0
+ *   scale    above 0, scale * log2(e) a finite float32
  *   out      [B][N][q_heads][D], of q's type, contiguous, 16-byte aligned
  *   out_lse  [B][N][q_heads] float32: log sum_s exp(scale * (q . K_s)); or NULL
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros
@@ -580,7 +580,8 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
  * row of either).  Queries that are not finite give unspecified rows.  K and V
  * enter exactly (E2M1 times a power of two is a bfloat16), products and sums are
  * float32 (V of 2^90 and more may overflow in them: they are divided by the
- * probabilities' sum at the end); with bfloat16 queries the probabilities round
+ * probabilities' sum at the end; a query one of whose visible scores, in base
+ * two, is no finite float32 gives an unspecified row); with bfloat16 queries the probabilities round
  * to bfloat16 before they meet V.
  * q_heads a multiple of heads; N <= 65536 (with a mask: N <= SPEC_MAX_NODES).
  * workspace: spec_kvq_attention_workspace_bytes(...) bytes (may be 0), any

@@ -353,6 +353,9 @@ bool kvq_sizes_ok(int B, int H, int N, int G) { return N <= 65536 && kvq_count_o
 // A launch has fewer than 2^32 threads.
 bool kvq_threads_ok(double workgroups, int threads) { return workgroups * threads < 4294967296.0; }
 
+// A softmax scale for exponentials in base two.
+float base_two(float scale) { return static_cast<float>(1.4426950408889634 * static_cast<double>(scale)); }
+
 int take_cache(const spec_kvq_cache_t* c, KvqCache& o) {
     if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return SPEC_EINVAL;
     if (c->B < 1 || c->heads < 1 || c->capacity < 1 || c->head_dim < 1) return SPEC_EINVAL;
@@ -1143,7 +1146,8 @@ int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads
     if (N < 1 || q_heads < 1 || q_heads % a.c.H != 0 || !prefix || !out || !aligned(prefix, 4) ||
         !aligned(counts, 4) || !aligned(out, 16) || !aligned(out_lse, 4) || mask_batch < 0)
         return SPEC_EINVAL;
-    if (!(scale > 0.f) || !isfinite(scale)) return SPEC_EINVAL;
+    const float cexp = base_two(scale);
+    if (!(scale > 0.f) || !isfinite(cexp)) return SPEC_EINVAL;
     if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (mask && N > SPEC_MAX_NODES) ||
         !kvq_threads_ok((static_cast<double>(a.c.B) * a.c.H + 8) * ((N * (q_heads / a.c.H) + 15) / 16), 512))
         return SPEC_EUNSUPPORTED;
@@ -1156,7 +1160,7 @@ int spec_kvq_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads
     a.counts = counts;
     a.mask = mask;
     a.mask_batch = mask_batch;
-    a.cexp = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.cexp = cexp;
     a.out = out;
     a.out_lse = out_lse;
     kvq_attention_plan(a);
@@ -1208,7 +1212,8 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
     if (!aligned(lse, 4) || !aligned(prefix, 4) || !aligned(path, 4) || !aligned(accept_len, 4) ||
         !aligned(scores, 4) || !aligned(positions, 4) || !aligned(seen, 4))
         return SPEC_EINVAL;
-    if (!(scale > 0.f) || !isfinite(scale)) return SPEC_EINVAL;
+    const float cexp = base_two(scale);
+    if (!(scale > 0.f) || !isfinite(cexp)) return SPEC_EINVAL;
     if (!kvq_sizes_ok(a.c.B, a.c.H, N, q_heads / a.c.H) || (path && path_stride > SPEC_MAX_NODES) ||
         !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H + 1024, 512) ||
         !kvq_threads_ok(static_cast<double>(a.c.B) * a.c.H * ((a.c.capacity + 255) / 256), 256))
@@ -1222,7 +1227,7 @@ int spec_kvq_score(const spec_kvq_rows_t* q, spec_dtype_t dtype, int q_heads, in
     a.path = path;
     a.path_stride = path ? path_stride : N;
     a.accept_len = accept_len;
-    a.cexp = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.cexp = cexp;
     a.scores = scores;
     a.positions = positions;
     a.seen = seen;

@@ -52,3 +52,13 @@ def test_counts_past_31_bits_do_not_wrap(monkeypatch, name, value):
         with pytest.raises(ValueError, match=name):
             call()
         assert not called
+
+
+@pytest.mark.parametrize("scale", [2.5e38, 3.4e38])
+def test_scales_whose_base_two_form_is_infinite(scale):
+    """scale * log2(e) is what the kernels multiply by: an infinite one would make NaN of a score of zero."""
+    import test_kvq_host as host
+    import rejection_sampling_verify_10_amd as R
+    c = host.cache(R)
+    assert host.attend(R, c, scale=scale) == host.EINVAL
+    assert host.score(R, c, scale=scale) == host.EINVAL
