@@ -144,20 +144,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
 }
-// That of the tile at slot `first`, for those of its slots that lie below `end`.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const uint8_t* head, long pos, long first, long end) {
-    return rsrc(head + first * pos, tile_slots(first, end) * static_cast<int>(pos));
+// That of tile t of a step whose slots start at p, `pos` bytes apart, with `slots` of the tile's there.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const uint8_t* p, int t, int pos, int slots) {
+    return rsrc(p + kTile * t * pos, slots * pos);
+}
+// tile_slots(slots_left(..)), in two: the compiler makes one clamp of both, on the vector unit, and a descriptor's
+// registers are scalar ones.
+__device__ __forceinline__ int scalar_slots(int first, int end) {
+    int left = slots_left(first, end);
+    asm("" : "+s"(left));
+    return tile_slots(left);
 }
 #endif
 // Codes and scales of slots first .. first+31 of those below `end`, as the lane of offsets ko, kso holds them; zeros for the
 // others.
 template <int D>
-__device__ __forceinline__ void load_k_step(const uint8_t* codes, const uint8_t* scales, long cp, long sp, long first, long end,
+__device__ __forceinline__ void load_k_step(const uint8_t* codes, const uint8_t* scales, long cp, long sp, int first, int end,
                                             uint32_t ko, uint32_t kso, uint32_t (&k)[2][D / 32], uint32_t (&ks)[2]) {
 #if SV_KVQ_DEVICE
+    const uint8_t *c = codes + first * cp, *s = scales + first * sp;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const auto rk = tile_rsrc(codes, cp, first + kTile * t, end), rks = tile_rsrc(scales, sp, first + kTile * t, end);
+        const int n = scalar_slots(first + kTile * t, end);
+        const auto rk = tile_rsrc(c, t, static_cast<int>(cp), n), rks = tile_rsrc(s, t, static_cast<int>(sp), n);
         if (D == 64) {
             const auto w = __builtin_amdgcn_raw_buffer_load_b64(rk, ko, 0, 0);
             k[t][0] = w[0], k[t][1] = w[1];

@@ -413,24 +413,31 @@ template <int D> struct Loader {
         vso = v_scale_offset(D, col, g, static_cast<int>(sp));
     }
     // keys kb .. kb+31 of those below lim
-    __device__ __forceinline__ void load_k(Raw<D>& r, long kb, long lim) const {
+    __device__ __forceinline__ void load_k(Raw<D>& r, int kb, int lim) const {
         load_k_step<D>(kc, ks, cp, sp, kb, lim, ko, kso, r.k, r.ks);
     }
-    __device__ __forceinline__ void load_v(Raw<D>& r, long kb, long lim) const {
+    __device__ __forceinline__ void load_v(Raw<D>& r, int kb, int lim) const {
 #if SV_KVQ_DEVICE
+        const int cp32 = static_cast<int>(cp), sp32 = static_cast<int>(sp);
+        const uint8_t *p = vc + kb * cp, *ps = vs + kb * sp;
         uint32_t o = vo, so = vso;
         asm volatile("" : "+v"(o), "+v"(so));           // the four offsets are formed every step, not kept
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const auto rv = tile_rsrc(vc, cp, kb + kTile * (j / 4), lim), rvs = tile_rsrc(vs, sp, kb + kTile * (j / 4), lim);
-            const uint32_t at = o + j % 4 * static_cast<int>(cp), sat = so + j % 4 * static_cast<int>(sp);
-            if (D == 64) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rv, at, 0, 0);
-            else if (D == 128) r.v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, at, 0, 0);
-            else {
-                const auto w = __builtin_amdgcn_raw_buffer_load_b64(rv, at, 0, 0);
-                r.v[j][0] = w[0], r.v[j][Raw<D>::kVW - 1] = w[1];
+        for (int t = 0; t < 2; ++t) {
+            const int n = scalar_slots(kb + kTile * t, lim);
+            const auto rv = tile_rsrc(p, t, cp32, n), rvs = tile_rsrc(ps, t, sp32, n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = o + i * cp32, sat = so + i * sp32;
+                uint32_t(&w)[Raw<D>::kVW] = r.v[4 * t + i];
+                if (D == 64) w[0] = __builtin_amdgcn_raw_buffer_load_b16(rv, at, 0, 0);
+                else if (D == 128) w[0] = __builtin_amdgcn_raw_buffer_load_b32(rv, at, 0, 0);
+                else {
+                    const auto x = __builtin_amdgcn_raw_buffer_load_b64(rv, at, 0, 0);
+                    w[0] = x[0], w[Raw<D>::kVW - 1] = x[1];
+                }
+                r.vs[4 * t + i] = __builtin_amdgcn_raw_buffer_load_b8(rvs, sat, 0, 0);
             }
-            r.vs[j] = __builtin_amdgcn_raw_buffer_load_b8(rvs, sat, 0, 0);
         }
 #endif
     }

@@ -16,11 +16,10 @@ namespace sv {
 constexpr int kTile = 16;                               // slots of a descriptor
 constexpr int kStep = 2 * kTile;                        // slots of one step
 
-// Slots of the tile at `first` that lie below `end`: the descriptor's bytes end behind them.
-constexpr int tile_slots(long first, long end) {
-    const long n = end - first;
-    return static_cast<int>(n < 0 ? 0 : n < kTile ? n : kTile);
-}
+// Slots of the tile at `first` that lie below `end`, of the `left` ones from there: the descriptor's bytes end behind them.
+// (Slots end at 2^30: 32 bits hold both.)
+constexpr int slots_left(int first, int end) { return end > first ? end - first : 0; }
+constexpr int tile_slots(int left) { return left < kTile ? left : kTile; }
 
 // K: lane (c, g), c < 16, g < 4, reads the g-th quarter of the tile's slot c, and the scale byte(s) of it.
 constexpr int k_slot(int c) { return c; }

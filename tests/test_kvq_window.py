@@ -35,7 +35,7 @@ int main() {
                     for (int n = -40; n <= 40; ++n)
                         for (int tile = 0; tile < kStep / kTile; ++tile) {
                             const long end = first + n, at = first + kTile * tile;
-                            const int slots = tile_slots(at, end);
+                            const int slots = tile_slots(slots_left((int)at, (int)end));
                             long there = 0;                 // counted one by one
                             for (int s = 0; s < kTile; ++s) there += at + s < end;
                             bool ok = slots == there && slots * cp < (1l << 31) && slots * sp < (1l << 31);
