@@ -513,6 +513,11 @@ int spec_kv_commit(void* kv, int planes, long long plane_stride, int B, long lon
  * so marks a row of the batch as unused.
  */
 
+/* The host knows no lengths, so how attention, score and evict are cut up goes by
+ * the cache's capacity and the batch's size: a call on short rows takes longer in
+ * a cache of many more slots than they need, and one row far longer than a large
+ * batch's others is not spread over the GPU.  Sums differ in their rounding alone. */
+
 /* One layer's cache.  Row (b, h, slot): codes at b*code_batch + h*code_head +
  * slot*code_pos bytes from k_codes / v_codes, scales likewise.  Codes: base and
  * strides multiples of 16 bytes; scales: of D/32 bytes.  No two rows may share
@@ -577,12 +582,12 @@ int spec_kvq_read(const spec_kvq_cache_t* cache, spec_dtype_t dtype, int N, cons
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros
  * and an out_lse of -inf.  What a query does not see never reaches it, whatever
  * its bytes; a NaN reaches it through a K row alone (spec_kvq_append marks the K
- * row of either).  Queries that are not finite give unspecified rows.  K and V
- * enter exactly (E2M1 times a power of two is a bfloat16), products and sums are
- * float32 (V of 2^90 and more may overflow in them: they are divided by the
- * probabilities' sum at the end; a query one of whose visible scores, in base
- * two, is no finite float32 gives an unspecified row); with bfloat16 queries the probabilities round
- * to bfloat16 before they meet V.
+ * row of either).  Queries that are not finite (or, float32, round to an infinite
+ * bfloat16) and those with a visible score that, in base two, is no finite float32
+ * give unspecified rows.  K and V enter exactly (E2M1 times a power of two is a
+ * bfloat16), products and sums are float32 (V of 2^90 and more may overflow in
+ * them: they are divided by the probabilities' sum at the end); with bfloat16
+ * queries the probabilities round to bfloat16 before they meet V.
  * q_heads a multiple of heads; N <= 65536 (with a mask: N <= SPEC_MAX_NODES).
  * workspace: spec_kvq_attention_workspace_bytes(...) bytes (may be 0), any
  * contents; left as scratch.

@@ -18,22 +18,29 @@
 // instruction, exactly (E2M1 times a power of two).  V pairs two elements of one
 // key where the product wants two keys of one element: one byte permute each.
 //
-// float32 queries enter as three bf16 parts, and so does P: exact both.
+// float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
+// queries P is the one bf16 of it: at most 2^-8 relative a key, of either sign,
+// which is the output's own rounding; the sum l, and so the lse, is of the
+// unrounded values.  Against 64 bits whole cases' outputs are off by 0.0022 of
+// their size, where float32 probabilities leave 0.0017 (the output's rounding);
+// two parts more would triple the second product.
 //
 // Where the rows are few the cache's bytes bound it, so the key axis is what is
 // spread: the waves of a workgroup take 32 keys each in turn and join through
 // LDS, and workgroups take units of the batch's whole key axis, alike whatever
 // the lengths, which a second kernel joins.
 //
-// Measured (8 cache heads, D = 128, bf16): 64 sequences of one token and 8 query
-// heads a cache head, ragged lengths to 8192: 74-78 us for 359 MB, 4.7 TB/s, the
-// bytes.  8 tokens x 4 heads at 131071 keys: 37 + 5 us for 143 MB, conversions
-// and bytes alike.  27-node trees x 4 heads, 32 sequences to 4096: 63-70 us for
-// 36 GFLOP, 550 TFLOP/s: of the cycles, the vector units are busy 58% (the
-// conversions of K and V, half rate, are nearly half of that) and the matrix
-// units 25%, and a wave does one or the other.  A prompt of 2 x 1023 tokens:
-// 56-68 us for 39 GFLOP, the same.  One token at 1000 keys: 8 us, the chain of
-// load, product, exponential, product, join.
+// Measured (8 cache heads, D = 128, bf16, whole calls): 64 sequences of one token
+// and 8 query heads a cache head, ragged lengths to 8192: 75-78 us for 359 MB, 4.7
+// TB/s, short of the 5.7 and more that kernels reach which only read: a lane has
+// one step of narrow loads (V: eight of 4 bytes and eight of 1) under way.  8
+// tokens x 4 heads at 131071 keys: 42 us for 143 MB, the join 5 of them,
+// conversions and bytes alike.  27-node trees x 4 heads, 32 sequences to 4096:
+// 64 us for 36 GFLOP, 570 TFLOP/s: of the cycles, the vector units are busy 58%
+// (the conversions of K and V, half rate, are nearly half of that) and the matrix
+// units 25%, and a wave does one or the other, in turn.  A prompt of 2 x 1023
+// tokens: 58-63 us for 39 GFLOP, the same.  One token in a cache of 1000 slots:
+// 9-10 us, the chain of load, product, exponential, product, join.
 
 #include "kvq.hpp"
 
@@ -721,8 +728,10 @@ template <int D, int DT> void attend(const KvqAttnArgs& a, hipStream_t s, Timing
 
 // The key axis is split so that a launch has about 512 workgroups (two a compute unit: 131071 keys, 8 heads, 32 rows
 // each: 39 + 5 us; 1024 workgroups 51 + 12, 256 41 + 5), into units of 256 keys at least.  A cache of up to 1024 slots
-// is not: its one launch beats two (1000 keys, 8 heads, one token: 9.6 us against 8 + 3.5 and a second launch), with
-// eight waves where the rows fit one tile.
+// is not: its one launch beats two (one token of 8 heads at 1000 keys: 9.8 us in a cache of 1024 slots, 12.3 in one of
+// 1025), with eight waves where the rows fit one tile.  Nor are batches whose row tiles alone are 512 workgroups, whatever
+// their lengths (the host knows none): one sequence of 131071 keys among 63 of 1000, 8 heads, is 720 us, and 370 among 62,
+// where it gets two units.
 void kvq_attention_plan(KvqAttnArgs& a) {
     a.q_tiles = a.M > 16 ? most_tiles(a.c.D, a.dtype) : 1;
     const int rows = 16 * a.q_tiles;

@@ -16,7 +16,7 @@
 // whose sums meet in the workspace.
 //
 // 32 batch rows of 8 heads at ragged lengths to 4096 (27-node trees, paths of up
-// to 6 nodes): 18 us a call for 52 MB, 2.9 TB/s; a workgroup's few steps hardly
+// to 6 nodes): 17.5-18 us a call for 52 MB, 2.9 TB/s; a workgroup's few steps hardly
 // cover the latency of its first loads.  2048 tokens x 4 heads against their own
 // 2048 keys, 8 heads: 46 us for 17 GFLOP, 374 TFLOP/s: the vector units are busy
 // 32% of the cycles and the matrix units 15%, the rest waits between short steps
@@ -343,10 +343,11 @@ template <int D, int DT> void score(const KvqScoreArgs& a, hipStream_t s, Timing
 
 }  // namespace
 
-// Workgroups: four a compute unit for rows in registers (27-node trees, 32 batch rows at 4096 keys: 21 us; half as many
-// 27, twice as many 24), two where the rows fill LDS (32 tokens x 4 heads, 8 batch rows at 30000 keys: 74 us; half as
-// many 92), and with the rows split as well four (2048 tokens x 4 heads on their own 2048 keys: 44 + 6 us; two 65 + 5,
-// eight 49 + 7).
+// Workgroups: four a compute unit for rows in registers (27-node trees, 32 batch rows at 4096 keys: half as many take 1.3
+// times as long, twice as many 1.15), two where the rows fill LDS (32 tokens x 4 heads, 8 batch rows at 30000 keys: 74 us;
+// half as many 92), and with the rows split as well four (2048 tokens x 4 heads on their own 2048 keys: kernels of 45 + 6
+// us; two 65 + 5, eight 49 + 7).  The keys' share goes by the capacity, the host knowing no lengths: that prompt is 50 us
+// in a cache of 2053 slots, 56 in 4096, 96 in 8192 and 143 from 32768 on, where most key blocks hold nothing.
 void kvq_score_plan(KvqScoreArgs& a) {
     // the most rows there can be (the host knows no lengths)
     const long rows = static_cast<long>(a.path && a.path_stride < a.N ? a.path_stride : a.N) * a.G;
