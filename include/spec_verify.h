@@ -670,6 +670,62 @@ int spec_accept_rate(const void* target_logits, spec_dtype_t dtype, const float*
                      int B, int K, int V, float temperature, int top_k,
                      float* out_alpha, void* workspace, size_t workspace_bytes, void* hip_stream);
 
+/*
+ * ---- Log probabilities of tokens ----
+ *
+ * What a server answers beside the tokens that verification emits, and what a
+ * draft model is trained on: log p(t) of given tokens under p = softmax(z / T),
+ * the rows' entropy, their likeliest tokens; and the gradient for the logits.
+ */
+
+/*
+ * spec_token_logprobs -- for each of R logit rows z (row r at logits +
+ * r*row_stride elements, V of them, any element's alignment), with y = z / T:
+ *   out_logprobs[r][m]  = y[t] - log sum_i exp(y_i), t = tokens[r][m]
+ *   out_entropy[r]      = -sum_i p_i log p_i
+ *   out_top_tokens[r], out_top_logprobs[r]: the top_n largest logits, larger first,
+ *                         the lower index first among equals (-1 and -inf where
+ *                         fewer than top_n are above -inf)
+ *   out_stats[r][3]     = what spec_token_logprobs_grad goes by: the largest logit,
+ *                         log2 of sum_i 2^(log2(e)/T * (z_i - it)), the entropy
+ * A logit of -inf has probability 0 (a token that has it, log probability -inf).
+ * A negative token is none: its log probability is 0.  A row all of whose tokens
+ * are negative is not read: log probabilities, entropy and statistics 0, tops -1
+ * and -inf; so out_tokens of a verification call can be given as it is.  A row
+ * with a NaN, a +inf or only -inf among its logits, or with a token of V or more,
+ * answers NaN (and -1).  Sums are float32 over a thread's elements, float64 after.
+ *   tokens         [R][M] int32, 0 <= M <= SPEC_TOPK_MAX (M 0: NULL, every row is read)
+ *   temperature    above 0; log2(e) / temperature a finite float32
+ *   top_n          0 <= top_n <= SPEC_TOPK_MAX
+ *   out_logprobs   [R][M] (NULL if M is 0); out_entropy [R], out_stats [R][3] float32, each
+ *                  may be NULL; out_top_tokens [R][top_n] int32, out_top_logprobs
+ *                  [R][top_n] float32 (NULL if top_n is 0)
+ * workspace: spec_token_logprobs_workspace_bytes(...) bytes (may be 0), zero-filled
+ * before its first use and left zero by every call, so that calls of any sizes
+ * may share one.  Calls that overlap on one workspace race.
+ */
+size_t spec_token_logprobs_workspace_bytes(int R, int V, int top_n, spec_dtype_t dtype);
+int spec_token_logprobs(const void* logits, spec_dtype_t dtype, int64_t row_stride, int R, int V,
+                        const int32_t* tokens, int M, float temperature, int top_n, float* out_logprobs,
+                        float* out_entropy, float* out_stats, int32_t* out_top_tokens, float* out_top_logprobs,
+                        void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * spec_token_logprobs_grad -- the gradient for the logits, of their type:
+ *   dz_i = (1/T) (sum_m g_m [i = t_m] - p_i sum_m g_m - h p_i (log p_i + H))
+ * where g = grad_logprobs[r], h = grad_entropy[r], H the entropy.  A token given
+ * more than once collects each of its gradients; negative tokens' do not count.
+ * Rows all of whose tokens are negative get zeros; rows that answered NaN get NaN.
+ *   tokens, temperature, stats   as spec_token_logprobs had and gave them (M >= 1)
+ *   grad_logprobs  [R][M] float32; grad_entropy [R] float32 or NULL
+ *   out_grad       row r at out_grad + r*grad_stride elements; may be the logits
+ *                  themselves (the same pointer and stride), else overlaps nothing
+ */
+int spec_token_logprobs_grad(const void* logits, spec_dtype_t dtype, int64_t row_stride, int R, int V,
+                             const int32_t* tokens, int M, const float* stats, const float* grad_logprobs,
+                             const float* grad_entropy, float temperature, void* out_grad, int64_t grad_stride,
+                             void* hip_stream);
+
 /* Zero-fills `workspace_bytes` (a multiple of 4) of a 256-byte aligned workspace
  * with a fill kernel on hip_stream (no memset node, so it may be captured). */
 int spec_workspace_init(void* workspace, size_t workspace_bytes, void* hip_stream);

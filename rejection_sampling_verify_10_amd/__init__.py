@@ -103,6 +103,12 @@ def lib() -> ctypes.CDLL:
         L.spec_kvq_evict_workspace_bytes.restype = Z
         L.spec_kvq_evict.argtypes = [P, P, P, P, P, I, I, I, P, P, P, P, P, Z, P]
         L.spec_kvq_evict.restype = I
+        L.spec_token_logprobs_workspace_bytes.argtypes = [I, I, I, I]
+        L.spec_token_logprobs_workspace_bytes.restype = Z
+        L.spec_token_logprobs.argtypes = [P, I, LL, I, I, P, I, F, I, P, P, P, P, P, P, Z, P]
+        L.spec_token_logprobs.restype = I
+        L.spec_token_logprobs_grad.argtypes = [P, I, LL, I, I, P, I, P, P, P, F, P, LL, P]
+        L.spec_token_logprobs_grad.restype = I
         L.spec_profile_events.argtypes = [P, P]
         L.spec_profile_events.restype = I
         L.spec_workspace_init.argtypes = [P, Z, P]
@@ -563,3 +569,4 @@ def read_probe(src: torch.Tensor, sink: torch.Tensor) -> None:
 
 from .kvq import (KVQCache, kvq_append, kvq_attention, kvq_attention_workspace_bytes, kvq_commit, kvq_evict,  # noqa: E402,F401
                   kvq_evict_workspace_bytes, kvq_read, kvq_score, kvq_score_workspace_bytes, new_kvq_cache)
+from .logprobs import (TokenLogprobs, token_logprobs, token_logprobs_grad, token_logprobs_workspace_bytes)  # noqa: E402,F401

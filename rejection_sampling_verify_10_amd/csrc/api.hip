@@ -12,6 +12,7 @@
 #include "common.hpp"
 #include "internal.hpp"
 #include "kvq.hpp"
+#include "logprob.hpp"
 
 using namespace sv;
 
@@ -390,6 +391,29 @@ int take_rows(const spec_kvq_rows_t* r, int dtype, KvqRows& o) {
         return SPEC_EINVAL;
     o.data = r->data;
     o.batch = r->batch, o.pos = r->pos, o.head = r->head;
+    return SPEC_OK;
+}
+
+// A launch has fewer than 2^32 threads.
+bool logprob_grid_ok(int R, int slices) { return static_cast<double>(R) * slices * kLpThreads < 4294967296.0; }
+bool logprob_sizes_ok(LogprobArgs a) {
+    if (a.R < 1 || a.V < 1 || a.V > SPEC_MAX_V || a.top_n < 0 || a.top_n > SPEC_TOPK_MAX) return false;
+    logprob_plan(a);
+    return logprob_grid_ok(a.R, a.slices);
+}
+void carve_logprobs(Carver& c, LogprobArgs& a) {
+    if (a.slices == 1) return;
+    a.done = c.take<unsigned>(static_cast<size_t>(a.R));
+    a.words = c.take<unsigned long long>(static_cast<size_t>(a.R) * a.slices * (kLpHead + a.top_n));
+}
+int check_logprobs(const void* logits, int dtype, int64_t row_stride, int R, int V, const int32_t* tokens, int M,
+                   float temperature, float& c) {
+    if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || !logits || R < 1 || V < 1 || M < 0 || (M > 0 && !tokens) ||
+        (R > 1 && row_stride < V) || !aligned(logits, esz_of(dtype)) || !aligned(tokens, 4))
+        return SPEC_EINVAL;
+    c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+    if (!(temperature > 0.f) || !isfinite(c) || !(c > 0.f)) return SPEC_EINVAL;
+    if (V > SPEC_MAX_V || M > SPEC_TOPK_MAX || row_stride > (1ll << 40)) return SPEC_EUNSUPPORTED;
     return SPEC_OK;
 }
 
@@ -1349,6 +1373,88 @@ int spec_accept_rate(const void* target_logits, spec_dtype_t dtype, const float*
         }
         SV_TRY(launch_alpha_dense(aa, s));
     }
+    return SPEC_OK;
+}
+
+size_t spec_token_logprobs_workspace_bytes(int R, int V, int top_n, spec_dtype_t dtype) {
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return 0;
+    LogprobArgs a{};
+    a.dtype = dtype;
+    a.R = R;
+    a.V = V;
+    a.top_n = top_n;
+    if (!logprob_sizes_ok(a)) return 0;
+    logprob_plan(a);
+    Carver c(nullptr);
+    carve_logprobs(c, a);
+    return c.off;
+}
+
+int spec_token_logprobs(const void* logits, spec_dtype_t dtype, int64_t row_stride, int R, int V,
+                        const int32_t* tokens, int M, float temperature, int top_n, float* out_logprobs,
+                        float* out_entropy, float* out_stats, int32_t* out_top_tokens, float* out_top_logprobs,
+                        void* workspace, size_t workspace_bytes, void* hip_stream) {
+    LogprobArgs a{};
+    const int rc0 = check_logprobs(logits, dtype, row_stride, R, V, tokens, M, temperature, a.c);
+    if (rc0) return rc0;
+    if (top_n < 0 || (M > 0 && !out_logprobs) || (top_n > 0 && (!out_top_tokens || !out_top_logprobs)) ||
+        !aligned(out_logprobs, 4) || !aligned(out_entropy, 4) || !aligned(out_stats, 4) ||
+        !aligned(out_top_tokens, 4) || !aligned(out_top_logprobs, 4))
+        return SPEC_EINVAL;
+    a.logits = logits;
+    a.stride = row_stride;
+    a.dtype = dtype;
+    a.R = R;
+    a.V = V;
+    a.tokens = tokens;
+    a.M = M;
+    a.top_n = top_n;
+    a.out_lp = out_logprobs;
+    a.out_entropy = out_entropy;
+    a.out_stats = out_stats;
+    a.out_top = out_top_tokens;
+    a.out_top_lp = out_top_logprobs;
+    if (!logprob_sizes_ok(a)) return SPEC_EUNSUPPORTED;
+    logprob_plan(a);
+    Carver size(nullptr);
+    carve_logprobs(size, a);
+    const int rc = check_workspace(workspace, workspace_bytes, size.off);
+    if (rc) return rc;
+    Carver c(workspace);
+    carve_logprobs(c, a);
+    ProfileScope prof;
+    SV_TRY(launch_logprobs(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+int spec_token_logprobs_grad(const void* logits, spec_dtype_t dtype, int64_t row_stride, int R, int V,
+                             const int32_t* tokens, int M, const float* stats, const float* grad_logprobs,
+                             const float* grad_entropy, float temperature, void* out_grad, int64_t grad_stride,
+                             void* hip_stream) {
+    LogprobGradArgs a{};
+    const int rc = check_logprobs(logits, dtype, row_stride, R, V, tokens, M, temperature, a.c);
+    if (rc) return rc;
+    if (M < 1 || !stats || !grad_logprobs || !out_grad || (R > 1 && grad_stride < V) || !aligned(stats, 4) ||
+        !aligned(grad_logprobs, 4) || !aligned(grad_entropy, 4) || !aligned(out_grad, esz_of(dtype)) ||
+        (out_grad == logits && R > 1 && grad_stride != row_stride))
+        return SPEC_EINVAL;
+    a.logits = logits;
+    a.grad = out_grad;
+    a.stride = row_stride;
+    a.grad_stride = grad_stride;
+    a.dtype = dtype;
+    a.R = R;
+    a.V = V;
+    a.tokens = tokens;
+    a.M = M;
+    a.stats = stats;
+    a.g_lp = grad_logprobs;
+    a.g_entropy = grad_entropy;
+    a.invT = 1.f / temperature;
+    a.slices = logprob_grad_slices(dtype, V);
+    if (!logprob_grid_ok(R, a.slices)) return SPEC_EUNSUPPORTED;
+    ProfileScope prof;
+    SV_TRY(launch_logprobs_grad(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
     return SPEC_OK;
 }
 

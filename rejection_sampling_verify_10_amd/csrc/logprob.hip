@@ -1,0 +1,488 @@
+// Log probabilities of given tokens under logit rows, with the rows' entropy and
+// most likely tokens; and the gradient of the two for the logits.
+//
+// With x_i = log2(e)/T * (z_i - m), m the row's largest logit, S = sum 2^x_i and
+// W = sum 2^x_i x_i:  log p(t) = ln2 * (x_t - log2 S),  H = ln2 * (log2 S - W/S).
+// x is never above 0 but for its rounding, so no exponential overflows.
+//
+// Forward: a workgroup holds a slice of a row in registers (16-byte vectors), so
+// the row is read once although its maximum comes before its sums.  The n-th
+// largest of the threads' maxima is at most the slice's n-th largest element, and
+// few elements reach it: those go to LDS and one wave sorts them.  The workgroups
+// of a row leave (m, S, W, list) in the workspace, and the last of them joins.
+
+#include <float.h>
+
+#include "logprob.hpp"
+
+namespace sv {
+
+namespace {
+
+constexpr int kWaves = kLpThreads / kWave;
+constexpr int kStage = 256, kCand = 512;                // vectors and elements that may reach the threshold before the exact rounds
+
+typedef u32x4 __attribute__((aligned(4))) u32x4_a4;
+typedef u32x4 __attribute__((aligned(2))) u32x4_a2;
+
+// 16 bytes at any element's address.
+template <int DT> __device__ __forceinline__ u32x4 load_vec(const void* row, long i) {
+    if (DT == 1) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(row) + i));
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(row) + i));
+}
+template <int DT> __device__ __forceinline__ void store_vec(void* row, long i, const u32x4& v) {
+    if (DT == 1) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(static_cast<uint16_t*>(row) + i));
+    else __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a4*>(static_cast<float*>(row) + i));
+}
+template <int DT> __device__ __forceinline__ float vec_max(const u32x4& v) {
+    if (DT == 1) {
+        float a = maximum3(bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]));
+        float b = maximum3(bf16_hi(v[1]), bf16_lo(v[2]), bf16_hi(v[2]));
+        return maximum3(maximum3(a, b, bf16_lo(v[3])), bf16_hi(v[3]), a);
+    }
+    const float a = maximum3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+    return __builtin_elementwise_maximum(a, __uint_as_float(v[3]));
+}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+constexpr float kLowest = -1e30f;                       // 0 * kLowest is 0, 0 * -inf is not a number
+constexpr double kLn2 = 0.69314718055994530942;
+
+// x of a logit, mc = m * c.  Where that is no finite float32 (a row of the type's lowest values, or close to its largest)
+// the difference is taken first.
+__device__ __forceinline__ float exponent(float z, float c, float mc) { return fmaxf(__builtin_fmaf(z, c, -mc), kLowest); }
+__device__ __forceinline__ float exponent_wide(float z, float c, float m) { return fmaxf((z - m) * c, kLowest); }
+__device__ __forceinline__ bool is_wide(float m, float c) { return !(fabsf(m * c) <= FLT_MAX); }
+
+// What the exponents of a slice are relative to: m*c as it was used.
+__device__ __forceinline__ double reference(float m, float c) {
+    return is_wide(m, c) ? static_cast<double>(m) * static_cast<double>(c) : static_cast<double>(m * c);
+}
+
+struct Smem {
+    float red[kWaves], red2[kWaves];
+    uint32_t keys[kLpThreads];
+    u32x4 stage[kStage];
+    int32_t stage_i[kStage];
+    pkey_t cand[kCand];
+    int staged, count;
+    pkey_t best[kWaves];
+};
+
+__device__ __forceinline__ float wave_maximum(float v) {    // NaN wins
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = __builtin_elementwise_maximum(v, xshfl(v, o));
+    return v;
+}
+
+// A row is asked for unless it has tokens and all are negative; bad: a token past the vocabulary.
+__device__ __forceinline__ bool row_used(const int32_t* tokens, int M, int V, int& tok, bool& bad) {
+    const int lane = threadIdx.x & (kWave - 1);
+    tok = lane < M ? tokens[lane] : -1;
+    bad = __ballot(tok >= V) != 0ull;
+    return M == 0 || __ballot(tok >= 0) != 0ull;
+}
+
+// What a row is told by: r = log2(e)/T * m, S and W over the elements relative to it.
+struct Sums {
+    double r;               // NaN: a NaN or +inf among the logits
+    double S, W;
+};
+
+// No probability is above 1, whatever the sum's rounding.
+__device__ __forceinline__ float log_prob(double base_two) { return static_cast<float>(fmin(base_two, 0.0) * kLn2); }
+
+// The row's results, by one wave: lane l holds the l-th best element (key), the row's sums are the same in every lane.
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, long r, const Sums& s, float m, pkey_t key, int tok,
+                                           float z_tok, bool bad) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const double lS = log2(s.S);
+    const bool ok = !bad && s.S > 0.0 && s.S < INFINITY;    // neither NaN, nor +inf, nor all -inf
+    const float nan = __builtin_nanf("");
+    if (lane < a.M) {
+        const double x = static_cast<double>(z_tok) * static_cast<double>(a.c) - s.r;
+        a.out_lp[r * a.M + lane] = tok < 0 && !bad ? 0.f : ok ? log_prob(x - lS) : nan;
+    }
+    if (lane == 0) {
+        const float h = ok ? static_cast<float>(fmax(0.0, (lS - s.W / s.S) * kLn2)) : nan;
+        if (a.out_entropy) a.out_entropy[r] = h;
+        if (a.out_stats) {
+            a.out_stats[kLpStats * r] = ok ? m : nan;
+            a.out_stats[kLpStats * r + 1] = ok ? static_cast<float>(lS) : nan;
+            a.out_stats[kLpStats * r + 2] = h;
+        }
+    }
+    if (lane < a.top_n) {
+        const bool have = ok && key > empty_key();
+        const double x = static_cast<double>(key_val(key)) * static_cast<double>(a.c) - s.r;
+        a.out_top[r * a.top_n + lane] = have ? key_idx(key) : -1;
+        a.out_top_lp[r * a.top_n + lane] = have ? log_prob(x - lS) : ok ? -INFINITY : nan;
+    }
+}
+
+template <int DT, int NV, bool TOP>
+__global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) {
+    using E = Elem<DT>;
+    constexpr int PV = E::kPerVec;
+    __shared__ Smem sm;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
+    const long r = blockIdx.x / a.slices;
+    const int slice = blockIdx.x % a.slices;
+    const char* row = static_cast<const char*>(a.logits) + r * a.stride * E::kBytes;
+    int tok;
+    bool bad;
+    if (!row_used(a.tokens + r * a.M, a.M, a.V, tok, bad)) {
+        if (slice == 0 && wave == 0) {
+            if (lane < a.M) a.out_lp[r * a.M + lane] = 0.f;
+            if (lane == 0 && a.out_entropy) a.out_entropy[r] = 0.f;
+            if (lane < kLpStats && a.out_stats) a.out_stats[kLpStats * r + lane] = 0.f;
+            if (lane < a.top_n) {
+                a.out_top[r * a.top_n + lane] = -1;
+                a.out_top_lp[r * a.top_n + lane] = -INFINITY;
+            }
+        }
+        return;
+    }
+
+    // the slice: vectors first .. of the row, and the row's last few elements with its last slice
+    const int vecs = a.V / PV, first = slice * (NV * kLpThreads);
+    u32x4 v[NV];
+    const uint32_t none = DT == 1 ? 0xff80ff80u : 0xff800000u;  // -inf
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = first + j * kLpThreads + tid;
+        v[j] = u32x4{none, none, none, none};
+        if (i < vecs) v[j] = load_vec<DT>(row, static_cast<long>(i) * PV);
+    }
+    const int rest = vecs * PV + tid;
+    const bool has_rest = slice == a.slices - 1 && rest < a.V;
+    const float z_rest = has_rest ? E::scalar(row, rest) : -INFINITY;
+    const float z_tok = tok >= 0 && !bad ? E::scalar(row, tok) : 0.f;
+
+    float tm = z_rest;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) tm = __builtin_elementwise_maximum(tm, vec_max<DT>(v[j]));
+    {
+        const float w = wave_maximum(tm);
+        if (lane == 0) sm.red[wave] = w;
+    }
+    float tau = INFINITY;
+    if (TOP) {
+        // the n-th largest of the threads' maxima: at least n elements reach it
+        uint32_t k = wave_sort_desc(order_key(tm));
+        sm.keys[tid] = k;
+        if (tid == 0) sm.count = sm.staged = 0;
+        __syncthreads();
+        uint32_t other[kWaves - 1];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) other[w - 1] = sm.keys[((wave + w) % kWaves) * kWave + (kWave - 1 - lane)];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) k = wave_bitonic_clean(max(k, other[w - 1]), true);
+        tau = fmaxf(order_value(lane_gather(k, a.top_n - 1)), -FLT_MAX);    // -inf is in no list
+    } else {
+        __syncthreads();
+    }
+    float m = sm.red[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = __builtin_elementwise_maximum(m, sm.red[w]);
+
+    // sums, and the vectors that reach the threshold
+    float S = 0.f, W = 0.f;
+    const float mc = m * a.c;
+    const bool wide = is_wide(m, a.c), some = m > -INFINITY && m < INFINITY;
+    const auto add = [&](float x) {
+        const float p = exp2_fast(x);
+        S += p;
+        W = __builtin_fmaf(p, x, W);
+    };
+    if (some) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            asm volatile("" : "+v"(v[j]));              // widened again, not kept: the row's slice fills the registers
+            if (!wide) {
+#pragma unroll
+                for (int e = 0; e < PV; ++e) add(exponent(E::get(v[j], e), a.c, mc));
+            }
+            if (TOP && vec_max<DT>(v[j]) >= tau) {
+                const int at = atomicAdd(&sm.staged, 1);
+                if (at < kStage) {
+                    sm.stage[at] = v[j];
+                    sm.stage_i[at] = (first + j * kLpThreads + tid) * PV;
+                }
+            }
+        }
+        if (wide) {
+#pragma unroll 1
+            for (int i = first + tid; i < min(vecs, first + NV * kLpThreads); i += kLpThreads)
+#pragma unroll 1
+                for (int e = 0; e < PV; ++e) add(exponent_wide(E::scalar(row, static_cast<long>(i) * PV + e), a.c, m));
+        }
+        if (has_rest) {
+            add(wide ? exponent_wide(z_rest, a.c, m) : exponent(z_rest, a.c, mc));
+            if (TOP && z_rest >= tau) {
+                const int at = atomicAdd(&sm.count, 1); // at most PV - 1 of them
+                sm.cand[at] = pair_key(z_rest, rest);
+            }
+        }
+    }
+    S = wave_sum(S);
+    W = wave_sum(W);
+    __syncthreads();
+    if (lane == 0) sm.red[wave] = S, sm.red2[wave] = W;
+    if (TOP) {
+        for (int i = tid; i < min(sm.staged, kStage); i += kLpThreads) {
+            const u32x4 w = sm.stage[i];
+#pragma unroll
+            for (int e = 0; e < PV; ++e) {
+                const float z = E::get(w, e);
+                if (z >= tau) {
+                    const int at = atomicAdd(&sm.count, 1);
+                    if (at < kCand) sm.cand[at] = pair_key(z, sm.stage_i[i] + e);
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    pkey_t key = empty_key();
+    if (TOP && some) {
+        const int count = sm.count;
+        if (sm.staged <= kStage && count <= kCand) {
+            if (wave == 0) {
+                for (int base = 0; base < count; base += kWave) {
+                    pkey_t k = base + lane < count ? sm.cand[base + lane] : empty_key();
+                    wave_sort_keys(k);
+                    if (base == 0) key = k;
+                    else wave_merge_keys(key, k);
+                }
+            }
+        } else {
+            // many equal elements: the best one below the last found, n times
+            const int end = slice == a.slices - 1 ? a.V : (first + NV * kLpThreads) * PV;
+            pkey_t last = ~0ull;
+            for (int n = 0; n < a.top_n; ++n) {
+                pkey_t best = 0;
+#pragma unroll 1
+                for (int i = first * PV + tid; i < end; i += kLpThreads) {
+                    const pkey_t k = pair_key(E::scalar(row, i), i);
+                    if (k < last && k > best) best = k;
+                }
+#pragma unroll
+                for (int o = 32; o > 0; o >>= 1) {
+                    const pkey_t other = xshfl(best, o);
+                    best = other > best ? other : best;
+                }
+                __syncthreads();
+                if (lane == 0) sm.best[wave] = best;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) best = sm.best[w] > best ? sm.best[w] : best;
+                if (best == 0 || key_val(best) == -INFINITY) break;
+                if (lane == n) key = best;
+                last = best;
+            }
+        }
+    }
+    if (wave != 0) return;
+    S = W = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) S += sm.red[w], W += sm.red2[w];
+    // a NaN or +inf is seen in the maximum; a slice of -inf alone has no sum
+    const bool odd = !(m < INFINITY);
+    Sums s;
+    s.S = odd ? __builtin_nan("") : static_cast<double>(S);
+    s.W = W;
+    s.r = reference(m, a.c);
+    if (a.slices == 1) {
+        finish_row(a, r, s, m, key, tok, z_tok, bad);
+        return;
+    }
+
+    // leave the slice's record; the last workgroup of the row joins them
+    const int per = kLpHead + a.top_n;
+    unsigned long long* rec = a.words + (r * a.slices + slice) * per;
+    if (lane == 0) {
+        st_agent64(rec, (static_cast<unsigned long long>(__float_as_uint(odd ? __builtin_nanf("") : m)) << 32));
+        st_agent64(rec + 1, (static_cast<unsigned long long>(__float_as_uint(S)) << 32) | __float_as_uint(W));
+    }
+    if (TOP && lane < a.top_n) st_agent64(rec + kLpHead + lane, key);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    unsigned ticket = 0;
+    if (lane == 0) ticket = __hip_atomic_fetch_add(a.done + r, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    ticket = __builtin_amdgcn_readfirstlane(ticket);
+    if (ticket != static_cast<unsigned>(a.slices) - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    if (lane == 0) __hip_atomic_store(a.done + r, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // lane l has slice l (at most 64 of them)
+    unsigned long long* base = a.words + r * a.slices * per;
+    float ms = -INFINITY, Ss = 0.f, Ws = 0.f;
+    if (lane < a.slices) {
+        const unsigned long long w0 = ld_agent64(base + lane * per), w1 = ld_agent64(base + lane * per + 1);
+        ms = __uint_as_float(static_cast<uint32_t>(w0 >> 32));
+        Ss = __uint_as_float(static_cast<uint32_t>(w1 >> 32));
+        Ws = __uint_as_float(static_cast<uint32_t>(w1));
+    }
+    if (TOP) {
+        for (int b = 0; b < a.slices; b += 4) {
+            pkey_t k[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                k[e] = b + e < a.slices && lane < a.top_n ? ld_agent64(base + (b + e) * per + kLpHead + lane) : empty_key();
+            wave_merge_keys(k[0], k[1]);
+            if (b + 2 < a.slices) {
+                wave_merge_keys(k[2], k[3]);
+                wave_merge_keys(k[0], k[2]);
+            }
+            if (b == 0) key = k[0];
+            else wave_merge_keys(key, k[0]);
+        }
+    }
+    for (int i = lane; i < a.slices * per; i += kWave) st_agent64(base + i, 0ull);      // left zero for the next call
+    const float mr = wave_maximum(ms);
+    const double rs = reference(ms, a.c);
+    s.r = reference(mr, a.c);
+    const double d = ms > -INFINITY ? rs - s.r : 0.0;
+    const double w = ms > -INFINITY ? exp2(d) : 0.0;
+    s.S = wave_sum(static_cast<double>(Ss) * w);
+    s.W = wave_sum(w > 0.0 ? w * (static_cast<double>(Ws) + static_cast<double>(Ss) * d) : 0.0);
+    if (!(mr < INFINITY)) s.S = __builtin_nan("");
+    finish_row(a, r, s, mr, key, tok, z_tok, bad);
+}
+
+// Gradient: dz_i = p_i (A + B x'_i) + (1/T) sum_m g_m [i = t_m], x' = log2 p_i, A = -(G + h H)/T, B = -h ln2 / T,
+// G = sum g_m.  One pass; the elements of given tokens are written once more, after the row's own pass.
+constexpr int kGradVecs = 4;
+
+template <int DT, bool ENT>
+__global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradArgs a) {
+    using E = Elem<DT>;
+    constexpr int PV = E::kPerVec;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const long r = blockIdx.x / a.slices;
+    const int slice = blockIdx.x % a.slices;
+    const char* row = static_cast<const char*>(a.logits) + r * a.stride * E::kBytes;
+    char* out = static_cast<char*>(a.grad) + r * a.grad_stride * E::kBytes;
+    const int vecs = a.V / PV, first = slice * (kGradVecs * kLpThreads);
+    int tok;
+    bool bad;
+    const bool used = row_used(a.tokens + r * a.M, a.M, a.V, tok, bad);
+    const int rest = vecs * PV + tid;
+    const bool has_rest = slice == a.slices - 1 && rest < a.V;
+    const auto put = [&](long i, float g) {
+        if (DT == 1) reinterpret_cast<__bf16*>(out)[i] = static_cast<__bf16>(g);
+        else reinterpret_cast<float*>(out)[i] = g;
+    };
+    if (!used) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j) {
+            const int i = first + j * kLpThreads + tid;
+            if (i < vecs) store_vec<DT>(out, static_cast<long>(i) * PV, zero);
+        }
+        if (has_rest) put(rest, 0.f);
+        return;
+    }
+    u32x4 v[kGradVecs];
+#pragma unroll
+    for (int j = 0; j < kGradVecs; ++j) {
+        const int i = first + j * kLpThreads + tid;
+        if (i < vecs) v[j] = load_vec<DT>(row, static_cast<long>(i) * PV);
+    }
+    const float z_rest = has_rest ? E::scalar(row, rest) : 0.f;
+    // the given tokens of this slice (lane m has token m, in every wave)
+    const bool last = slice == a.slices - 1;
+    const bool mine = !bad && tok >= first * PV && (last || tok < (first + kGradVecs * kLpThreads) * PV);
+    const float z_tok = mine ? E::scalar(row, tok) : 0.f;
+    const float g = a.g_lp && tok >= 0 && lane < a.M ? a.g_lp[r * a.M + lane] : 0.f;
+    const float m = a.stats[kLpStats * r], l = bad ? __builtin_nanf("") : a.stats[kLpStats * r + 1];
+    const float h = ENT ? a.g_entropy[r] : 0.f, H = ENT ? a.stats[kLpStats * r + 2] : 0.f;
+    const float G = wave_sum(g);
+    const float A = -a.invT * __builtin_fmaf(h, H, G), B = -a.invT * h * static_cast<float>(kLn2);
+    float same = 0.f;                                   // gradients of all mentions of this lane's token
+    for (int j = 0; j < a.M; ++j) same += bcast(tok, j) == tok ? bcast(g, j) : 0.f;
+    const bool wide = is_wide(m, a.c);
+    const float mc = m * a.c;
+    const auto at = [&](float z) {
+        const float x = (wide ? exponent_wide(z, a.c, m) : exponent(z, a.c, mc)) - l;
+        const float p = exp2_fast(x);
+        return ENT ? p * __builtin_fmaf(B, x, A) : p * A;
+    };
+    __syncthreads();                                    // the gradient may take the logits' place: z_tok is read
+#pragma unroll
+    for (int j = 0; j < kGradVecs; ++j) {
+        const int i = first + j * kLpThreads + tid;
+        if (i >= vecs) continue;
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (DT == 1) {
+                typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                const bf16x2 pr = {static_cast<__bf16>(at(bf16_lo(v[j][e]))), static_cast<__bf16>(at(bf16_hi(v[j][e])))};
+                o[e] = __builtin_bit_cast(uint32_t, pr);
+            } else {
+                o[e] = __float_as_uint(at(__uint_as_float(v[j][e])));
+            }
+        }
+        store_vec<DT>(out, static_cast<long>(i) * PV, o);
+    }
+    if (has_rest) put(rest, at(z_rest));
+    if (__ballot(mine) == 0ull) return;                 // the same in every wave
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");  // those stores are done before the tokens' own follow
+    __syncthreads();
+    if (tid < kWave && mine) put(tok, __builtin_fmaf(a.invT, same, at(z_tok)));
+}
+
+template <int DT, int NV> void logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(a.R) * a.slices));
+    if (a.top_n > 0) launch_timed(t, logprobs_kernel<DT, NV, true>, grid, dim3(kLpThreads), 0, s, a);
+    else launch_timed(t, logprobs_kernel<DT, NV, false>, grid, dim3(kLpThreads), 0, s, a);
+}
+template <int DT> void logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
+    if (a.vecs == 1) logprobs<DT, 1>(a, s, t);
+    else if (a.vecs == 4) logprobs<DT, 4>(a, s, t);
+    else logprobs<DT, 16>(a, s, t);
+}
+
+int slices_of(int V, int dtype, int vecs) {
+    const int elems = vecs * kLpThreads * (dtype == 1 ? 8 : 4);
+    const int n = (V + elems - 1) / elems;
+    return n < 1 ? 1 : n;
+}
+
+}  // namespace
+
+// A slice is as large as registers allow where the rows fill the GPU, and smaller where they are few, so that their loads
+// spread over the compute units.
+void logprob_plan(LogprobArgs& a) {
+    a.vecs = kLpMaxVecs;
+    const int small[] = {1, 4};
+    for (int v : small) {
+        const int n = slices_of(a.V, a.dtype, v);
+        if (n <= kWave && static_cast<long>(a.R) * n <= 512) {
+            a.vecs = v;
+            break;
+        }
+    }
+    a.slices = slices_of(a.V, a.dtype, a.vecs);
+}
+
+hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
+    if (a.dtype == 1) logprobs<1>(a, s, t);
+    else logprobs<0>(a, s, t);
+    return hipGetLastError();
+}
+
+int logprob_grad_slices(int dtype, int V) { return slices_of(V, dtype, kGradVecs); }
+
+hipError_t launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s, Timing t) {
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(a.R) * a.slices));
+    if (a.dtype == 1) {
+        if (a.g_entropy) launch_timed(t, logprobs_grad_kernel<1, true>, grid, dim3(kLpThreads), 0, s, a);
+        else launch_timed(t, logprobs_grad_kernel<1, false>, grid, dim3(kLpThreads), 0, s, a);
+    } else {
+        if (a.g_entropy) launch_timed(t, logprobs_grad_kernel<0, true>, grid, dim3(kLpThreads), 0, s, a);
+        else launch_timed(t, logprobs_grad_kernel<0, false>, grid, dim3(kLpThreads), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace sv

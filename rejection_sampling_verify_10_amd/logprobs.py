@@ -1,0 +1,124 @@
+"""Log probabilities of given tokens, with the rows' entropy and likeliest tokens, and their gradient.
+
+The binding of ``spec_token_logprobs`` and ``spec_token_logprobs_grad`` (``include/spec_verify.h`` states what every
+argument means).  After a verification:
+
+    tokens, accept_len = verify_chain(logits, ...)                       # [B, K+1], -1 behind the emitted ones
+    r = token_logprobs(logits, tokens, temperature, top_n=5)             # rows behind the emitted tokens are not read
+
+Training a draft model on M tokens a position (ids [.., M]) and their gradients g = d loss / d log probability:
+
+    r = token_logprobs(logits, ids)
+    dlogits = token_logprobs_grad(logits, ids, r.stats, g)
+"""
+
+from __future__ import annotations
+
+from typing import NamedTuple, Optional, Tuple
+
+import torch
+
+from . import SPEC_TOPK_MAX, lib
+from .kvq import _CODES, _call, _scratch, _tensor
+
+
+class TokenLogprobs(NamedTuple):
+    logprobs: torch.Tensor                      # of the tokens' shape, float32
+    entropy: torch.Tensor                       # [..], one a row, float32
+    stats: torch.Tensor                         # [.., 3] float32, for token_logprobs_grad
+    top_tokens: Optional[torch.Tensor]          # [.., top_n] int32, None without
+    top_logprobs: Optional[torch.Tensor]        # [.., top_n] float32
+
+
+def _logit_rows(t: torch.Tensor, name: str) -> Tuple[int, int, Tuple[int, ...]]:
+    """(rows, elements between rows, leading shape) of logits [.., V] whose leading dimensions lie evenly in memory."""
+    if t.dtype not in _CODES:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be [.., V]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    rows, step = 1, t.shape[-1]
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if rows == 1:
+            step = stride
+        elif stride != rows * step:
+            raise ValueError(f"the rows of {name} must lie at one distance from each other")
+        rows *= size
+    if rows > 1 and step < t.shape[-1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    if 0 in t.shape:
+        raise ValueError(f"{name} must have at least one row")
+    return rows, step, tuple(t.shape[:-1])
+
+
+def _tokens(tokens: torch.Tensor, lead: Tuple[int, ...], device) -> Tuple[int, int]:
+    """(address, tokens a row): of the leading shape (one a row), or with a dimension of M more."""
+    one = tokens.dim() == len(lead)
+    M = 1 if one else tokens.shape[-1] if tokens.dim() else 0
+    if not one and not 1 <= M <= SPEC_TOPK_MAX:
+        raise ValueError(f"tokens must have between 1 and {SPEC_TOPK_MAX} a row")
+    return _tensor(tokens, "tokens", torch.int32, torch.Size(lead if one else lead + (M,)), device), M
+
+
+def token_logprobs_workspace_bytes(rows: int, V: int, top_n: int = 0, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of :func:`token_logprobs`'s workspace (:func:`new_workspace` makes one)."""
+    return int(lib().spec_token_logprobs_workspace_bytes(rows, V, top_n, _CODES[dtype]))
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], temperature: float = 1.0, top_n: int = 0, *,
+                   workspace: Optional[torch.Tensor] = None) -> TokenLogprobs:
+    """Log probabilities of ``tokens`` under softmax(logits / temperature) (``spec_token_logprobs``).
+
+    logits [.., V] bf16 or f32 (rows at any one distance from each other); tokens int32 of the leading shape, or with
+    M <= 64 a row in a last dimension, or None (every row's entropy and tops alone; logprobs is then empty).  Negative
+    tokens are none, and rows without a token are not read: their log probabilities and entropy are 0, their tops -1
+    and -inf.  ``workspace`` (:func:`new_workspace`; zero-filled once, calls leave it zero) avoids one a call.
+    """
+    rows, step, lead = _logit_rows(logits, "logits")
+    V, dev, top_n = logits.shape[-1], logits.device, int(top_n)
+    if not 0 <= top_n <= SPEC_TOPK_MAX:
+        raise ValueError(f"top_n must lie in [0, {SPEC_TOPK_MAX}]")
+    tp, M = (None, 0) if tokens is None else _tokens(tokens, lead, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    lp = torch.empty(lead + (0,) if tokens is None else tokens.shape, **f32)
+    entropy, stats = torch.empty(lead, **f32), torch.empty(lead + (3,), **f32)
+    top = torch.empty(lead + (top_n,), dtype=torch.int32, device=dev) if top_n else None
+    top_lp = torch.empty(lead + (top_n,), **f32) if top_n else None
+    need = token_logprobs_workspace_bytes(rows, V, top_n, logits.dtype)
+    if need and workspace is None:
+        workspace = torch.zeros(need + 256, dtype=torch.uint8, device=dev)
+    wp, _ws = _scratch(need, dev, workspace)
+    _call(lib().spec_token_logprobs, "spec_token_logprobs", dev, logits.data_ptr(), _CODES[logits.dtype], step, rows, V,
+          tp, M, float(temperature), top_n, lp.data_ptr() if M else None, entropy.data_ptr(), stats.data_ptr(),
+          top.data_ptr() if top_n else None, top_lp.data_ptr() if top_n else None, wp, need)
+    return TokenLogprobs(lp, entropy, stats, top, top_lp)
+
+
+def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.Tensor, grad_logprobs: torch.Tensor,
+                        grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0, *,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient for the logits (``spec_token_logprobs_grad``), of their shape and type.
+
+    logits, tokens, temperature: as :func:`token_logprobs` had them, stats: as it gave them; grad_logprobs of the
+    tokens' shape and grad_entropy of the leading one, float32.  ``out``: a tensor to write to, of any row distance;
+    the logits themselves may be given, anything else must not overlap them.
+    """
+    rows, step, lead = _logit_rows(logits, "logits")
+    dev = logits.device
+    tp, M = _tokens(tokens, lead, dev)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
+        raise ValueError("out must have the logits' shape, type and device")
+    out_step = _logit_rows(out, "out")[1]
+    _call(lib().spec_token_logprobs_grad, "spec_token_logprobs_grad", dev, logits.data_ptr(), _CODES[logits.dtype], step,
+          rows, logits.shape[-1], tp, M, _tensor(stats, "stats", torch.float32, torch.Size(lead + (3,)), dev),
+          _tensor(grad_logprobs, "grad_logprobs", torch.float32, tokens.shape, dev),
+          None if grad_entropy is None else _tensor(grad_entropy, "grad_entropy", torch.float32, torch.Size(lead), dev),
+          float(temperature), out.data_ptr(), out_step)
+    return out

@@ -1,0 +1,248 @@
+"""Token log probabilities and their gradient on the GPU against float64 (logprob_ref)."""
+
+import numpy as np
+import pytest
+
+import logprob_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def R():
+    import torch
+    import rejection_sampling_verify_10_amd as R
+    assert torch.cuda.is_available(), "GPU test without a GPU"
+    R.lib()
+    return R
+
+
+def dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def logits(rng, rows, V, dtype, pad=0, size=3.0):
+    """Rows of a wider tensor (pad elements between them) and their values."""
+    import torch
+    z = size * rng.standard_normal((rows, V + pad)) - 1.1 * np.log(1 + rng.permutation(V + pad))
+    t = dev(z.astype(np.float32))
+    t = (t.bfloat16() if dtype == "bf16" else t)[:, :V]
+    return t, t.float().cpu().numpy()
+
+
+def check(r, want, top_n):
+    lp, h = r.logprobs.cpu().numpy().reshape(len(want), -1), r.entropy.cpu().numpy().ravel()
+    for i, w in enumerate(want):
+        np.testing.assert_array_equal(np.isfinite(lp[i]), np.isfinite(w["lp"]), err_msg=f"row {i}")
+        np.testing.assert_array_equal(np.isnan(lp[i]), np.isnan(w["lp"]))
+        ok = np.isfinite(w["lp"])
+        assert (np.abs(lp[i][ok] - w["lp"][ok]) <= w["lp_tol"][ok]).all(), (i, lp[i], w["lp"], w["lp_tol"])
+        assert np.isnan(h[i]) == np.isnan(w["h"])
+        if not np.isnan(w["h"]):
+            assert abs(h[i] - w["h"]) <= w["h_tol"], (i, h[i], w["h"], w["h_tol"])
+        if top_n:
+            ids, tl = r.top_tokens.cpu().numpy().reshape(-1, top_n)[i], r.top_logprobs.cpu().numpy().reshape(-1, top_n)[i]
+            np.testing.assert_array_equal(ids, w["top"], err_msg=f"row {i}")
+            ok = np.isfinite(w["top_lp"])
+            np.testing.assert_array_equal(np.isfinite(tl), ok)
+            np.testing.assert_array_equal(np.isnan(tl), np.isnan(w["top_lp"]))
+            assert (np.abs(tl[ok] - w["top_lp"][ok]) <= w["top_tol"][ok]).all()
+
+
+def check_grad(got, want, tol):
+    got = got.float().cpu().numpy().reshape(want.shape)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    ok = ~np.isnan(want)
+    off = np.abs(got - want)[ok] - tol[ok]
+    assert (off <= 0).all(), off.max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V,M,top,T,pad", [
+    (1, 1, 1, 1, 1.0, 0), (3, 2, 2, 64, 0.7, 0), (2, 7, 1, 5, 1.0, 0), (4, 9, 3, 64, 1.3, 3), (5, 255, 64, 20, 1.0, 0),
+    (3, 4097, 1, 5, 0.7, 7), (700, 1001, 2, 3, 1.0, 0), (2, 32000, 8, 20, 1.0, 0), (9, 50257, 1, 1, 0.25, 0),
+    (1, 128256, 1, 5, 1.0, 0), (520, 20011, 1, 64, 1.0, 5), (200, 128256, 1, 20, 0.7, 0), (1, 262147, 1, 0, 1.0, 0),
+])
+def test_forward_and_gradient(R, dtype, rows, V, M, top, T, pad):
+    rng = np.random.default_rng([rows, V, M, top])
+    z, zv = logits(rng, rows, V, dtype, pad)
+    tokens = rng.integers(0, V, (rows, M)).astype(np.int32)
+    tokens[rng.random((rows, M)) < 0.2] = -1                   # some tokens missing, some rows without any
+    if rows > 2:
+        tokens[1] = -1
+    r = R.token_logprobs(z, dev(tokens), T, top)
+    few = np.arange(rows) if rows * V < 3e6 else rng.choice(rows, 24, replace=False)
+    want = ref.forward(zv[few], tokens[few], T, top)
+    pick = lambda t: None if t is None else t[dev(few.astype(np.int64))]     # noqa: E731
+    check(R.TokenLogprobs(*map(pick, r)), want, top)
+    g = rng.standard_normal((rows, M)).astype(np.float32)
+    gh = rng.standard_normal(rows).astype(np.float32)
+    for entropy in (None, gh):
+        got = R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), None if entropy is None else dev(entropy), T)
+        assert got.dtype == z.dtype and got.shape == z.shape
+        check_grad(pick(got), *ref.backward(zv[few], tokens[few], g[few], None if entropy is None else entropy[few], T, dtype))
+
+
+def odd_rows(V, dtype):
+    """Rows that an implementation may stumble over."""
+    import torch
+    rng = np.random.default_rng(5)
+    low = torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min
+    base = rng.standard_normal((11, V)).astype(np.float32)
+    base[0, 1:] = -np.inf                                     # one token left
+    base[1, : V // 2] = -np.inf                               # half masked
+    base[2, V // 2:] = low                                    # masked by the type's lowest value
+    base[3] = low                                             # nothing but it
+    base[4] = -np.inf                                         # nothing at all: NaN
+    base[5, V - 1] = np.nan
+    base[6, 3] = np.inf
+    base[7] = 0.5                                             # ties everywhere
+    base[8, ::3] = 7.0                                        # many ties at the top
+    base[9] = 1e-30 * base[9]
+    base[10] = 3e4 * base[10]
+    z = dev(base)
+    z = z.bfloat16() if dtype == "bf16" else z
+    return z, z.float().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [64, 1003, 70001])
+@pytest.mark.parametrize("T", [1.0, 0.01])
+def test_odd_rows(R, dtype, V, T):
+    z, zv = odd_rows(V, dtype)
+    n = z.shape[0]
+    tokens = np.stack([np.zeros(n), np.full(n, V - 1), np.full(n, 1)], 1).astype(np.int32)
+    r = R.token_logprobs(z, dev(tokens), T, 20)
+    want = ref.forward(zv, tokens, T, 20)
+    # differences of the lowest value from a number next to it pass float32's range
+    for w in want:
+        for k in ("lp", "top_lp"):
+            with np.errstate(over="ignore"):
+                w[k] = np.where(np.isfinite(w[k]), w[k].astype(np.float32), w[k]).astype(np.float64)
+    check(r, want, 20)
+    g, gh = np.ones((n, 3), np.float32), np.full(n, 0.5, np.float32)
+    check_grad(R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), dev(gh), T),
+               *ref.backward(zv, tokens, g, gh, T, dtype))
+
+
+def test_tokens_out_of_range_and_none(R):
+    rng = np.random.default_rng(1)
+    z, zv = logits(rng, 4, 1000, "f32")
+    tokens = np.array([[5, 1000], [-1, -7], [-1, 999], [2 ** 31 - 1, 3]], np.int32)
+    r = R.token_logprobs(z, dev(tokens), 1.0, 2)
+    check(r, ref.forward(zv, tokens, 1.0, 2), 2)
+    g = rng.standard_normal((4, 2)).astype(np.float32)
+    check_grad(R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g)), *ref.backward(zv, tokens, g, None, 1.0, "f32"))
+    # no tokens: every row is read
+    r = R.token_logprobs(z, None, 1.0, 3)
+    assert r.logprobs.numel() == 0
+    check(r, ref.forward(zv, np.zeros((4, 0), np.int32), 1.0, 3), 3)
+
+
+def test_rows_without_tokens_are_not_read(R):
+    import torch
+    z = torch.full((2, 5000), float("nan"), device="cuda")
+    z[0] = 1.0
+    tokens = dev(np.array([3, -1], np.int32))
+    r = R.token_logprobs(z, tokens, 1.0, 2)
+    assert abs(r.logprobs[0].item() + np.log(5000)) < 1e-5 and r.logprobs[1].item() == 0 and r.entropy[1].item() == 0
+    assert r.top_tokens.tolist() == [[0, 1], [-1, -1]]
+    g = R.token_logprobs_grad(z, tokens, r.stats, torch.ones(2, device="cuda"))
+    assert (g[1] == 0).all() and not torch.isnan(g).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_same_token_twice_and_in_place(R, dtype):
+    rng = np.random.default_rng(2)
+    z, zv = logits(rng, 6, 9001, dtype, pad=3)
+    tokens = rng.integers(0, 9001, (6, 4)).astype(np.int32)
+    tokens[:, 2] = tokens[:, 0]
+    tokens[3] = 9000
+    g, gh = rng.standard_normal((6, 4)).astype(np.float32), rng.standard_normal(6).astype(np.float32)
+    r = R.token_logprobs(z, dev(tokens))
+    want, tol = ref.backward(zv, tokens, g, gh, 1.0, dtype)
+    first = R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), dev(gh))
+    check_grad(first, want, tol)
+    got = R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), dev(gh), out=z)
+    assert got is z and (got == first).all()
+
+
+def test_gradient_against_differences(R):
+    """Central differences of the float64 forward along random directions: their error is the third derivative's, eps^2."""
+    rng = np.random.default_rng(3)
+    z, zv = logits(rng, 3, 301, "f32")
+    tokens = rng.integers(0, 301, (3, 2)).astype(np.int32)
+    g, gh = rng.standard_normal((3, 2)).astype(np.float32), rng.standard_normal(3).astype(np.float32)
+    T = 0.8
+    r = R.token_logprobs(z, dev(tokens), T)
+    grad = R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), dev(gh), T).double().cpu().numpy()
+
+    def loss(a):
+        w = ref.forward(a, tokens, T, 0)
+        return sum((g[i] * w[i]["lp"]).sum() + gh[i] * w[i]["h"] for i in range(3))
+
+    for _ in range(5):
+        d = rng.standard_normal(zv.shape)
+        eps = 1e-5
+        slope = (loss(zv + eps * d) - loss(zv - eps * d)) / (2 * eps)
+        assert abs((grad * d).sum() - slope) < 1e-4 * (1 + np.abs(grad * d).sum())
+
+
+def test_workspace_is_shared_and_left_zero(R):
+    import torch
+    rng = np.random.default_rng(4)
+    sizes = [(1, 128256, 5), (3, 50000, 64), (2, 128256, 0), (40, 128256, 20)]
+    need = max(R.token_logprobs_workspace_bytes(r, V, n, torch.float32) for r, V, n in sizes)
+    ws = R.new_workspace(need, torch.device("cuda", 0))
+    for rows, V, n in sizes + sizes[::-1]:
+        z, zv = logits(rng, rows, V, "f32")
+        tokens = rng.integers(0, V, (rows, 1)).astype(np.int32)
+        few = slice(0, min(rows, 3))
+        r = R.token_logprobs(z, dev(tokens), 1.0, n, workspace=ws)
+        assert not ws.any()
+        check(R.TokenLogprobs(*(None if t is None else t[few] for t in r)), ref.forward(zv[few], tokens[few], 1.0, n), n)
+
+
+def test_captured_and_replayed(R):
+    import torch
+    rng = np.random.default_rng(6)
+    z, _ = logits(rng, 8, 128256, "bf16")
+    tokens = dev(rng.integers(0, 128256, (8, 1)).astype(np.int32))
+    g = torch.ones(8, 1, device="cuda")
+    ws = R.new_workspace(R.token_logprobs_workspace_bytes(8, 128256, 5), z.device)
+    run = lambda: (lambda r: (*r, R.token_logprobs_grad(z, tokens, r.stats, g)))(R.token_logprobs(z, tokens, 1.0, 5, workspace=ws))  # noqa: E731
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for k in range(3):
+        z.copy_(logits(rng, 8, 128256, "bf16")[0])
+        eager = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
+
+
+def test_emitted_tokens_of_a_verification(R):
+    """The chain's verification and its answer's log probabilities, as a server asks for them."""
+    import torch
+    rng = np.random.default_rng(7)
+    B, K, V = 5, 4, 32000
+    z, zv = logits(rng, B * (K + 1), V, "bf16")
+    z = z.view(B, K + 1, V)
+    q = torch.softmax(z[:, :K].float() + 0.5 * torch.randn(B, K, V, device="cuda"), -1)
+    x = torch.multinomial(q.view(-1, V), 1).view(B, K).to(torch.int32)
+    tokens, alen = R.verify_chain(z, q, x, torch.rand(B, K + 1, device="cuda"), 1.0, 0)
+    r = R.token_logprobs(z, tokens, 1.0, 3)
+    assert r.logprobs.shape == (B, K + 1) and r.top_tokens.shape == (B, K + 1, 3)
+    flat = tokens.cpu().numpy().reshape(-1, 1)
+    want = ref.forward(zv, flat, 1.0, 3)
+    check(r, want, 3)
+    emitted = (torch.arange(K + 1, device="cuda") <= alen.view(-1, 1))
+    assert torch.equal(emitted, tokens >= 0) and (r.logprobs[emitted] < 0).all() and (r.logprobs[~emitted] == 0).all()
