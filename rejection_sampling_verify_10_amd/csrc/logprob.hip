@@ -5,11 +5,14 @@
 // W = sum 2^x_i x_i:  log p(t) = ln2 * (x_t - log2 S),  H = ln2 * (log2 S - W/S).
 // x is never above 0 but for its rounding, so no exponential overflows.
 //
-// Forward: a workgroup holds a slice of a row in registers (16-byte vectors), so
-// the row is read once although its maximum comes before its sums.  The n-th
-// largest of the threads' maxima is at most the slice's n-th largest element, and
-// few elements reach it: those go to LDS and one wave sorts them.  The workgroups
-// of a row leave (m, S, W, list) in the workspace, and the last of them joins.
+// Forward: a workgroup holds a slice of a row in registers (16-byte vectors).  Each
+// wave takes its vectors as they arrive, against a running reference that moves
+// only where an element passes it by 2^40, so that exponentials overlap the loads.
+// Of the likeliest: each wave's q-th largest thread maximum, q = ceil(n / 4), bounds
+// the slice's n-th largest element from below, and few elements reach the least of
+// the four; the vectors that hold them are found in the registers once more, go to
+// LDS, and one wave sorts them.  The workgroups of a row leave (m, S, W, list) in
+// the workspace, and the last of them joins.
 
 #include <float.h>
 
@@ -43,7 +46,16 @@ template <int DT> __device__ __forceinline__ float vec_max(const u32x4& v) {
     const float a = maximum3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
     return __builtin_elementwise_maximum(a, __uint_as_float(v[3]));
 }
+// This wave's stores have been acknowledged.  Words stored at agent scope are then past the XCD's L2, so that a ticket taken
+// after it promises them to a reader at agent scope; a fence would write back all that the L2 holds (the gradient of 2048 rows
+// took ten times as long with one).
+__device__ __forceinline__ void stores_done() {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#endif
+}
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+constexpr float kSlack = 40.f;                          // 2^40 * 2^20 elements * 40 is far from float32's end
 constexpr float kLowest = -1e30f;                       // 0 * kLowest is 0, 0 * -inf is not a number
 constexpr double kLn2 = 0.69314718055994530942;
 
@@ -59,8 +71,8 @@ __device__ __forceinline__ double reference(float m, float c) {
 }
 
 struct Smem {
-    float red[kWaves], red2[kWaves];
-    uint32_t keys[kLpThreads];
+    float red[kWaves], sums[kWaves][3];
+    uint32_t keys[kWaves], alone[kWaves];
     u32x4 stage[kStage];
     int32_t stage_i[kStage];
     pkey_t cand[kCand];
@@ -158,51 +170,67 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     const float z_rest = has_rest ? E::scalar(row, rest) : -INFINITY;
     const float z_tok = tok >= 0 && !bad ? E::scalar(row, tok) : 0.f;
 
-    float tm = z_rest;
+    // sums relative to `ref`, the same in a wave's lanes
+    float tm = -INFINITY, ref = -FLT_MAX, S = 0.f, W = 0.f;
+    const auto add = [&](float x) {
+        const float p = exp2_fast(x);
+        S += p;
+        W = __builtin_fmaf(p, x, W);
+    };
+    constexpr int kGroup = 4;                           // vectors between two looks at the reference
+    const auto look = [&](float mx) {
+        tm = __builtin_elementwise_maximum(tm, mx);
+        if (__ballot(mx * a.c > ref + kSlack) != 0ull) {
+            const float to = fmaxf(ref, wave_max(mx) * a.c), d = ref - to, w = exp2_fast(d);
+            W = w > 0.f ? w * __builtin_fmaf(S, d, W) : 0.f;
+            S *= w;
+            ref = to;
+        }
+    };
 #pragma unroll
-    for (int j = 0; j < NV; ++j) tm = __builtin_elementwise_maximum(tm, vec_max<DT>(v[j]));
+    for (int j = 0; j < NV; j += kGroup) {
+        float mx = vec_max<DT>(v[j]);
+#pragma unroll
+        for (int e = 1; e < kGroup; ++e) mx = __builtin_elementwise_maximum(mx, vec_max<DT>(v[j + e]));
+        look(mx);
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {
+#pragma unroll
+            for (int i = 0; i < PV; ++i) add(exponent(E::get(v[j + e], i), a.c, ref));
+        }
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) asm volatile("" : "+v"(v[j + e]));     // widened again later, not kept
+    }
+    if (slice == a.slices - 1) {
+        look(z_rest);
+        if (has_rest) add(exponent(z_rest, a.c, ref));
+    }
     {
         const float w = wave_maximum(tm);
         if (lane == 0) sm.red[wave] = w;
     }
     float tau = INFINITY;
     if (TOP) {
-        // the n-th largest of the threads' maxima: at least n elements reach it
-        uint32_t k = wave_sort_desc(order_key(tm));
-        sm.keys[tid] = k;
+        const uint32_t k = wave_sort_desc(order_key(tm));
+        if (lane == (a.top_n + kWaves - 1) / kWaves - 1) sm.keys[wave] = k;
+        if (lane == a.top_n - 1) sm.alone[wave] = k;
         if (tid == 0) sm.count = sm.staged = 0;
-        __syncthreads();
-        uint32_t other[kWaves - 1];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) other[w - 1] = sm.keys[((wave + w) % kWaves) * kWave + (kWave - 1 - lane)];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) k = wave_bitonic_clean(max(k, other[w - 1]), true);
-        tau = fmaxf(order_value(lane_gather(k, a.top_n - 1)), -FLT_MAX);    // -inf is in no list
-    } else {
-        __syncthreads();
     }
+    __syncthreads();
     float m = sm.red[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = __builtin_elementwise_maximum(m, sm.red[w]);
-
-    // sums, and the vectors that reach the threshold
-    float S = 0.f, W = 0.f;
-    const float mc = m * a.c;
     const bool wide = is_wide(m, a.c), some = m > -INFINITY && m < INFINITY;
-    const auto add = [&](float x) {
-        const float p = exp2_fast(x);
-        S += p;
-        W = __builtin_fmaf(p, x, W);
-    };
-    if (some) {
+    if (TOP && some) {
+        uint32_t k = sm.keys[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) k = min(k, sm.keys[w]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) k = max(k, sm.alone[w]);       // a short slice leaves waves without elements
+        tau = fmaxf(order_value(k), -FLT_MAX);          // -inf is in no list (nor its order_value's NaN)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            asm volatile("" : "+v"(v[j]));              // widened again, not kept: the row's slice fills the registers
-            if (!wide) {
-#pragma unroll
-                for (int e = 0; e < PV; ++e) add(exponent(E::get(v[j], e), a.c, mc));
-            }
-            if (TOP && vec_max<DT>(v[j]) >= tau) {
+            if (vec_max<DT>(v[j]) >= tau) {
                 const int at = atomicAdd(&sm.staged, 1);
                 if (at < kStage) {
                     sm.stage[at] = v[j];
@@ -210,24 +238,24 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
                 }
             }
         }
-        if (wide) {
-#pragma unroll 1
-            for (int i = first + tid; i < min(vecs, first + NV * kLpThreads); i += kLpThreads)
-#pragma unroll 1
-                for (int e = 0; e < PV; ++e) add(exponent_wide(E::scalar(row, static_cast<long>(i) * PV + e), a.c, m));
+        if (has_rest && z_rest >= tau) {
+            const int at = atomicAdd(&sm.count, 1);     // at most PV - 1 of them
+            sm.cand[at] = pair_key(z_rest, rest);
         }
-        if (has_rest) {
-            add(wide ? exponent_wide(z_rest, a.c, m) : exponent(z_rest, a.c, mc));
-            if (TOP && z_rest >= tau) {
-                const int at = atomicAdd(&sm.count, 1); // at most PV - 1 of them
-                sm.cand[at] = pair_key(z_rest, rest);
-            }
-        }
+    }
+    if (some && wide) {
+        // m*c is no finite number: the sums once more, from the differences
+        S = W = 0.f;
+#pragma unroll 1
+        for (int i = first * PV + tid; i < min(vecs, first + NV * kLpThreads) * PV; i += kLpThreads)
+            add(exponent_wide(E::scalar(row, i), a.c, m));
+        if (has_rest) add(exponent_wide(z_rest, a.c, m));
+        ref = 0.f;
     }
     S = wave_sum(S);
     W = wave_sum(W);
     __syncthreads();
-    if (lane == 0) sm.red[wave] = S, sm.red2[wave] = W;
+    if (lane == 0) sm.sums[wave][0] = S, sm.sums[wave][1] = W, sm.sums[wave][2] = ref;
     if (TOP) {
         for (int i = tid; i < min(sm.staged, kStage); i += kLpThreads) {
             const u32x4 w = sm.stage[i];
@@ -283,11 +311,16 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
         }
     }
     if (wave != 0) return;
+    // the waves' sums, relative to m*c (or to m where that is no finite number)
+    const bool odd = !(m < INFINITY);                   // NaN or +inf; a slice of -inf alone has no sum
+    const float mc = wide ? 0.f : m * a.c;
     S = W = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) S += sm.red[w], W += sm.red2[w];
-    // a NaN or +inf is seen in the maximum; a slice of -inf alone has no sum
-    const bool odd = !(m < INFINITY);
+    if (some) {
+        const float d = lane < kWaves ? sm.sums[lane & 3][2] - mc : -INFINITY, f = exp2_fast(d);
+        const float Sw = sm.sums[lane & 3][0], Ww = sm.sums[lane & 3][1];
+        S = wave_sum(f > 0.f ? Sw * f : 0.f);
+        W = wave_sum(f > 0.f ? f * __builtin_fmaf(Sw, d, Ww) : 0.f);
+    }
     Sums s;
     s.S = odd ? __builtin_nan("") : static_cast<double>(S);
     s.W = W;
@@ -305,12 +338,12 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
         st_agent64(rec + 1, (static_cast<unsigned long long>(__float_as_uint(S)) << 32) | __float_as_uint(W));
     }
     if (TOP && lane < a.top_n) st_agent64(rec + kLpHead + lane, key);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    stores_done();
     unsigned ticket = 0;
     if (lane == 0) ticket = __hip_atomic_fetch_add(a.done + r, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     ticket = __builtin_amdgcn_readfirstlane(ticket);
+    asm volatile("" ::: "memory");
     if (ticket != static_cast<unsigned>(a.slices) - 1) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     if (lane == 0) __hip_atomic_store(a.done + r, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // lane l has slice l (at most 64 of them)
     unsigned long long* base = a.words + r * a.slices * per;
@@ -322,18 +355,23 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
         Ws = __uint_as_float(static_cast<uint32_t>(w1));
     }
     if (TOP) {
-        for (int b = 0; b < a.slices; b += 4) {
+        // all lists as one: 64 keys at a time, four loads under way
+        const int total = a.slices * a.top_n;
+        const auto entry = [&](int i) {
+            const int l = i / a.top_n;
+            return ld_agent64(base + l * per + kLpHead + (i - l * a.top_n));
+        };
+        for (int b = 0; b < total; b += 4 * kWave) {
             pkey_t k[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                k[e] = b + e < a.slices && lane < a.top_n ? ld_agent64(base + (b + e) * per + kLpHead + lane) : empty_key();
-            wave_merge_keys(k[0], k[1]);
-            if (b + 2 < a.slices) {
-                wave_merge_keys(k[2], k[3]);
-                wave_merge_keys(k[0], k[2]);
+            for (int e = 0; e < 4; ++e) k[e] = b + e * kWave + lane < total ? entry(b + e * kWave + lane) : empty_key();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (b + e * kWave >= total) break;
+                wave_sort_keys(k[e]);
+                if (b + e == 0) key = k[0];
+                else wave_merge_keys(key, k[e]);
             }
-            if (b == 0) key = k[0];
-            else wave_merge_keys(key, k[0]);
         }
     }
     for (int i = lane; i < a.slices * per; i += kWave) st_agent64(base + i, 0ull);      // left zero for the next call
@@ -426,7 +464,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradAr
     }
     if (has_rest) put(rest, at(z_rest));
     if (__ballot(mine) == 0ull) return;                 // the same in every wave
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");  // those stores are done before the tokens' own follow
+    stores_done();                                      // the row's own pass is in place before the tokens' elements follow
     __syncthreads();
     if (tid < kWave && mine) put(tok, __builtin_fmaf(a.invT, same, at(z_tok)));
 }
@@ -437,8 +475,7 @@ template <int DT, int NV> void logprobs(const LogprobArgs& a, hipStream_t s, Tim
     else launch_timed(t, logprobs_kernel<DT, NV, false>, grid, dim3(kLpThreads), 0, s, a);
 }
 template <int DT> void logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
-    if (a.vecs == 1) logprobs<DT, 1>(a, s, t);
-    else if (a.vecs == 4) logprobs<DT, 4>(a, s, t);
+    if (a.vecs == 4) logprobs<DT, 4>(a, s, t);
     else logprobs<DT, 16>(a, s, t);
 }
 
@@ -454,14 +491,8 @@ int slices_of(int V, int dtype, int vecs) {
 // spread over the compute units.
 void logprob_plan(LogprobArgs& a) {
     a.vecs = kLpMaxVecs;
-    const int small[] = {1, 4};
-    for (int v : small) {
-        const int n = slices_of(a.V, a.dtype, v);
-        if (n <= kWave && static_cast<long>(a.R) * n <= 512) {
-            a.vecs = v;
-            break;
-        }
-    }
+    const int n = slices_of(a.V, a.dtype, 4);
+    if (n <= kWave && static_cast<long>(a.R) * n <= 512) a.vecs = 4;
     a.slices = slices_of(a.V, a.dtype, a.vecs);
 }
 
