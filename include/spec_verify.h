@@ -671,6 +671,122 @@ int spec_accept_rate(const void* target_logits, spec_dtype_t dtype, const float*
                      float* out_alpha, void* workspace, size_t workspace_bytes, void* hip_stream);
 
 /*
+ * ---- A paged key/value cache, and attention behind shared prefixes ----
+ *
+ * A server's sequences grow by unknown amounts and many begin alike.  These
+ * calls keep K and V in pages of a pool, hand the pages out on the GPU, and let
+ * any number of batch rows attend to one stored prefix:
+ *   spec_page_step (pages and slots for the step's new tokens), spec_paged_append
+ *   (their rows), spec_paged_plan (once a step), spec_paged_attention (every layer),
+ *   LM head, verification; for a tree spec_paged_append again with the accepted
+ *   path, which puts its rows in place.
+ *
+ * A table row t has tables[t][0 .. held[t]-1], the pages of its slots 0 .. in
+ * order: slot s is slot s % page_size of page tables[t][s / page_size], and the
+ * number tables[t][s / page_size] * page_size + s % page_size names it.  Rows of the
+ * batch come first; rows behind them may hold prefixes.
+ */
+
+/*
+ * spec_page_step -- pages for N new tokens a row.  Row t needs
+ * ceil((lengths[t] + counts[t]) / page_size) pages (counts NULL: N), and none
+ * where lengths[t] < 0 (a sequence that has ended).  The free pages are a ring:
+ * entries head .. head + free - 1 of `ring` (mod pages), state = {head, free}.
+ * Rows that need more than they hold take pages from its head, in the order of the
+ * rows, as long as they last; the first row that does not get all its own gets
+ * none, nor does any after it that needs some.  Rows that need fewer put those
+ * they do not need behind its tail (in order, row by row); they are handed out by
+ * later calls.  Entries of `tables` from the need on are left as they were.
+ *   tables       [T][width] int32, rows table_stride elements apart; held [T]; ring
+ *                [pages]; state [2]: read and written
+ *   lengths [T], counts [T] or NULL, int32
+ *   out_held, out_state   where held and state go: the arrays read (in place), or ones
+ *                that overlap nothing
+ *   out_granted  [T] int32: counts[t] (0 for a row that has ended), or -1: not enough pages,
+ *                counts[t] outside [0, N], more than width pages needed, or held[t] outside
+ *                [0, width]; nothing of such a row changes.  It can be the `counts` of the
+ *                calls below, which leave rows of -1 out.
+ *   out_slots    [T][N] int32: the slot of token n (its place is lengths[t] + n), -1 for
+ *                n >= granted[t], and where the page's number is none of the pool's
+ * A state outside [0, pages) and [0, pages] serves no row and is left as it is.
+ * page_size a power of two from 16 to 1024, T and N at most 65536, pages * page_size and
+ * width * page_size at most 2^30.
+ * workspace: 256 bytes, zero-filled before its first use and left zero.
+ */
+#define SPEC_PAGE_STEP_WORKSPACE_BYTES 256
+int spec_page_step(int32_t* tables, int64_t table_stride, int T, int width, int page_size, int pages,
+                   const int32_t* held, const int32_t* state, int32_t* ring, const int32_t* lengths,
+                   const int32_t* counts, int N, int32_t* out_held, int32_t* out_state, int32_t* out_granted,
+                   int32_t* out_slots, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* One layer's pages, bfloat16: row (page, slot of it, head) at k (and v) + page*page_stride +
+ * slot*slot_stride + head*head_stride elements.  Bases and strides multiples of 16 bytes; no two
+ * rows may share memory (the stride of a dimension of one element does not count).  head_dim 64,
+ * 128 or 256; heads at most 65535; slot_stride at most 2^20. */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t pages, page_size, heads, head_dim;
+    int64_t page_stride, slot_stride, head_stride;
+} spec_paged_cache_t;
+
+/*
+ * spec_paged_append -- K and V rows into slots[b][n], b < B, n < N (rows of `slots`
+ * slots_stride elements apart).  Without a path, slot n gets row (b, n).  With one, an
+ * accepted path as verification gives it, slot n gets row (b, path[b][n]) for n <=
+ * accept_len[b] (none where that is negative or not below N).  A slot of -1, or outside
+ * the pool, gets nothing, nor does one whose path entry is outside [0, source_n).
+ *   k, v      rows of (b, n, head), SPEC_F32 (rounded to nearest, ties to even) or SPEC_BF16;
+ *             source_n of them a batch row (without a path at least N)
+ * Two tokens on one slot leave either's row.
+ */
+int spec_paged_append(const spec_paged_cache_t* cache, const spec_kvq_rows_t* k, const spec_kvq_rows_t* v,
+                      spec_dtype_t dtype, int B, int N, int source_n, const int32_t* slots, int64_t slots_stride,
+                      const int32_t* path, int path_stride, const int32_t* accept_len, void* hip_stream);
+
+/*
+ * spec_paged_plan -- how the attention of a step is cut up, from its lengths: made once,
+ * for every layer whose calls have these sizes.
+ *   lengths    [T] int32: committed slots of each table row; the new tokens of batch row
+ *              b < B <= T lie behind them, counts[b] of them (NULL: N)
+ *   prefix_row [B] int32 or NULL: the table row whose committed slots come before
+ *              batch row b's own (negative: none).  Neighbouring rows with the same one share
+ *              the reading of it.
+ *   plan       spec_paged_plan_bytes(...) bytes, 256-byte aligned, any contents; with_prefix:
+ *              whether prefix_row is given
+ * A batch row with lengths[b] < 0, counts[b] outside [0, N], more slots than width * page_size,
+ * or a prefix_row of T or more, or one whose length is outside [0, width * page_size], is an error row.
+ */
+size_t spec_paged_plan_bytes(int B, int N, int q_heads, int heads, int with_prefix);
+int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int page_size, const int32_t* lengths,
+                    const int32_t* counts, const int32_t* prefix_row, void* plan, size_t plan_bytes,
+                    void* hip_stream);
+
+/*
+ * spec_paged_attention -- softmax attention of N new tokens' queries.  Query (b, n, hq)
+ * reads head hq / (q_heads / heads).  It sees every slot of its prefix, every
+ * committed one of its own, and of the new ones lengths[b] + m (m < counts[b]) those with m <= n
+ * (mask NULL) or with mask[b][n][m] != 0.
+ *   q          rows of (b, n, hq), SPEC_F32 or SPEC_BF16; mask, scale, out, out_lse: as for
+ *              spec_kvq_attention
+ *   tables     [T][width], rows table_stride elements apart; B, N, q_heads, width and page_size as
+ *              the plan was made with.  A call whose sizes are not the plan's writes nothing.
+ * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros and an out_lse
+ * of -inf.  What a query does not see never reaches it, whatever its bytes.  One that sees a slot
+ * whose K or V holds a NaN or an infinity gives unspecified numbers; one that sees a slot whose
+ * page is none of the pool's gives NaN.  Products and sums are float32; with bfloat16
+ * queries the probabilities round to bfloat16 before they meet V.
+ * workspace: spec_paged_attention_workspace_bytes(...) bytes (may be 0), any contents;
+ * left as scratch.
+ */
+size_t spec_paged_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim, int with_prefix);
+int spec_paged_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int B, int N, int q_heads,
+                         const spec_paged_cache_t* cache, const int32_t* tables, int64_t table_stride, int width,
+                         const void* plan, size_t plan_bytes, int with_prefix, const uint8_t* mask,
+                         int64_t mask_batch, float scale, void* out, float* out_lse, void* workspace,
+                         size_t workspace_bytes, void* hip_stream);
+
+/*
  * ---- Log probabilities of tokens ----
  *
  * What a server answers beside the tokens that verification emits, and what a

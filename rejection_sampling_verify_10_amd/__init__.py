@@ -103,6 +103,18 @@ def lib() -> ctypes.CDLL:
         L.spec_kvq_evict_workspace_bytes.restype = Z
         L.spec_kvq_evict.argtypes = [P, P, P, P, P, I, I, I, P, P, P, P, P, Z, P]
         L.spec_kvq_evict.restype = I
+        L.spec_page_step.argtypes = [P, LL, I, I, I, I, P, P, P, P, P, I, P, P, P, P, P, Z, P]
+        L.spec_page_step.restype = I
+        L.spec_paged_append.argtypes = [P, P, P, I, I, I, I, P, LL, P, I, P, P]
+        L.spec_paged_append.restype = I
+        L.spec_paged_plan_bytes.argtypes = [I, I, I, I, I]
+        L.spec_paged_plan_bytes.restype = Z
+        L.spec_paged_plan.argtypes = [I, I, I, I, I, I, I, P, P, P, P, Z, P]
+        L.spec_paged_plan.restype = I
+        L.spec_paged_attention_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        L.spec_paged_attention_workspace_bytes.restype = Z
+        L.spec_paged_attention.argtypes = [P, I, I, I, I, P, P, LL, I, P, Z, I, P, LL, F, P, P, P, Z, P]
+        L.spec_paged_attention.restype = I
         L.spec_token_logprobs_workspace_bytes.argtypes = [I, I, I, I]
         L.spec_token_logprobs_workspace_bytes.restype = Z
         L.spec_token_logprobs.argtypes = [P, I, LL, I, I, P, I, F, I, P, P, P, P, P, P, Z, P]
@@ -570,3 +582,5 @@ def read_probe(src: torch.Tensor, sink: torch.Tensor) -> None:
 from .kvq import (KVQCache, kvq_append, kvq_attention, kvq_attention_workspace_bytes, kvq_commit, kvq_evict,  # noqa: E402,F401
                   kvq_evict_workspace_bytes, kvq_read, kvq_score, kvq_score_workspace_bytes, new_kvq_cache)
 from .logprobs import (TokenLogprobs, token_logprobs, token_logprobs_grad, token_logprobs_workspace_bytes)  # noqa: E402,F401
+from .paged import (PagedCache, PagedPlan, PagePool, new_page_pool, new_paged_cache, page_step, paged_append,  # noqa: E402,F401
+                    paged_attention, paged_attention_workspace_bytes, paged_plan)

@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["alpha.hip", "api.hip", "dense_tr.hip", "dense_walk.hip", "eagle2.hip", "kv_commit.hip", "kvq_append.hip",
-           "kvq_attention.hip", "kvq_evict.hip", "kvq_score.hip", "lmhead.hip", "logprob.hip", "nucleus.hip", "rowstats.hip",
+           "kvq_attention.hip", "kvq_evict.hip", "kvq_score.hip", "lmhead.hip", "logprob.hip", "nucleus.hip", "paged_append.hip", "paged_attention.hip",
+           "paged_plan.hip", "paged_step.hip", "rowstats.hip",
            "topk.hip", "tree_cluster.hip", "tree_sample.hip", "verify.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

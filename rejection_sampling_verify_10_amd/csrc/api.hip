@@ -13,6 +13,7 @@
 #include "internal.hpp"
 #include "kvq.hpp"
 #include "logprob.hpp"
+#include "paged.hpp"
 
 using namespace sv;
 
@@ -392,6 +393,65 @@ int take_rows(const spec_kvq_rows_t* r, int dtype, KvqRows& o) {
     o.data = r->data;
     o.batch = r->batch, o.pos = r->pos, o.head = r->head;
     return SPEC_OK;
+}
+
+bool page_size_ok(int n) { return n >= 16 && n <= 1024 && (n & (n - 1)) == 0; }
+int log2_of(int n) {
+    int l = 0;
+    while ((1 << l) < n) ++l;
+    return l;
+}
+bool slots_ok(int pages, int page_size) { return static_cast<int64_t>(pages) * page_size <= (1 << 30); }
+
+int take_pages(const spec_paged_cache_t* c, PagedCache& o) {
+    if (!c || !c->k || !c->v || c->pages < 1 || c->heads < 1 || c->head_dim < 1 || !page_size_ok(c->page_size))
+        return SPEC_EINVAL;
+    if (!kvq_dim_ok(c->head_dim) || c->heads > 65535 || !slots_ok(c->pages, c->page_size)) return SPEC_EUNSUPPORTED;
+    const int64_t D = c->head_dim;
+    // the stride of a dimension of one element never counts (a page has sixteen slots and more)
+    o.page_stride = c->pages == 1 ? 0 : c->page_stride;
+    o.slot_stride = c->slot_stride;
+    o.head_stride = c->heads == 1 ? 0 : c->head_stride;
+    if (o.page_stride < 0 || o.head_stride < 0 || o.page_stride % 8 || o.slot_stride % 8 || o.head_stride % 8 ||
+        (c->pages > 1 && o.page_stride < D) || o.slot_stride < D || (c->heads > 1 && o.head_stride < D) ||
+        !aligned(c->k, 16) || !aligned(c->v, 16))
+        return SPEC_EINVAL;
+    if (o.slot_stride > (1 << 20) || o.page_stride > (1ll << 40) || o.head_stride > (1ll << 40)) return SPEC_EUNSUPPORTED;
+    o.k = static_cast<uint16_t*>(c->k);
+    o.v = static_cast<uint16_t*>(c->v);
+    o.pages = c->pages;
+    o.page_log2 = log2_of(c->page_size);
+    o.H = c->heads;
+    o.D = c->head_dim;
+    return SPEC_OK;
+}
+
+// The plan's sizes; false where a call of them is past the limits.
+bool paged_sizes(PagedPlanArgs& a, int q_heads, int heads, bool with_prefix) {
+    static const int32_t some = 0;
+    if (!kvq_sizes_ok(a.B, heads, a.N, q_heads / heads)) return false;
+    a.G = q_heads / heads;
+    a.M = a.N * a.G;
+    a.prefix_row = with_prefix ? &some : nullptr;       // only whether there is one counts
+    paged_plan_sizes(a, heads);
+    const double workgroups = static_cast<double>(a.max_units) * heads, rows = static_cast<double>(a.B) * a.N * q_heads;
+    // parts are joined 1024 / D rows a workgroup of 256, at most 16 threads a row each
+    return kvq_threads_ok(workgroups, 256) && rows * 64 < 4294967296.0 && a.max_parts < (1ll << 31);
+}
+bool paged_args_ok(int B, int N, int q_heads, int heads) {
+    return B >= 1 && N >= 1 && heads >= 1 && q_heads >= 1 && q_heads % heads == 0;
+}
+void carve_paged_plan(Carver& c, const PagedPlanArgs& a, PagedPlan& p) {
+    p.head = c.take<int32_t>(kPgHead);
+    p.unit = c.take<PagedUnit>(static_cast<size_t>(a.max_units));
+    p.shared = c.take<PagedShared>(static_cast<size_t>(a.B));
+    p.own = c.take<PagedOwn>(static_cast<size_t>(a.B) * a.own_tiles);
+}
+void carve_paged_parts(Carver& c, const PagedPlanArgs& a, int heads, int head_dim, PagedAttnArgs& o) {
+    if (!a.max_parts) return;
+    const size_t rows = static_cast<size_t>(a.max_parts) * heads;
+    o.part_o = c.take<float>(rows * head_dim);
+    o.part_ml = c.take<float>(rows * 2);
 }
 
 // A launch has fewer than 2^32 threads.
@@ -1373,6 +1433,184 @@ int spec_accept_rate(const void* target_logits, spec_dtype_t dtype, const float*
         }
         SV_TRY(launch_alpha_dense(aa, s));
     }
+    return SPEC_OK;
+}
+
+int spec_page_step(int32_t* tables, int64_t table_stride, int T, int width, int page_size, int pages,
+                   const int32_t* held, const int32_t* state, int32_t* ring, const int32_t* lengths,
+                   const int32_t* counts, int N, int32_t* out_held, int32_t* out_state, int32_t* out_granted,
+                   int32_t* out_slots, void* workspace, size_t workspace_bytes, void* hip_stream) {
+    if (!tables || T < 1 || width < 1 || pages < 1 || N < 1 || !page_size_ok(page_size) || (T > 1 && table_stride < width) ||
+        !held || !state || !ring || !lengths || !out_held || !out_state || !out_granted || !out_slots ||
+        !aligned(tables, 4) || !aligned(held, 4) || !aligned(state, 4) || !aligned(ring, 4) || !aligned(lengths, 4) ||
+        !aligned(counts, 4) || !aligned(out_held, 4) || !aligned(out_state, 4) || !aligned(out_granted, 4) ||
+        !aligned(out_slots, 4))
+        return SPEC_EINVAL;
+    if (T > 65536 || N > 65536 || !slots_ok(pages, page_size) || !slots_ok(width, page_size) || table_stride > (1ll << 40))
+        return SPEC_EUNSUPPORTED;
+    const int rc = check_workspace(workspace, workspace_bytes, SPEC_PAGE_STEP_WORKSPACE_BYTES);
+    if (rc) return rc;
+    PageStepArgs a{};
+    a.tables = tables;
+    a.table_stride = table_stride;
+    a.T = T;
+    a.width = width;
+    a.pages = pages;
+    a.page_log2 = log2_of(page_size);
+    a.N = N;
+    a.held = held;
+    a.state = state;
+    a.ring = ring;
+    a.lengths = lengths;
+    a.counts = counts;
+    a.out_held = out_held;
+    a.out_state = out_state;
+    a.out_granted = out_granted;
+    a.out_slots = out_slots;
+    a.done = static_cast<unsigned*>(workspace);
+    ProfileScope prof;
+    SV_TRY(launch_page_step(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+int spec_paged_append(const spec_paged_cache_t* cache, const spec_kvq_rows_t* k, const spec_kvq_rows_t* v,
+                      spec_dtype_t dtype, int B, int N, int source_n, const int32_t* slots, int64_t slots_stride,
+                      const int32_t* path, int path_stride, const int32_t* accept_len, void* hip_stream) {
+    PagedAppendArgs a{};
+    int rc = take_pages(cache, a.c);
+    if (rc) return rc;
+    KvqRows rk, rv;
+    rc = take_rows(k, dtype, rk);
+    if (rc) return rc;
+    rc = take_rows(v, dtype, rv);
+    if (rc) return rc;
+    if (B < 1 || N < 1 || source_n < 1 || (!path && source_n < N) || !slots || !aligned(slots, 4) || (B > 1 && slots_stride < N) ||
+        (path && (!accept_len || path_stride < N)) || !aligned(path, 4) || !aligned(accept_len, 4))
+        return SPEC_EINVAL;
+    if (!kvq_sizes_ok(B, a.c.H, N, 1) || !kvq_threads_ok(static_cast<double>(B) * a.c.H * N + 256, a.c.D / 8) ||
+        slots_stride > (1ll << 40))
+        return SPEC_EUNSUPPORTED;
+    a.k = {rk.data, rk.batch, rk.pos, rk.head};
+    a.v = {rv.data, rv.batch, rv.pos, rv.head};
+    a.dtype = dtype;
+    a.B = B;
+    a.N = N;
+    a.source_n = source_n;
+    a.slots = slots;
+    a.slots_stride = slots_stride;
+    a.path = path;
+    a.path_stride = path_stride;
+    a.accept_len = accept_len;
+    ProfileScope prof;
+    SV_TRY(launch_paged_append(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+size_t spec_paged_plan_bytes(int B, int N, int q_heads, int heads, int with_prefix) {
+    if (!paged_args_ok(B, N, q_heads, heads)) return 0;
+    PagedPlanArgs a{};
+    a.B = B;
+    a.N = N;
+    if (!paged_sizes(a, q_heads, heads, with_prefix != 0)) return 0;
+    Carver c(nullptr);
+    carve_paged_plan(c, a, a.p);
+    return c.off;
+}
+
+int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int page_size, const int32_t* lengths,
+                    const int32_t* counts, const int32_t* prefix_row, void* plan, size_t plan_bytes,
+                    void* hip_stream) {
+    if (!paged_args_ok(B, N, q_heads, heads) || T < B || width < 1 || !page_size_ok(page_size) || !lengths ||
+        !aligned(lengths, 4) || !aligned(counts, 4) || !aligned(prefix_row, 4))
+        return SPEC_EINVAL;
+    PagedPlanArgs a{};
+    a.B = B;
+    a.N = N;
+    a.T = T;
+    if (!slots_ok(width, page_size) || !paged_sizes(a, q_heads, heads, prefix_row != nullptr)) return SPEC_EUNSUPPORTED;
+    a.width = width;
+    a.page_log2 = log2_of(page_size);
+    a.lengths = lengths;
+    a.counts = counts;
+    a.prefix_row = prefix_row;
+    Carver size(nullptr);
+    carve_paged_plan(size, a, a.p);
+    const int rc = check_workspace(plan, plan_bytes, size.off);
+    if (rc) return rc;
+    Carver c(plan);
+    carve_paged_plan(c, a, a.p);
+    ProfileScope prof;
+    SV_TRY(launch_paged_plan(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
+    return SPEC_OK;
+}
+
+size_t spec_paged_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim, int with_prefix) {
+    if (!paged_args_ok(B, N, q_heads, heads) || !kvq_dim_ok(head_dim)) return 0;
+    PagedPlanArgs p{};
+    p.B = B;
+    p.N = N;
+    if (!paged_sizes(p, q_heads, heads, with_prefix != 0)) return 0;
+    Carver c(nullptr);
+    PagedAttnArgs a{};
+    carve_paged_parts(c, p, heads, head_dim, a);
+    return c.off;
+}
+
+int spec_paged_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int B, int N, int q_heads,
+                         const spec_paged_cache_t* cache, const int32_t* tables, int64_t table_stride, int width,
+                         const void* plan, size_t plan_bytes, int with_prefix, const uint8_t* mask,
+                         int64_t mask_batch, float scale, void* out, float* out_lse, void* workspace,
+                         size_t workspace_bytes, void* hip_stream) {
+    PagedAttnArgs a{};
+    int rc = take_pages(cache, a.c);
+    if (rc) return rc;
+    KvqRows rq;
+    rc = take_rows(q, dtype, rq);
+    if (rc) return rc;
+    if (!paged_args_ok(B, N, q_heads, a.c.H) || !tables || !aligned(tables, 4) || width < 1 || table_stride < width ||
+        !out || !aligned(out, 16) || !aligned(out_lse, 4) || mask_batch < 0)
+        return SPEC_EINVAL;
+    const float cexp = base_two(scale);
+    if (!(scale > 0.f) || !isfinite(cexp)) return SPEC_EINVAL;
+    PagedPlanArgs p{};
+    p.B = B;
+    p.N = N;
+    if (!slots_ok(width, cache->page_size) || table_stride > (1ll << 40) || (mask && N > SPEC_MAX_NODES) ||
+        !paged_sizes(p, q_heads, a.c.H, with_prefix != 0))
+        return SPEC_EUNSUPPORTED;
+    Carver plan_size(nullptr);
+    carve_paged_plan(plan_size, p, a.p);
+    rc = check_workspace(const_cast<void*>(plan), plan_bytes, plan_size.off);
+    if (rc) return rc;
+    Carver pc(const_cast<void*>(plan));                 // read alone
+    carve_paged_plan(pc, p, a.p);
+    Carver size(nullptr);
+    carve_paged_parts(size, p, a.c.H, a.c.D, a);
+    rc = check_workspace(workspace, workspace_bytes, size.off);
+    if (rc) return rc;
+    Carver c(workspace);
+    carve_paged_parts(c, p, a.c.H, a.c.D, a);
+    a.q = {rq.data, rq.batch, rq.pos, rq.head};
+    a.dtype = dtype;
+    a.B = B;
+    a.N = N;
+    a.Hq = q_heads;
+    a.G = p.G;
+    a.M = p.M;
+    a.tables = tables;
+    a.table_stride = table_stride;
+    a.own_rows = p.own_rows;
+    a.own_tiles = p.own_tiles;
+    a.with_prefix = with_prefix != 0;
+    a.capacity = width * cache->page_size;
+    a.max_units = p.max_units;
+    a.mask = mask;
+    a.mask_batch = mask_batch;
+    a.cexp = cexp;
+    a.out = out;
+    a.out_lse = out_lse;
+    ProfileScope prof;
+    SV_TRY(launch_paged_attention(a, static_cast<hipStream_t>(hip_stream), prof.timing()));
     return SPEC_OK;
 }
 

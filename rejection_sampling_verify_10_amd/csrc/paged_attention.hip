@@ -1,0 +1,501 @@
+// Softmax attention over a paged cache: a prefix that many batch rows share, each
+// row's own slots and the visible new ones.
+//
+// One pass over the keys with a running maximum and sum: S = q . K_s,
+// P = exp2(c*(S - m)), O += P V_s, c = scale*log2(e); units of a plan
+// (paged_plan.hip) that belong together join at the end.
+//
+// A workgroup stages 64 keys of K and V in LDS and its four waves work on them: 32
+// query rows each, or (few rows) the same 32 rows, two waves a half of the keys
+// and of the values' elements each.  On 32x32x16 bf16 MFMAs in the transposed form,
+// S^T = K Q^T and O^T = V^T P^T, a lane has one query: lane (c, h), c = lane%32,
+// h = lane/32, ends up with scores of query c against keys 8a + 4h + i (a, i < 4),
+// and those, rounded to bf16, ARE the second product's operand when its
+// contraction runs over keys in that order.  V's operand wants four keys of one
+// element: the transposing LDS read gives them.  LDS rows are permuted in 16-byte
+// chunks so that neither read has bank conflicts.
+//
+// float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
+// queries P is the one bf16 of it, which is the output's own rounding.
+
+#include "kvq.hpp"
+#include "paged.hpp"
+
+namespace sv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHalf = 32;                               // keys a wave takes at a time
+constexpr float kSlack = 8.f;                           // powers of two a score may pass the running maximum by
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
+#if SV_KVQ_DEVICE
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+#else
+    return c;
+#endif
+}
+// Four 16-bit elements down a column of the 4 x 16 tile that sixteen lanes point at, four elements each.
+__device__ __forceinline__ u32x2 read_transposed(const unsigned char* p) {
+#if SV_KVQ_DEVICE
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p)));
+#else
+    return u32x2{0u, 0u};
+#endif
+}
+
+// LDS rows of D elements in 16-byte chunks.  K: sixteen keys' same chunk falls on sixteen different ones of 256 bytes; V: four
+// keys' same pair of chunks on four different pairs.
+template <int D> __device__ __forceinline__ constexpr int k_turn(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
+template <int D> __device__ __forceinline__ constexpr int v_turn(int key) { return D == 64 ? 2 * ((key >> 1) & 3) : 2 * (key & 7); }
+template <int D> __device__ __forceinline__ constexpr int k_at(int key, int chunk) { return key * 2 * D + ((chunk ^ k_turn<D>(key)) << 4); }
+template <int D> __device__ __forceinline__ constexpr int v_at(int key, int chunk) { return key * 2 * D + ((chunk ^ v_turn<D>(key)) << 4); }
+
+template <int D> struct Lds {
+    unsigned char k[2][kPgTile * 2 * D];
+    unsigned char v[2][kPgTile * 2 * D];
+    unsigned odd[2][2];             // keys of a tile that are no numbers, as bits
+};
+
+// Query row r of a unit's job: its batch row, token and head.
+struct QueryRow {
+    int b, n, g;
+};
+__device__ __forceinline__ QueryRow query_row(const PagedAttnArgs& a, int b0, int r) {
+    QueryRow q;
+    const int row = r / a.M, in = r - row * a.M;
+    q.b = b0 + row;
+    q.n = in / a.G;
+    q.g = in - q.n * a.G;
+    return q;
+}
+
+// A tile's keys on their way from global memory: the thread's chunks, chunk i of the thread in 16-key group group(i).
+template <int D> struct Stage {
+    static constexpr int kRow = D / 8;                  // chunks a row
+    static constexpr int kN = kPgTile * kRow / kThreads;
+    u32x4 k[kN], v[kN];
+    unsigned bad;                                       // groups whose page is none
+
+    // keys first .. first+63 of those below `end`; the others repeat the last group
+    __device__ __forceinline__ void load(const PagedAttnArgs& a, const int32_t* table, int h, int first, int end) {
+        const int tid = threadIdx.x;
+        const int in = (tid / kRow) % 16, chunk = tid % kRow;
+        bad = 0;
+        long long base[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int key = min(first + 16 * j, (end - 1) & ~15);
+            int page = table[key >> a.c.page_log2];
+            if (page < 0 || page >= a.c.pages) {
+                page = 0;
+                bad |= 1u << j;
+            }
+            base[j] = page * a.c.page_stride + (key & ((1 << a.c.page_log2) - 1)) * a.c.slot_stride + h * a.c.head_stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            // D = 128: chunk i is in group i; 64: in 2i, or 2i + 1 in the upper waves; 256: in i/2
+            const long long at = (D == 128   ? base[i % 4] + in * a.c.slot_stride
+                                  : D == 64  ? (wave_id() < 2 ? base[2 * i % 4] : base[(2 * i + 1) % 4]) + in * a.c.slot_stride
+                                             : base[i / 2 % 4] + ((tid / kRow) + 8 * (i & 1)) * a.c.slot_stride) + 8 * chunk;
+            k[i] = *reinterpret_cast<const u32x4*>(a.c.k + at);
+            v[i] = *reinterpret_cast<const u32x4*>(a.c.v + at);
+        }
+    }
+    __device__ __forceinline__ static int key(int i) { return threadIdx.x / kRow + kThreads / kRow * i; }
+    __device__ __forceinline__ void store(Lds<D>& l, int buf) const {
+        const int chunk = threadIdx.x % kRow;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            *reinterpret_cast<u32x4*>(l.k[buf] + k_at<D>(key(i), chunk)) = k[i];
+            *reinterpret_cast<u32x4*>(l.v[buf] + v_at<D>(key(i), chunk)) = v[i];
+        }
+    }
+    // V's elements that are no numbers would reach queries that give their key no weight: they become zeros, and the key
+    // is noted, for the queries that see it.
+    __device__ __forceinline__ void clean(Lds<D>& l, int buf) {
+        if (threadIdx.x < 2) {
+            const unsigned b = bad >> (2 * threadIdx.x);
+            l.odd[buf][threadIdx.x] = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            unsigned any = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned w = v[i][e];
+                const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
+                any |= lo | hi;
+                v[i][e] = (lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u);
+            }
+            if (any) atomicOr(&l.odd[buf][key(i) / 32], 1u << (key(i) % 32));
+        }
+    }
+};
+
+template <int D, int NQ, int DT>
+__device__ __forceinline__ void load_query(const PagedRows& q, long long off, bool live, int h2, u32x4 (&out)[NQ][D / 16]) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        const long long i = off + 16 * s + 8 * h2;
+        if (DT == 1) {
+            const u32x4 z = {0, 0, 0, 0};
+            out[0][s] = live ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(q.data) + i) : z;
+        } else {
+            float x[8] = {};
+            if (live) {
+                const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(q.data) + i);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(q.data) + i + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = a[e], x[4 + e] = b[e];
+            }
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                    x[2 * e] -= bf16_lo(w[e]);
+                    x[2 * e + 1] -= bf16_hi(w[e]);
+                }
+                out[p][s] = w;
+            }
+        }
+    }
+}
+
+// A wave's 32 queries: Q, and the running maximum, sum and output (NT tiles of 32 elements of O^T).
+template <int D, int DT, int NT> struct Wave {
+    static constexpr int NQ = DT == 1 ? 1 : 3;
+    u32x4 Q[NQ][D / 16];
+    f32x16 O[NT];
+    float m, l;
+    __device__ __forceinline__ Wave() : m(-INFINITY), l(0.f) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) O[t][i] = 0.f;
+    }
+
+    // One half tile: keys 32*kh .. of the staged ones, V's element tiles t0 ..; hide(S) for the tiles with keys that not
+    // every query sees.
+    template <typename Hide>
+    __device__ __forceinline__ void step(const Lds<D>& lds, int buf, int kh, int t0, float cexp, float slack, bool edge, const Hide& hide) {
+        const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
+        f32x16 S;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i] = 0.f;
+        const unsigned char* kp = lds.k[buf];
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            const u32x4 A = *reinterpret_cast<const u32x4*>(kp + k_at<D>(kh * kHalf + c, 2 * s + h2));
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) S = mfma32(A, Q[p][s], S);
+        }
+        if (edge) hide(S);
+
+        float mx = S[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, S[i]);
+        if (__ballot(mx > m + slack) != 0ull) {
+            mx = fmaxf(mx, xshfl(mx, 32));
+            const float mn = fmaxf(m, mx);
+            const float al = m == -INFINITY ? 0.f : exp2_fast((m - mn) * cexp);
+            l *= al;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) O[t] *= al;
+            m = mn;
+        }
+        const float mc = m == -INFINITY ? 0.f : m * cexp;
+        u32x4 P[NQ][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = exp2_fast(__builtin_fmaf(S[8 * s + i], cexp, -mc));
+                l += p[i];
+            }
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    P[x][s][e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+                    p[2 * e] -= bf16_lo(P[x][s][e]);
+                    p[2 * e + 1] -= bf16_hi(P[x][s][e]);
+                }
+            }
+        }
+
+        const unsigned char* vp = lds.v[buf];
+        const int key = kh * kHalf + 4 * h2 + (lane & 15) / 4;     // + 16s, + 8 more for the upper four
+        const int chunk = 2 * ((lane >> 4) & 1) + (lane & 3) / 2, at = 8 * (lane & 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const u32x2 lo = read_transposed(vp + v_at<D>(key + 16 * s, chunk + 4 * (t0 + t)) + at);
+                const u32x2 hi = read_transposed(vp + v_at<D>(key + 16 * s + 8, chunk + 4 * (t0 + t)) + at);
+                const u32x4 A = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) O[t] = mfma32(A, P[x][s], O[t]);
+            }
+        }
+    }
+};
+
+// The new tokens that a query of a masked call sees, as bits.
+__device__ __forceinline__ unsigned long long read_mask(const PagedAttnArgs& a, int b, int tok, int cnt) {
+    const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
+    const uint8_t* row = a.mask + b * a.mask_batch + static_cast<long long>(max(tok, 0)) * a.N;
+    unsigned bits = 0;
+    for (int e = 0; e < 32; ++e) {
+        const int node = 32 * h2 + e;
+        bits |= static_cast<unsigned>((row[min(node, a.N - 1)] != 0) & (node < cnt)) << e;
+    }
+    const unsigned other = xshfl(bits, 32);
+    const unsigned lo = h2 ? other : bits, hi = h2 ? bits : other;
+    return (static_cast<unsigned long long>(hi) << 32) | lo;
+}
+
+// Rows of O^T tile t0 + t, register i: element 32*(t0 + t) + 8*(i/4) + 4*h2 + i%4 of query c, to the call's output or a part.
+template <int D, int DT, int NT>
+__device__ __forceinline__ void write_rows(const PagedAttnArgs& a, const PagedUnit& u, int h, int r, int t0, bool first,
+                                           const f32x16 (&O)[NT], float m, float l, bool live) {
+    const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
+    if (r >= u.rows) return;
+    if (u.part >= 0) {
+        const long long at = (static_cast<long long>(u.part) + (r - u.row0)) * a.c.H + h;
+        if (h2 == 0 && first) {
+            a.part_ml[2 * at] = m;
+            a.part_ml[2 * at + 1] = l;
+        }
+        float* o = a.part_o + at * D + 4 * h2;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4*>(o + 32 * (t0 + t) + 8 * i) =
+                    f32x4{O[t][4 * i], O[t][4 * i + 1], O[t][4 * i + 2], O[t][4 * i + 3]};
+        return;
+    }
+    const QueryRow q = query_row(a, u.b0, r);
+    const long long at = (static_cast<long long>(q.b) * a.N + q.n) * a.Hq + h * a.G + q.g;
+    const bool empty = !live || l == 0.f;
+    const float inv = empty ? 0.f : 1.f / l;
+    if (h2 == 0 && first && a.out_lse)
+        a.out_lse[at] = empty ? -INFINITY : (m * a.cexp + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long d = at * D + 32 * (t0 + t) + 8 * i + 4 * h2;
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : O[t][4 * i + e] * inv;
+            if (DT == 1)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + d) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+            else
+                *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + d) = f32x4{o[0], o[1], o[2], o[3]};
+        }
+}
+
+// One unit.  WIDE: wave w has query rows 32w .. of it; else all waves have the same 32, wave w keys 32*(w%2) .. of each tile
+// and half w/2 of the output's elements.
+template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
+    constexpr int NT = WIDE ? D / 32 : D / 64;
+    const int wave = wave_id(), lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
+    const int r = u.row0 + (WIDE ? kHalf * wave : 0) + c, t0 = WIDE ? 0 : (wave >> 1) * NT;
+    const bool shared = u.table != u.b0 || u.cnt == 0;
+    const bool there = r < u.rows;
+    const QueryRow q = query_row(a, u.b0, there ? r : u.row0);
+    const int tok = there && (shared || q.n < u.cnt) ? q.n : -1;
+    Wave<D, DT, NT> w;
+    load_query<D, Wave<D, DT, NT>::NQ, DT>(a.q, q.b * a.q.batch + q.n * a.q.pos + (static_cast<long long>(h) * a.G + q.g) * a.q.head,
+                                           there, h2, w.Q);
+    const bool working = WIDE ? u.row0 + kHalf * wave < u.rows : true;
+    // slots below `seen` are seen by every query of the unit
+    const int tok0 = u.row0 / a.G;
+    const int seen = shared ? u.k1 : min(u.k1, a.mask ? u.pre : u.pre + tok0 + 1);
+    unsigned long long tree = 0;
+    if (!shared && a.mask && u.k1 > u.pre) tree = read_mask(a, q.b, tok, u.cnt);
+    const float slack = fminf(kSlack / a.cexp, 1e30f);
+    const int32_t* table = a.tables + u.table * a.table_stride;
+
+    Stage<D> st;
+    const auto put = [&](int first, int buf) {          // what is staged for keys first .. to LDS
+        if (first + kPgTile > seen || st.bad) st.clean(lds, buf);
+        st.store(lds, buf);
+    };
+    bool odd_page = false;
+    if (u.k0 < u.k1) {
+        st.load(a, table, h, u.k0, u.k1);
+        odd_page = st.bad != 0;
+        put(u.k0, 0);
+    }
+    int buf = 0;
+    for (int kt = u.k0; kt < u.k1; kt += kPgTile, buf ^= 1) {
+        __syncthreads();
+        const bool edge = kt + kPgTile > seen || odd_page, more = kt + kPgTile < u.k1;
+        if (more) st.load(a, table, h, kt + kPgTile, u.k1);
+        if (working) {
+            const auto hide = [&](int kh) {
+                return [&, kh](f32x16& S) {
+                    const unsigned odd = lds.odd[buf][kh];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int in = 8 * (i / 4) + 4 * h2 + i % 4, key = kt + kHalf * kh + in, node = key - u.pre;
+                        const bool sees = key < u.k1 && (node < 0 || (a.mask ? node < 64 && ((tree >> (node & 63)) & 1ull) : node <= tok));
+                        S[i] = !sees ? -INFINITY : (odd >> in) & 1u ? __builtin_nanf("") : S[i];
+                    }
+                };
+            };
+            if (WIDE) {
+                w.step(lds, buf, 0, 0, a.cexp, slack, edge, hide(0));
+                w.step(lds, buf, 1, 0, a.cexp, slack, edge, hide(1));
+            } else {
+                const int kh = wave & 1;
+                w.step(lds, buf, kh, t0, a.cexp, slack, edge, hide(kh));
+            }
+        }
+        if (more) {
+            odd_page = st.bad != 0;
+            put(kt + kPgTile, buf ^ 1);
+        }
+    }
+    w.l += xshfl(w.l, 32);
+    if (!WIDE) {
+        // join the two halves of the keys
+        __syncthreads();
+        f32x16(*const sh)[kWave] = reinterpret_cast<f32x16(*)[kWave]>(&lds);
+        float(*const ml)[kWave] = reinterpret_cast<float(*)[kWave]>(sh + 2 * NT);
+        if (wave & 1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sh[(wave >> 1) * NT + t][lane] = w.O[t];
+            ml[wave - 1][lane] = w.m;
+            ml[wave][lane] = w.l;
+        }
+        __syncthreads();
+        if (wave & 1) return;
+        const float om = ml[wave][lane], ol = ml[wave + 1][lane];
+        const float mn = fmaxf(w.m, om);
+        const float wa = w.m == -INFINITY ? 0.f : exp2_fast((w.m - mn) * a.cexp);
+        const float wb = om == -INFINITY ? 0.f : exp2_fast((om - mn) * a.cexp);
+        w.m = mn;
+        // a sum that is NaN stays NaN whatever its maximum
+        w.l = w.l * wa + ol * wb;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) w.O[t] = w.O[t] * wa + sh[(wave >> 1) * NT + t][lane] * wb;
+    }
+    if (working) write_rows<D, DT, NT>(a, u, h, r, t0, t0 == 0, w.O, w.m, w.l, tok >= 0);
+}
+
+// Whether the plan was made for a call of these sizes (one that was not names rows that are not there).
+__device__ __forceinline__ bool plan_fits(const PagedAttnArgs& a) {
+    const int32_t* h = a.p.head;
+    return h[1] == a.B && h[2] == a.N && h[3] == a.M && h[4] == a.with_prefix && h[5] == a.capacity;
+}
+
+constexpr int occupancy(int D, int DT) { return D == 256 || (D == 128 && DT == 0) ? 1 : 2; }
+
+template <int D, int DT>
+__global__ __launch_bounds__(kThreads, occupancy(D, DT)) void paged_attention_kernel(PagedAttnArgs a) {
+    __shared__ __attribute__((aligned(256))) Lds<D> lds;
+    const int unit = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
+    if (!plan_fits(a) || unit >= a.p.head[0]) return;
+    const PagedUnit u = a.p.unit[unit];
+    if (u.wide) attend<D, DT, true>(a, u, h, lds);
+    else attend<D, DT, false>(a, u, h, lds);
+}
+
+// Joins the parts of each query row: D/4 neighbouring threads a row, four elements each.
+template <int D, int DT>
+__global__ __launch_bounds__(kThreads) void paged_join_kernel(PagedAttnArgs a, long long rows) {
+    constexpr int kLanes = D / 4, kRows = kThreads / kLanes;
+    const int d = static_cast<int>(threadIdx.x % kLanes) * 4;
+    const long long at = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kLanes;     // (b, n, query head)
+    if (at >= rows || !plan_fits(a)) return;
+    const int hq = static_cast<int>(at % a.Hq), h = hq / a.G;
+    const long long bn = at / a.Hq;
+    const int b = static_cast<int>(bn / a.N), n = static_cast<int>(bn % a.N);
+    const int r = n * a.G + hq % a.G;
+    const PagedOwn own = a.p.own[static_cast<long long>(b) * a.own_tiles + r / a.own_rows];
+    if (own.count == 0) return;                         // written by its one unit
+    const PagedShared sh = a.p.shared[b];
+    float m = -INFINITY, l = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    const auto join = [&](long long first, long long step, int count) {
+        for (int s0 = 0; s0 < count; s0 += 4) {
+            // four parts at a time: their loads are independent
+            float ms[4], ls[4];
+            f32x4 os[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const long long p = (first + min(s0 + e, count - 1) * step) * a.c.H + h;
+                ms[e] = a.part_ml[2 * p];
+                ls[e] = a.part_ml[2 * p + 1];
+                os[e] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + d);
+            }
+            float mn = m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mn = fmaxf(mn, ms[e]);
+            const float w = m == -INFINITY ? 0.f : exp2_fast((m - mn) * a.cexp);
+            l *= w;
+            o *= w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float we = ms[e] == -INFINITY || s0 + e >= count ? 0.f : exp2_fast((ms[e] - mn) * a.cexp);
+                l += s0 + e < count ? ls[e] * we : 0.f;
+                o += os[e] * we;
+            }
+            m = mn;
+        }
+    };
+    if (n < sh.live) {
+        join(static_cast<long long>(sh.first) + r, sh.step, sh.count);
+        join(static_cast<long long>(own.first) + r % a.own_rows, a.own_rows, own.count);
+    }
+    const bool empty = l == 0.f;
+    const float inv = empty ? 0.f : 1.f / l;
+    if (d == 0 && a.out_lse) a.out_lse[at] = empty ? -INFINITY : (m * a.cexp + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : o[e] * inv;
+    if (DT == 1)
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * D + d) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    else
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at * D + d) = o;
+}
+
+template <int D, int DT> void attend(const PagedAttnArgs& a, hipStream_t s, Timing t) {
+    const dim3 grid(static_cast<unsigned>(a.max_units * a.c.H));
+    launch_timed(t, paged_attention_kernel<D, DT>, grid, dim3(kThreads), 0, s, a);
+    if (!a.part_o) return;
+    constexpr int rows_wg = kThreads / (D / 4);
+    const long long rows = static_cast<long long>(a.B) * a.N * a.Hq;
+    paged_join_kernel<D, DT><<<dim3(static_cast<unsigned>((rows + rows_wg - 1) / rows_wg)), kThreads, 0, s>>>(a, rows);
+}
+
+}  // namespace
+
+hipError_t launch_paged_attention(const PagedAttnArgs& a, hipStream_t s, Timing t) {
+    if (a.dtype == 1) {
+        if (a.c.D == 64) attend<64, 1>(a, s, t);
+        else if (a.c.D == 128) attend<128, 1>(a, s, t);
+        else attend<256, 1>(a, s, t);
+    } else {
+        if (a.c.D == 64) attend<64, 0>(a, s, t);
+        else if (a.c.D == 128) attend<128, 0>(a, s, t);
+        else attend<256, 0>(a, s, t);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace sv

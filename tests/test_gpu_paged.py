@@ -1,0 +1,506 @@
+"""The paged cache on the GPU against its definitions (paged_ref): pages of a step and rows in them (exact), attention
+behind shared prefixes against float64, and a run of them together with a verification."""
+
+import numpy as np
+import pytest
+
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def R():
+    import torch
+    import rejection_sampling_verify_10_amd as R
+    assert torch.cuda.is_available(), "GPU test without a GPU"
+    R.lib()
+    return R
+
+
+def dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def ints(v):
+    return dev(np.asarray(v, np.int32))
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+# ---- pages ----
+
+def make_pool(R, rng, T, width, P, fill=0.4, spare=0):
+    """A pool in the middle of its life: rows of random lengths, free pages anywhere in the ring."""
+    import torch
+    held = np.minimum(rng.integers(0, max(1, int(width * fill)) + 1, T), width).astype(np.int32)
+    pages = int(held.sum()) + spare + 1
+    ids = rng.permutation(pages).astype(np.int32)
+    tables = np.full((T, width + 3), -5, np.int32)
+    at = 0
+    for t in range(T):
+        tables[t, :held[t]] = ids[at:at + held[t]]
+        at += held[t]
+    head, free = int(rng.integers(0, pages)), pages - at
+    ring = np.full(pages, -9, np.int32)
+    ring[(head + np.arange(free)) % pages] = ids[at:]
+    t = dev(tables)[:, :width]                                # rows of a wider tensor
+    return R.PagePool(t, ints(held), ints(ring), ints([head, free]), P)
+
+
+def pool_arrays(pool):
+    return [x.cpu().numpy().copy() for x in (pool.tables, pool.held, pool.ring, pool.state)]
+
+
+@pytest.mark.parametrize("T,width,P,N,spare", [
+    (1, 1, 16, 1, 0), (1, 40, 16, 600, 30), (3, 8, 64, 5, 0), (7, 5, 16, 16, 40), (300, 9, 32, 7, 500), (257, 70, 16, 1025, 9000),
+    (700, 6, 128, 64, 300), (1500, 4, 16, 3, 100), (16, 300, 32, 8192, 4000),
+])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_page_step(R, T, width, P, N, spare, in_place):
+    import torch
+    rng = np.random.default_rng([T, width, N])
+    pool = make_pool(R, rng, T, width, P, spare=spare)
+    for step in range(5):
+        tables, held, ring, state = pool_arrays(pool)
+        lengths = np.maximum(held * P - rng.integers(0, 2 * P, T), 0).astype(np.int32)
+        lengths[rng.random(T) < 0.2] = -1                     # ended
+        back = rng.random(T) < 0.2
+        lengths[back] = lengths[back] // 3                    # much was rejected
+        counts = rng.integers(0, N + 1, T).astype(np.int32)
+        if T > 4:                                             # numbers that make no sense
+            counts[1], counts[2], lengths[3] = N + 1, -1, width * P
+        use = None if step == 4 else counts
+        want = ref.page_step(tables, held, ring, state, lengths, use, N, P)
+        oh, os = (None, None) if in_place else (torch.full_like(pool.held, 77), torch.full_like(pool.state, 77))
+        granted, slots = R.page_step(pool, ints(lengths), N, counts=None if use is None else ints(use), out_held=oh, out_state=os)
+        got = (granted, slots, pool.tables, pool.held if in_place else oh, pool.ring, pool.state if in_place else os)
+        for name, g, w in zip(("granted", "slots", "tables", "held", "ring", "state"), got, want):
+            assert np.array_equal(g.cpu().numpy(), w), (name, step)
+        assert (pool.tables.as_strided((T, 3), (width + 3, 1), width) == -5).all() and not pool._workspace.any()
+        if not in_place:
+            assert np.array_equal(pool.held.cpu().numpy(), held) and np.array_equal(pool.state.cpu().numpy(), state)
+            pool.held.copy_(oh)
+            pool.state.copy_(os)
+
+
+def test_pages_run_out_in_the_order_of_the_rows(R):
+    pool = R.new_page_pool(5, 4, 6, 16, "cuda")
+    granted, slots = R.page_step(pool, ints([0, 0, 0, 0, 0]), 40, counts=ints([33, 16, 40, 0, 10]))
+    assert granted.tolist() == [33, 16, -1, 0, -1]            # the third does not fit, so the fifth gets none either
+    assert pool.held.tolist() == [3, 1, 0, 0, 0] and pool.state.tolist() == [4, 2]
+    assert slots[1, :16].tolist() == list(range(48, 64)) and (slots[1, 16:] == -1).all() and (slots[2] == -1).all()
+    # the first ends: its pages are free again, for the next call
+    granted, _ = R.page_step(pool, ints([-1, 16, 0, 0, 0]), 40, counts=ints([7, 0, 40, 0, 32]))
+    assert granted.tolist() == [0, 0, -1, 0, -1] and pool.state.tolist() == [4, 5]
+    granted, slots = R.page_step(pool, ints([-1, 16, 0, 0, 0]), 40, counts=ints([0, 0, 40, 0, 32]))
+    assert granted.tolist() == [0, 0, 40, 0, 32] and pool.state.tolist() == [3, 0]
+    assert pool.tables[2, :3].tolist() == [4, 5, 0] and pool.tables[4, :2].tolist() == [1, 2]
+    assert slots[4, :17].tolist() == list(range(16, 32)) + [32]
+
+
+@pytest.mark.parametrize("state", [(-1, 3), (6, 3), (0, -1), (0, 7), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_a_ring_out_of_range_serves_nobody(R, state):
+    pool = R.new_page_pool(2, 4, 6, 16, "cuda")
+    pool.state.copy_(ints(state))
+    granted, slots = R.page_step(pool, ints([0, -1]), 3)
+    assert granted.tolist() == [-1, -1] and (slots == -1).all() and pool.held.tolist() == [0, 0]
+    assert pool.state.tolist() == list(state) and (pool.tables == -1).all() and pool.ring.tolist() == list(range(6))
+
+
+def test_pages_that_are_none_have_no_slots(R):
+    pool = R.new_page_pool(1, 4, 3, 16, "cuda")
+    pool.ring.copy_(ints([3, -1, 2]))
+    granted, slots = R.page_step(pool, ints([0]), 48)
+    assert granted.tolist() == [48] and (slots[0, :32] == -1).all() and slots[0, 32:].tolist() == list(range(32, 48))
+
+
+# ---- rows ----
+
+LAYOUTS = {"slots": (0, 1, 2), "heads": (0, 2, 1), "outer": (2, 0, 1), "inner": (1, 2, 0)}
+
+
+def make_cache(R, rng, pages, P, H, D, layout="slots", fill=None):
+    """Pages of normal rows (or one bit pattern), dimensions in any order of memory."""
+    import torch
+    order = LAYOUTS[layout]
+    shape = [(pages, P, H)[i] for i in order]
+    back = [order.index(i) for i in range(3)]
+    out = []
+    for _ in range(2):
+        if fill is None:
+            x = rng.standard_normal((*shape, D)).astype(np.float32)
+            x[..., 3::29] *= 4.0
+            t = torch.from_numpy(x).cuda().bfloat16()
+        else:
+            t = torch.full((*shape, D), fill, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+        out.append(t.permute(*back, 3))
+    return R.PagedCache(*out)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "f32"), (128, "f32"), (256, "f32")])
+def test_append(R, D, dtype, layout):
+    import torch
+    rng = np.random.default_rng(D)
+    B, N, H, P, pages = 3, 21, 3, 16, 9
+    cache = make_cache(R, rng, pages, P, H, D, layout)
+    kv = torch.from_numpy(rng.standard_normal((B, N, 2, H, D)).astype(np.float32)).cuda()
+    kv[0, 0, 0, 0, :3] = torch.tensor([float("nan"), float("inf"), -1e-45])
+    kv = kv.bfloat16() if dtype == "bf16" else kv
+    k, v = kv[:, :, 0], kv[:, :, 1]
+    slots = rng.permutation(pages * P)[:B * N].reshape(B, N).astype(np.int32)
+    slots[0, 5], slots[1, 6], slots[2, 7], slots[2, 8] = -1, pages * P, 2 ** 31 - 1, -2 ** 31
+    want = [t.clone() for t in (cache.k_pages, cache.v_pages)]
+    for b in range(B):
+        for n in range(N):
+            if 0 <= slots[b, n] < pages * P:
+                for w, x in zip(want, (k, v)):
+                    w[slots[b, n] // P, slots[b, n] % P] = x[b, n].bfloat16()
+    wide = torch.full((B, N + 2), -1, dtype=torch.int32, device="cuda")
+    wide[:, :N] = ints(slots)
+    R.paged_append(cache, k, v, wide[:, :N])
+    for got, w in zip((cache.k_pages, cache.v_pages), want):
+        assert torch.equal(got.contiguous().view(torch.int16), w.contiguous().view(torch.int16))
+    # an accepted path: rows 0, 2, 5, .. of the step again, in the first slots
+    path = np.full((B, 4), -1, np.int32)
+    path[0], path[1, :2], path[2] = [0, 2, 5, 20], [0, 3], [0, 1, -1, 30]
+    alen = [3, 1, 3]
+    for b in range(B):
+        for i in range(alen[b] + 1):
+            if 0 <= slots[b, i] < pages * P and 0 <= path[b, i] < N:
+                for w, x in zip(want, (k, v)):
+                    w[slots[b, i] // P, slots[b, i] % P] = x[b, path[b, i]].bfloat16()
+    R.paged_append(cache, k, v, ints(slots), path=ints(path), accept_len=ints(alen))
+    R.paged_append(cache, v, k, ints(slots), path=ints(path), accept_len=ints([-1, -1, 4]))     # nothing
+    for got, w in zip((cache.k_pages, cache.v_pages), want):
+        assert torch.equal(got.contiguous().view(torch.int16), w.contiguous().view(torch.int16))
+
+
+# ---- attention ----
+
+def tree_masks(rng, B, N):
+    m = np.zeros((B, N, N), np.uint8)
+    for b in range(B):
+        for n in range(N):
+            if n:
+                m[b, n] = m[b, rng.integers(max(0, n - 5), n)]
+            m[b, n, n] = 1
+    return m
+
+
+def queries(rng, B, N, Hq, D, dtype, size=1.5):
+    import torch
+    q = torch.from_numpy((size * rng.standard_normal((B, N, Hq, D))).astype(np.float32)).cuda()
+    return q.bfloat16() if dtype == "bf16" else q
+
+
+def make_tables(rng, pages, P, lens, N, B, width):
+    """Tables of shuffled pages for rows of `lens` committed slots (N new ones behind those of the first B)."""
+    ids = rng.permutation(pages)
+    tables = np.full((len(lens), width), -1, np.int32)
+    at = 0
+    for t, n in enumerate(lens):
+        k = -(-(max(n, 0) + (N if t < B else 0)) // P)
+        tables[t, :min(k, width)] = ids[at:at + min(k, width)]
+        at += k
+    assert at <= pages
+    return tables
+
+
+def check(R, q, cache, tables, lens, B, counts=None, prefix_row=None, mask=None, scale=None, got=None):
+    """Every output within the roundings that the arithmetic allows."""
+    import torch
+    N, Hq, D = q.shape[1:]
+    if got is None:
+        plan = R.paged_plan(cache, ints(tables), ints(lens), N, Hq, B=B, counts=None if counts is None else ints(counts),
+                            prefix_row=None if prefix_row is None else ints(prefix_row))
+        got = R.paged_attention(q, cache, plan, mask=None if mask is None else dev(mask), scale=scale)
+    bf16 = q.dtype == torch.bfloat16
+    scale = D ** -0.5 if scale is None else scale
+    m = None if mask is None else np.broadcast_to(mask, (B, N, N))
+    # a probability rounds to bf16 before it meets V with bf16 queries, and so does the output
+    want, wlse, tol, ltol = ref.attend(f64(q), f64(cache.k_pages), f64(cache.v_pages), tables, lens, B, counts, prefix_row, m,
+                                       scale, 2.0 ** -8 if bf16 else U)
+    tol = tol + (2.0 ** -8 if bf16 else U) * 1.01 * np.abs(want)
+    out, lse = f64(got[0]), f64(got[1])
+    bad = ~(np.abs(out - want) <= tol + 1e-37)
+    assert not bad.any(), (np.argwhere(bad)[:3], out[bad][:3], want[bad][:3], tol[bad][:3])
+    assert np.array_equal(np.isneginf(lse), np.isneginf(wlse))
+    live = ~np.isneginf(wlse)
+    assert (np.abs(lse - wlse, where=live, out=np.zeros_like(lse)) <= ltol + 1e-30)[live].all()
+    assert (out[~live] == 0).all()
+    return got
+
+
+CASES = [
+    # B, N, H, G, D, P, lengths, prefixes (lengths), mask
+    dict(B=1, N=1, H=1, G=1, D=64, P=16, lens=[0], pre=[]),
+    dict(B=3, N=1, H=2, G=4, D=128, P=16, lens=[5, 0, 63], pre=[]),
+    dict(B=4, N=1, H=8, G=4, D=128, P=16, lens=[100, 1, 64, 31], pre=[500]),
+    dict(B=5, N=3, H=2, G=3, D=64, P=32, lens=[17, 200, 0, 64, 333], pre=[127, 128]),
+    dict(B=6, N=8, H=2, G=4, D=128, P=64, lens=[70, 0, 129, 1000, 3, 5], pre=[1, 1023]),
+    dict(B=4, N=27, H=2, G=5, D=128, P=16, lens=[70, 0, 129, 400], pre=[300], tree=True),
+    dict(B=2, N=64, H=1, G=2, D=256, P=128, lens=[65, 1], pre=[70, 0], tree=True),
+    dict(B=2, N=100, H=2, G=2, D=64, P=16, lens=[37, 0], pre=[200]),
+    dict(B=2, N=193, H=1, G=3, D=128, P=16, lens=[0, 70], pre=[]),
+    dict(B=1, N=2, H=2, G=2, D=256, P=1024, lens=[3000], pre=[2047]),
+    dict(B=40, N=1, H=1, G=8, D=128, P=16, lens=[(37 * i) % 101 for i in range(40)], pre=[333, 64]),
+    dict(B=2, N=5, H=16, G=1, D=64, P=16, lens=[5000, 77], pre=[]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(c[k]) for k in ("B", "N", "H", "G", "D", "P")))
+def test_attention(R, case, dtype):
+    rng = np.random.default_rng(case["D"] + case["N"])
+    B, N, H, G, D, P = (case[k] for k in ("B", "N", "H", "G", "D", "P"))
+    lens = case["lens"] + case["pre"]
+    width = max(-(-(n + N) // P) for n in lens)
+    pages = sum(-(-(n + N) // P) for n in lens) + 2
+    cache = make_cache(R, rng, pages, P, H, D, list(LAYOUTS)[case["N"] % 4])
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    prefix = None
+    if case["pre"]:
+        prefix = np.array([B + b * len(case["pre"]) // B for b in range(B)])
+        if B > 3:
+            prefix[1] = -1                                    # one without, inside a run
+    mask = tree_masks(rng, B, N) if case.get("tree") else None
+    q = queries(rng, B, N, H * G, D, dtype)
+    check(R, q, cache, tables, lens, B, prefix_row=prefix, mask=mask)
+    counts = rng.integers(0, N + 1, B)
+    check(R, q, cache, tables, lens, B, counts=counts, prefix_row=prefix, mask=mask, scale=0.3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_share_nothing_alternate_or_are_errors(R, dtype):
+    rng = np.random.default_rng(9)
+    B, N, H, G, D, P = 9, 2, 2, 2, 64, 16
+    lens = [10, -1, 30, 161, 20, 0, 40, 50, 60, 100, 130, -3, 1000]
+    width = 10
+    pages = 200
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = rng.integers(0, pages, (13, width)).astype(np.int32)      # pages may be shared at will
+    prefix = [9, 9, 10, 9, 13, 9, 11, 12, 0]                  # 13 is no row, 11 has no length, 12 too long; the last: batch row 0
+    counts = [2, 2, 3, 2, 2, -1, 2, 2, 1]
+    q = queries(rng, B, N, H * G, D, dtype)
+    got = check(R, q, cache, tables, lens, B, counts=counts, prefix_row=prefix)
+    assert (got[0][[1, 2, 3, 4, 5, 6, 7]] == 0).all()
+    check(R, q, cache, tables, lens, B, prefix_row=prefix)
+    check(R, q, cache, tables, lens, B, counts=counts)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (128, "f32")])
+def test_what_is_not_seen_does_not_reach(R, D, dtype):
+    """NaN and infinities behind the sequences' ends, in other pages, and in tokens a query's mask hides."""
+    import torch
+    rng = np.random.default_rng(D)
+    B, N, H, G, P = 2, 6, 2, 3, 16
+    lens, width, pages = [37, 5, 41], 4, 16
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    mask = np.repeat(np.eye(N, dtype=np.uint8)[None], B, 0)
+    mask[:, :, 0] = 1
+    mask[0, 4] = 0                                            # sees no new token
+    used = torch.zeros(pages, P, dtype=torch.bool, device="cuda")
+    for t, n in enumerate(lens):
+        for s in range(n + (N if t < B else 0)):
+            used[tables[t, s // P], s % P] = True
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"))):
+        cache.k_pages[~used] = bad
+        cache.v_pages[~used] = bad
+        q = queries(rng, B, N, H * G, D, dtype)
+        check(R, q, cache, tables, lens, B, prefix_row=[2, 2], mask=mask)
+        # token 3's rows are bad: every other token's output is as it was
+        clean = [t.clone() for t in (cache.k_pages, cache.v_pages)]
+        plan = R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, prefix_row=ints([2, 2]))
+        first = R.paged_attention(q, cache, plan, mask=dev(mask))
+        for b in range(B):
+            s = lens[b] + 3
+            (cache.v_pages if i < 2 else cache.k_pages)[tables[b, s // P], s % P, :, 7] = bad
+        second = R.paged_attention(q, cache, plan, mask=dev(mask))
+        others = [0, 1, 2, 4, 5]
+        assert torch.equal(first[0][:, others], second[0][:, others]) and torch.equal(first[1][:, others], second[1][:, others])
+        assert torch.isfinite(first[0]).all()
+        if i == 0:
+            assert torch.isnan(second[0][:, 3]).any()
+        cache.k_pages.copy_(clean[0])
+        cache.v_pages.copy_(clean[1])
+
+
+def test_pages_that_are_none(R):
+    """A table that names a page outside the pool: the queries that see its slots answer NaN, the others what they did."""
+    import torch
+    rng = np.random.default_rng(2)
+    B, N, H, G, D, P = 3, 2, 1, 2, 128, 16
+    lens, width, pages = [40, 40, 200, 90], 16, 40
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    q = queries(rng, B, N, H * G, D, "bf16")
+    args = dict(B=B, prefix_row=ints([3, -1, 3]))
+    first = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints(lens), N, H * G, **args))
+    for bad in (-1, pages, 2 ** 31 - 1, -2 ** 31):
+        broken = tables.copy()
+        broken[1, 1] = bad
+        got = R.paged_attention(q, cache, R.paged_plan(cache, ints(broken), ints(lens), N, H * G, **args))
+        assert torch.isnan(got[0][1]).all() and torch.isnan(got[1][1]).all()
+        assert torch.equal(got[0][[0, 2]], first[0][[0, 2]]) and torch.equal(got[1][[0, 2]], first[1][[0, 2]])
+        broken = tables.copy()
+        broken[3, 5] = bad                                    # in the prefix of the other two
+        got = R.paged_attention(q, cache, R.paged_plan(cache, ints(broken), ints(lens), N, H * G, **args))
+        assert torch.isnan(got[0][[0, 2]]).all() and torch.equal(got[0][1], first[0][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,H,G,D,P,shared,tail", [
+    (24, 1, 8, 8, 128, 16, 9000, 300), (3, 8, 2, 4, 64, 64, 30011, 100), (1, 1, 1, 1, 128, 16, 70000, 3), (8, 20, 4, 4, 128, 16, 2500, 900),
+])
+def test_long_prefixes(R, B, N, H, G, D, P, shared, tail, dtype):
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, tail + 1, B)] + [shared]
+    width = -(-max(shared, tail + N) // P)
+    pages = sum(-(-(n + N) // P) for n in lens)
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    check(R, queries(rng, B, N, H * G, D, dtype), cache, tables, lens, B, prefix_row=[B] * B)
+
+
+def test_a_plan_of_other_sizes_writes_nothing(R):
+    import ctypes
+    import torch
+    rng = np.random.default_rng(1)
+    cache = make_cache(R, rng, 8, 16, 2, 64)
+    tables, lens = ints([[0, 1], [2, 3]]), ints([5, 9])
+    plan = R.paged_plan(cache, tables, lens, 3, 4)
+    other = R.paged_plan(cache, tables, lens, 2, 4)
+    plan._buffer, plan._ptr = other._buffer, other._ptr       # as a C caller might mix them up
+    out = (torch.full((2, 3, 4, 64), 7.0, device="cuda"), torch.full((2, 3, 4), 7.0, device="cuda"))
+    q = queries(rng, 2, 3, 4, 64, "f32")
+    R.paged_attention(q, cache, plan, out=out)
+    assert (out[0] == 7).all() and (out[1] == 7).all()
+
+
+def test_streams_and_graphs(R):
+    """Captured together and replayed on new lengths, with eager calls between; and on a stream of its own."""
+    import torch
+    rng = np.random.default_rng(12)
+    B, N, H, G, D, P = 6, 3, 2, 4, 128, 16
+    pages, width = 200, 40
+    cache = make_cache(R, rng, pages, P, H, D)
+    pool = R.new_page_pool(B + 1, width, pages, P, "cuda")
+    lengths, counts = ints([0] * (B + 1)), ints([0] * (B + 1))
+    kv = torch.from_numpy(rng.standard_normal((B, 2, N, H, D)).astype(np.float32)).cuda().bfloat16()
+    q = queries(rng, B, N, H * G, D, "bf16")
+    prefix = ints([B] * B)
+
+    def step(plan=None):
+        granted, slots = R.page_step(pool, lengths, N, counts=counts)
+        R.paged_append(cache, kv[:, 0], kv[:, 1], slots[:B])
+        plan = R.paged_plan(cache, pool.tables, lengths, N, H * G, B=B, counts=granted[:B], prefix_row=prefix, out=plan)
+        return (granted, slots, *R.paged_attention(q, cache, plan)), plan
+
+    def reset(seed):
+        g = np.random.default_rng(seed)
+        new = R.new_page_pool(B + 1, width, pages, P, "cuda")
+        for to, src in ((pool.tables, new.tables), (pool.held, new.held), (pool.ring, new.ring), (pool.state, new.state)):
+            to.copy_(src)
+        lens = g.integers(0, 130, B + 1)
+        R.page_step(pool, ints([0] * (B + 1)), 300, counts=ints(lens))       # room for what is committed
+        lengths.copy_(ints(lens))
+        counts.copy_(ints(g.integers(0, N + 1, B + 1)))
+        torch.cuda.synchronize()
+
+    side = torch.cuda.Stream()
+    reset(0)
+    with torch.cuda.stream(side):
+        _, plan = step()
+    side.synchronize()
+    reset(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = step(plan)
+    for seed in range(1, 4):
+        reset(seed)
+        eager = [t.clone() for t in step()[0]]
+        reset(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
+        reset(seed)
+        with torch.cuda.stream(side):
+            other = step()[0]
+        side.synchronize()
+        for a, b in zip(other, eager):
+            assert torch.equal(a, b)
+
+
+def test_a_speculative_run(R):
+    """Prompts into the pages, drafts behind them, verification, accepted rows in place, and log probabilities: three
+    steps against attention over each sequence's own rows kept apart."""
+    import torch
+    rng = np.random.default_rng(21)
+    B, N, H, G, D, P, V = 3, 7, 2, 2, 64, 16, 1000
+    T, width, pages = B + 1, 8, 40
+    cache = make_cache(R, rng, pages, P, H, D, fill=0x7fc0)   # NaN where nothing was written
+    pool = R.new_page_pool(T, width, pages, P, "cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")      # noqa: E731
+    kept = [[[], []] for _ in range(T)]                       # K and V rows of every table row, as they should be
+
+    lengths, counts = ints([0] * T), [30, 1, 17, 45]
+    granted, slots = R.page_step(pool, lengths, 45, counts=ints(counts))
+    k, v = rand(T, 45, H, D), rand(T, 45, H, D)
+    R.paged_append(cache, k, v, slots)
+    for t in range(T):
+        kept[t][0].append(k[t, :counts[t]])
+        kept[t][1].append(v[t, :counts[t]])
+    lengths = ints(counts)
+    prefix = ints([B, B, B])
+    parents = [-1, 0, 0, 1, 1, 2, 3]
+    mask = np.zeros((N, N), np.uint8)
+    for n in range(N):
+        mask[n, n] = 1
+        if n:
+            mask[n] |= mask[parents[n]]
+    for step in range(3):
+        granted, slots = R.page_step(pool, lengths, N, counts=ints([N] * B + [0]))
+        assert granted.tolist() == [N] * B + [0]
+        plan = R.paged_plan(cache, pool.tables, lengths, N, H * G, B=B, counts=granted[:B], prefix_row=prefix)
+        k, v, q = rand(B, N, H, D), rand(B, N, H, D), rand(B, N, H * G, D)
+        R.paged_append(cache, k, v, slots[:B])
+        out, lse = R.paged_attention(q, cache, plan, mask=dev(mask))
+        for b in range(B):
+            K, W = (torch.cat(kept[B][i] + kept[b][i] + [x[b]]).bfloat16().double() for i, x in ((0, k), (1, v)))
+            s = torch.stack([q[b, :, hq].double() @ K[:, hq // G].T for hq in range(H * G)]) / D ** 0.5
+            s[:, :, -N:].masked_fill_(dev(mask) == 0, float("-inf"))
+            want = torch.stack([s[hq].softmax(-1) @ W[:, hq // G] for hq in range(H * G)], 1)
+            assert (out[b] - want).abs().max() < 1e-4 and (lse[b] - s.logsumexp(-1).T).abs().max() < 1e-4
+        logits = 2 * rand(B, N, V)
+        nodes = logits.argmax(-1).to(torch.int32)[:, [0 if p < 0 else p for p in parents]]
+        nodes[:, 2] = 3                                       # some nodes are wrong
+        nodes[1, 1] = 5
+        path, tokens, alen = R.verify_tree_greedy(logits, nodes, parents)
+        R.paged_append(cache, k, v, slots[:B], path=path, accept_len=alen)
+        r = R.token_logprobs(logits.gather(1, path.clamp(min=0).long().unsqueeze(-1).expand(-1, -1, V)), tokens, top_n=1)
+        for b in range(B):
+            d = int(alen[b])
+            at = path[b, :d + 1].long()
+            kept[b][0].append(k[b, at])
+            kept[b][1].append(v[b, at])
+            rows = logits[b, at].double().log_softmax(-1)
+            want = rows.gather(1, tokens[b, :d + 1].long().view(-1, 1)).view(-1)
+            assert (r.logprobs[b, :d + 1] - want).abs().max() < 1e-5 and (r.logprobs[b, d + 1:] == 0).all()
+            assert torch.equal(r.top_tokens[b, :d + 1, 0], tokens[b, :d + 1])      # greedy: the likeliest
+        lengths = lengths + torch.cat((alen + 1, ints([0])))
+    assert alen.max() > 0
+    # one sequence ends, its pages are handed out again
+    lengths[1] = -1
+    free = int(pool.state[1])
+    granted, _ = R.page_step(pool, lengths, 1, counts=ints([0, 0, 0, 0]))
+    assert granted.tolist() == [0, 0, 0, 0] and pool.held[1] == 0 and int(pool.state[1]) > free
