@@ -5,15 +5,16 @@
 // P = exp2(c*(S - m)), O += P V_s, c = scale*log2(e); units of a plan
 // (paged_plan.hip) that belong together join at the end.
 //
-// A workgroup stages 64 keys of K and V in LDS and its four waves work on them: 32
-// query rows each, or (few rows) the same 32 rows, two waves a half of the keys
-// and of the values' elements each.  On 32x32x16 bf16 MFMAs in the transposed form,
-// S^T = K Q^T and O^T = V^T P^T, a lane has one query: lane (c, h), c = lane%32,
-// h = lane/32, ends up with scores of query c against keys 8a + 4h + i (a, i < 4),
-// and those, rounded to bf16, ARE the second product's operand when its
-// contraction runs over keys in that order.  V's operand wants four keys of one
-// element: the transposing LDS read gives them.  LDS rows are permuted in 16-byte
-// chunks so that neither read has bank conflicts.
+// A workgroup brings 32 keys of K and V at a time into one of several LDS buffers,
+// by loads that go there directly, a few tiles ahead of the one its four waves work
+// on: 32 query rows each, or (few rows) the same 32 rows, each wave a quarter of the
+// output's elements.  On 32x32x16 bf16 MFMAs in the transposed form, S^T = K Q^T
+// and O^T = V^T P^T, a lane has one query: lane (c, h), c = lane%32, h = lane/32,
+// ends up with scores of query c against keys 8a + 4h + i (a, i < 4), and those,
+// rounded to bf16, ARE the second product's operand when its contraction runs
+// over keys in that order.  V's operand wants four keys of one element: the
+// transposing LDS read gives them.  LDS rows are permuted in 16-byte chunks so that
+// neither read has bank conflicts.
 //
 // float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
 // queries P is the one bf16 of it, which is the output's own rounding.
@@ -26,7 +27,9 @@ namespace sv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHalf = 32;                               // keys a wave takes at a time
+constexpr int kWaves = kThreads / kWave;
+constexpr int kTileKeys = 32;                           // keys of a tile
+constexpr int kWindow = kWave;                          // 16-key groups whose pages a wave holds, one a lane
 constexpr float kSlack = 8.f;                           // powers of two a score may pass the running maximum by
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -57,10 +60,13 @@ template <int D> __device__ __forceinline__ constexpr int v_turn(int key) { retu
 template <int D> __device__ __forceinline__ constexpr int k_at(int key, int chunk) { return key * 2 * D + ((chunk ^ k_turn<D>(key)) << 4); }
 template <int D> __device__ __forceinline__ constexpr int v_at(int key, int chunk) { return key * 2 * D + ((chunk ^ v_turn<D>(key)) << 4); }
 
+// Tiles under way: as many as leave room for another workgroup on the compute unit.
+constexpr int stages(int D) { return D == 256 ? 4 : D == 128 ? 4 : 6; }
 template <int D> struct Lds {
-    unsigned char k[2][kPgTile * 2 * D];
-    unsigned char v[2][kPgTile * 2 * D];
-    unsigned odd[2][2];             // keys of a tile that are no numbers, as bits
+    unsigned char k[stages(D)][kTileKeys * 2 * D];
+    unsigned char v[stages(D)][kTileKeys * 2 * D];
+    int32_t page[2][kWindow];
+    unsigned odd;                   // keys of the tile that are no numbers, as bits
 };
 
 // Query row r of a unit's job: its batch row, token and head.
@@ -76,70 +82,119 @@ __device__ __forceinline__ QueryRow query_row(const PagedAttnArgs& a, int b0, in
     return q;
 }
 
-// A tile's keys on their way from global memory: the thread's chunks, chunk i of the thread in 16-key group group(i).
-template <int D> struct Stage {
-    static constexpr int kRow = D / 8;                  // chunks a row
-    static constexpr int kN = kPgTile * kRow / kThreads;
-    u32x4 k[kN], v[kN];
-    unsigned bad;                                       // groups whose page is none
+#if SV_KVQ_DEVICE
+// 16 (or 4) bytes a lane from base + offset to LDS at `to` + 16 (4) * lane.  As assembly, so that the compiler does not wait for
+// them at every read of LDS; the loads write no register.
+__device__ __forceinline__ void load_lds16(unsigned to, unsigned offset, unsigned long long base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds4(unsigned to, unsigned offset, unsigned long long base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+    return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)(p)));
+}
+#else
+__device__ __forceinline__ void load_lds16(unsigned, unsigned, unsigned long long) {}
+__device__ __forceinline__ void load_lds4(unsigned, unsigned, unsigned long long) {}
+template <int N> __device__ __forceinline__ void wait_loads() {}
+__device__ __forceinline__ void wait_lds() {}
+__device__ __forceinline__ void barrier() {}
+__device__ __forceinline__ unsigned lds_address(const void*) { return 0; }
+#endif
 
-    // keys first .. first+63 of those below `end`; the others repeat the last group
-    __device__ __forceinline__ void load(const PagedAttnArgs& a, const int32_t* table, int h, int first, int end) {
-        const int tid = threadIdx.x;
-        const int in = (tid / kRow) % 16, chunk = tid % kRow;
-        bad = 0;
-        long long base[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int key = min(first + 16 * j, (end - 1) & ~15);
-            int page = table[key >> a.c.page_log2];
-            if (page < 0 || page >= a.c.pages) {
-                page = 0;
-                bad |= 1u << j;
-            }
-            base[j] = page * a.c.page_stride + (key & ((1 << a.c.page_log2) - 1)) * a.c.slot_stride + h * a.c.head_stride;
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            // D = 128: chunk i is in group i; 64: in 2i, or 2i + 1 in the upper waves; 256: in i/2
-            const long long at = (D == 128   ? base[i % 4] + in * a.c.slot_stride
-                                  : D == 64  ? (wave_id() < 2 ? base[2 * i % 4] : base[(2 * i + 1) % 4]) + in * a.c.slot_stride
-                                             : base[i / 2 % 4] + ((tid / kRow) + 8 * (i & 1)) * a.c.slot_stride) + 8 * chunk;
-            k[i] = *reinterpret_cast<const u32x4*>(a.c.k + at);
-            v[i] = *reinterpret_cast<const u32x4*>(a.c.v + at);
-        }
-    }
-    __device__ __forceinline__ static int key(int i) { return threadIdx.x / kRow + kThreads / kRow * i; }
-    __device__ __forceinline__ void store(Lds<D>& l, int buf) const {
-        const int chunk = threadIdx.x % kRow;
+// Brings tiles of a unit's keys to LDS.  A wave's load is 1 KiB: kKeys keys; wave w has loads w*kN .. of a tile, which lie in
+// one of its two 16-key groups.  Groups past the end repeat the last one.
+template <int D> struct Loader {
+    static constexpr int kRow = D / 8, kKeys = kWave / kRow, kN = kTileKeys / kKeys / kWaves;
+    static constexpr int kLoads = 2 * kN;               // of a wave, a tile
+    const PagedAttnArgs& a;
+    const int32_t* table;
+    Lds<D>& lds;
+    int h, k0, end;
+    unsigned ko[kN], vo[kN];                            // the lane's offsets from its group's first row, bytes
+    int page;                                           // lane i: the page of group i of this window
+    unsigned long long bad;                             // groups of the window that have none
+
+    __device__ __forceinline__ Loader(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds)
+        : a(a), table(a.tables + u.table * a.table_stride), lds(lds), h(h), k0(u.k0), end(u.k1) {
+        const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            *reinterpret_cast<u32x4*>(l.k[buf] + k_at<D>(key(i), chunk)) = k[i];
-            *reinterpret_cast<u32x4*>(l.v[buf] + v_at<D>(key(i), chunk)) = v[i];
+            const int key = (wave * kN + i) * kKeys + lane / kRow, chunk = lane % kRow;
+            const unsigned row = static_cast<unsigned>(key & 15) * static_cast<unsigned>(a.c.slot_stride) * 2u;
+            ko[i] = row + ((chunk ^ k_turn<D>(key)) << 4);
+            vo[i] = row + ((chunk ^ v_turn<D>(key)) << 4);
         }
     }
-    // V's elements that are no numbers would reach queries that give their key no weight: they become zeros, and the key
-    // is noted, for the queries that see it.
-    __device__ __forceinline__ void clean(Lds<D>& l, int buf) {
-        if (threadIdx.x < 2) {
-            const unsigned b = bad >> (2 * threadIdx.x);
-            l.odd[buf][threadIdx.x] = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            unsigned any = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const unsigned w = v[i][e];
-                const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
-                any |= lo | hi;
-                v[i][e] = (lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u);
-            }
-            if (any) atomicOr(&l.odd[buf][key(i) / 32], 1u << (key(i) % 32));
-        }
+    __device__ __forceinline__ int last_group() const { return (end - 1) & ~15; }
+    // Entry of the table that lane's group of window w has.
+    __device__ __forceinline__ int entry(int w) const {
+        const int lane = threadIdx.x & (kWave - 1);
+        return min(k0 + 16 * (w * kWindow + lane), last_group()) >> a.c.page_log2;
     }
+    __device__ __forceinline__ void take(int p) {
+        const bool none = p < 0 || p >= a.c.pages;
+        bad = __ballot(none);
+        page = none ? 0 : p;
+    }
+    __device__ __forceinline__ void first_window() { take(table[entry(0)]); }
+    __device__ __forceinline__ void next_window(int w) { take(lds.page[w & 1][threadIdx.x & (kWave - 1)]); }
+    __device__ __forceinline__ void fetch_window(int w) const {         // one load of wave 0's
+        if (wave_id() == 0)
+            load_lds4(lds_address(lds.page[w & 1]), static_cast<unsigned>(entry(w)) * 4u, reinterpret_cast<unsigned long long>(table));
+    }
+    // Tile t to buffer `to`; its groups are in the window at hand.
+    __device__ __forceinline__ void load(int t, int to) const {
+        const int wave = wave_id();
+        const int group = 2 * t + (wave >= kWaves / 2 ? 1 : 0);
+        const int key = min(k0 + 16 * group, last_group());
+        const int pg = bcast(page, group & (kWindow - 1));
+        const long long row = pg * a.c.page_stride + (key & ((1 << a.c.page_log2) - 1)) * a.c.slot_stride + h * a.c.head_stride;
+        const unsigned long long kb = reinterpret_cast<unsigned long long>(a.c.k + row), vb = reinterpret_cast<unsigned long long>(a.c.v + row);
+        const unsigned at = wave * kN * 1024;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) load_lds16(lds_address(lds.k[to]) + at + 1024 * i, ko[i], kb);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) load_lds16(lds_address(lds.v[to]) + at + 1024 * i, vo[i], vb);
+    }
+    // Of tile t (in the window at hand): its groups without a page, as two bits.
+    __device__ __forceinline__ unsigned none(int t) const { return static_cast<unsigned>(bad >> (2 * t & (kWindow - 1))) & 3u; }
 };
+
+// V's elements that are no numbers would reach queries that give their key no weight: they become zeros, and the key is
+// noted, for the queries that see it.
+template <int D> __device__ __forceinline__ void clean(Lds<D>& lds, int buf, unsigned none) {
+    constexpr int kRow = D / 8;
+    if (threadIdx.x == 0) lds.odd = (none & 1 ? 0xffffu : 0u) | (none & 2 ? 0xffff0000u : 0u);
+    wait_lds();
+    barrier();
+    for (int i = threadIdx.x; i < kTileKeys * kRow; i += kThreads) {
+        u32x4* p = reinterpret_cast<u32x4*>(lds.v[buf]) + i;
+        u32x4 w = *p;
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned x = w[e];
+            const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+            any |= lo | hi;
+            w[e] = (lo ? 0u : x & 0xffffu) | (hi ? 0u : x & 0xffff0000u);
+        }
+        if (any) {
+            *p = w;
+            atomicOr(&lds.odd, 1u << (i / kRow));
+        }
+    }
+    wait_lds();
+    barrier();
+}
 
 template <int D, int NQ, int DT>
 __device__ __forceinline__ void load_query(const PagedRows& q, long long off, bool live, int h2, u32x4 (&out)[NQ][D / 16]) {
@@ -185,10 +240,9 @@ template <int D, int DT, int NT> struct Wave {
             for (int i = 0; i < 16; ++i) O[t][i] = 0.f;
     }
 
-    // One half tile: keys 32*kh .. of the staged ones, V's element tiles t0 ..; hide(S) for the tiles with keys that not
-    // every query sees.
+    // One tile, V's element tiles t0 ..; hide(S) for the tiles with keys that not every query sees.
     template <typename Hide>
-    __device__ __forceinline__ void step(const Lds<D>& lds, int buf, int kh, int t0, float cexp, float slack, bool edge, const Hide& hide) {
+    __device__ __forceinline__ void step(const Lds<D>& lds, int buf, int t0, float cexp, float slack, bool edge, const Hide& hide) {
         const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
         f32x16 S;
 #pragma unroll
@@ -196,18 +250,20 @@ template <int D, int DT, int NT> struct Wave {
         const unsigned char* kp = lds.k[buf];
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-            const u32x4 A = *reinterpret_cast<const u32x4*>(kp + k_at<D>(kh * kHalf + c, 2 * s + h2));
+            const u32x4 A = *reinterpret_cast<const u32x4*>(kp + k_at<D>(c, 2 * s + h2));
 #pragma unroll
             for (int p = 0; p < NQ; ++p) S = mfma32(A, Q[p][s], S);
         }
         if (edge) hide(S);
 
-        float mx = S[0];
+        float mx = S[0];                                // NaN propagates, and moves no maximum
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, S[i]);
+        for (int i = 1; i < 15; i += 2) mx = maximum3(mx, S[i], S[i + 1]);
+        mx = __builtin_elementwise_maximum(mx, S[15]);
         if (__ballot(mx > m + slack) != 0ull) {
-            mx = fmaxf(mx, xshfl(mx, 32));
-            const float mn = fmaxf(m, mx);
+            // each query by itself: what one sees moves no other's maximum
+            mx = __builtin_elementwise_maximum(mx, xshfl(mx, 32));
+            const float mn = mx > m + slack ? mx : m;
             const float al = m == -INFINITY ? 0.f : exp2_fast((m - mn) * cexp);
             l *= al;
 #pragma unroll
@@ -236,7 +292,7 @@ template <int D, int DT, int NT> struct Wave {
         }
 
         const unsigned char* vp = lds.v[buf];
-        const int key = kh * kHalf + 4 * h2 + (lane & 15) / 4;     // + 16s, + 8 more for the upper four
+        const int key = 4 * h2 + (lane & 15) / 4;       // + 16s, + 8 more for the upper four
         const int chunk = 2 * ((lane >> 4) & 1) + (lane & 3) / 2, at = 8 * (lane & 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -308,93 +364,74 @@ __device__ __forceinline__ void write_rows(const PagedAttnArgs& a, const PagedUn
         }
 }
 
-// One unit.  WIDE: wave w has query rows 32w .. of it; else all waves have the same 32, wave w keys 32*(w%2) .. of each tile
-// and half w/2 of the output's elements.
+// One unit.  WIDE: wave w has query rows 32w .. of it; else all waves have the same 32, and wave w a quarter of the output's
+// elements (D = 64: two waves a half).
 template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
-    constexpr int NT = WIDE ? D / 32 : D / 64;
+    constexpr int kStages = stages(D), kAhead = kStages - 1, kPer = kWindow / 2;    // kPer: tiles of a window of pages
+    constexpr int NT = WIDE ? D / 32 : D == 64 ? 1 : D / 128;
     const int wave = wave_id(), lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
-    const int r = u.row0 + (WIDE ? kHalf * wave : 0) + c, t0 = WIDE ? 0 : (wave >> 1) * NT;
+    const int r = u.row0 + (WIDE ? 32 * wave : 0) + c, t0 = WIDE ? 0 : wave * NT % (D / 32);
     const bool shared = u.table != u.b0 || u.cnt == 0;
     const bool there = r < u.rows;
     const QueryRow q = query_row(a, u.b0, there ? r : u.row0);
     const int tok = there && (shared || q.n < u.cnt) ? q.n : -1;
+    const int tiles = (u.k1 - u.k0 + kTileKeys - 1) / kTileKeys;
+
+    Loader<D> ld(a, u, h, lds);
+    if (tiles > 0) {
+        ld.first_window();
+        for (int t = 0; t < min(kAhead, tiles); ++t) ld.load(t, t);
+        if (tiles > kPer) ld.fetch_window(1);
+    }
     Wave<D, DT, NT> w;
     load_query<D, Wave<D, DT, NT>::NQ, DT>(a.q, q.b * a.q.batch + q.n * a.q.pos + (static_cast<long long>(h) * a.G + q.g) * a.q.head,
                                            there, h2, w.Q);
-    const bool working = WIDE ? u.row0 + kHalf * wave < u.rows : true;
+    const bool working = WIDE ? u.row0 + 32 * wave < u.rows : D > 64 || wave < 2;
     // slots below `seen` are seen by every query of the unit
     const int tok0 = u.row0 / a.G;
     const int seen = shared ? u.k1 : min(u.k1, a.mask ? u.pre : u.pre + tok0 + 1);
     unsigned long long tree = 0;
     if (!shared && a.mask && u.k1 > u.pre) tree = read_mask(a, q.b, tok, u.cnt);
     const float slack = fminf(kSlack / a.cexp, 1e30f);
-    const int32_t* table = a.tables + u.table * a.table_stride;
 
-    Stage<D> st;
-    const auto put = [&](int first, int buf) {          // what is staged for keys first .. to LDS
-        if (first + kPgTile > seen || st.bad) st.clean(lds, buf);
-        st.store(lds, buf);
-    };
-    bool odd_page = false;
-    if (u.k0 < u.k1) {
-        st.load(a, table, h, u.k0, u.k1);
-        odd_page = st.bad != 0;
-        put(u.k0, 0);
-    }
+    // The window of pages is that of the tile to be loaded; the tile worked on may lie in the one before.
+    unsigned long long bad = ld.bad, bad_before = 0;
     int buf = 0;
-    for (int kt = u.k0; kt < u.k1; kt += kPgTile, buf ^= 1) {
-        __syncthreads();
-        const bool edge = kt + kPgTile > seen || odd_page, more = kt + kPgTile < u.k1;
-        if (more) st.load(a, table, h, kt + kPgTile, u.k1);
-        if (working) {
-            const auto hide = [&](int kh) {
-                return [&, kh](f32x16& S) {
-                    const unsigned odd = lds.odd[buf][kh];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int in = 8 * (i / 4) + 4 * h2 + i % 4, key = kt + kHalf * kh + in, node = key - u.pre;
-                        const bool sees = key < u.k1 && (node < 0 || (a.mask ? node < 64 && ((tree >> (node & 63)) & 1ull) : node <= tok));
-                        S[i] = !sees ? -INFINITY : (odd >> in) & 1u ? __builtin_nanf("") : S[i];
-                    }
-                };
-            };
-            if (WIDE) {
-                w.step(lds, buf, 0, 0, a.cexp, slack, edge, hide(0));
-                w.step(lds, buf, 1, 0, a.cexp, slack, edge, hide(1));
-            } else {
-                const int kh = wave & 1;
-                w.step(lds, buf, kh, t0, a.cexp, slack, edge, hide(kh));
+    for (int t = 0; t < tiles; ++t) {
+        if (t + kAhead <= tiles) wait_loads<(kAhead - 1) * Loader<D>::kLoads>();
+        else wait_loads<0>();
+        barrier();
+        const int next = t + kAhead;
+        if (next < tiles) {
+            if (next % kPer == 0) {
+                ld.next_window(next / kPer);
+                bad_before = bad;
+                bad = ld.bad;
             }
+            ld.load(next, buf == 0 ? kStages - 1 : buf - 1);
+            // the next window's pages, long before they are wanted
+            if (next % kPer == 1 && next > kPer && next + kPer - 1 < tiles) ld.fetch_window(next / kPer + 1);
         }
-        if (more) {
-            odd_page = st.bad != 0;
-            put(kt + kPgTile, buf ^ 1);
+        const int first = u.k0 + t * kTileKeys;
+        const bool same = t / kPer == min(next, tiles - 1) / kPer;
+        const unsigned none = static_cast<unsigned>((same ? bad : bad_before) >> (2 * t & (kWindow - 1))) & 3u;
+        const bool edge = first + kTileKeys > seen || none != 0;
+        if (edge) clean<D>(lds, buf, none);
+        if (working) {
+            const auto hide = [&](f32x16& S) {
+                const unsigned odd = lds.odd;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int in = 8 * (i / 4) + 4 * h2 + i % 4, key = first + in, node = key - u.pre;
+                    const bool sees = key < u.k1 && (node < 0 || (a.mask ? node < 64 && ((tree >> (node & 63)) & 1ull) : node <= tok));
+                    S[i] = !sees ? -INFINITY : (odd >> in) & 1u ? __builtin_nanf("") : S[i];
+                }
+            };
+            w.step(lds, buf, t0, a.cexp, slack, edge, hide);
         }
+        buf = buf + 1 == kStages ? 0 : buf + 1;
     }
     w.l += xshfl(w.l, 32);
-    if (!WIDE) {
-        // join the two halves of the keys
-        __syncthreads();
-        f32x16(*const sh)[kWave] = reinterpret_cast<f32x16(*)[kWave]>(&lds);
-        float(*const ml)[kWave] = reinterpret_cast<float(*)[kWave]>(sh + 2 * NT);
-        if (wave & 1) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) sh[(wave >> 1) * NT + t][lane] = w.O[t];
-            ml[wave - 1][lane] = w.m;
-            ml[wave][lane] = w.l;
-        }
-        __syncthreads();
-        if (wave & 1) return;
-        const float om = ml[wave][lane], ol = ml[wave + 1][lane];
-        const float mn = fmaxf(w.m, om);
-        const float wa = w.m == -INFINITY ? 0.f : exp2_fast((w.m - mn) * a.cexp);
-        const float wb = om == -INFINITY ? 0.f : exp2_fast((om - mn) * a.cexp);
-        w.m = mn;
-        // a sum that is NaN stays NaN whatever its maximum
-        w.l = w.l * wa + ol * wb;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) w.O[t] = w.O[t] * wa + sh[(wave >> 1) * NT + t][lane] * wb;
-    }
     if (working) write_rows<D, DT, NT>(a, u, h, r, t0, t0 == 0, w.O, w.m, w.l, tok >= 0);
 }
 
