@@ -19,6 +19,8 @@
 // float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
 // queries P is the one bf16 of it, which is the output's own rounding.
 
+#include <type_traits>
+
 #include "kvq.hpp"
 #include "paged.hpp"
 
@@ -60,11 +62,10 @@ template <int D> __device__ __forceinline__ constexpr int v_turn(int key) { retu
 template <int D> __device__ __forceinline__ constexpr int k_at(int key, int chunk) { return key * 2 * D + ((chunk ^ k_turn<D>(key)) << 4); }
 template <int D> __device__ __forceinline__ constexpr int v_at(int key, int chunk) { return key * 2 * D + ((chunk ^ v_turn<D>(key)) << 4); }
 
-// Tiles under way: as many as leave room for another workgroup on the compute unit.
-constexpr int stages(int D) { return D == 256 ? 4 : D == 128 ? 4 : 6; }
+constexpr int kStages = 4;                              // tiles under way; a power of two, at most half a window
 template <int D> struct Lds {
-    unsigned char k[stages(D)][kTileKeys * 2 * D];
-    unsigned char v[stages(D)][kTileKeys * 2 * D];
+    unsigned char k[kStages][kTileKeys * 2 * D];
+    unsigned char v[kStages][kTileKeys * 2 * D];
     int32_t page[2][kWindow];
     unsigned odd;                   // keys of the tile that are no numbers, as bits
 };
@@ -120,12 +121,14 @@ template <int D> struct Loader {
     Lds<D>& lds;
     int h, k0, end;
     unsigned ko[kN], vo[kN];                            // the lane's offsets from its group's first row, bytes
-    int page;                                           // lane i: the page of group i of this window
-    unsigned long long bad;                             // groups of the window that have none
+    unsigned to;                                        // LDS address of the wave's loads in the first buffer of K
+    long long first;                                    // lane i: where group i of this window begins, bytes
+    unsigned long long bad;                             // groups of the window that have no page
 
     __device__ __forceinline__ Loader(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds)
         : a(a), table(a.tables + u.table * a.table_stride), lds(lds), h(h), k0(u.k0), end(u.k1) {
         const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+        to = lds_address(lds.k[0]) + wave * kN * 1024;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int key = (wave * kN + i) * kKeys + lane / kRow, chunk = lane % kRow;
@@ -135,38 +138,35 @@ template <int D> struct Loader {
         }
     }
     __device__ __forceinline__ int last_group() const { return (end - 1) & ~15; }
-    // Entry of the table that lane's group of window w has.
-    __device__ __forceinline__ int entry(int w) const {
-        const int lane = threadIdx.x & (kWave - 1);
-        return min(k0 + 16 * (w * kWindow + lane), last_group()) >> a.c.page_log2;
+    // First key of the lane's group of window w.
+    __device__ __forceinline__ int group_key(int w) const {
+        return min(k0 + 16 * (w * kWindow + static_cast<int>(threadIdx.x & (kWave - 1))), last_group());
     }
-    __device__ __forceinline__ void take(int p) {
-        const bool none = p < 0 || p >= a.c.pages;
+    __device__ __forceinline__ void take(int w, int page) {
+        const bool none = page < 0 || page >= a.c.pages;
         bad = __ballot(none);
-        page = none ? 0 : p;
+        first = 2 * ((none ? 0 : page) * a.c.page_stride + (group_key(w) & ((1 << a.c.page_log2) - 1)) * a.c.slot_stride +
+                     h * a.c.head_stride);
     }
-    __device__ __forceinline__ void first_window() { take(table[entry(0)]); }
-    __device__ __forceinline__ void next_window(int w) { take(lds.page[w & 1][threadIdx.x & (kWave - 1)]); }
+    __device__ __forceinline__ void first_window() { take(0, table[group_key(0) >> a.c.page_log2]); }
+    __device__ __forceinline__ void next_window(int w) { take(w, lds.page[w & 1][threadIdx.x & (kWave - 1)]); }
     __device__ __forceinline__ void fetch_window(int w) const {         // one load of wave 0's
         if (wave_id() == 0)
-            load_lds4(lds_address(lds.page[w & 1]), static_cast<unsigned>(entry(w)) * 4u, reinterpret_cast<unsigned long long>(table));
+            load_lds4(lds_address(lds.page[w & 1]), static_cast<unsigned>(group_key(w) >> a.c.page_log2) * 4u,
+                      reinterpret_cast<unsigned long long>(table));
     }
-    // Tile t to buffer `to`; its groups are in the window at hand.
-    __device__ __forceinline__ void load(int t, int to) const {
-        const int wave = wave_id();
-        const int group = 2 * t + (wave >= kWaves / 2 ? 1 : 0);
-        const int key = min(k0 + 16 * group, last_group());
-        const int pg = bcast(page, group & (kWindow - 1));
-        const long long row = pg * a.c.page_stride + (key & ((1 << a.c.page_log2) - 1)) * a.c.slot_stride + h * a.c.head_stride;
-        const unsigned long long kb = reinterpret_cast<unsigned long long>(a.c.k + row), vb = reinterpret_cast<unsigned long long>(a.c.v + row);
-        const unsigned at = wave * kN * 1024;
+    // Tile t to buffer `buf`; its groups are in the window at hand.
+    __device__ __forceinline__ void load(int t, int buf) const {
+        const int group = (2 * t + (wave_id() >= kWaves / 2 ? 1 : 0)) & (kWindow - 1);
+        const unsigned long long off = (static_cast<unsigned long long>(bcast(static_cast<int>(first >> 32), group)) << 32) |
+                                       static_cast<unsigned>(bcast(static_cast<int>(first), group));
+        const unsigned long long kb = reinterpret_cast<unsigned long long>(a.c.k) + off, vb = reinterpret_cast<unsigned long long>(a.c.v) + off;
+        const unsigned at = to + buf * (kTileKeys * 2 * D);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) load_lds16(lds_address(lds.k[to]) + at + 1024 * i, ko[i], kb);
+        for (int i = 0; i < kN; ++i) load_lds16(at + 1024 * i, ko[i], kb);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) load_lds16(lds_address(lds.v[to]) + at + 1024 * i, vo[i], vb);
+        for (int i = 0; i < kN; ++i) load_lds16(at + kStages * kTileKeys * 2 * D + 1024 * i, vo[i], vb);
     }
-    // Of tile t (in the window at hand): its groups without a page, as two bits.
-    __device__ __forceinline__ unsigned none(int t) const { return static_cast<unsigned>(bad >> (2 * t & (kWindow - 1))) & 3u; }
 };
 
 // V's elements that are no numbers would reach queries that give their key no weight: they become zeros, and the key is
@@ -227,33 +227,56 @@ __device__ __forceinline__ void load_query(const PagedRows& q, long long off, bo
     }
 }
 
-// A wave's 32 queries: Q, and the running maximum, sum and output (NT tiles of 32 elements of O^T).
+// A wave's 32 queries: Q, and the running maximum, sum and output (NT tiles of 32 elements of O^T, from tile t0 on).
 template <int D, int DT, int NT> struct Wave {
     static constexpr int NQ = DT == 1 ? 1 : 3;
+    // V's operands are read before the scores' products where there are registers to hold them.
+    static constexpr bool kEarlyV = D == 64 || (D == 128 && DT == 1);
     u32x4 Q[NQ][D / 16];
     f32x16 O[NT];
     float m, l;
-    __device__ __forceinline__ Wave() : m(-INFINITY), l(0.f) {
+    u32x4 K[D / 16];                                    // of the tile to come
+    u32x4 V[kEarlyV ? 2 : 1][NT];
+    unsigned ka, va;                                    // the lane's LDS offsets in a buffer of K and V
+    __device__ __forceinline__ explicit Wave(int t0) : m(-INFINITY), l(0.f) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) O[t][i] = 0.f;
+        const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
+        ka = k_at<D>(c, h2);
+        va = v_at<D>(4 * h2 + (lane & 15) / 4, 2 * ((lane >> 4) & 1) + (lane & 3) / 2 + 4 * t0) + 8 * (lane & 1);
+    }
+    // Chunks are turned by an exclusive or, so that of another chunk is one away: k_at(c, 2s + h2) = ka ^ 32s, and v_at with
+    // 4t more is va ^ 64t (t0 a multiple of NT, a power of two). Sixteen keys on is the same turn.
+    __device__ __forceinline__ void read_k(const Lds<D>& lds, int buf) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) K[s] = *reinterpret_cast<const u32x4*>(lds.k[buf] + (ka ^ (32 * s)));
+    }
+    __device__ __forceinline__ void read_v(const Lds<D>& lds, int buf, int s, u32x4 (&out)[NT]) const {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const unsigned char* p = lds.v[buf] + (va ^ (64 * t)) + 16 * s * 2 * D;
+            const u32x2 lo = read_transposed(p), hi = read_transposed(p + 8 * 2 * D);
+            out[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
     }
 
-    // One tile, V's element tiles t0 ..; hide(S) for the tiles with keys that not every query sees.
+    // The scores' half of a tile, from K: P, and the maximum and sums. hide(S) for tiles with keys that not every query sees.
     template <typename Hide>
-    __device__ __forceinline__ void step(const Lds<D>& lds, int buf, int t0, float cexp, float slack, bool edge, const Hide& hide) {
-        const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
+    __device__ __forceinline__ void weigh(const Lds<D>& lds, int buf, float cexp, float slack, bool edge, const Hide& hide,
+                                          u32x4 (&P)[NQ][2]) {
+        if (kEarlyV) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) read_v(lds, buf, s, V[s % (kEarlyV ? 2 : 1)]);
+        }
         f32x16 S;
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[i] = 0.f;
-        const unsigned char* kp = lds.k[buf];
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-            const u32x4 A = *reinterpret_cast<const u32x4*>(kp + k_at<D>(c, 2 * s + h2));
+        for (int s = 0; s < D / 16; ++s)
 #pragma unroll
-            for (int p = 0; p < NQ; ++p) S = mfma32(A, Q[p][s], S);
-        }
+            for (int p = 0; p < NQ; ++p) S = mfma32(K[s], Q[p][s], S);
         if (edge) hide(S);
 
         float mx = S[0];                                // NaN propagates, and moves no maximum
@@ -271,7 +294,6 @@ template <int D, int DT, int NT> struct Wave {
             m = mn;
         }
         const float mc = m == -INFINITY ? 0.f : m * cexp;
-        u32x4 P[NQ][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float p[8];
@@ -290,20 +312,16 @@ template <int D, int DT, int NT> struct Wave {
                 }
             }
         }
-
-        const unsigned char* vp = lds.v[buf];
-        const int key = 4 * h2 + (lane & 15) / 4;       // + 16s, + 8 more for the upper four
-        const int chunk = 2 * ((lane >> 4) & 1) + (lane & 3) / 2, at = 8 * (lane & 1);
+    }
+    // The values' half. V's operands are in registers, or still in the buffer.
+    __device__ __forceinline__ void add(const Lds<D>& lds, int buf, const u32x4 (&P)[NQ][2]) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
+            if (!kEarlyV) read_v(lds, buf, s, V[0]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const u32x2 lo = read_transposed(vp + v_at<D>(key + 16 * s, chunk + 4 * (t0 + t)) + at);
-                const u32x2 hi = read_transposed(vp + v_at<D>(key + 16 * s + 8, chunk + 4 * (t0 + t)) + at);
-                const u32x4 A = {lo[0], lo[1], hi[0], hi[1]};
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) O[t] = mfma32(A, P[x][s], O[t]);
-            }
+                for (int x = 0; x < NQ; ++x) O[t] = mfma32(V[kEarlyV ? s : 0][t], P[x][s], O[t]);
         }
     }
 };
@@ -366,9 +384,14 @@ __device__ __forceinline__ void write_rows(const PagedAttnArgs& a, const PagedUn
 
 // One unit.  WIDE: wave w has query rows 32w .. of it; else all waves have the same 32, and wave w a quarter of the output's
 // elements (D = 64: two waves a half).
+//
+// An iteration: V's operands of its tile are read and the scores formed from K's, read before; then the next tile has
+// arrived, this one's buffer takes the tile four further on, K's operands of the next are read, and the output follows.
 template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
-    constexpr int kStages = stages(D), kAhead = kStages - 1, kPer = kWindow / 2;    // kPer: tiles of a window of pages
+    constexpr int kPer = kWindow / 2;                   // tiles of a window of pages
     constexpr int NT = WIDE ? D / 32 : D == 64 ? 1 : D / 128;
+    constexpr int kLoads = Loader<D>::kLoads;
+    using W = Wave<D, DT, NT>;
     const int wave = wave_id(), lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
     const int r = u.row0 + (WIDE ? 32 * wave : 0) + c, t0 = WIDE ? 0 : wave * NT % (D / 32);
     const bool shared = u.table != u.b0 || u.cnt == 0;
@@ -378,14 +401,9 @@ template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const
     const int tiles = (u.k1 - u.k0 + kTileKeys - 1) / kTileKeys;
 
     Loader<D> ld(a, u, h, lds);
-    if (tiles > 0) {
-        ld.first_window();
-        for (int t = 0; t < min(kAhead, tiles); ++t) ld.load(t, t);
-        if (tiles > kPer) ld.fetch_window(1);
-    }
-    Wave<D, DT, NT> w;
-    load_query<D, Wave<D, DT, NT>::NQ, DT>(a.q, q.b * a.q.batch + q.n * a.q.pos + (static_cast<long long>(h) * a.G + q.g) * a.q.head,
-                                           there, h2, w.Q);
+    if (tiles > 0) ld.first_window();
+    W w(t0);
+    load_query<D, W::NQ, DT>(a.q, q.b * a.q.batch + q.n * a.q.pos + (static_cast<long long>(h) * a.G + q.g) * a.q.head, there, h2, w.Q);
     const bool working = WIDE ? u.row0 + 32 * wave < u.rows : D > 64 || wave < 2;
     // slots below `seen` are seen by every query of the unit
     const int tok0 = u.row0 / a.G;
@@ -393,31 +411,25 @@ template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const
     unsigned long long tree = 0;
     if (!shared && a.mask && u.k1 > u.pre) tree = read_mask(a, q.b, tok, u.cnt);
     const float slack = fminf(kSlack / a.cexp, 1e30f);
-
     // The window of pages is that of the tile to be loaded; the tile worked on may lie in the one before.
-    unsigned long long bad = ld.bad, bad_before = 0;
-    int buf = 0;
-    for (int t = 0; t < tiles; ++t) {
-        if (t + kAhead <= tiles) wait_loads<(kAhead - 1) * Loader<D>::kLoads>();
-        else wait_loads<0>();
-        barrier();
-        const int next = t + kAhead;
-        if (next < tiles) {
-            if (next % kPer == 0) {
-                ld.next_window(next / kPer);
-                bad_before = bad;
-                bad = ld.bad;
-            }
-            ld.load(next, buf == 0 ? kStages - 1 : buf - 1);
-            // the next window's pages, long before they are wanted
-            if (next % kPer == 1 && next > kPer && next + kPer - 1 < tiles) ld.fetch_window(next / kPer + 1);
-        }
-        const int first = u.k0 + t * kTileKeys;
-        const bool same = t / kPer == min(next, tiles - 1) / kPer;
-        const unsigned none = static_cast<unsigned>((same ? bad : bad_before) >> (2 * t & (kWindow - 1))) & 3u;
-        const bool edge = first + kTileKeys > seen || none != 0;
+    unsigned long long bad = tiles > 0 ? ld.bad : 0, bad_before = 0;
+
+    for (int t = 0; t < min(kStages, tiles); ++t) ld.load(t, t);
+    if (tiles > kPer) ld.fetch_window(1);
+#pragma unroll
+    for (int p = 0; p < W::NQ; ++p)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(w.Q[p][i]));    // they are there: no wait for them in the loop
+    wait_loads<0>();
+    barrier();
+    if (tiles > 0 && working) w.read_k(lds, 0);
+
+    const auto iterate = [&](auto buffer, int t, bool edge, unsigned none) {
+        const int buf = buffer;
         if (edge) clean<D>(lds, buf, none);
+        u32x4 P[W::NQ][2];
         if (working) {
+            const int first = u.k0 + t * kTileKeys;
             const auto hide = [&](f32x16& S) {
                 const unsigned odd = lds.odd;
 #pragma unroll
@@ -427,9 +439,42 @@ template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const
                     S[i] = !sees ? -INFINITY : (odd >> in) & 1u ? __builtin_nanf("") : S[i];
                 }
             };
-            w.step(lds, buf, t0, a.cexp, slack, edge, hide);
+            w.weigh(lds, buf, a.cexp, slack, edge, hide, P);
+            if (!W::kEarlyV) w.add(lds, buf, P);
         }
-        buf = buf + 1 == kStages ? 0 : buf + 1;
+        if (t + kStages <= tiles) wait_loads<(kStages - 2) * kLoads>();
+        else wait_loads<0>();
+        wait_lds();                                     // this wave has read all it wants of the buffer
+        barrier();
+        const int next = t + kStages;
+        if (next < tiles) {
+            if (next % kPer == 0) {
+                ld.next_window(next / kPer);
+                bad_before = bad;
+                bad = ld.bad;
+            }
+            ld.load(next, buf);
+            // the next window's pages, long before they are wanted
+            if (next % kPer == 1 && next > kPer && next + kPer - 1 < tiles) ld.fetch_window(next / kPer + 1);
+        }
+        if (working) {
+            if (t + 1 < tiles) w.read_k(lds, (buf + 1) % kStages);
+            if (W::kEarlyV) w.add(lds, buf, P);
+        }
+    };
+    int t = 0;
+    // four at a time, their buffers known, while every query sees every key
+    const int whole = max(0, seen - u.k0) / kTileKeys;
+    for (; t + kStages <= whole && (bad | bad_before) == 0; t += kStages) {
+        iterate(std::integral_constant<int, 0>(), t, false, 0u);
+        iterate(std::integral_constant<int, 1>(), t + 1, false, 0u);
+        iterate(std::integral_constant<int, 2>(), t + 2, false, 0u);
+        iterate(std::integral_constant<int, 3>(), t + 3, false, 0u);
+    }
+    for (; t < tiles; ++t) {
+        const bool same = t / kPer == min(t + kStages - 1, tiles - 1) / kPer;     // the last tile loaded is in the window at hand
+        const unsigned none = static_cast<unsigned>((same ? bad : bad_before) >> (2 * t & (kWindow - 1))) & 3u;
+        iterate(t % kStages, t, t >= whole || none != 0, none);
     }
     w.l += xshfl(w.l, 32);
     if (working) write_rows<D, DT, NT>(a, u, h, r, t0, t0 == 0, w.O, w.m, w.l, tok >= 0);
