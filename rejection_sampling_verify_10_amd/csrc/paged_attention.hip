@@ -5,19 +5,21 @@
 // P = exp2(c*(S - m)), O += P V_s, c = scale*log2(e); units of a plan
 // (paged_plan.hip) that belong together join at the end.
 //
-// A workgroup brings 32 keys of K and V at a time into one of several LDS buffers,
-// by loads that go there directly, a few tiles ahead of the one its four waves work
-// on: 32 query rows each, or (few rows) the same 32 rows, each wave a quarter of the
-// output's elements.  On 32x32x16 bf16 MFMAs in the transposed form, S^T = K Q^T
-// and O^T = V^T P^T, a lane has one query: lane (c, h), c = lane%32, h = lane/32,
-// ends up with scores of query c against keys 8a + 4h + i (a, i < 4), and those,
-// rounded to bf16, ARE the second product's operand when its contraction runs
-// over keys in that order.  V's operand wants four keys of one element: the
-// transposing LDS read gives them.  LDS rows are permuted in 16-byte chunks so that
-// neither read has bank conflicts.
+// K and V come to LDS in tiles of 32 keys, by loads that go there directly.  A unit
+// of up to 128 query rows: its four waves have 32 rows each and share the tiles,
+// which are brought four ahead.  One of up to 32: its waves have the same rows and
+// every fourth tile each, all by themselves, and join at the end.  On 32x32x16 bf16
+// MFMAs in the transposed form, S^T = K Q^T and O^T = V^T P^T, a lane has one query:
+// lane (c, h), c = lane%32, h = lane/32, ends up with scores of query c against keys
+// 8a + 4h + i (a, i < 4), and those, rounded to bf16, ARE the second product's
+// operand when its contraction runs over keys in that order.  V's operand wants
+// four keys of one element: the transposing LDS read gives them.  LDS rows are
+// permuted in 16-byte chunks so that neither read has bank conflicts.
 //
 // float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
 // queries P is the one bf16 of it, which is the output's own rounding.
+
+#include <stddef.h>
 
 #include <type_traits>
 
@@ -66,8 +68,8 @@ constexpr int kStages = 4;                              // tiles under way; a po
 template <int D> struct Lds {
     unsigned char k[kStages][kTileKeys * 2 * D];
     unsigned char v[kStages][kTileKeys * 2 * D];
-    int32_t page[2][kWindow];
-    unsigned odd;                   // keys of the tile that are no numbers, as bits
+    int32_t page[kWaves][kWindow];
+    float ml[kWaves][2][kWave];
 };
 
 // Query row r of a unit's job: its batch row, token and head.
@@ -111,27 +113,29 @@ __device__ __forceinline__ void barrier() {}
 __device__ __forceinline__ unsigned lds_address(const void*) { return 0; }
 #endif
 
-// Brings tiles of a unit's keys to LDS.  A wave's load is 1 KiB: kKeys keys; wave w has loads w*kN .. of a tile, which lie in
-// one of its two 16-key groups.  Groups past the end repeat the last one.
-template <int D> struct Loader {
-    static constexpr int kRow = D / 8, kKeys = kWave / kRow, kN = kTileKeys / kKeys / kWaves;
-    static constexpr int kLoads = 2 * kN;               // of a wave, a tile
+// Brings tiles of a unit's keys to LDS. A load of a wave is 1 KiB: kKeys keys. Four waves share a tile's loads (each has some of
+// one of its two 16-key groups), or a wave makes them all (ALONE), to the buffer of its number. Groups past the end repeat
+// the last one. The pages of 64 groups, a window, are held one a lane.
+template <int D, bool ALONE> struct Loader {
+    static constexpr int kRow = D / 8, kKeys = kWave / kRow;
+    static constexpr int kN = ALONE ? 16 / kKeys : kTileKeys / kKeys / kWaves;      // loads of a group
+    static constexpr int kLoads = 2 * kN;               // of K and V, a tile (not ALONE)
     const PagedAttnArgs& a;
     const int32_t* table;
     Lds<D>& lds;
     int h, k0, end;
     unsigned ko[kN], vo[kN];                            // the lane's offsets from its group's first row, bytes
-    unsigned to;                                        // LDS address of the wave's loads in the first buffer of K
+    unsigned to;                                        // LDS address of the wave's loads in the first buffer of K (ALONE: in its own)
     long long first;                                    // lane i: where group i of this window begins, bytes
     unsigned long long bad;                             // groups of the window that have no page
 
     __device__ __forceinline__ Loader(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds)
         : a(a), table(a.tables + u.table * a.table_stride), lds(lds), h(h), k0(u.k0), end(u.k1) {
         const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
-        to = lds_address(lds.k[0]) + wave * kN * 1024;
+        to = ALONE ? lds_address(lds.k[wave]) : lds_address(lds.k[0]) + wave * kN * 1024;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int key = (wave * kN + i) * kKeys + lane / kRow, chunk = lane % kRow;
+            const int key = ((ALONE ? 0 : wave * kN) + i) * kKeys + lane / kRow, chunk = lane % kRow;
             const unsigned row = static_cast<unsigned>(key & 15) * static_cast<unsigned>(a.c.slot_stride) * 2u;
             ko[i] = row + ((chunk ^ k_turn<D>(key)) << 4);
             vo[i] = row + ((chunk ^ v_turn<D>(key)) << 4);
@@ -149,52 +153,40 @@ template <int D> struct Loader {
                      h * a.c.head_stride);
     }
     __device__ __forceinline__ void first_window() { take(0, table[group_key(0) >> a.c.page_log2]); }
-    __device__ __forceinline__ void next_window(int w) { take(w, lds.page[w & 1][threadIdx.x & (kWave - 1)]); }
-    __device__ __forceinline__ void fetch_window(int w) const {         // one load of wave 0's
-        if (wave_id() == 0)
-            load_lds4(lds_address(lds.page[w & 1]), static_cast<unsigned>(group_key(w) >> a.c.page_log2) * 4u,
+    __device__ __forceinline__ int32_t* slot(int w) const { return lds.page[ALONE ? wave_id() : w & 1]; }
+    __device__ __forceinline__ void next_window(int w) { take(w, slot(w)[threadIdx.x & (kWave - 1)]); }
+    __device__ __forceinline__ void fetch_window(int w) const {         // one load of the wave's (or of the first one's)
+        if (ALONE || wave_id() == 0)
+            load_lds4(lds_address(slot(w)), static_cast<unsigned>(group_key(w) >> a.c.page_log2) * 4u,
                       reinterpret_cast<unsigned long long>(table));
     }
-    // Tile t to buffer `buf`; its groups are in the window at hand.
+    // Where a group of the window at hand begins in the pages, bytes.
+    __device__ __forceinline__ unsigned long long where(int group) const {
+        return (static_cast<unsigned long long>(bcast(static_cast<int>(first >> 32), group & (kWindow - 1))) << 32) |
+               static_cast<unsigned>(bcast(static_cast<int>(first), group & (kWindow - 1)));
+    }
+    __device__ __forceinline__ void load_group(const uint16_t* pages, unsigned long long off, unsigned at, const unsigned (&o)[kN]) const {
+        const unsigned long long base = reinterpret_cast<unsigned long long>(pages) + off;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) load_lds16(at + 1024 * i, o[i], base);
+    }
+    static constexpr unsigned kV = kStages * kTileKeys * 2 * D;         // from K's buffers to V's
+    // Tile t, whose groups are in the window at hand, to buffer `buf` (not ALONE).
     __device__ __forceinline__ void load(int t, int buf) const {
-        const int group = (2 * t + (wave_id() >= kWaves / 2 ? 1 : 0)) & (kWindow - 1);
-        const unsigned long long off = (static_cast<unsigned long long>(bcast(static_cast<int>(first >> 32), group)) << 32) |
-                                       static_cast<unsigned>(bcast(static_cast<int>(first), group));
-        const unsigned long long kb = reinterpret_cast<unsigned long long>(a.c.k) + off, vb = reinterpret_cast<unsigned long long>(a.c.v) + off;
-        const unsigned at = to + buf * (kTileKeys * 2 * D);
+        const unsigned long long off = where(2 * t + (wave_id() >= kWaves / 2 ? 1 : 0));
+        load_group(a.c.k, off, to + buf * (kTileKeys * 2 * D), ko);
+        load_group(a.c.v, off, to + buf * (kTileKeys * 2 * D) + kV, vo);
+    }
+    // ALONE: K's half of it and V's.
+    __device__ __forceinline__ void load_k(int t) const {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) load_lds16(at + 1024 * i, ko[i], kb);
+        for (int g = 0; g < 2; ++g) load_group(a.c.k, where(2 * t + g), to + g * 1024 * kN, ko);
+    }
+    __device__ __forceinline__ void load_v(int t) const {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) load_lds16(at + kStages * kTileKeys * 2 * D + 1024 * i, vo[i], vb);
+        for (int g = 0; g < 2; ++g) load_group(a.c.v, where(2 * t + g), to + kV + g * 1024 * kN, vo);
     }
 };
-
-// V's elements that are no numbers would reach queries that give their key no weight: they become zeros, and the key is
-// noted, for the queries that see it.
-template <int D> __device__ __forceinline__ void clean(Lds<D>& lds, int buf, unsigned none) {
-    constexpr int kRow = D / 8;
-    if (threadIdx.x == 0) lds.odd = (none & 1 ? 0xffffu : 0u) | (none & 2 ? 0xffff0000u : 0u);
-    wait_lds();
-    barrier();
-    for (int i = threadIdx.x; i < kTileKeys * kRow; i += kThreads) {
-        u32x4* p = reinterpret_cast<u32x4*>(lds.v[buf]) + i;
-        u32x4 w = *p;
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned x = w[e];
-            const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
-            any |= lo | hi;
-            w[e] = (lo ? 0u : x & 0xffffu) | (hi ? 0u : x & 0xffff0000u);
-        }
-        if (any) {
-            *p = w;
-            atomicOr(&lds.odd, 1u << (i / kRow));
-        }
-    }
-    wait_lds();
-    barrier();
-}
 
 template <int D, int NQ, int DT>
 __device__ __forceinline__ void load_query(const PagedRows& q, long long off, bool live, int h2, u32x4 (&out)[NQ][D / 16]) {
@@ -227,8 +219,9 @@ __device__ __forceinline__ void load_query(const PagedRows& q, long long off, bo
     }
 }
 
-// A wave's 32 queries: Q, and the running maximum, sum and output (NT tiles of 32 elements of O^T, from tile t0 on).
-template <int D, int DT, int NT> struct Wave {
+// A wave's 32 queries: Q, and the running maximum, sum and output (NT tiles of 32 elements of O^T).
+template <int D, int DT> struct Wave {
+    static constexpr int NT = D / 32;
     static constexpr int NQ = DT == 1 ? 1 : 3;
     // V's operands are read before the scores' products where there are registers to hold them.
     static constexpr bool kEarlyV = D == 64 || (D == 128 && DT == 1);
@@ -238,17 +231,17 @@ template <int D, int DT, int NT> struct Wave {
     u32x4 K[D / 16];                                    // of the tile to come
     u32x4 V[kEarlyV ? 2 : 1][NT];
     unsigned ka, va;                                    // the lane's LDS offsets in a buffer of K and V
-    __device__ __forceinline__ explicit Wave(int t0) : m(-INFINITY), l(0.f) {
+    __device__ __forceinline__ Wave() : m(-INFINITY), l(0.f) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) O[t][i] = 0.f;
         const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
         ka = k_at<D>(c, h2);
-        va = v_at<D>(4 * h2 + (lane & 15) / 4, 2 * ((lane >> 4) & 1) + (lane & 3) / 2 + 4 * t0) + 8 * (lane & 1);
+        va = v_at<D>(4 * h2 + (lane & 15) / 4, 2 * ((lane >> 4) & 1) + (lane & 3) / 2) + 8 * (lane & 1);
     }
     // Chunks are turned by an exclusive or, so that of another chunk is one away: k_at(c, 2s + h2) = ka ^ 32s, and v_at with
-    // 4t more is va ^ 64t (t0 a multiple of NT, a power of two). Sixteen keys on is the same turn.
+    // chunks 4t more is va ^ 64t. Eight keys on is the same turn.
     __device__ __forceinline__ void read_k(const Lds<D>& lds, int buf) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) K[s] = *reinterpret_cast<const u32x4*>(lds.k[buf] + (ka ^ (32 * s)));
@@ -262,23 +255,53 @@ template <int D, int DT, int NT> struct Wave {
         }
     }
 
-    // The scores' half of a tile, from K: P, and the maximum and sums. hide(S) for tiles with keys that not every query sees.
-    template <typename Hide>
-    __device__ __forceinline__ void weigh(const Lds<D>& lds, int buf, float cexp, float slack, bool edge, const Hide& hide,
-                                          u32x4 (&P)[NQ][2]) {
-        if (kEarlyV) {
+    __device__ __forceinline__ void read_v(const Lds<D>& lds, int buf) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) read_v(lds, buf, s, V[s % (kEarlyV ? 2 : 1)]);
+        for (int s = 0; s < 2; ++s) read_v(lds, buf, s, V[kEarlyV ? s : 0]);
+    }
+    __device__ __forceinline__ f32x16 scores() const {  // of K's tile
+        f32x16 s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) s = mfma32(K[i], Q[p][i], s);
+        return s;
+    }
+    // V's elements that are no numbers would reach queries that give their key no weight: they become zeros in an operand,
+    // and the keys they belong to come back as bits.
+    __device__ __forceinline__ static unsigned clean(u32x4& w) {
+        unsigned odd = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool lo = (w[e] & 0x7f80u) == 0x7f80u, hi = (w[e] & 0x7f800000u) == 0x7f800000u;
+            odd |= (lo ? 1u : 0u) << (2 * e) | (hi ? 2u : 0u) << (2 * e);
+            w[e] = (lo ? 0u : w[e] & 0xffffu) | (hi ? 0u : w[e] & 0xffff0000u);
         }
-        f32x16 S;
+        return odd;
+    }
+    // The keys of the lane's scores, as bits, that are no numbers: V's elements of them (cleaned, where they are held), and
+    // those of groups without a page.
+    __device__ __forceinline__ unsigned odd_keys(const Lds<D>& lds, int buf, unsigned none) {
+        const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
+        unsigned odd = (none & 1 ? 0xffu : 0u) | (none & 2 ? 0xff00u : 0u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[i] = 0.f;
+        for (int s = 0; s < 2; ++s) {
+            if (!kEarlyV) read_v(lds, buf, s, V[0]);
+            unsigned any = 0;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
+            for (int t = 0; t < NT; ++t) any |= clean(V[kEarlyV ? s : 0][t]);
 #pragma unroll
-            for (int p = 0; p < NQ; ++p) S = mfma32(K[s], Q[p][s], S);
-        if (edge) hide(S);
-
+            for (int j = 0; j < 8; ++j) {
+                const unsigned long long all = __ballot((any >> j) & 1u);
+                odd |= (static_cast<unsigned>(h2 ? all >> 32 : all) ? 1u : 0u) << (8 * s + j);
+            }
+        }
+        return odd;
+    }
+    // P of a tile's scores, and the maximum and sums.
+    __device__ __forceinline__ void weigh(const f32x16& S, float cexp, float slack, u32x4 (&P)[NQ][2]) {
         float mx = S[0];                                // NaN propagates, and moves no maximum
 #pragma unroll
         for (int i = 1; i < 15; i += 2) mx = maximum3(mx, S[i], S[i + 1]);
@@ -313,11 +336,17 @@ template <int D, int DT, int NT> struct Wave {
             }
         }
     }
-    // The values' half. V's operands are in registers, or still in the buffer.
-    __device__ __forceinline__ void add(const Lds<D>& lds, int buf, const u32x4 (&P)[NQ][2]) {
+    // O += V P. V's operands are in registers, or still in the buffer (and perhaps to be cleaned).
+    __device__ __forceinline__ void add(const Lds<D>& lds, int buf, const u32x4 (&P)[NQ][2], bool edge) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            if (!kEarlyV) read_v(lds, buf, s, V[0]);
+            if (!kEarlyV) {
+                read_v(lds, buf, s, V[0]);
+                if (edge) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) clean(V[0][t]);
+                }
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -382,67 +411,86 @@ __device__ __forceinline__ void write_rows(const PagedAttnArgs& a, const PagedUn
         }
 }
 
-// One unit.  WIDE: wave w has query rows 32w .. of it; else all waves have the same 32, and wave w a quarter of the output's
-// elements (D = 64: two waves a half).
+// What the query of a lane sees: its token (-1: none there) and, in a tree, the new tokens as bits.
+struct Sight {
+    const PagedAttnArgs& a;
+    const PagedUnit& u;
+    int tok, seen;                  // slots below `seen` are seen by every query of the unit
+    bool shared;
+    unsigned long long tree;
+    __device__ __forceinline__ Sight(const PagedAttnArgs& a, const PagedUnit& u, const QueryRow& q, bool there) : a(a), u(u) {
+        shared = u.table != u.b0 || u.cnt == 0;
+        tok = there && (shared || q.n < u.cnt) ? q.n : -1;
+        seen = shared ? u.k1 : min(u.k1, a.mask ? u.pre : u.pre + u.row0 / a.G + 1);
+        tree = !shared && a.mask && u.k1 > u.pre ? read_mask(a, q.b, tok, u.cnt) : 0;
+    }
+    // Scores of the tile that begins at key `first`: -inf where the query does not see the key, NaN where the key is none.
+    __device__ __forceinline__ void hide(f32x16& S, int first, unsigned odd) const {
+        const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int key = first + 8 * (i / 4) + 4 * h2 + i % 4, node = key - u.pre;
+            const bool sees = key < u.k1 && (node < 0 || (a.mask ? node < 64 && ((tree >> (node & 63)) & 1ull) : node <= tok));
+            S[i] = !sees ? -INFINITY : (odd >> i) & 1u ? __builtin_nanf("") : S[i];
+        }
+    }
+};
+
+template <int D, int DT> __device__ __forceinline__ void load_queries(const PagedAttnArgs& a, const QueryRow& q, int h, bool there, Wave<D, DT>& w) {
+    using W = Wave<D, DT>;
+    const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
+    load_query<D, W::NQ, DT>(a.q, q.b * a.q.batch + q.n * a.q.pos + (static_cast<long long>(h) * a.G + q.g) * a.q.head, there, h2, w.Q);
+}
+// They are there: the compiler places no wait for them, which would be one for the tiles too, in the loop.
+template <int D, int DT> __device__ __forceinline__ void queries_loaded(Wave<D, DT>& w) {
+#pragma unroll
+    for (int p = 0; p < Wave<D, DT>::NQ; ++p)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(w.Q[p][i]));
+}
+
+constexpr int kPer = kWindow / 2;                       // tiles of a window of pages
+
+// A unit of up to 128 query rows: wave w has rows 32w .. of it.
 //
 // An iteration: V's operands of its tile are read and the scores formed from K's, read before; then the next tile has
 // arrived, this one's buffer takes the tile four further on, K's operands of the next are read, and the output follows.
-template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
-    constexpr int kPer = kWindow / 2;                   // tiles of a window of pages
-    constexpr int NT = WIDE ? D / 32 : D == 64 ? 1 : D / 128;
-    constexpr int kLoads = Loader<D>::kLoads;
-    using W = Wave<D, DT, NT>;
-    const int wave = wave_id(), lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
-    const int r = u.row0 + (WIDE ? 32 * wave : 0) + c, t0 = WIDE ? 0 : wave * NT % (D / 32);
-    const bool shared = u.table != u.b0 || u.cnt == 0;
+template <int D, int DT> __device__ __forceinline__ void attend_wide(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
+    using W = Wave<D, DT>;
+    using L = Loader<D, false>;
+    const int r = u.row0 + 32 * wave_id() + static_cast<int>(threadIdx.x & 31);
     const bool there = r < u.rows;
     const QueryRow q = query_row(a, u.b0, there ? r : u.row0);
-    const int tok = there && (shared || q.n < u.cnt) ? q.n : -1;
     const int tiles = (u.k1 - u.k0 + kTileKeys - 1) / kTileKeys;
 
-    Loader<D> ld(a, u, h, lds);
+    L ld(a, u, h, lds);
     if (tiles > 0) ld.first_window();
-    W w(t0);
-    load_query<D, W::NQ, DT>(a.q, q.b * a.q.batch + q.n * a.q.pos + (static_cast<long long>(h) * a.G + q.g) * a.q.head, there, h2, w.Q);
-    const bool working = WIDE ? u.row0 + 32 * wave < u.rows : D > 64 || wave < 2;
-    // slots below `seen` are seen by every query of the unit
-    const int tok0 = u.row0 / a.G;
-    const int seen = shared ? u.k1 : min(u.k1, a.mask ? u.pre : u.pre + tok0 + 1);
-    unsigned long long tree = 0;
-    if (!shared && a.mask && u.k1 > u.pre) tree = read_mask(a, q.b, tok, u.cnt);
+    W w;
+    load_queries(a, q, h, there, w);
+    const bool working = u.row0 + 32 * wave_id() < u.rows;
+    const Sight sight(a, u, q, there);
     const float slack = fminf(kSlack / a.cexp, 1e30f);
     // The window of pages is that of the tile to be loaded; the tile worked on may lie in the one before.
     unsigned long long bad = tiles > 0 ? ld.bad : 0, bad_before = 0;
 
     for (int t = 0; t < min(kStages, tiles); ++t) ld.load(t, t);
     if (tiles > kPer) ld.fetch_window(1);
-#pragma unroll
-    for (int p = 0; p < W::NQ; ++p)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(w.Q[p][i]));    // they are there: no wait for them in the loop
+    queries_loaded(w);
     wait_loads<0>();
     barrier();
     if (tiles > 0 && working) w.read_k(lds, 0);
 
     const auto iterate = [&](auto buffer, int t, bool edge, unsigned none) {
         const int buf = buffer;
-        if (edge) clean<D>(lds, buf, none);
         u32x4 P[W::NQ][2];
         if (working) {
-            const int first = u.k0 + t * kTileKeys;
-            const auto hide = [&](f32x16& S) {
-                const unsigned odd = lds.odd;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int in = 8 * (i / 4) + 4 * h2 + i % 4, key = first + in, node = key - u.pre;
-                    const bool sees = key < u.k1 && (node < 0 || (a.mask ? node < 64 && ((tree >> (node & 63)) & 1ull) : node <= tok));
-                    S[i] = !sees ? -INFINITY : (odd >> in) & 1u ? __builtin_nanf("") : S[i];
-                }
-            };
-            w.weigh(lds, buf, a.cexp, slack, edge, hide, P);
-            if (!W::kEarlyV) w.add(lds, buf, P);
+            if (W::kEarlyV) w.read_v(lds, buf);
+            f32x16 S = w.scores();
+            if (edge) sight.hide(S, u.k0 + t * kTileKeys, w.odd_keys(lds, buf, none));
+            w.weigh(S, a.cexp, slack, P);
+            if (!W::kEarlyV) w.add(lds, buf, P, edge);
         }
-        if (t + kStages <= tiles) wait_loads<(kStages - 2) * kLoads>();
+        if (t + kStages <= tiles) wait_loads<(kStages - 2) * L::kLoads>();
         else wait_loads<0>();
         wait_lds();                                     // this wave has read all it wants of the buffer
         barrier();
@@ -459,12 +507,12 @@ template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const
         }
         if (working) {
             if (t + 1 < tiles) w.read_k(lds, (buf + 1) % kStages);
-            if (W::kEarlyV) w.add(lds, buf, P);
+            if (W::kEarlyV) w.add(lds, buf, P, edge);
         }
     };
     int t = 0;
     // four at a time, their buffers known, while every query sees every key
-    const int whole = max(0, seen - u.k0) / kTileKeys;
+    const int whole = max(0, sight.seen - u.k0) / kTileKeys;
     for (; t + kStages <= whole && (bad | bad_before) == 0; t += kStages) {
         iterate(std::integral_constant<int, 0>(), t, false, 0u);
         iterate(std::integral_constant<int, 1>(), t + 1, false, 0u);
@@ -477,7 +525,87 @@ template <int D, int DT, bool WIDE> __device__ __forceinline__ void attend(const
         iterate(t % kStages, t, t >= whole || none != 0, none);
     }
     w.l += xshfl(w.l, 32);
-    if (working) write_rows<D, DT, NT>(a, u, h, r, t0, t0 == 0, w.O, w.m, w.l, tok >= 0);
+    if (working) write_rows<D, DT, W::NT>(a, u, h, r, 0, true, w.O, w.m, w.l, sight.tok >= 0);
+}
+
+// A unit of up to 32 query rows: wave w has tiles w, w + 4, .. of its keys. Nothing passes between the waves before the end: a
+// wave's operands are in registers when its next tile is brought over the one they came from.
+template <int D, int DT> __device__ __forceinline__ void attend_narrow(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
+    using W = Wave<D, DT>;
+    const int wave = wave_id(), lane = threadIdx.x & (kWave - 1);
+    const int r = u.row0 + (lane & 31);
+    const bool there = r < u.rows;
+    const QueryRow q = query_row(a, u.b0, there ? r : u.row0);
+    const int tiles = (u.k1 - u.k0 + kTileKeys - 1) / kTileKeys;
+
+    Loader<D, true> ld(a, u, h, lds);
+    if (tiles > 0) ld.first_window();
+    if (wave < tiles) {
+        ld.load_k(wave);
+        ld.load_v(wave);
+        if (tiles > kPer) ld.fetch_window(1);
+    }
+    W w;
+    load_queries(a, q, h, there, w);
+    const Sight sight(a, u, q, there);
+    const float slack = fminf(kSlack / a.cexp, 1e30f);
+    queries_loaded(w);
+    for (int t = wave; t < tiles; t += kWaves) {
+        const unsigned none = static_cast<unsigned>(ld.bad >> (2 * t & (kWindow - 1))) & 3u;
+        const int first = u.k0 + t * kTileKeys, next = t + kWaves;
+        const bool edge = first + kTileKeys > sight.seen || none != 0;
+        wait_loads<0>();
+        w.read_k(lds, wave);
+        if (W::kEarlyV) w.read_v(lds, wave);
+        wait_lds();
+        if (next < tiles) {
+            if (next / kPer != t / kPer) {
+                ld.next_window(next / kPer);
+                if ((next / kPer + 1) * kPer < tiles) ld.fetch_window(next / kPer + 1);
+            }
+            ld.load_k(next);
+            if (W::kEarlyV) ld.load_v(next);
+        }
+        f32x16 S = w.scores();
+        u32x4 P[W::NQ][2];
+        if (edge) sight.hide(S, first, w.odd_keys(lds, wave, none));
+        w.weigh(S, a.cexp, slack, P);
+        w.add(lds, wave, P, edge);
+        if (!W::kEarlyV && next < tiles) {
+            wait_lds();
+            ld.load_v(next);
+        }
+    }
+    // join the waves: each leaves its sums, and takes a quarter of the elements (D = 64: two waves a half)
+    w.l += xshfl(w.l, 32);
+    f32x16(*const sh)[W::NT][kWave] = reinterpret_cast<f32x16(*)[W::NT][kWave]>(&lds);
+    static_assert(sizeof(f32x16) * kWaves * W::NT * kWave == offsetof(Lds<D>, page), "the sums take the buffers' place");
+    wait_lds();
+    barrier();
+#pragma unroll
+    for (int t = 0; t < W::NT; ++t) sh[wave][t][lane] = w.O[t];
+    lds.ml[wave][0][lane] = w.m;
+    lds.ml[wave][1][lane] = w.l;
+    wait_lds();
+    barrier();
+    constexpr int kOwn = W::NT < kWaves ? 1 : W::NT / kWaves;
+    if (wave * kOwn >= W::NT) return;
+    float m = lds.ml[0][0][lane], l = 0.f;
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) m = fmaxf(m, lds.ml[i][0][lane]);
+    f32x16 O[kOwn];
+#pragma unroll
+    for (int t = 0; t < kOwn; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) O[t][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        const float mi = lds.ml[i][0][lane], f = mi == -INFINITY ? 0.f : exp2_fast((mi - m) * a.cexp);
+        l += lds.ml[i][1][lane] * f;                    // a sum that is NaN stays NaN whatever its maximum
+#pragma unroll
+        for (int t = 0; t < kOwn; ++t) O[t] += sh[i][wave * kOwn + t][lane] * f;
+    }
+    write_rows<D, DT, kOwn>(a, u, h, r, wave * kOwn, wave == 0, O, m, l, sight.tok >= 0);
 }
 
 // Whether the plan was made for a call of these sizes (one that was not names rows that are not there).
@@ -492,10 +620,10 @@ template <int D, int DT>
 __global__ __launch_bounds__(kThreads, occupancy(D, DT)) void paged_attention_kernel(PagedAttnArgs a) {
     __shared__ __attribute__((aligned(256))) Lds<D> lds;
     const int unit = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
+    const PagedUnit u = a.p.unit[unit];                 // there is room for it, whether or not the plan has one
     if (!plan_fits(a) || unit >= a.p.head[0]) return;
-    const PagedUnit u = a.p.unit[unit];
-    if (u.wide) attend<D, DT, true>(a, u, h, lds);
-    else attend<D, DT, false>(a, u, h, lds);
+    if (u.wide) attend_wide<D, DT>(a, u, h, lds);
+    else attend_narrow<D, DT>(a, u, h, lds);
 }
 
 // Joins the parts of each query row: D/4 neighbouring threads a row, four elements each.
