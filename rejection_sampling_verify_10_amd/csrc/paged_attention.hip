@@ -34,6 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTileKeys = 32;                           // keys of a tile
 constexpr int kWindow = kWave;                          // 16-key groups whose pages a wave holds, one a lane
+constexpr int kBatch = 8;                               // parts under way in the join
 constexpr float kSlack = 8.f;                           // powers of two a score may pass the running maximum by
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -281,18 +282,33 @@ template <int D, int DT> struct Wave {
         }
         return odd;
     }
+    // Nonzero where an element's exponent is all ones: a half's exponent and one more make its top bit, and no carry.
+    __device__ __forceinline__ static unsigned not_finite(const u32x4& w) {
+        unsigned any = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= (w[e] & 0x7f807f80u) + 0x00800080u;
+        return any & 0x80008000u;
+    }
     // The keys of the lane's scores, as bits, that are no numbers: V's elements of them (cleaned, where they are held), and
-    // those of groups without a page.
+    // those of groups without a page. Seldom any: the tile is looked over first.
     __device__ __forceinline__ unsigned odd_keys(const Lds<D>& lds, int buf, unsigned none) {
         const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
         unsigned odd = (none & 1 ? 0xffu : 0u) | (none & 2 ? 0xff00u : 0u);
+        unsigned some = 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (!kEarlyV) read_v(lds, buf, s, V[0]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) some |= not_finite(V[kEarlyV ? s : 0][t]);
+        }
+        if (__ballot(some != 0) == 0ull) return odd;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (!kEarlyV) read_v(lds, buf, s, V[0]);
             unsigned any = 0;
 #pragma unroll
             for (int t = 0; t < NT; ++t) any |= clean(V[kEarlyV ? s : 0][t]);
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 8; ++j) {
                 const unsigned long long all = __ballot((any >> j) & 1u);
                 odd |= (static_cast<unsigned>(h2 ? all >> 32 : all) ? 1u : 0u) << (8 * s + j);
@@ -424,14 +440,27 @@ struct Sight {
         seen = shared ? u.k1 : min(u.k1, a.mask ? u.pre : u.pre + u.row0 / a.G + 1);
         tree = !shared && a.mask && u.k1 > u.pre ? read_mask(a, q.b, tok, u.cnt) : 0;
     }
-    // Scores of the tile that begins at key `first`: -inf where the query does not see the key, NaN where the key is none.
+    // The keys of the tile that begins at `first` that the query sees, as bits.
+    __device__ __forceinline__ unsigned sees(int first) const {
+        const auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
+        const int node = first - u.pre;                 // the new token that the tile's first key is (negative: a committed slot)
+        unsigned bits;
+        if (a.mask) {
+            const unsigned long long nodes = node >= 64 ? 0ull : node >= 0 ? tree >> node : node > -32 ? tree << -node : 0ull;
+            bits = static_cast<unsigned>(nodes) | below(-node);
+        } else {
+            bits = below(tok + 1 - node);
+        }
+        return bits & below(u.k1 - first);
+    }
+    // Scores of that tile: -inf where the query does not see the key, NaN where the key is none.
     __device__ __forceinline__ void hide(f32x16& S, int first, unsigned odd) const {
-        const int h2 = (threadIdx.x & (kWave - 1)) >> 5;
+        const unsigned bits = sees(first) >> (4 * ((threadIdx.x & (kWave - 1)) >> 5));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int key = first + 8 * (i / 4) + 4 * h2 + i % 4, node = key - u.pre;
-            const bool sees = key < u.k1 && (node < 0 || (a.mask ? node < 64 && ((tree >> (node & 63)) & 1ull) : node <= tok));
-            S[i] = !sees ? -INFINITY : (odd >> i) & 1u ? __builtin_nanf("") : S[i];
+        for (int i = 0; i < 16; ++i) S[i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? S[i] : -INFINITY;
+        if (__ballot(odd != 0) != 0ull) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = ((bits >> (8 * (i / 4) + i % 4)) & (odd >> i)) & 1u ? __builtin_nanf("") : S[i];
         }
     }
 };
@@ -626,62 +655,65 @@ __global__ __launch_bounds__(kThreads, occupancy(D, DT)) void paged_attention_ke
     else attend_narrow<D, DT>(a, u, h, lds);
 }
 
-// Joins the parts of each query row: D/4 neighbouring threads a row, four elements each.
+// Joins the parts of each query row: D/4 neighbouring lanes a row, four elements each. The lanes first weigh the row's parts, one
+// each, so that the parts' loads wait for nothing.
 template <int D, int DT>
-__global__ __launch_bounds__(kThreads) void paged_join_kernel(PagedAttnArgs a, long long rows) {
+__global__ __launch_bounds__(kThreads) void paged_join_kernel(PagedAttnArgs a, unsigned rows) {
     constexpr int kLanes = D / 4, kRows = kThreads / kLanes;
-    const int d = static_cast<int>(threadIdx.x % kLanes) * 4;
-    const long long at = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kLanes;     // (b, n, query head)
-    if (at >= rows || !plan_fits(a)) return;
-    const int hq = static_cast<int>(at % a.Hq), h = hq / a.G;
-    const long long bn = at / a.Hq;
-    const int b = static_cast<int>(bn / a.N), n = static_cast<int>(bn % a.N);
-    const int r = n * a.G + hq % a.G;
+    const int sub = static_cast<int>(threadIdx.x) % kLanes, d = 4 * sub;
+    const unsigned at = blockIdx.x * kRows + threadIdx.x / kLanes;      // (b, n, query head): fewer than 2^31 of them
+    if (at >= rows) return;                             // kLanes lanes at a time
+    const unsigned bn = at / a.Hq, hq = at - bn * a.Hq, h = hq / a.G;
+    const int b = static_cast<int>(bn / a.N), n = static_cast<int>(bn - static_cast<unsigned>(b) * a.N);
+    const int r = n * a.G + static_cast<int>(hq - h * a.G);
     const PagedOwn own = a.p.own[static_cast<long long>(b) * a.own_tiles + r / a.own_rows];
-    if (own.count == 0) return;                         // written by its one unit
     const PagedShared sh = a.p.shared[b];
+    if (!plan_fits(a) || own.count == 0) return;        // written by its one unit
+    const int count = n < sh.live ? sh.count + own.count : 0;
+    const auto part = [&](int i) {                      // the prefix's parts, then the row's own
+        const long long p = i < sh.count ? sh.first + static_cast<long long>(i) * sh.step + r
+                                         : own.first + static_cast<long long>(i - sh.count) * a.own_rows + r % a.own_rows;
+        return p * a.c.H + h;
+    };
     float m = -INFINITY, l = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    const auto join = [&](long long first, long long step, int count) {
-        for (int s0 = 0; s0 < count; s0 += 4) {
-            // four parts at a time: their loads are independent
-            float ms[4], ls[4];
-            f32x4 os[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const long long p = (first + min(s0 + e, count - 1) * step) * a.c.H + h;
-                ms[e] = a.part_ml[2 * p];
-                ls[e] = a.part_ml[2 * p + 1];
-                os[e] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + d);
-            }
-            float mn = m;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mn = fmaxf(mn, ms[e]);
-            const float w = m == -INFINITY ? 0.f : exp2_fast((m - mn) * a.cexp);
-            l *= w;
-            o *= w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float we = ms[e] == -INFINITY || s0 + e >= count ? 0.f : exp2_fast((ms[e] - mn) * a.cexp);
-                l += s0 + e < count ? ls[e] * we : 0.f;
-                o += os[e] * we;
-            }
-            m = mn;
+    for (int i0 = 0; i0 < count; i0 += kLanes) {
+        float mi = -INFINITY, li = 0.f;
+        if (i0 + sub < count) {
+            const long long p = part(i0 + sub);
+            mi = a.part_ml[2 * p];
+            li = a.part_ml[2 * p + 1];
         }
-    };
-    if (n < sh.live) {
-        join(static_cast<long long>(sh.first) + r, sh.step, sh.count);
-        join(static_cast<long long>(own.first) + r % a.own_rows, a.own_rows, own.count);
+        float mn = fmaxf(m, mi);
+#pragma unroll
+        for (int x = 1; x < kLanes; x <<= 1) mn = fmaxf(mn, __shfl_xor(mn, x, kLanes));
+        const float before = m == -INFINITY ? 0.f : exp2_fast((m - mn) * a.cexp);
+        const float w = mi == -INFINITY ? 0.f : exp2_fast((mi - mn) * a.cexp);
+        float lw = li * w;                              // a sum that is NaN stays NaN whatever its maximum
+#pragma unroll
+        for (int x = 1; x < kLanes; x <<= 1) lw += __shfl_xor(lw, x, kLanes);
+        l = l * before + lw;
+        o *= before;
+        m = mn;
+        const int here = min(kLanes, count - i0);
+        for (int i = 0; i < here; i += kBatch) {
+            f32x4 os[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) os[e] = *reinterpret_cast<const f32x4*>(a.part_o + part(i0 + min(i + e, here - 1)) * D + d);
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) o += os[e] * (i + e < here ? __shfl(w, i + e, kLanes) : 0.f);
+        }
     }
     const bool empty = l == 0.f;
     const float inv = empty ? 0.f : 1.f / l;
     if (d == 0 && a.out_lse) a.out_lse[at] = empty ? -INFINITY : (m * a.cexp + __builtin_amdgcn_logf(l)) * 0.69314718056f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : o[e] * inv;
+    const long long to = static_cast<long long>(at) * D + d;
     if (DT == 1)
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * D + d) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + to) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
     else
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at * D + d) = o;
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o;
 }
 
 template <int D, int DT> void attend(const PagedAttnArgs& a, hipStream_t s, Timing t) {
@@ -690,7 +722,7 @@ template <int D, int DT> void attend(const PagedAttnArgs& a, hipStream_t s, Timi
     if (!a.part_o) return;
     constexpr int rows_wg = kThreads / (D / 4);
     const long long rows = static_cast<long long>(a.B) * a.N * a.Hq;
-    paged_join_kernel<D, DT><<<dim3(static_cast<unsigned>((rows + rows_wg - 1) / rows_wg)), kThreads, 0, s>>>(a, rows);
+    paged_join_kernel<D, DT><<<dim3(static_cast<unsigned>((rows + rows_wg - 1) / rows_wg)), kThreads, 0, s>>>(a, static_cast<unsigned>(rows));
 }
 
 }  // namespace
