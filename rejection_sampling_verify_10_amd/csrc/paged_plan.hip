@@ -4,10 +4,12 @@
 // Consecutive batch rows with the same prefix are a run: all their query rows form
 // one matrix against the prefix, in tiles of 128 (32, where there are no more), so
 // each tile's keys are read once for all of them.  A batch row's own slots are met
-// by its own query rows.  Key axes are cut into units of at most `per` chunks,
-// the same for all, so that they cost alike; a unit is a workgroup for each head.
-// Units of prefixes come first (they are the longer ones) with the tiles that read
-// the same keys side by side.
+// by its own query rows.  A job, one tile against its key axis, is cut into equal
+// units; a unit is a workgroup for each head.  The size that no unit passes is the
+// least for which the units of more than half of it find places at once, or a few
+// steps above; the smaller ones fill the gaps, because units are launched the
+// longest first (in 64 classes of length).  The tiles that read the same keys stay
+// side by side.
 
 #include "paged.hpp"
 
@@ -17,6 +19,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kClasses = kWave;         // of length, the longest first
+constexpr int kSteps = 8;               // sizes of a unit that are tried, each a sixteenth above the one before
 
 // Sum over the block's threads below this one, and over all.
 __device__ __forceinline__ long long block_exclusive(long long v, long long& total, long long (&sh)[kWaves]) {
@@ -66,10 +70,17 @@ __device__ __forceinline__ int own_limit(const PagedPlanArgs& a, const Row& r, i
     return r.pre + (a.N <= kPgMaskN ? r.cnt : min(last + 1, r.cnt));
 }
 __device__ __forceinline__ int chunks(int slots) { return (slots + kPgChunk - 1) / kPgChunk; }
-__device__ __forceinline__ int parts_of(int slots, int per) {
-    const int n = (chunks(slots) + per - 1) / per;
-    return n < 1 ? 1 : n;
-}
+
+// A job of `n` chunks for units of at most `most`: its parts, and the chunks of each but the last. (Whether 128 query rows meet
+// them or 32: the few take as long, waiting for memory.)
+struct Cut {
+    int parts, each;
+    __device__ __forceinline__ Cut(int n, int most) {
+        parts = max((n + most - 1) / most, 1);
+        each = max((n + parts - 1) / parts, 1);
+        parts = max((n + each - 1) / each, 1);
+    }
+};
 
 struct Run {
     int b0, rows, prefix, shared, tile, tiles;  // tile: query rows of a unit
@@ -79,7 +90,8 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
     __shared__ long long sh[kWaves];
     __shared__ int lead[kThreads + 1];
     __shared__ Run run[kThreads];
-    __shared__ long long run_unit[kThreads], run_part[kThreads];
+    __shared__ long long run_part[kThreads];
+    __shared__ int place[kClasses];                     // where the next unit of a class goes
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
     const long long items = static_cast<long long>(a.B) * a.own_tiles;
 
@@ -117,24 +129,66 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
         return static_cast<int>(count);
     };
 
-    // chunks of all key axes, and what a unit gets of them
-    int per = 1 << 30;
-    if (a.target > 0) {
-        long long mine = 0;
+    // f(chunks, tiles) for each job (or all tiles of a run at once)
+    const auto each_job = [&](const auto& f) {
         for (int b0 = 0; a.prefix_row && b0 < a.B; b0 += kThreads) {
             Run r;
             runs(b0, r);
-            mine += static_cast<long long>(r.tiles) * chunks(r.shared);
+            if (r.tiles) f(chunks(r.shared), r.tiles);
         }
         for (long long j = tid; j < items; j += kThreads)
-            mine += chunks(own_limit(a, read_row(a, static_cast<int>(j / a.own_tiles)), static_cast<int>(j % a.own_tiles)));
+            f(chunks(own_limit(a, read_row(a, static_cast<int>(j / a.own_tiles)), static_cast<int>(j % a.own_tiles))), 1);
+    };
+    // the chunks that no unit passes
+    int most = 1 << 29;
+    if (a.target > 0) {
+        long long cost = 0;
+        each_job([&](int n, int tiles) { cost += static_cast<long long>(n) * tiles; });
         long long total;
-        block_exclusive(mine, total, sh);
-        const long long each = (total + a.target - 1) / a.target;
-        per = static_cast<int>(each < 2 ? 2 : each);
+        block_exclusive(cost, total, sh);
+        most = static_cast<int>(max((total + a.target - 1) / a.target, 1ll));
+        for (int step = 0; step < kSteps; ++step) {
+            long long large = 0;
+            each_job([&](int n, int tiles) {
+                const Cut c(n, most);
+                if (2 * c.each > most) large += static_cast<long long>(c.parts) * tiles;
+            });
+            block_exclusive(large, total, sh);
+            if (total <= a.target) break;
+            most += most / 16 + 1;
+        }
     }
+    const int finest = (most + kClasses - 1) / kClasses;
+    const auto class_of = [&](int each) { return max(kClasses - 1 - each / finest, 0); };
+    if (tid < kClasses) place[tid] = 0;
+    __syncthreads();
+    each_job([&](int n, int tiles) {
+        const Cut c(n, most);
+        atomicAdd(&place[class_of(c.each)], c.parts * tiles);
+    });
+    __syncthreads();
+    if (wave == 0) {
+        static_assert(kClasses == kWave, "a class a lane");
+        const int n = place[lane];
+        int before = n;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int t = __shfl_up(before, o, kWave);
+            if (lane >= o) before += t;
+        }
+        place[lane] = before - n;
+        if (lane == kWave - 1) {
+            a.p.head[0] = before;
+            a.p.head[1] = a.B;
+            a.p.head[2] = a.N;
+            a.p.head[3] = a.M;
+            a.p.head[4] = a.prefix_row != nullptr;
+            a.p.head[5] = a.width << a.page_log2;
+        }
+    }
+    __syncthreads();
 
-    long long units = 0, parts = 0;
+    long long parts = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         if (b < a.B) {
@@ -144,16 +198,19 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
         if (!a.prefix_row) continue;
         Run mine;
         const int count = runs(b0, mine);
-        const int splits = mine.tiles ? parts_of(mine.shared, per) : 0;
-        long long total, part_total;
-        const long long u = block_exclusive(static_cast<long long>(mine.tiles) * splits, total, sh);
-        const long long p = block_exclusive(static_cast<long long>(mine.tiles) * splits * mine.tile, part_total, sh);
-        if (tid < count) run[tid] = mine, run_unit[tid] = units + u, run_part[tid] = parts + p;
+        const Cut cut(chunks(mine.shared), most);
+        long long part_total;
+        const long long p = block_exclusive(static_cast<long long>(mine.tiles) * cut.parts * mine.tile, part_total, sh);
+        if (tid < count) run[tid] = mine, run_part[tid] = parts + p;
         __syncthreads();
         for (int k = wave; k < count; k += kWaves) {
             const Run r = run[k];
             if (!r.tiles) continue;
-            const int n = parts_of(r.shared, per), step = per * kPgChunk;
+            const Cut c(chunks(r.shared), most);
+            const int n = c.parts, step = c.each * kPgChunk;
+            int u = 0;
+            if (lane == 0) u = atomicAdd(&place[class_of(c.each)], n * r.tiles);
+            u = __builtin_amdgcn_readfirstlane(u);
             for (int i = lane; i < n * r.tiles; i += kWave) {
                 const int s = i / r.tiles, tile = i % r.tiles;
                 PagedUnit w{};
@@ -166,7 +223,7 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
                 w.pre = r.shared;
                 w.part = static_cast<int>(run_part[k] + static_cast<long long>(i) * r.tile);
                 w.wide = r.tile == kPgWide;
-                a.p.unit[run_unit[k] + i] = w;
+                a.p.unit[u + i] = w;
             }
             for (int row = lane; row < r.rows / a.M; row += kWave) {
                 PagedShared* at = a.p.shared + r.b0 + row;
@@ -175,7 +232,6 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
                 at->count = n;
             }
         }
-        units += total;
         parts += part_total;
         __syncthreads();
     }
@@ -183,27 +239,27 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
         const long long j = j0 + tid;
         const int b = static_cast<int>(j / a.own_tiles), i = static_cast<int>(j % a.own_tiles);
         Row r{};
-        int limit = 0, n = 0;
-        bool joined = false;
+        int limit = 0;
         if (j < items) {
             r = read_row(a, b);
             limit = own_limit(a, r, i);
-            n = parts_of(limit, per);
-            joined = n > 1 || (r.shared > 0 && r.cnt > 0);
         }
-        long long total, part_total;
-        const long long u = units + block_exclusive(n, total, sh);
+        const Cut c(chunks(limit), most);
+        const int n = c.parts, step = c.each * kPgChunk;
+        const bool joined = j < items && (n > 1 || (r.shared > 0 && r.cnt > 0));
+        long long part_total;
         const long long p = parts + block_exclusive(joined ? static_cast<long long>(n) * a.own_rows : 0, part_total, sh);
         if (j < items) {
             a.p.own[j] = PagedOwn{static_cast<int>(p), joined ? n : 0};
+            const int u = atomicAdd(&place[class_of(c.each)], n);
             for (int s = 0; s < n; ++s) {
                 PagedUnit w{};
                 w.b0 = b;
                 w.row0 = i * a.own_rows;
                 w.rows = a.M;
                 w.table = b;
-                w.k0 = n > 1 ? s * per * kPgChunk : 0;
-                w.k1 = s == n - 1 ? limit : w.k0 + per * kPgChunk;
+                w.k0 = n > 1 ? s * step : 0;
+                w.k1 = s == n - 1 ? limit : w.k0 + step;
                 w.pre = r.pre;
                 w.cnt = r.cnt;
                 w.part = joined ? static_cast<int>(p) + s * a.own_rows : -1;
@@ -211,16 +267,7 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
                 a.p.unit[u + s] = w;
             }
         }
-        units += total;
         parts += part_total;
-    }
-    if (tid == 0) {
-        a.p.head[0] = static_cast<int>(units);
-        a.p.head[1] = a.B;
-        a.p.head[2] = a.N;
-        a.p.head[3] = a.M;
-        a.p.head[4] = a.prefix_row != nullptr;
-        a.p.head[5] = a.width << a.page_log2;
     }
 }
 
