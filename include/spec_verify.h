@@ -709,8 +709,8 @@ int spec_accept_rate(const void* target_logits, spec_dtype_t dtype, const float*
  *   out_slots    [T][N] int32: the slot of token n (its place is lengths[t] + n), -1 for
  *                n >= granted[t], and where the page's number is none of the pool's
  * A state outside [0, pages) and [0, pages] serves no row and is left as it is.
- * page_size a power of two from 16 to 1024, T and N at most 65536, pages * page_size and
- * width * page_size at most 2^30.
+ * page_size a power of two from 16 to 1024, T and N at most 65536 and T * N below 2^31,
+ * pages * page_size and width * page_size at most 2^30.
  * workspace: 256 bytes, zero-filled before its first use and left zero.
  */
 #define SPEC_PAGE_STEP_WORKSPACE_BYTES 256

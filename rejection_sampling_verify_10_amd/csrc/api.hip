@@ -1446,7 +1446,7 @@ int spec_page_step(int32_t* tables, int64_t table_stride, int T, int width, int 
         !aligned(counts, 4) || !aligned(out_held, 4) || !aligned(out_state, 4) || !aligned(out_granted, 4) ||
         !aligned(out_slots, 4))
         return SPEC_EINVAL;
-    if (T > 65536 || N > 65536 || !slots_ok(pages, page_size) || !slots_ok(width, page_size) || table_stride > (1ll << 40))
+    if (T > 65536 || N > 65536 || static_cast<int64_t>(T) * N >= (1ll << 31) || !slots_ok(pages, page_size) || !slots_ok(width, page_size) || table_stride > (1ll << 40))
         return SPEC_EUNSUPPORTED;
     const int rc = check_workspace(workspace, workspace_bytes, SPEC_PAGE_STEP_WORKSPACE_BYTES);
     if (rc) return rc;
@@ -1467,6 +1467,7 @@ int spec_page_step(int32_t* tables, int64_t table_stride, int T, int width, int 
     a.out_state = out_state;
     a.out_granted = out_granted;
     a.out_slots = out_slots;
+    a.apart = out_held != held && out_state != state;
     a.done = static_cast<unsigned*>(workspace);
     ProfileScope prof;
     SV_TRY(launch_page_step(a, static_cast<hipStream_t>(hip_stream), prof.timing()));

@@ -21,7 +21,8 @@ struct PageStepArgs {
     int32_t* out_state;             // [2], may be state
     int32_t* out_granted;           // [T]
     int32_t* out_slots;             // [T][N]
-    unsigned* done;                 // workgroups that have read their inputs; zero before and after a call
+    int apart;                      // out_held and out_state are other arrays than held and state
+    unsigned* done;                 // workgroups that have read their inputs; zero before and after a call (unless apart)
 };
 hipError_t launch_page_step(const PageStepArgs& a, hipStream_t s, Timing t = {});
 

@@ -3,11 +3,16 @@
 // of the step's tokens.
 //
 // Every workgroup sums the whole batch's needs for itself (three small arrays, from
-// the L2) and then serves its own sequences, so nothing passes between workgroups
-// and one launch does.  The arrays a call reads may be the ones it writes, so what
-// others still read (pages held, the ring's ends) is written by the last workgroup
-// that has read them.  Taken pages lie between the ring's head and its tail, pages
-// given back behind the tail: no entry is both read and written.
+// the L2; a row a thread) and then serves its own sequences, so nothing passes
+// between workgroups and one launch does.  Where a call writes the arrays that it
+// reads, what others still read (pages held, the ring's ends) is written by the last
+// workgroup that has read them.  Taken pages lie between the ring's head and its
+// tail, pages given back behind the tail: no entry is both read and written.
+//
+// Bound by latency: three dependent loads, a sum, a store, and a ticket where it
+// writes in place.
+
+#include <type_traits>
 
 #include "paged.hpp"
 
@@ -15,15 +20,16 @@ namespace sv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kPart = 1024;         // tokens of a row that a workgroup finds the slots of
+constexpr int kRowsMax = 128;       // rows of a workgroup
 
 struct Need {
     int len, cnt, held, need;
     bool ok;                        // the row's numbers make sense and fit its table
-    __device__ __forceinline__ int grow() const { return ok ? max(need - held, 0) : 0; }
-    __device__ __forceinline__ int drop() const { return ok ? max(held - need, 0) : 0; }
+    __device__ __forceinline__ unsigned grow() const { return ok ? static_cast<unsigned>(max(need - held, 0)) : 0u; }
+    __device__ __forceinline__ unsigned drop() const { return ok ? static_cast<unsigned>(max(held - need, 0)) : 0u; }
 };
 __device__ __forceinline__ Need read_need(const PageStepArgs& a, int t) {
     Need n;
@@ -39,19 +45,29 @@ __device__ __forceinline__ Need read_need(const PageStepArgs& a, int t) {
     return n;
 }
 
-// Exclusive sums over the block's threads, and their totals.
+// Sums stop at 2^30, which no pool's pages reach: only whether they fit counts past that.
+__device__ __forceinline__ unsigned add(unsigned a, unsigned b) { return min(a + b, 1u << 30); }
+__device__ __forceinline__ unsigned wave_inclusive(unsigned v) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const auto shifted = [](unsigned x, auto ctl) {
+        return static_cast<unsigned>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctl)::value, 0xf, 0xf, true));
+    };
+    v = add(v, shifted(v, std::integral_constant<int, 0x111>()));       // row_shr:1, 2, 4, 8
+    v = add(v, shifted(v, std::integral_constant<int, 0x112>()));
+    v = add(v, shifted(v, std::integral_constant<int, 0x114>()));
+    v = add(v, shifted(v, std::integral_constant<int, 0x118>()));
+    const unsigned r0 = bcast(static_cast<int>(v), 15), r1 = add(r0, bcast(static_cast<int>(v), 31)),
+                   r2 = add(r1, bcast(static_cast<int>(v), 47));
+    const int row = lane >> 4;
+    return add(v, row == 0 ? 0u : row == 1 ? r0 : row == 2 ? r1 : r2);
+}
+// Sums over the block's threads up to this one, and over all of them.
 struct Pair {
-    long long grow, drop;
+    unsigned grow, drop;
 };
-__device__ __forceinline__ long long shift_up(long long v, int o) { return __shfl_up(v, o, kWave); }
-__device__ __forceinline__ Pair block_exclusive(Pair v, Pair& total, Pair (&sh)[kWaves]) {
+__device__ __forceinline__ Pair block_inclusive(Pair v, Pair& total, Pair (&sh)[kWaves]) {
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
-    Pair i = v;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const long long g = shift_up(i.grow, o), d = shift_up(i.drop, o);
-        if (lane >= o) i.grow += g, i.drop += d;
-    }
+    const Pair i = {wave_inclusive(v.grow), wave_inclusive(v.drop)};
     __syncthreads();
     if (lane == kWave - 1) sh[wave] = i;
     __syncthreads();
@@ -59,10 +75,11 @@ __device__ __forceinline__ Pair block_exclusive(Pair v, Pair& total, Pair (&sh)[
     total = {0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) before.grow += sh[w].grow, before.drop += sh[w].drop;
-        total.grow += sh[w].grow, total.drop += sh[w].drop;
+        if (w == wave) before = total;
+        total.grow = add(total.grow, sh[w].grow);
+        total.drop = add(total.drop, sh[w].drop);
     }
-    return {before.grow + i.grow - v.grow, before.drop + i.drop - v.drop};
+    return {add(before.grow, i.grow), add(before.drop, i.drop)};
 }
 
 struct Served {                     // a row of this workgroup's, in LDS
@@ -76,48 +93,42 @@ __device__ __forceinline__ int wrap(unsigned x, int pages) {
 
 __global__ __launch_bounds__(kThreads) void page_step_kernel(PageStepArgs a, int rows_wg, int parts) {
     __shared__ Pair sh[kWaves];
-    __shared__ Served mine[kThreads];
+    __shared__ Served mine[kRowsMax];
+    __shared__ unsigned most[kWaves];
     __shared__ unsigned ticket;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int part = blockIdx.x % parts;
     const int first = blockIdx.x / parts * rows_wg, end = min(a.T, first + rows_wg);
     const int head = a.state[0], free_pages = a.state[1];
     const bool ring_ok = head >= 0 && head < a.pages && free_pages >= 0 && free_pages <= a.pages;
-    const long long supply = ring_ok ? free_pages : 0;
+    const unsigned supply = ring_ok ? free_pages : 0;
 
     Pair base = {0, 0};
-    long long taken = 0;            // pages of the rows that are served: they are the first ones
+    unsigned taken = 0;             // the sum of the rows that grow and are served: the last one that fits
+    Need n{};
+    bool served = false;
     for (int t0 = 0; t0 < a.T; t0 += kThreads) {
         const int t = t0 + tid;
-        Need n{};
+        n = Need{};
         if (t < a.T) n = read_need(a, t);
         n.ok = n.ok && ring_ok;
-        Pair total, at = block_exclusive({t < a.T ? n.grow() : 0, t < a.T ? n.drop() : 0}, total, sh);
-        at.grow += base.grow, at.drop += base.drop;
-        const bool served = n.ok && (n.grow() == 0 || at.grow + n.grow() <= supply);
+        Pair total, upto = block_inclusive({n.grow(), n.drop()}, total, sh);
+        upto.grow = add(base.grow, upto.grow), upto.drop = add(base.drop, upto.drop);
+        served = n.ok && (n.grow() == 0 || upto.grow <= supply);
+        if (served && n.grow() > 0) taken = upto.grow;
         if (t >= first && t < end) {
             Served s;
             s.len = n.len, s.cnt = served ? n.cnt : -1, s.held = n.held, s.need = served ? n.need : n.held;
-            s.take = served ? static_cast<int>((head + at.grow) % a.pages) : 0;
-            s.give = served ? static_cast<int>((head + supply + at.drop) % a.pages) : 0;
+            s.take = served ? static_cast<int>((head + upto.grow - n.grow()) % a.pages) : 0;
+            s.give = served ? static_cast<int>((head + supply + upto.drop - n.drop()) % a.pages) : 0;
             s.row = t;
             mine[t - first] = s;
-            if (part == 0) a.out_granted[t] = s.cnt;
+            if (part == 0) {
+                a.out_granted[t] = s.cnt;
+                if (a.apart) a.out_held[t] = s.need;
+            }
         }
-        base.grow += total.grow, base.drop += total.drop;
-        // a row that grows is served while the sum up to it fits, so the last sum that fits is what is taken
-        const long long fits = t < a.T && served && n.grow() > 0 ? at.grow + n.grow() : 0;
-        long long most = fits;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const long long other = __shfl_xor(most, o, kWave);
-            most = other > most ? other : most;
-        }
-        __syncthreads();
-        if ((tid & (kWave - 1)) == 0) sh[wave_id()].grow = most;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) taken = sh[w].grow > taken ? sh[w].grow : taken;
+        base.grow = add(base.grow, total.grow), base.drop = add(base.drop, total.drop);
     }
     __syncthreads();
 
@@ -132,50 +143,65 @@ __global__ __launch_bounds__(kThreads) void page_step_kernel(PageStepArgs a, int
                 a.ring[wrap(static_cast<unsigned>(s.give) + (j - s.need), a.pages)] = table[j];
         }
         const int last = min(a.N, (part + 1) * kPart);
-        for (int n = part * kPart + at; n < last; n += step) {
+        for (int i = part * kPart + at; i < last; i += step) {
             int slot = -1;
-            if (n < s.cnt) {
-                const int pos = s.len + n, j = pos >> a.page_log2;
+            if (i < s.cnt) {
+                const int pos = s.len + i, j = pos >> a.page_log2;
                 const int page = j < s.held ? table[j] : fresh(j);
                 if (page >= 0 && page < a.pages) slot = (page << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
             }
-            slots[n] = slot;
+            slots[i] = slot;
         }
     };
     if (rows_wg == 1) {
         serve(mine[0], tid, kThreads);
     } else {
-        for (int i = wave_id(); i < end - first; i += kWaves) serve(mine[i], tid & (kWave - 1), kWave);
+        for (int i = wave_id(); i < end - first; i += kWaves) serve(mine[i], lane, kWave);
     }
 
-    // the last workgroup writes what the others read
+    // the ring's ends, and the pages held: in place by the last workgroup, which knows that the others have read them
+    if (a.apart) {
+        if (blockIdx.x != 0) return;
+    } else {
+        __syncthreads();
+        if (tid == 0) ticket = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (ticket != gridDim.x - 1) return;
+        if (tid == 0) __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const unsigned w = wave_max_u32(taken);
+    if (lane == 0) most[wave_id()] = w;
     __syncthreads();
-    if (tid == 0) ticket = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (ticket != gridDim.x - 1) return;
     if (tid == 0) {
-        __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int i = 1; i < kWaves; ++i) taken = max(taken, most[i]);
+        taken = max(taken, most[0]);
         a.out_state[0] = ring_ok ? static_cast<int>((head + taken) % a.pages) : head;
         a.out_state[1] = ring_ok ? static_cast<int>(free_pages - taken + base.drop) : free_pages;
     }
-    Pair sum = {0, 0};
+    if (a.apart) return;
+    if (a.T <= kThreads) {
+        if (tid < a.T) a.out_held[tid] = served ? n.need : n.held;
+        return;
+    }
+    unsigned grown = 0;
     for (int t0 = 0; t0 < a.T; t0 += kThreads) {
         const int t = t0 + tid;
-        Need n{};
+        n = Need{};
         if (t < a.T) n = read_need(a, t);
         n.ok = n.ok && ring_ok;
-        Pair total, at = block_exclusive({t < a.T ? n.grow() : 0, 0}, total, sh);
-        const bool served = n.ok && (n.grow() == 0 || sum.grow + at.grow + n.grow() <= supply);
-        if (t < a.T) a.out_held[t] = served ? n.need : n.held;
-        sum.grow += total.grow;
+        Pair total;
+        const Pair upto = block_inclusive({n.grow(), 0}, total, sh);
+        if (t < a.T) a.out_held[t] = n.ok && (n.grow() == 0 || add(grown, upto.grow) <= supply) ? n.need : n.held;
+        grown = add(grown, total.grow);
     }
 }
 
 }  // namespace
 
 hipError_t launch_page_step(const PageStepArgs& a, hipStream_t s, Timing t) {
-    // a workgroup a row up to 256 of them, and one for each 1024 tokens of it
-    const int rows_wg = (a.T + 255) / 256, parts = (a.N + kPart - 1) / kPart;
+    // a wave a row, or a workgroup for each 1024 tokens of one
+    const int parts = (a.N + kPart - 1) / kPart;
+    const int rows_wg = parts > 1 ? 1 : a.T <= 512 * kWaves ? kWaves : (a.T + 511) / 512;
     const dim3 grid(static_cast<unsigned>((a.T + rows_wg - 1) / rows_wg) * parts);
     launch_timed(t, page_step_kernel, grid, dim3(kThreads), 0, s, a, rows_wg, parts);
     return hipGetLastError();

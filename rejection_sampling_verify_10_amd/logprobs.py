@@ -14,7 +14,7 @@ Training a draft model on M tokens a position (ids [.., M]) and their gradients 
 
 from __future__ import annotations
 
-from typing import NamedTuple, Optional, Tuple
+from typing import Dict, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -56,13 +56,41 @@ def _logit_rows(t: torch.Tensor, name: str) -> Tuple[int, int, Tuple[int, ...]]:
     return rows, step, tuple(t.shape[:-1])
 
 
-def _tokens(tokens: torch.Tensor, lead: Tuple[int, ...], device) -> Tuple[int, int]:
-    """(address, tokens a row): of the leading shape (one a row), or with a dimension of M more."""
-    one = tokens.dim() == len(lead)
-    M = 1 if one else tokens.shape[-1] if tokens.dim() else 0
-    if not one and not 1 <= M <= SPEC_TOPK_MAX:
-        raise ValueError(f"tokens must have between 1 and {SPEC_TOPK_MAX} a row")
-    return _tensor(tokens, "tokens", torch.int32, torch.Size(lead if one else lead + (M,)), device), M
+class _Sizes(NamedTuple):
+    rows: int
+    step: int                                   # elements between the logits' rows
+    M: int                                      # tokens a row
+    lead: Tuple[int, ...]
+    workspace: int
+
+
+_sizes: Dict[tuple, _Sizes] = {}                # of the calls made so far, by their shapes
+
+
+def _call_sizes(logits: torch.Tensor, tokens: Optional[torch.Tensor], top_n: int) -> _Sizes:
+    """What a call's shapes say, checked: tokens are of the logits' leading shape, or have a dimension of M more."""
+    if logits.dtype not in _CODES:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
+    key = (logits.shape, logits.stride(), logits.dtype, None if tokens is None else tokens.shape, top_n)
+    s = _sizes.get(key)
+    if s is None:
+        rows, step, lead = _logit_rows(logits, "logits")
+        if not 0 <= top_n <= SPEC_TOPK_MAX:
+            raise ValueError(f"top_n must lie in [0, {SPEC_TOPK_MAX}]")
+        M = 0
+        if tokens is not None:
+            M = 1 if tokens.dim() == len(lead) else tokens.shape[-1] if tokens.dim() else 0
+            if not 1 <= M <= SPEC_TOPK_MAX:
+                raise ValueError(f"tokens must have between 1 and {SPEC_TOPK_MAX} a row")
+            if tuple(tokens.shape) not in (lead, lead + (M,)):
+                raise ValueError(f"tokens must have shape {lead} or {lead + (M,)}, got {tuple(tokens.shape)}")
+        s = _Sizes(rows, step, M, lead, token_logprobs_workspace_bytes(rows, logits.shape[-1], top_n, logits.dtype))
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        _sizes[key] = s
+    return s
 
 
 def token_logprobs_workspace_bytes(rows: int, V: int, top_n: int = 0, dtype: torch.dtype = torch.bfloat16) -> int:
@@ -79,23 +107,25 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], tempera
     tokens are none, and rows without a token are not read: their log probabilities and entropy are 0, their tops -1
     and -inf.  ``workspace`` (:func:`new_workspace`; zero-filled once, calls leave it zero) avoids one a call.
     """
-    rows, step, lead = _logit_rows(logits, "logits")
-    V, dev, top_n = logits.shape[-1], logits.device, int(top_n)
-    if not 0 <= top_n <= SPEC_TOPK_MAX:
-        raise ValueError(f"top_n must lie in [0, {SPEC_TOPK_MAX}]")
-    tp, M = (None, 0) if tokens is None else _tokens(tokens, lead, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    lp = torch.empty(lead + (0,) if tokens is None else tokens.shape, **f32)
-    entropy, stats = torch.empty(lead, **f32), torch.empty(lead + (3,), **f32)
-    top = torch.empty(lead + (top_n,), dtype=torch.int32, device=dev) if top_n else None
-    top_lp = torch.empty(lead + (top_n,), **f32) if top_n else None
-    need = token_logprobs_workspace_bytes(rows, V, top_n, logits.dtype)
-    if need and workspace is None:
-        workspace = torch.zeros(need + 256, dtype=torch.uint8, device=dev)
-    wp, _ws = _scratch(need, dev, workspace)
+    top_n = int(top_n)
+    rows, step, M, lead, need = _call_sizes(logits, tokens, top_n)
+    V, dev = logits.shape[-1], logits.device
+    f32, new = torch.float32, logits.new_empty
+    tp = None if tokens is None else _tensor(tokens, "tokens", torch.int32, tokens.shape, dev)
+    lp = new(lead + (0,) if tokens is None else tokens.shape, dtype=f32)
+    entropy, stats = new(lead, dtype=f32), new(lead + (3,), dtype=f32)
+    top = top_lp = top_ptr = top_lp_ptr = None
+    if top_n:
+        top, top_lp = new(lead + (top_n,), dtype=torch.int32), new(lead + (top_n,), dtype=f32)
+        top_ptr, top_lp_ptr = top.data_ptr(), top_lp.data_ptr()
+    wp = None
+    if need:
+        if workspace is None:
+            workspace = torch.zeros(need + 256, dtype=torch.uint8, device=dev)
+        wp, workspace = _scratch(need, dev, workspace)
     _call(lib().spec_token_logprobs, "spec_token_logprobs", dev, logits.data_ptr(), _CODES[logits.dtype], step, rows, V,
-          tp, M, float(temperature), top_n, lp.data_ptr() if M else None, entropy.data_ptr(), stats.data_ptr(),
-          top.data_ptr() if top_n else None, top_lp.data_ptr() if top_n else None, wp, need)
+          tp, M, temperature, top_n, lp.data_ptr() if M else None, entropy.data_ptr(), stats.data_ptr(), top_ptr, top_lp_ptr,
+          wp, need)
     return TokenLogprobs(lp, entropy, stats, top, top_lp)
 
 
@@ -108,17 +138,19 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch
     tokens' shape and grad_entropy of the leading one, float32.  ``out``: a tensor to write to, of any row distance;
     the logits themselves may be given, anything else must not overlap them.
     """
-    rows, step, lead = _logit_rows(logits, "logits")
+    rows, step, M, lead, _ = _call_sizes(logits, tokens, 0)
     dev = logits.device
-    tp, M = _tokens(tokens, lead, dev)
+    tp = _tensor(tokens, "tokens", torch.int32, tokens.shape, dev)
+    out_step = logits.shape[-1]
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = logits.new_empty(logits.shape)
     elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
         raise ValueError("out must have the logits' shape, type and device")
-    out_step = _logit_rows(out, "out")[1]
+    else:
+        out_step = _logit_rows(out, "out")[1]
     _call(lib().spec_token_logprobs_grad, "spec_token_logprobs_grad", dev, logits.data_ptr(), _CODES[logits.dtype], step,
-          rows, logits.shape[-1], tp, M, _tensor(stats, "stats", torch.float32, torch.Size(lead + (3,)), dev),
+          rows, logits.shape[-1], tp, M, _tensor(stats, "stats", torch.float32, lead + (3,), dev),
           _tensor(grad_logprobs, "grad_logprobs", torch.float32, tokens.shape, dev),
-          None if grad_entropy is None else _tensor(grad_entropy, "grad_entropy", torch.float32, torch.Size(lead), dev),
-          float(temperature), out.data_ptr(), out_step)
+          None if grad_entropy is None else _tensor(grad_entropy, "grad_entropy", torch.float32, lead, dev),
+          temperature, out.data_ptr(), out_step)
     return out

@@ -68,6 +68,9 @@ class PagePool:
         self.T, self.width, self.pages, self.page_size, self.device = T, width, ring.shape[0], int(page_size), dev
         self._workspace = torch.zeros(512, dtype=torch.uint8, device=dev)
         self._wp = (self._workspace.data_ptr() + 255) // 256 * 256
+        self._sizes = (tables.data_ptr(), tables.stride(0) if T > 1 else width, T, width, self.page_size, self.pages)
+        self._lists = (held.data_ptr(), state.data_ptr())
+        self._ring = ring.data_ptr()
 
 
 def new_page_pool(T: int, width: int, pages: int, page_size: int, device) -> PagePool:
@@ -91,15 +94,13 @@ def page_step(pool: PagePool, lengths: torch.Tensor, N: int, *, counts: Optional
     N = int(N)
     if not 1 <= N <= 65536:
         raise ValueError(f"N must lie in [1, 65536], got {N}")
-    dev, row = pool.device, (pool.T,)
-    out_held = pool.held if out_held is None else out_held
-    out_state = pool.state if out_state is None else out_state
-    granted = torch.empty(row, dtype=torch.int32, device=dev)
-    slots = torch.empty((pool.T, N), dtype=torch.int32, device=dev)
-    _call(lib().spec_page_step, "spec_page_step", dev, pool.tables.data_ptr(), pool.tables.stride(0) if pool.T > 1 else pool.width,
-          pool.T, pool.width, pool.page_size, pool.pages, pool.held.data_ptr(), pool.state.data_ptr(), pool.ring.data_ptr(),
-          _tensor(lengths, "lengths", torch.int32, row, dev), _optional(counts, "counts", torch.int32, row, dev), N,
-          _tensor(out_held, "out_held", torch.int32, row, dev), _tensor(out_state, "out_state", torch.int32, (2,), dev),
+    dev, T = pool.device, pool.T
+    held, state = pool._lists
+    granted, slots = lengths.new_empty((T,)), lengths.new_empty((T, N))
+    _call(lib().spec_page_step, "spec_page_step", dev, *pool._sizes, held, state, pool._ring,
+          _tensor(lengths, "lengths", torch.int32, (T,), dev), _optional(counts, "counts", torch.int32, (T,), dev), N,
+          held if out_held is None else _tensor(out_held, "out_held", torch.int32, (T,), dev),
+          state if out_state is None else _tensor(out_state, "out_state", torch.int32, (2,), dev),
           granted.data_ptr(), slots.data_ptr(), pool._wp, 256)
     return granted, slots
 
