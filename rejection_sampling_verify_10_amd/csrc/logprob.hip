@@ -5,14 +5,17 @@
 // W = sum 2^x_i x_i:  log p(t) = ln2 * (x_t - log2 S),  H = ln2 * (log2 S - W/S).
 // x is never above 0 but for its rounding, so no exponential overflows.
 //
-// Forward: a workgroup holds a slice of a row in registers (16-byte vectors).  Each
+// Forward: a workgroup streams a row, or a slice of one where the rows are few.  Each
 // wave takes its vectors as they arrive, against a running reference that moves
 // only where an element passes it by 2^40, so that exponentials overlap the loads.
-// Of the likeliest: each wave's q-th largest thread maximum, q = ceil(n / 4), bounds
-// the slice's n-th largest element from below, and few elements reach the least of
-// the four; the vectors that hold them are found in the registers once more, go to
-// LDS, and one wave sorts them.  The workgroups of a row leave (m, S, W, list) in
-// the workspace, and the last of them joins.
+// Of the likeliest: the first eight vectors a thread stay in registers until their
+// threads' maxima say what the rest is measured by.  The n-th largest of them bounds
+// the row's n-th largest element from below, and few elements reach it: the
+// vectors that hold some go to LDS, those of the rest of the row as they come, and
+// each element's place among them is counted.  (Where the first
+// vectors tell too little, the row is looked through again with the bound of all.)
+// The workgroups of a row leave (m, S, W, list) in the workspace, and the last of
+// them joins.
 
 #include <float.h>
 
@@ -23,7 +26,9 @@ namespace sv {
 namespace {
 
 constexpr int kWaves = kLpThreads / kWave;
-constexpr int kStage = 256, kCand = 512;                // vectors and elements that may reach the threshold before the exact rounds
+constexpr int kLpVecs = 8, kFewVecs = 4;                // 16-byte vectors of a thread under way; of a small slice, all of them
+constexpr int kLpWorkgroups = 256;
+constexpr int kStage = kWave, kCand = kLpThreads;       // vectors of a wave, and elements, that may reach the threshold
 
 typedef u32x4 __attribute__((aligned(4))) u32x4_a4;
 typedef u32x4 __attribute__((aligned(2))) u32x4_a2;
@@ -72,12 +77,12 @@ __device__ __forceinline__ double reference(float m, float c) {
 
 struct Smem {
     float red[kWaves], sums[kWaves][3];
-    uint32_t keys[kWaves], alone[kWaves];
-    u32x4 stage[kStage];
-    int32_t stage_i[kStage];
+    uint32_t lists[2][kWaves][kWave];
+    u32x4 stage[kWaves][kStage];
+    int32_t stage_i[kWaves][kStage];
     pkey_t cand[kCand];
-    int staged, count;
-    pkey_t best[kWaves];
+    int count, full;                // full: a wave had more vectors than its part of the stage holds
+    pkey_t best[kWave];
 };
 
 __device__ __forceinline__ float wave_maximum(float v) {    // NaN wins
@@ -155,21 +160,23 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
         return;
     }
 
-    // the slice: vectors first .. of the row, and the row's last few elements with its last slice
-    const int vecs = a.V / PV, first = slice * (NV * kLpThreads);
+    // the slice: vectors first .. last - 1 of the row, and the row's last few elements with its last slice
+    const int vecs = a.V / PV, first = slice * a.per, last = min(vecs, first + a.per);
+    const auto fetch = [&](int i) {
+        const uint32_t none = DT == 1 ? 0xff80ff80u : 0xff800000u;     // -inf
+        u32x4 w = {none, none, none, none};
+        if (i < last) w = load_vec<DT>(row, static_cast<long>(i) * PV);
+        return w;
+    };
     u32x4 v[NV];
-    const uint32_t none = DT == 1 ? 0xff80ff80u : 0xff800000u;  // -inf
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = first + j * kLpThreads + tid;
-        v[j] = u32x4{none, none, none, none};
-        if (i < vecs) v[j] = load_vec<DT>(row, static_cast<long>(i) * PV);
-    }
+    for (int j = 0; j < NV; ++j) v[j] = fetch(first + j * kLpThreads + tid);
     const int rest = vecs * PV + tid;
     const bool has_rest = slice == a.slices - 1 && rest < a.V;
     const float z_rest = has_rest ? E::scalar(row, rest) : -INFINITY;
     const float z_tok = tok >= 0 && !bad ? E::scalar(row, tok) : 0.f;
 
+    constexpr int kGroup = 4;                           // vectors between two looks at the reference
     // sums relative to `ref`, the same in a wave's lanes
     float tm = -INFINITY, ref = -FLT_MAX, S = 0.f, W = 0.f;
     const auto add = [&](float x) {
@@ -177,7 +184,6 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
         S += p;
         W = __builtin_fmaf(p, x, W);
     };
-    constexpr int kGroup = 4;                           // vectors between two looks at the reference
     const auto look = [&](float mx) {
         tm = __builtin_elementwise_maximum(tm, mx);
         if (__ballot(mx * a.c > ref + kSlack) != 0ull) {
@@ -187,19 +193,100 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
             ref = to;
         }
     };
+    // A group of vectors, the first of them number `at` of the row. -inf makes a NaN of W (0 * -inf), and the group is taken again
+    // with its exponents held above that; what stands for vectors past the end is -inf too, and left out.
+    const auto sum = [&](const u32x4* w, int at) {
+        const float S0 = S, W0 = W;
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {
+            const float before = W;
+#pragma unroll
+            for (int i = 0; i < PV; ++i) add(__builtin_fmaf(E::get(w[e], i), a.c, -ref));
+            W = at + e * kLpThreads < last ? W : before;
+        }
+        if (__ballot(W != W) != 0ull) {
+            S = S0, W = W0;
+#pragma unroll 1
+            for (int i = 0; i < PV; ++i) {
+#pragma unroll
+                for (int e = 0; e < kGroup; ++e) {
+                    const int at = i / (PV / 4);
+                    const uint32_t x = at == 0 ? w[e][0] : at == 1 ? w[e][1] : at == 2 ? w[e][2] : w[e][3];
+                    add(exponent(DT == 0 ? __uint_as_float(x) : i & 1 ? bf16_hi(x) : bf16_lo(x), a.c, ref));
+                }
+            }
+        }
+    };
+    // Vectors with an element that reaches tau, to the wave's part of the stage (past its end they are only counted).
+    float tau = INFINITY;
+    int staged = 0;                                     // the same in a wave's lanes
+    const auto offer = [&](const u32x4& w, float mx, int i) {
+        const unsigned long long hits = __ballot(mx >= tau);
+        if (hits == 0ull) return;
+        const int at = staged + __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(hits >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(hits), 0));
+        if (mx >= tau && at < kStage) {
+            sm.stage[wave][at] = w;
+            sm.stage_i[wave][at] = i * PV;
+        }
+        staged += __popcll(hits);
+    };
+    // A lower bound of the n-th largest of the elements that the threads' maxima are of: the n-th largest of those (the waves'
+    // sorted lists, merged two by two).
+    const auto bound = [&](float top) {
+        uint32_t k = wave_sort_desc(order_key(top));
+        if (tid == 0) sm.count = sm.full = 0;
+        staged = 0;
+#pragma unroll
+        for (int w = 1; w < kWaves; w <<= 1) {
+            uint32_t(&list)[kWaves][kWave] = sm.lists[w == 2 ? 1 : 0];
+            if (w == 4) __syncthreads();                // the first lists have been read
+            list[wave][lane] = k;
+            __syncthreads();
+            k = wave_bitonic_clean(max(k, list[wave ^ w][kWave - 1 - lane]), true);
+        }
+        return fmaxf(order_value(lane_gather(k, a.top_n - 1)), -FLT_MAX);       // -inf is in no list
+    };
+
 #pragma unroll
     for (int j = 0; j < NV; j += kGroup) {
         float mx = vec_max<DT>(v[j]);
 #pragma unroll
         for (int e = 1; e < kGroup; ++e) mx = __builtin_elementwise_maximum(mx, vec_max<DT>(v[j + e]));
         look(mx);
-#pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-#pragma unroll
-            for (int i = 0; i < PV; ++i) add(exponent(E::get(v[j + e], i), a.c, ref));
-        }
+        sum(v + j, first + j * kLpThreads + tid);
 #pragma unroll
         for (int e = 0; e < kGroup; ++e) asm volatile("" : "+v"(v[j + e]));     // widened again later, not kept
+    }
+    u32x4 ahead[kGroup];                                // under way while the bound is found
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) ahead[j] = fetch(first + (NV + j) * kLpThreads + tid);
+    if (TOP) tau = bound(tm);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = first + j * kLpThreads + tid;
+        if (TOP) offer(v[j], vec_max<DT>(v[j]), i);
+        v[j] = j < kGroup ? ahead[j] : fetch(i + NV * kLpThreads);
+    }
+    // the rest of the slice, each register's next vector under way as soon as it is free
+#pragma unroll 1
+    for (int base = first + NV * kLpThreads; base < last; base += NV * kLpThreads) {
+#pragma unroll
+        for (int j = 0; j < NV; j += kGroup) {
+            float own[kGroup], mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) {
+                own[e] = vec_max<DT>(v[j + e]);
+                mx = __builtin_elementwise_maximum(mx, own[e]);
+            }
+            look(mx);
+            sum(v + j, base + j * kLpThreads + tid);
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) {
+                const int i = base + (j + e) * kLpThreads + tid;
+                if (TOP) offer(v[j + e], own[e], i);
+                v[j + e] = fetch(i + NV * kLpThreads);
+            }
+        }
     }
     if (slice == a.slices - 1) {
         look(z_rest);
@@ -208,91 +295,93 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     {
         const float w = wave_maximum(tm);
         if (lane == 0) sm.red[wave] = w;
-    }
-    float tau = INFINITY;
-    if (TOP) {
-        const uint32_t k = wave_sort_desc(order_key(tm));
-        if (lane == (a.top_n + kWaves - 1) / kWaves - 1) sm.keys[wave] = k;
-        if (lane == a.top_n - 1) sm.alone[wave] = k;
-        if (tid == 0) sm.count = sm.staged = 0;
+        if (TOP && staged > kStage) sm.full = 1;
     }
     __syncthreads();
     float m = sm.red[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = __builtin_elementwise_maximum(m, sm.red[w]);
     const bool wide = is_wide(m, a.c), some = m > -INFINITY && m < INFINITY;
-    if (TOP && some) {
-        uint32_t k = sm.keys[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) k = min(k, sm.keys[w]);
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) k = max(k, sm.alone[w]);       // a short slice leaves waves without elements
-        tau = fmaxf(order_value(k), -FLT_MAX);          // -inf is in no list (nor its order_value's NaN)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (vec_max<DT>(v[j]) >= tau) {
-                const int at = atomicAdd(&sm.staged, 1);
-                if (at < kStage) {
-                    sm.stage[at] = v[j];
-                    sm.stage_i[at] = (first + j * kLpThreads + tid) * PV;
-                }
-            }
-        }
-        if (has_rest && z_rest >= tau) {
-            const int at = atomicAdd(&sm.count, 1);     // at most PV - 1 of them
-            sm.cand[at] = pair_key(z_rest, rest);
-        }
-    }
     if (some && wide) {
         // m*c is no finite number: the sums once more, from the differences
         S = W = 0.f;
 #pragma unroll 1
-        for (int i = first * PV + tid; i < min(vecs, first + NV * kLpThreads) * PV; i += kLpThreads)
-            add(exponent_wide(E::scalar(row, i), a.c, m));
+        for (int i = first * PV + tid; i < last * PV; i += kLpThreads) add(exponent_wide(E::scalar(row, i), a.c, m));
         if (has_rest) add(exponent_wide(z_rest, a.c, m));
         ref = 0.f;
     }
     S = wave_sum(S);
     W = wave_sum(W);
-    __syncthreads();
     if (lane == 0) sm.sums[wave][0] = S, sm.sums[wave][1] = W, sm.sums[wave][2] = ref;
-    if (TOP) {
-        for (int i = tid; i < min(sm.staged, kStage); i += kLpThreads) {
-            const u32x4 w = sm.stage[i];
-#pragma unroll
-            for (int e = 0; e < PV; ++e) {
-                const float z = E::get(w, e);
-                if (z >= tau) {
-                    const int at = atomicAdd(&sm.count, 1);
-                    if (at < kCand) sm.cand[at] = pair_key(z, sm.stage_i[i] + e);
-                }
-            }
-        }
-    }
-    __syncthreads();
 
     pkey_t key = empty_key();
     if (TOP && some) {
-        const int count = sm.count;
-        if (sm.staged <= kStage && count <= kCand) {
-            if (wave == 0) {
-                for (int base = 0; base < count; base += kWave) {
-                    pkey_t k = base + lane < count ? sm.cand[base + lane] : empty_key();
-                    wave_sort_keys(k);
-                    if (base == 0) key = k;
-                    else wave_merge_keys(key, k);
-                }
+        if (sm.full) {                                  // the same in every thread
+            __syncthreads();
+            tau = bound(tm);
+#pragma unroll 1
+            for (int base = first; base < last; base += kLpThreads) {
+                const u32x4 w = fetch(base + tid);
+                offer(w, vec_max<DT>(w), base + tid);
             }
+            if (staged > kStage) sm.full = 1;
+            __syncthreads();
+        }
+        // a staged vector a lane: its elements that reach tau go behind those of the lanes, and the waves, before
+        const bool one = lane < min(staged, kStage);
+        const u32x4 w = sm.stage[wave][lane];
+        const int at0 = sm.stage_i[wave][lane];
+        int hits = 0;
+#pragma unroll
+        for (int e = 0; e < PV; ++e) hits += one && E::get(w, e) >= tau ? 1 : 0;
+        hits += has_rest && z_rest >= tau ? 1 : 0;
+        int upto = hits;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int t = __shfl_up(upto, o, kWave);
+            if (lane >= o) upto += t;
+        }
+        int at = 0;
+        if (lane == kWave - 1) at = atomicAdd(&sm.count, upto);
+        at = bcast(at, kWave - 1) + upto - hits;
+#pragma unroll
+        for (int e = 0; e < PV; ++e) {
+            const float z = E::get(w, e);
+            if (one && z >= tau) {
+                if (at < kCand) sm.cand[at] = pair_key(z, at0 + e);
+                ++at;
+            }
+        }
+        if (has_rest && z_rest >= tau && at < kCand) sm.cand[at] = pair_key(z_rest, rest);
+        __syncthreads();
+        const int count = sm.count;
+        if (!sm.full && count <= kCand) {
+            // kShare neighbouring threads an element (all of them at once, or in turns): as many are better as its place says
+            if (tid < kWave) sm.best[tid] = empty_key();
+            __syncthreads();
+            constexpr int kShare = 4;
+            for (int base = 0; base < count; base += kLpThreads / kShare) {
+                const int mine = base + tid / kShare;
+                const pkey_t k = mine < count ? sm.cand[mine] : 0;
+                int place = 0;
+#pragma unroll 4
+                for (int i = tid % kShare; i < count; i += kShare) place += sm.cand[i] > k;
+                place += xshfl(place, 1);
+                place += xshfl(place, 2);
+                if (mine < count && place < a.top_n) sm.best[place] = k;
+            }
+            __syncthreads();
+            key = sm.best[lane];
         } else {
             // many equal elements: the best one below the last found, n times
-            const int end = slice == a.slices - 1 ? a.V : (first + NV * kLpThreads) * PV;
-            pkey_t last = ~0ull;
+            const int end = slice == a.slices - 1 ? a.V : last * PV;
+            pkey_t found = ~0ull;
             for (int n = 0; n < a.top_n; ++n) {
                 pkey_t best = 0;
 #pragma unroll 1
                 for (int i = first * PV + tid; i < end; i += kLpThreads) {
                     const pkey_t k = pair_key(E::scalar(row, i), i);
-                    if (k < last && k > best) best = k;
+                    if (k < found && k > best) best = k;
                 }
 #pragma unroll
                 for (int o = 32; o > 0; o >>= 1) {
@@ -306,9 +395,11 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
                 for (int w = 0; w < kWaves; ++w) best = sm.best[w] > best ? sm.best[w] : best;
                 if (best == 0 || key_val(best) == -INFINITY) break;
                 if (lane == n) key = best;
-                last = best;
+                found = best;
             }
         }
+    } else {
+        __syncthreads();
     }
     if (wave != 0) return;
     // the waves' sums, relative to m*c (or to m where that is no finite number)
@@ -316,8 +407,9 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     const float mc = wide ? 0.f : m * a.c;
     S = W = 0.f;
     if (some) {
-        const float d = lane < kWaves ? sm.sums[lane & 3][2] - mc : -INFINITY, f = exp2_fast(d);
-        const float Sw = sm.sums[lane & 3][0], Ww = sm.sums[lane & 3][1];
+        const int w = lane % kWaves;
+        const float d = lane < kWaves ? sm.sums[w][2] - mc : -INFINITY, f = exp2_fast(d);
+        const float Sw = sm.sums[w][0], Ww = sm.sums[w][1];
         S = wave_sum(f > 0.f ? Sw * f : 0.f);
         W = wave_sum(f > 0.f ? f * __builtin_fmaf(Sw, d, Ww) : 0.f);
     }
@@ -388,10 +480,10 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
 
 // Gradient: dz_i = p_i (A + B x'_i) + (1/T) sum_m g_m [i = t_m], x' = log2 p_i, A = -(G + h H)/T, B = -h ln2 / T,
 // G = sum g_m.  One pass; the elements of given tokens are written once more, after the row's own pass.
-constexpr int kGradVecs = 4;
+constexpr int kGradVecs = 4, kGradThreads = 256;
 
 template <int DT, bool ENT>
-__global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradArgs a) {
+__global__ __launch_bounds__(kGradThreads) void logprobs_grad_kernel(LogprobGradArgs a) {
     using E = Elem<DT>;
     constexpr int PV = E::kPerVec;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -399,7 +491,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradAr
     const int slice = blockIdx.x % a.slices;
     const char* row = static_cast<const char*>(a.logits) + r * a.stride * E::kBytes;
     char* out = static_cast<char*>(a.grad) + r * a.grad_stride * E::kBytes;
-    const int vecs = a.V / PV, first = slice * (kGradVecs * kLpThreads);
+    const int vecs = a.V / PV, first = slice * (kGradVecs * kGradThreads);
     int tok;
     bool bad;
     const bool used = row_used(a.tokens + r * a.M, a.M, a.V, tok, bad);
@@ -413,7 +505,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradAr
         const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int j = 0; j < kGradVecs; ++j) {
-            const int i = first + j * kLpThreads + tid;
+            const int i = first + j * kGradThreads + tid;
             if (i < vecs) store_vec<DT>(out, static_cast<long>(i) * PV, zero);
         }
         if (has_rest) put(rest, 0.f);
@@ -422,13 +514,13 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradAr
     u32x4 v[kGradVecs];
 #pragma unroll
     for (int j = 0; j < kGradVecs; ++j) {
-        const int i = first + j * kLpThreads + tid;
+        const int i = first + j * kGradThreads + tid;
         if (i < vecs) v[j] = load_vec<DT>(row, static_cast<long>(i) * PV);
     }
     const float z_rest = has_rest ? E::scalar(row, rest) : 0.f;
     // the given tokens of this slice (lane m has token m, in every wave)
     const bool last = slice == a.slices - 1;
-    const bool mine = !bad && tok >= first * PV && (last || tok < (first + kGradVecs * kLpThreads) * PV);
+    const bool mine = !bad && tok >= first * PV && (last || tok < (first + kGradVecs * kGradThreads) * PV);
     const float z_tok = mine ? E::scalar(row, tok) : 0.f;
     const float g = a.g_lp && tok >= 0 && lane < a.M ? a.g_lp[r * a.M + lane] : 0.f;
     const float m = a.stats[kLpStats * r], l = bad ? __builtin_nanf("") : a.stats[kLpStats * r + 1];
@@ -447,7 +539,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobGradAr
     __syncthreads();                                    // the gradient may take the logits' place: z_tok is read
 #pragma unroll
     for (int j = 0; j < kGradVecs; ++j) {
-        const int i = first + j * kLpThreads + tid;
+        const int i = first + j * kGradThreads + tid;
         if (i >= vecs) continue;
         u32x4 o;
 #pragma unroll
@@ -475,25 +567,27 @@ template <int DT, int NV> void logprobs(const LogprobArgs& a, hipStream_t s, Tim
     else launch_timed(t, logprobs_kernel<DT, NV, false>, grid, dim3(kLpThreads), 0, s, a);
 }
 template <int DT> void logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
-    if (a.vecs == 4) logprobs<DT, 4>(a, s, t);
-    else logprobs<DT, 16>(a, s, t);
-}
-
-int slices_of(int V, int dtype, int vecs) {
-    const int elems = vecs * kLpThreads * (dtype == 1 ? 8 : 4);
-    const int n = (V + elems - 1) / elems;
-    return n < 1 ? 1 : n;
+    if (a.per <= kFewVecs * kLpThreads) logprobs<DT, kFewVecs>(a, s, t);
+    else logprobs<DT, kLpVecs>(a, s, t);
 }
 
 }  // namespace
 
-// A slice is as large as registers allow where the rows fill the GPU, and smaller where they are few, so that their loads
-// spread over the compute units.
+// A workgroup a row where the rows fill the GPU twice over (two fit a compute unit); fewer rows are cut up, so that their loads
+// spread over the compute units, into slices of four vectors a thread at least.
 void logprob_plan(LogprobArgs& a) {
-    a.vecs = kLpMaxVecs;
-    const int n = slices_of(a.V, a.dtype, 4);
-    if (n <= kWave && static_cast<long>(a.R) * n <= 512) a.vecs = 4;
-    a.slices = slices_of(a.V, a.dtype, a.vecs);
+    const int vecs = a.V / (a.dtype == 1 ? 8 : 4), least = kFewVecs * kLpThreads;
+    const int wanted = a.R < kLpWorkgroups ? (kLpWorkgroups + a.R - 1) / a.R : 1;
+    int per = (vecs + wanted - 1) / wanted;
+    per = (per + kLpThreads - 1) / kLpThreads * kLpThreads;
+    if (per < least) per = least;
+    a.slices = (vecs + per - 1) / per;
+    if (a.slices > kWave) {                             // joined one a lane
+        per = ((vecs + kWave - 1) / kWave + kLpThreads - 1) / kLpThreads * kLpThreads;
+        a.slices = (vecs + per - 1) / per;
+    }
+    if (a.slices < 1) a.slices = 1;
+    a.per = per;
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
@@ -502,16 +596,19 @@ hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
     return hipGetLastError();
 }
 
-int logprob_grad_slices(int dtype, int V) { return slices_of(V, dtype, kGradVecs); }
+int logprob_grad_slices(int dtype, int V) {
+    const int elems = kGradVecs * kGradThreads * (dtype == 1 ? 8 : 4), n = (V + elems - 1) / elems;
+    return n < 1 ? 1 : n;
+}
 
 hipError_t launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s, Timing t) {
     const dim3 grid(static_cast<unsigned>(static_cast<long>(a.R) * a.slices));
     if (a.dtype == 1) {
-        if (a.g_entropy) launch_timed(t, logprobs_grad_kernel<1, true>, grid, dim3(kLpThreads), 0, s, a);
-        else launch_timed(t, logprobs_grad_kernel<1, false>, grid, dim3(kLpThreads), 0, s, a);
+        if (a.g_entropy) launch_timed(t, logprobs_grad_kernel<1, true>, grid, dim3(kGradThreads), 0, s, a);
+        else launch_timed(t, logprobs_grad_kernel<1, false>, grid, dim3(kGradThreads), 0, s, a);
     } else {
-        if (a.g_entropy) launch_timed(t, logprobs_grad_kernel<0, true>, grid, dim3(kLpThreads), 0, s, a);
-        else launch_timed(t, logprobs_grad_kernel<0, false>, grid, dim3(kLpThreads), 0, s, a);
+        if (a.g_entropy) launch_timed(t, logprobs_grad_kernel<0, true>, grid, dim3(kGradThreads), 0, s, a);
+        else launch_timed(t, logprobs_grad_kernel<0, false>, grid, dim3(kGradThreads), 0, s, a);
     }
     return hipGetLastError();
 }

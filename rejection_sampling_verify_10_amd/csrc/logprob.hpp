@@ -6,8 +6,7 @@
 
 namespace sv {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpMaxVecs = 16;      // 16-byte vectors a thread holds: slices of up to 64 KiB
+constexpr int kLpThreads = 512;
 constexpr int kLpStats = 3;         // floats of a row's statistics: largest logit, log2 of the sum, entropy
 
 struct LogprobArgs {
@@ -22,7 +21,7 @@ struct LogprobArgs {
     float* out_stats;               // [R][kLpStats] or null
     int32_t* out_top;               // [R][top_n]
     float* out_top_lp;              // [R][top_n]
-    int vecs, slices;               // vectors a thread, workgroups a row
+    int per, slices;                // vectors of a workgroup, workgroups a row
     unsigned long long* words;      // [R][slices][kLpHead + top_n] (slices > 1), zero before and after a call
     unsigned* done;                 // [R] slices that have written theirs, zero before and after a call
 };
@@ -42,7 +41,7 @@ struct LogprobGradArgs {
     int slices;                     // workgroups a row
 };
 
-// Fills vecs and slices.
+// Fills per and slices.
 void logprob_plan(LogprobArgs& a);
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s, Timing t = {});
 hipError_t launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s, Timing t = {});
