@@ -704,8 +704,8 @@ int spec_accept_rate(const void* target_logits, spec_dtype_t dtype, const float*
  *                that overlap nothing
  *   out_granted  [T] int32: counts[t] (0 for a row that has ended), or -1: not enough pages,
  *                counts[t] outside [0, N], more than width pages needed, or held[t] outside
- *                [0, width]; nothing of such a row changes.  It can be the `counts` of the
- *                calls below, which leave rows of -1 out.
+ *                [0, min(width, pages)]; nothing of such a row changes.  It can be the `counts`
+ *                of the calls below, which leave rows of -1 out.
  *   out_slots    [T][N] int32: the slot of token n (its place is lengths[t] + n), -1 for
  *                n >= granted[t], and where the page's number is none of the pool's
  * A state outside [0, pages) and [0, pages] serves no row and is left as it is.
@@ -769,8 +769,8 @@ int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int 
  * (mask NULL) or with mask[b][n][m] != 0.
  *   q          rows of (b, n, hq), SPEC_F32 or SPEC_BF16; mask, scale, out, out_lse: as for
  *              spec_kvq_attention
- *   tables     [T][width], rows table_stride elements apart; B, N, q_heads, width and page_size as
- *              the plan was made with.  A call whose sizes are not the plan's writes nothing.
+ *   tables     [T][width], rows table_stride elements apart; B, N, q_heads, heads, width and page_size
+ *              as the plan was made with.  A call whose sizes are not the plan's writes nothing.
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros and an out_lse
  * of -inf.  What a query does not see never reaches it, whatever its bytes.  One that sees a slot
  * whose K or V holds a NaN or an infinity gives unspecified numbers; one that sees a slot whose

@@ -432,8 +432,9 @@ bool paged_sizes(PagedPlanArgs& a, int q_heads, int heads, bool with_prefix) {
     if (!kvq_sizes_ok(a.B, heads, a.N, q_heads / heads)) return false;
     a.G = q_heads / heads;
     a.M = a.N * a.G;
+    a.heads = heads;
     a.prefix_row = with_prefix ? &some : nullptr;       // only whether there is one counts
-    paged_plan_sizes(a, heads);
+    paged_plan_sizes(a);
     const double workgroups = static_cast<double>(a.max_units) * heads, rows = static_cast<double>(a.B) * a.N * q_heads;
     // parts are joined 1024 / D rows a workgroup of 256, at most 16 threads a row each
     return kvq_threads_ok(workgroups, 256) && rows * 64 < 4294967296.0 && a.max_parts < (1ll << 31);

@@ -536,7 +536,10 @@ __global__ __launch_bounds__(kGradThreads) void logprobs_grad_kernel(LogprobGrad
         const float p = exp2_fast(x);
         return ENT ? p * __builtin_fmaf(B, x, A) : p * A;
     };
-    __syncthreads();                                    // the gradient may take the logits' place: z_tok is read
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" ::"v"(z_tok));                      // the gradient may take the logits' place: z_tok has arrived
+#endif
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kGradVecs; ++j) {
         const int i = first + j * kGradThreads + tid;

@@ -78,7 +78,7 @@ struct PagedOwn {
     int first, count;
 };
 
-constexpr int kPgHead = 6;
+constexpr int kPgHead = 7;
 struct PagedPlan {                  // device memory
     int32_t* head;                  // [kPgHead]: units, and the sizes it was made for
     PagedUnit* unit;                // [max_units]
@@ -86,7 +86,7 @@ struct PagedPlan {                  // device memory
     PagedOwn* own;                  // [B][own_tiles]
 };
 struct PagedPlanArgs {
-    int B, N, T, M, width, page_log2;
+    int B, N, T, M, heads, width, page_log2;
     const int32_t* lengths;         // [T]
     const int32_t* counts;          // [B] or null
     const int32_t* prefix_row;      // [B] or null
@@ -96,7 +96,7 @@ struct PagedPlanArgs {
     long long max_units, max_parts; // most units, and rows of parts
     PagedPlan p;
 };
-void paged_plan_sizes(PagedPlanArgs& a, int heads);
+void paged_plan_sizes(PagedPlanArgs& a);
 hipError_t launch_paged_plan(const PagedPlanArgs& a, hipStream_t s, Timing t = {});
 
 struct PagedAttnArgs {

@@ -184,6 +184,7 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
             a.p.head[3] = a.M;
             a.p.head[4] = a.prefix_row != nullptr;
             a.p.head[5] = a.width << a.page_log2;
+            a.p.head[6] = a.heads;
         }
     }
     __syncthreads();
@@ -275,11 +276,11 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
 
 // The key axes are split into about 512 workgroups (two a compute unit); a batch whose own rows alone are as many is not
 // split, unless there are prefixes.
-void paged_plan_sizes(PagedPlanArgs& a, int heads) {
+void paged_plan_sizes(PagedPlanArgs& a) {
     a.own_rows = a.M <= kPgNarrow ? kPgNarrow : kPgWide;
     a.own_tiles = (a.M + a.own_rows - 1) / a.own_rows;
     const long long own = static_cast<long long>(a.B) * a.own_tiles;
-    const long long target = (512 + heads - 1) / heads;
+    const long long target = (512 + a.heads - 1) / a.heads;
     a.target = a.prefix_row || own < target ? static_cast<int>(target) : 0;
     // a unit more than the split for each job; a run's rows come to one tile more than fit
     const long long rows = static_cast<long long>(a.B) * a.M;

@@ -39,7 +39,8 @@ __device__ __forceinline__ Need read_need(const PageStepArgs& a, int t) {
     const bool live = n.len >= 0;
     const long long end = live ? static_cast<long long>(n.len) + n.cnt : 0;
     const long long need = (end + (1 << a.page_log2) - 1) >> a.page_log2;
-    n.ok = n.held >= 0 && n.held <= a.width && (!live || (n.cnt >= 0 && n.cnt <= a.N)) && need <= a.width;
+    // (more pages than there are would wrap around the ring twice)
+    n.ok = n.held >= 0 && n.held <= min(a.width, a.pages) && (!live || (n.cnt >= 0 && n.cnt <= a.N)) && need <= a.width;
     n.need = n.ok ? static_cast<int>(need) : 0;
     if (!live) n.cnt = 0;
     return n;

@@ -22,7 +22,7 @@ def page_step(tables, held, ring, state, lengths, counts, N, P):
             c, need = 0, 0
         else:
             need = -(-(n + c) // P)
-        if not 0 <= have <= width or not 0 <= c <= N or need > width:
+        if not 0 <= have <= min(width, pages) or not 0 <= c <= N or need > width:
             continue
         grow = max(need - have, 0)
         asked += grow

@@ -113,6 +113,15 @@ def test_a_ring_out_of_range_serves_nobody(R, state):
     assert pool.state.tolist() == list(state) and (pool.tables == -1).all() and pool.ring.tolist() == list(range(6))
 
 
+def test_more_pages_held_than_there_are(R):
+    """Such a row's numbers make no sense: it is not served, and the ring keeps its other entries."""
+    pool = R.new_page_pool(2, 40, 3, 16, "cuda")
+    pool.held.copy_(ints([30, 0]))
+    granted, slots = R.page_step(pool, ints([-1, 0]), 3)
+    assert granted.tolist() == [-1, 3] and slots.tolist() == [[-1, -1, -1], [0, 1, 2]]
+    assert pool.held.tolist() == [30, 1] and pool.state.tolist() == [1, 2] and pool.ring.tolist() == [0, 1, 2]
+
+
 def test_pages_that_are_none_have_no_slots(R):
     pool = R.new_page_pool(1, 4, 3, 16, "cuda")
     pool.ring.copy_(ints([3, -1, 2]))
@@ -383,6 +392,52 @@ def test_a_plan_of_other_sizes_writes_nothing(R):
     q = queries(rng, 2, 3, 4, 64, "f32")
     R.paged_attention(q, cache, plan, out=out)
     assert (out[0] == 7).all() and (out[1] == 7).all()
+
+
+def test_a_plan_of_other_heads_writes_nothing(R):
+    """As many query rows a head, but the plan cuts them up by the number of heads."""
+    import torch
+    rng = np.random.default_rng(2)
+    tables, lens = ints([[0, 1], [2, 3], [4, 5]]), ints([5, 9, 20])
+    four, two = make_cache(R, rng, 8, 16, 4, 64), make_cache(R, rng, 8, 16, 2, 64)
+    plan = R.paged_plan(four, tables, lens, 3, 8, B=2, prefix_row=ints([2, 2]))
+    other = R.paged_plan(two, tables, lens, 3, 4, B=2, prefix_row=ints([2, 2]))
+    assert other.bytes > plan.bytes
+    plan._buffer, plan._ptr, plan.bytes = other._buffer, other._ptr, other.bytes
+    out = (torch.full((2, 3, 8, 64), 7.0, device="cuda"), torch.full((2, 3, 8), 7.0, device="cuda"))
+    R.paged_attention(queries(rng, 2, 3, 8, 64, "f32"), four, plan, out=out)
+    assert (out[0] == 7).all() and (out[1] == 7).all()
+
+
+@pytest.mark.parametrize("layout", ["slots", "outer"])
+def test_offsets_past_32_bits(R, layout):
+    """Pages all over a cache of more than 2^32 bytes (and 2^31 elements): what a small cache of the same rows gives."""
+    import torch
+    rng = np.random.default_rng(6)
+    B, N, H, G, D, P = 3, 2, 8, 2, 128, 16
+    lens, width = [300, 40, 700], 50
+    few, many = 120, 140001
+    shape = [(many, P, H)[i] for i in LAYOUTS[layout]] + [D]
+    back = [LAYOUTS[layout].index(i) for i in range(3)] + [3]
+    big = R.PagedCache(*(torch.empty(shape, dtype=torch.bfloat16, device="cuda").permute(*back) for _ in range(2)))
+    small = make_cache(R, rng, few, P, H, D)
+    at = np.append(rng.choice(many - 1, few - 1, replace=False), many - 1)       # where its pages lie in the big one
+    for to, src in ((big.k_pages, small.k_pages), (big.v_pages, small.v_pages)):
+        to[dev(at)] = src
+    tables = make_tables(rng, few, P, lens, N, 2, width)
+    tables[2][:3] = few - 1, tables[2][1], few - 1
+    far = np.where(tables < 0, -1, at[tables])
+    kv = torch.from_numpy(rng.standard_normal((2, 2, N, H, D)).astype(np.float32)).cuda()
+    q = queries(rng, 2, N, H * G, D, "bf16")
+    got = []
+    for cache, t in ((small, tables), (big, far)):
+        slots = np.array([[t[b, (lens[b] + n) // P] * P + (lens[b] + n) % P for n in range(N)] for b in range(2)])
+        R.paged_append(cache, kv[:, 0], kv[:, 1], ints(slots))
+        plan = R.paged_plan(cache, ints(t), ints(lens), N, H * G, B=2, prefix_row=ints([2, 2]))
+        got.append(R.paged_attention(q, cache, plan))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]) and torch.isfinite(got[0][0]).all()
+    for a, b in ((small.k_pages, big.k_pages), (small.v_pages, big.v_pages)):
+        assert torch.equal(a.contiguous(), b[dev(at)].contiguous())
 
 
 def test_streams_and_graphs(R):
