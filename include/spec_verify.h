@@ -757,10 +757,10 @@ int spec_paged_append(const spec_paged_cache_t* cache, const spec_kvq_rows_t* k,
  * A batch row with lengths[b] < 0, counts[b] outside [0, N], more slots than width * page_size,
  * or a prefix_row of T or more, or one whose length is outside [0, width * page_size], is an error row.
  */
-size_t spec_paged_plan_bytes(int B, int N, int q_heads, int heads, int with_prefix);
-int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int page_size, const int32_t* lengths,
-                    const int32_t* counts, const int32_t* prefix_row, void* plan, size_t plan_bytes,
-                    void* hip_stream);
+size_t spec_paged_plan_bytes(int B, int N, int q_heads, int heads, int head_dim, int with_prefix);
+int spec_paged_plan(int B, int N, int q_heads, int heads, int head_dim, int T, int width, int page_size,
+                    const int32_t* lengths, const int32_t* counts, const int32_t* prefix_row, void* plan,
+                    size_t plan_bytes, void* hip_stream);
 
 /*
  * spec_paged_attention -- softmax attention of N new tokens' queries.  Query (b, n, hq)
@@ -769,8 +769,8 @@ int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int 
  * (mask NULL) or with mask[b][n][m] != 0.
  *   q          rows of (b, n, hq), SPEC_F32 or SPEC_BF16; mask, scale, out, out_lse: as for
  *              spec_kvq_attention
- *   tables     [T][width], rows table_stride elements apart; B, N, q_heads, heads, width and page_size
- *              as the plan was made with.  A call whose sizes are not the plan's writes nothing.
+ *   tables     [T][width], rows table_stride elements apart; B, N, q_heads, heads, head_dim, width and
+ *              page_size as the plan was made with.  A call whose sizes are not the plan's writes nothing.
  * A query that sees no slot, tokens n >= counts[b] and error rows answer zeros and an out_lse
  * of -inf.  What a query does not see never reaches it, whatever its bytes.  One that sees a slot
  * whose K or V holds a NaN or an infinity gives unspecified numbers; one that sees a slot whose

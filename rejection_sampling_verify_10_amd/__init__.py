@@ -107,9 +107,9 @@ def lib() -> ctypes.CDLL:
         L.spec_page_step.restype = I
         L.spec_paged_append.argtypes = [P, P, P, I, I, I, I, P, LL, P, I, P, P]
         L.spec_paged_append.restype = I
-        L.spec_paged_plan_bytes.argtypes = [I, I, I, I, I]
+        L.spec_paged_plan_bytes.argtypes = [I, I, I, I, I, I]
         L.spec_paged_plan_bytes.restype = Z
-        L.spec_paged_plan.argtypes = [I, I, I, I, I, I, I, P, P, P, P, Z, P]
+        L.spec_paged_plan.argtypes = [I, I, I, I, I, I, I, I, P, P, P, P, Z, P]
         L.spec_paged_plan.restype = I
         L.spec_paged_attention_workspace_bytes.argtypes = [I, I, I, I, I, I]
         L.spec_paged_attention_workspace_bytes.restype = Z

@@ -427,12 +427,13 @@ int take_pages(const spec_paged_cache_t* c, PagedCache& o) {
 }
 
 // The plan's sizes; false where a call of them is past the limits.
-bool paged_sizes(PagedPlanArgs& a, int q_heads, int heads, bool with_prefix) {
+bool paged_sizes(PagedPlanArgs& a, int q_heads, int heads, int head_dim, bool with_prefix) {
     static const int32_t some = 0;
     if (!kvq_sizes_ok(a.B, heads, a.N, q_heads / heads)) return false;
     a.G = q_heads / heads;
     a.M = a.N * a.G;
     a.heads = heads;
+    a.D = head_dim;
     a.prefix_row = with_prefix ? &some : nullptr;       // only whether there is one counts
     paged_plan_sizes(a);
     const double workgroups = static_cast<double>(a.max_units) * heads, rows = static_cast<double>(a.B) * a.N * q_heads;
@@ -1508,20 +1509,20 @@ int spec_paged_append(const spec_paged_cache_t* cache, const spec_kvq_rows_t* k,
     return SPEC_OK;
 }
 
-size_t spec_paged_plan_bytes(int B, int N, int q_heads, int heads, int with_prefix) {
-    if (!paged_args_ok(B, N, q_heads, heads)) return 0;
+size_t spec_paged_plan_bytes(int B, int N, int q_heads, int heads, int head_dim, int with_prefix) {
+    if (!paged_args_ok(B, N, q_heads, heads) || !kvq_dim_ok(head_dim)) return 0;
     PagedPlanArgs a{};
     a.B = B;
     a.N = N;
-    if (!paged_sizes(a, q_heads, heads, with_prefix != 0)) return 0;
+    if (!paged_sizes(a, q_heads, heads, head_dim, with_prefix != 0)) return 0;
     Carver c(nullptr);
     carve_paged_plan(c, a, a.p);
     return c.off;
 }
 
-int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int page_size, const int32_t* lengths,
-                    const int32_t* counts, const int32_t* prefix_row, void* plan, size_t plan_bytes,
-                    void* hip_stream) {
+int spec_paged_plan(int B, int N, int q_heads, int heads, int head_dim, int T, int width, int page_size,
+                    const int32_t* lengths, const int32_t* counts, const int32_t* prefix_row, void* plan,
+                    size_t plan_bytes, void* hip_stream) {
     if (!paged_args_ok(B, N, q_heads, heads) || T < B || width < 1 || !page_size_ok(page_size) || !lengths ||
         !aligned(lengths, 4) || !aligned(counts, 4) || !aligned(prefix_row, 4))
         return SPEC_EINVAL;
@@ -1529,7 +1530,7 @@ int spec_paged_plan(int B, int N, int q_heads, int heads, int T, int width, int 
     a.B = B;
     a.N = N;
     a.T = T;
-    if (!slots_ok(width, page_size) || !paged_sizes(a, q_heads, heads, prefix_row != nullptr)) return SPEC_EUNSUPPORTED;
+    if (!kvq_dim_ok(head_dim) || !slots_ok(width, page_size) || !paged_sizes(a, q_heads, heads, head_dim, prefix_row != nullptr)) return SPEC_EUNSUPPORTED;
     a.width = width;
     a.page_log2 = log2_of(page_size);
     a.lengths = lengths;
@@ -1551,7 +1552,7 @@ size_t spec_paged_attention_workspace_bytes(int B, int N, int q_heads, int heads
     PagedPlanArgs p{};
     p.B = B;
     p.N = N;
-    if (!paged_sizes(p, q_heads, heads, with_prefix != 0)) return 0;
+    if (!paged_sizes(p, q_heads, heads, head_dim, with_prefix != 0)) return 0;
     Carver c(nullptr);
     PagedAttnArgs a{};
     carve_paged_parts(c, p, heads, head_dim, a);
@@ -1578,7 +1579,7 @@ int spec_paged_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int B, in
     p.B = B;
     p.N = N;
     if (!slots_ok(width, cache->page_size) || table_stride > (1ll << 40) || (mask && N > SPEC_MAX_NODES) ||
-        !paged_sizes(p, q_heads, a.c.H, with_prefix != 0))
+        !paged_sizes(p, q_heads, a.c.H, a.c.D, with_prefix != 0))
         return SPEC_EUNSUPPORTED;
     Carver plan_size(nullptr);
     carve_paged_plan(plan_size, p, a.p);
@@ -1603,7 +1604,7 @@ int spec_paged_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int B, in
     a.table_stride = table_stride;
     a.own_rows = p.own_rows;
     a.own_tiles = p.own_tiles;
-    a.with_prefix = with_prefix != 0;
+    a.shape = p.shape;
     a.capacity = width * cache->page_size;
     a.max_units = p.max_units;
     a.mask = mask;

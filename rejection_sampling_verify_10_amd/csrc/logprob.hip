@@ -576,8 +576,8 @@ template <int DT> void logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
 
 }  // namespace
 
-// A workgroup a row where the rows fill the GPU twice over (two fit a compute unit); fewer rows are cut up, so that their loads
-// spread over the compute units, into slices of four vectors a thread at least.
+// A workgroup a row where there is a row for each compute unit (512 rows of 128256 bf16 logits: 27 us, two workgroups a row 38);
+// fewer rows are cut up, so that their loads spread over the compute units, into slices of four vectors a thread at least.
 void logprob_plan(LogprobArgs& a) {
     const int vecs = a.V / (a.dtype == 1 ? 8 : 4), least = kFewVecs * kLpThreads;
     const int wanted = a.R < kLpWorkgroups ? (kLpWorkgroups + a.R - 1) / a.R : 1;

@@ -78,7 +78,7 @@ struct PagedOwn {
     int first, count;
 };
 
-constexpr int kPgHead = 7;
+constexpr int kPgHead = 6;
 struct PagedPlan {                  // device memory
     int32_t* head;                  // [kPgHead]: units, and the sizes it was made for
     PagedUnit* unit;                // [max_units]
@@ -86,13 +86,14 @@ struct PagedPlan {                  // device memory
     PagedOwn* own;                  // [B][own_tiles]
 };
 struct PagedPlanArgs {
-    int B, N, T, M, heads, width, page_log2;
+    int B, N, T, M, heads, D, width, page_log2;
     const int32_t* lengths;         // [T]
     const int32_t* counts;          // [B] or null
     const int32_t* prefix_row;      // [B] or null
     // from the sizes alone (paged_plan_sizes)
     int G, own_rows, own_tiles;     // query rows a unit of own slots, units a batch row
     int target;                     // units the key axes are split into, 0: not at all
+    int shape;                      // heads, D and whether there are prefixes, as far as the plan goes by them
     long long max_units, max_parts; // most units, and rows of parts
     PagedPlan p;
 };
@@ -106,7 +107,7 @@ struct PagedAttnArgs {
     const int32_t* tables;
     long long table_stride;
     PagedPlan p;
-    int own_rows, own_tiles, with_prefix, capacity;
+    int own_rows, own_tiles, shape, capacity;
     long long max_units;
     const uint8_t* mask;
     long long mask_batch;

@@ -642,10 +642,10 @@ template <int D, int DT> __device__ __forceinline__ void attend_narrow(const Pag
 // Whether the plan was made for a call of these sizes (one that was not names rows that are not there).
 __device__ __forceinline__ bool plan_fits(const PagedAttnArgs& a) {
     const int32_t* h = a.p.head;
-    return h[1] == a.B && h[2] == a.N && h[3] == a.M && h[4] == a.with_prefix && h[5] == a.capacity && h[6] == a.c.H;
+    return h[1] == a.B && h[2] == a.N && h[3] == a.M && h[4] == a.shape && h[5] == a.capacity;
 }
 
-constexpr int occupancy(int D, int DT) { return D == 256 || (D == 128 && DT == 0) ? 1 : 2; }
+constexpr int occupancy(int D, int DT) { return D == 256 ? 1 : 2; }
 
 template <int D, int DT>
 __global__ __launch_bounds__(kThreads, occupancy(D, DT)) void paged_attention_kernel(PagedAttnArgs a) {

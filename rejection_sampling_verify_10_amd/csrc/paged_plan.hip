@@ -22,19 +22,28 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kClasses = kWave;         // of length, the longest first
 constexpr int kSteps = 8;               // sizes of a unit that are tried, each a sixteenth above the one before
 
-// Sum over the block's threads below this one, and over all.
-__device__ __forceinline__ long long block_exclusive(long long v, long long& total, long long (&sh)[kWaves]) {
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
-    long long i = v;
+__device__ __forceinline__ unsigned wave_add(unsigned v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += xshfl(v, o);
+    return v;
+}
+__device__ __forceinline__ unsigned wave_inclusive(unsigned v) {
+    const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
-        const long long t = __shfl_up(i, o, kWave);
-        if (lane >= o) i += t;
+        const unsigned t = __shfl_up(v, o, kWave);
+        if (lane >= o) v += t;
     }
+    return v;
+}
+// Sum over the block's threads below this one, and over all (fewer than 2^31 rows of parts).
+__device__ __forceinline__ unsigned block_exclusive(unsigned v, unsigned& total, unsigned (&sh)[kWaves]) {
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+    const unsigned i = wave_inclusive(v);
     __syncthreads();
     if (lane == kWave - 1) sh[wave] = i;
     __syncthreads();
-    long long before = 0;
+    unsigned before = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -44,9 +53,9 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long& tot
     return before + i - v;
 }
 
-struct Row {
+struct Row {                        // an error row: no new tokens, no prefix
     int pre, cnt, prefix, shared;   // own committed slots, new tokens, table row and slots of its prefix
-    bool ok;
+    __device__ __forceinline__ int run() const { return shared > 0 && cnt > 0 ? prefix : -1; }
 };
 __device__ __forceinline__ Row read_row(const PagedPlanArgs& a, int b) {
     Row r;
@@ -54,233 +63,263 @@ __device__ __forceinline__ Row read_row(const PagedPlanArgs& a, int b) {
     r.pre = a.lengths[b];
     r.cnt = a.counts ? a.counts[b] : a.N;
     r.prefix = a.prefix_row ? a.prefix_row[b] : -1;
-    r.ok = r.pre >= 0 && r.cnt >= 0 && r.cnt <= a.N && static_cast<long long>(r.pre) + r.cnt <= capacity && r.prefix < a.T;
+    bool ok = r.pre >= 0 && r.cnt >= 0 && r.cnt <= a.N && static_cast<long long>(r.pre) + r.cnt <= capacity && r.prefix < a.T;
     r.shared = 0;
     if (r.prefix >= 0 && r.prefix < a.T) {
         r.shared = a.lengths[r.prefix];
-        r.ok = r.ok && r.shared >= 0 && r.shared <= capacity;
+        ok = ok && r.shared >= 0 && r.shared <= capacity;
     }
-    if (!r.ok) r.pre = r.cnt = r.shared = 0;
+    if (!ok) r.pre = r.cnt = r.shared = 0;
     return r;
 }
 // Slots of its own that the i-th tile of a batch row's query rows looks at (windows that may have a mask: all of them).
 __device__ __forceinline__ int own_limit(const PagedPlanArgs& a, const Row& r, int i) {
+    if (a.own_tiles == 1) return r.cnt > 0 ? r.pre + r.cnt : 0;
     const int first = i * a.own_rows / a.G, last = (min((i + 1) * a.own_rows, a.M) - 1) / a.G;     // tokens
-    if (!r.ok || first >= r.cnt) return 0;
+    if (first >= r.cnt) return 0;
     return r.pre + (a.N <= kPgMaskN ? r.cnt : min(last + 1, r.cnt));
 }
 __device__ __forceinline__ int chunks(int slots) { return (slots + kPgChunk - 1) / kPgChunk; }
 
+// ceil(n / d) for n < 2^24: the float quotient is off by less than one.
+__device__ __forceinline__ int ceil_div(int n, int d) {
+    const int q = static_cast<int>(static_cast<float>(n) * __builtin_amdgcn_rcpf(static_cast<float>(d)));
+    const int r = n - q * d;                            // -d < r < 2d
+    return q + (r > 0 ? 1 : 0) + (r > d ? 1 : 0);
+}
 // A job of `n` chunks for units of at most `most`: its parts, and the chunks of each but the last. (Whether 128 query rows meet
 // them or 32: the few take as long, waiting for memory.)
 struct Cut {
     int parts, each;
     __device__ __forceinline__ Cut(int n, int most) {
-        parts = max((n + most - 1) / most, 1);
-        each = max((n + parts - 1) / parts, 1);
-        parts = max((n + each - 1) / each, 1);
+        each = max(ceil_div(n, max(ceil_div(n, most), 1)), 1);
+        parts = max(ceil_div(n, each), 1);
     }
 };
 
 struct Run {
     int b0, rows, prefix, shared, tile, tiles;  // tile: query rows of a unit
+    int unit, part;                             // its first ones
 };
 
+__device__ __forceinline__ void write_unit(PagedUnit* to, const PagedUnit& u) {
+    static_assert(sizeof(PagedUnit) == 48, "three vectors");
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    const i32x4 w[3] = {{u.b0, u.row0, u.rows, u.table}, {u.k0, u.k1, u.pre, u.cnt}, {u.part, u.wide, 0, 0}};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<i32x4*>(to)[i] = w[i];
+}
+
 __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
-    __shared__ long long sh[kWaves];
-    __shared__ int lead[kThreads + 1];
-    __shared__ Run run[kThreads];
-    __shared__ long long run_part[kThreads];
+    __shared__ unsigned sh[kWaves];
+    __shared__ Row rows[kThreads];
+    __shared__ Run run[kThreads + 1];
+    __shared__ unsigned long long cost;                 // chunks of all jobs
+    __shared__ unsigned large[kSteps];
     __shared__ int place[kClasses];                     // where the next unit of a class goes
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
-    const long long items = static_cast<long long>(a.B) * a.own_tiles;
+    if (tid == 0) cost = 0;
+    if (tid < kSteps) large[tid] = 0;
+    if (tid < kClasses) place[tid] = 0;
 
-    // The runs among batch rows b0 .. b0 + 1023 (a run ends there too): thread t has the t-th; their number.
-    const auto runs = [&](int b0, Run& mine) {
+    // Batch rows are looked at 1024 at a time, a row a thread (a run ends there too); where there are no more, once.
+    int runs = 0, mine = 0;                             // of these rows; this thread's row's
+    const auto look = [&](int b0) {
+        if (b0 > 0 || a.B > kThreads) __syncthreads();  // the rows before have been used
         const int b = b0 + tid;
-        Row r{};
+        Row r = {0, 0, -1, 0};
         if (b < a.B) r = read_row(a, b);
-        const int here = r.ok && r.shared > 0 && r.cnt > 0 ? r.prefix : -1;
-        int before = __shfl_up(here, 1, kWave);
+        rows[tid] = r;
         __syncthreads();
-        if (lane == kWave - 1) sh[wave] = here;
+        if (!a.prefix_row) return;
+        const bool first = b < a.B && (tid == 0 || r.run() != rows[tid - 1].run());
+        const unsigned long long leads = __ballot(first);
+        if (lane == 0) sh[wave] = __popcll(leads);
         __syncthreads();
-        if (lane == 0) before = wave > 0 ? static_cast<int>(sh[wave - 1]) : -2;
-        const bool first = b < a.B && here != before;
-        long long count;
-        const int rank = static_cast<int>(block_exclusive(first ? 1 : 0, count, sh));
-        if (first) {
-            lead[rank] = b;
-            run[rank].prefix = here;
-            run[rank].shared = r.shared;
+        unsigned before = 0, count = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += sh[w];
+            count += sh[w];
         }
-        if (tid == 0) lead[count] = min(a.B, b0 + kThreads);
+        runs = static_cast<int>(count);
+        mine = static_cast<int>(before) + __popcll(leads & (~0ull >> (kWave - 1 - lane))) - 1;
+        if (first) run[mine].b0 = b, run[mine].prefix = r.run(), run[mine].shared = r.run() >= 0 ? r.shared : 0;
+        if (tid == 0) run[count].b0 = min(a.B, b0 + kThreads);
         __syncthreads();
-        mine = Run{};
-        if (tid < count) {
-            mine.b0 = lead[tid];
-            mine.prefix = run[tid].prefix;
-            mine.shared = mine.prefix >= 0 ? run[tid].shared : 0;
-            mine.rows = (lead[tid + 1] - lead[tid]) * a.M;
-            mine.tile = mine.rows <= kPgNarrow ? kPgNarrow : kPgWide;
-            mine.tiles = mine.shared > 0 ? (mine.rows + mine.tile - 1) / mine.tile : 0;
+        if (tid < runs) {
+            Run& to = run[tid];
+            to.rows = (run[tid + 1].b0 - to.b0) * a.M;
+            to.tile = to.rows <= kPgNarrow ? kPgNarrow : kPgWide;
+            to.tiles = to.shared > 0 ? (to.rows + to.tile - 1) / to.tile : 0;
         }
         __syncthreads();
-        return static_cast<int>(count);
     };
+    const auto items = [&](int b0) { return (min(a.B, b0 + kThreads) - b0) * a.own_tiles; };
+    // f(chunks, tiles) for every stride-th job among these rows (all tiles of a run are one)
+    const auto each_job = [&](int b0, int from, int stride, const auto& f) {
+        for (int k = from; k < runs; k += stride)
+            if (run[k].tiles) f(chunks(run[k].shared), run[k].tiles);
+        const int n = items(b0);
+        for (int j = from; j < n; j += stride) {
+            const int row = a.own_tiles == 1 ? j : j / a.own_tiles;
+            f(chunks(own_limit(a, rows[row], j - row * a.own_tiles)), 1);
+        }
+    };
+    const bool several = a.B > kThreads;
+    look(0);
 
-    // f(chunks, tiles) for each job (or all tiles of a run at once)
-    const auto each_job = [&](const auto& f) {
-        for (int b0 = 0; a.prefix_row && b0 < a.B; b0 += kThreads) {
-            Run r;
-            runs(b0, r);
-            if (r.tiles) f(chunks(r.shared), r.tiles);
-        }
-        for (long long j = tid; j < items; j += kThreads)
-            f(chunks(own_limit(a, read_row(a, static_cast<int>(j / a.own_tiles)), static_cast<int>(j % a.own_tiles))), 1);
-    };
     // the chunks that no unit passes
     int most = 1 << 29;
     if (a.target > 0) {
-        long long cost = 0;
-        each_job([&](int n, int tiles) { cost += static_cast<long long>(n) * tiles; });
-        long long total;
-        block_exclusive(cost, total, sh);
-        most = static_cast<int>(max((total + a.target - 1) / a.target, 1ll));
-        for (int step = 0; step < kSteps; ++step) {
-            long long large = 0;
-            each_job([&](int n, int tiles) {
-                const Cut c(n, most);
-                if (2 * c.each > most) large += static_cast<long long>(c.parts) * tiles;
-            });
-            block_exclusive(large, total, sh);
-            if (total <= a.target) break;
-            most += most / 16 + 1;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            if (b0 > 0) look(b0);
+            unsigned long long sum = 0;                 // below 2^23 chunks * 2^19 tiles a job
+            each_job(b0, tid, kThreads, [&](int n, int tiles) { sum += static_cast<unsigned long long>(n) * tiles; });
+            const unsigned lo = wave_add(static_cast<unsigned>(sum) & 0xffffffu), hi = wave_add(static_cast<unsigned>(sum >> 24));
+            if (lane == 0 && (lo | hi)) atomicAdd(&cost, (static_cast<unsigned long long>(hi) << 24) + lo);
         }
+        __syncthreads();
+        const int least = static_cast<int>(max((cost + a.target - 1) / a.target, 1ull));
+        const auto raised = [](int m) { return m + m / 16 + 1; };
+        // two waves a size
+        const int step = wave % kSteps;
+        int size = least;
+        for (int i = 0; i < step; ++i) size = raised(size);
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            if (several) look(b0);
+            unsigned sum = 0;
+            each_job(b0, tid / (kWave * kSteps) * kWave + lane, kThreads / kSteps, [&](int n, int tiles) {
+                const Cut c(n, size);
+                if (2 * c.each > size) sum += static_cast<unsigned>(c.parts * tiles);
+            });
+            sum = wave_add(sum);
+            if (lane == 0 && sum) atomicAdd(&large[step], sum);
+        }
+        __syncthreads();
+        most = least;
+        for (int i = 0; i < kSteps && large[i] > static_cast<unsigned>(a.target); ++i) most = raised(most);
     }
     const int finest = (most + kClasses - 1) / kClasses;
     const auto class_of = [&](int each) { return max(kClasses - 1 - each / finest, 0); };
-    if (tid < kClasses) place[tid] = 0;
-    __syncthreads();
-    each_job([&](int n, int tiles) {
-        const Cut c(n, most);
-        atomicAdd(&place[class_of(c.each)], c.parts * tiles);
-    });
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        if (several) look(b0);
+        each_job(b0, tid, kThreads, [&](int n, int tiles) {
+            const Cut c(n, most);
+            atomicAdd(&place[class_of(c.each)], c.parts * tiles);
+        });
+    }
     __syncthreads();
     if (wave == 0) {
         static_assert(kClasses == kWave, "a class a lane");
-        const int n = place[lane];
-        int before = n;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const int t = __shfl_up(before, o, kWave);
-            if (lane >= o) before += t;
-        }
-        place[lane] = before - n;
+        const int n = place[lane], upto = static_cast<int>(wave_inclusive(static_cast<unsigned>(n)));
+        place[lane] = upto - n;
         if (lane == kWave - 1) {
-            a.p.head[0] = before;
+            a.p.head[0] = upto;
             a.p.head[1] = a.B;
             a.p.head[2] = a.N;
             a.p.head[3] = a.M;
-            a.p.head[4] = a.prefix_row != nullptr;
+            a.p.head[4] = a.shape;
             a.p.head[5] = a.width << a.page_log2;
-            a.p.head[6] = a.heads;
         }
     }
     __syncthreads();
 
-    long long parts = 0;
+    unsigned parts = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        if (several) look(b0);
         const int b = b0 + tid;
-        if (b < a.B) {
-            const Row r = read_row(a, b);
-            a.p.shared[b] = PagedShared{0, 0, 0, r.ok ? r.cnt : 0};
-        }
-        if (!a.prefix_row) continue;
-        Run mine;
-        const int count = runs(b0, mine);
-        const Cut cut(chunks(mine.shared), most);
-        long long part_total;
-        const long long p = block_exclusive(static_cast<long long>(mine.tiles) * cut.parts * mine.tile, part_total, sh);
-        if (tid < count) run[tid] = mine, run_part[tid] = parts + p;
-        __syncthreads();
-        for (int k = wave; k < count; k += kWaves) {
-            const Run r = run[k];
-            if (!r.tiles) continue;
+        if (a.prefix_row) {
+            Run r{};
+            if (tid < runs) r = run[tid];
             const Cut c(chunks(r.shared), most);
-            const int n = c.parts, step = c.each * kPgChunk;
-            int u = 0;
-            if (lane == 0) u = atomicAdd(&place[class_of(c.each)], n * r.tiles);
-            u = __builtin_amdgcn_readfirstlane(u);
-            for (int i = lane; i < n * r.tiles; i += kWave) {
-                const int s = i / r.tiles, tile = i % r.tiles;
-                PagedUnit w{};
-                w.b0 = r.b0;
-                w.row0 = tile * r.tile;
-                w.rows = r.rows;
-                w.table = r.prefix;
-                w.k0 = s * step;
-                w.k1 = s == n - 1 ? r.shared : w.k0 + step;
-                w.pre = r.shared;
-                w.part = static_cast<int>(run_part[k] + static_cast<long long>(i) * r.tile);
-                w.wide = r.tile == kPgWide;
-                a.p.unit[u + i] = w;
+            unsigned total;
+            const unsigned p = block_exclusive(static_cast<unsigned>(r.tiles * c.parts * r.tile), total, sh);
+            if (r.tiles) {
+                run[tid].part = static_cast<int>(parts + p);
+                run[tid].unit = atomicAdd(&place[class_of(c.each)], c.parts * r.tiles);
             }
-            for (int row = lane; row < r.rows / a.M; row += kWave) {
-                PagedShared* at = a.p.shared + r.b0 + row;
-                at->first = static_cast<int>(run_part[k]) + row * a.M;
-                at->step = r.tiles * r.tile;
-                at->count = n;
+            parts += total;
+            __syncthreads();
+            for (int k = wave; k < runs; k += kWaves) {
+                const Run r = run[k];
+                if (!r.tiles) continue;
+                const Cut c(chunks(r.shared), most);
+                const int step = c.each * kPgChunk;
+                for (int i = lane; i < c.parts * r.tiles; i += kWave) {
+                    const int s = i / r.tiles, tile = i - s * r.tiles;
+                    PagedUnit w{};
+                    w.b0 = r.b0;
+                    w.row0 = tile * r.tile;
+                    w.rows = r.rows;
+                    w.table = r.prefix;
+                    w.k0 = s * step;
+                    w.k1 = s == c.parts - 1 ? r.shared : w.k0 + step;
+                    w.pre = r.shared;
+                    w.part = r.part + i * r.tile;
+                    w.wide = r.tile == kPgWide;
+                    write_unit(a.p.unit + r.unit + i, w);
+                }
             }
         }
-        parts += part_total;
-        __syncthreads();
-    }
-    for (long long j0 = 0; j0 < items; j0 += kThreads) {
-        const long long j = j0 + tid;
-        const int b = static_cast<int>(j / a.own_tiles), i = static_cast<int>(j % a.own_tiles);
-        Row r{};
-        int limit = 0;
-        if (j < items) {
-            r = read_row(a, b);
-            limit = own_limit(a, r, i);
+        if (b < a.B) {
+            PagedShared sd = {0, 0, 0, rows[tid].cnt};
+            if (a.prefix_row && run[mine].tiles) {
+                const Run& r = run[mine];
+                sd.first = r.part + (b - r.b0) * a.M;
+                sd.step = r.tiles * r.tile;
+                sd.count = Cut(chunks(r.shared), most).parts;
+            }
+            a.p.shared[b] = sd;
         }
-        const Cut c(chunks(limit), most);
-        const int n = c.parts, step = c.each * kPgChunk;
-        const bool joined = j < items && (n > 1 || (r.shared > 0 && r.cnt > 0));
-        long long part_total;
-        const long long p = parts + block_exclusive(joined ? static_cast<long long>(n) * a.own_rows : 0, part_total, sh);
-        if (j < items) {
-            a.p.own[j] = PagedOwn{static_cast<int>(p), joined ? n : 0};
-            const int u = atomicAdd(&place[class_of(c.each)], n);
-            for (int s = 0; s < n; ++s) {
+        const int n = items(b0);
+        for (int j0 = 0; j0 < n; j0 += kThreads) {
+            const int j = j0 + tid, row = a.own_tiles == 1 ? j : j / a.own_tiles, i = j - row * a.own_tiles;
+            Row r = {0, 0, -1, 0};
+            int limit = 0;
+            if (j < n) {
+                r = rows[row];
+                limit = own_limit(a, r, i);
+            }
+            const Cut c(chunks(limit), most);
+            const int step = c.each * kPgChunk;
+            const bool joined = j < n && (c.parts > 1 || r.run() >= 0);
+            unsigned total;
+            const unsigned p = parts + block_exclusive(joined ? static_cast<unsigned>(c.parts * a.own_rows) : 0u, total, sh);
+            parts += total;
+            if (j >= n) continue;
+            a.p.own[static_cast<long long>(b0) * a.own_tiles + j] = PagedOwn{static_cast<int>(p), joined ? c.parts : 0};
+            const int u = atomicAdd(&place[class_of(c.each)], c.parts);
+            for (int s = 0; s < c.parts; ++s) {
                 PagedUnit w{};
-                w.b0 = b;
+                w.b0 = b0 + row;
                 w.row0 = i * a.own_rows;
                 w.rows = a.M;
-                w.table = b;
-                w.k0 = n > 1 ? s * step : 0;
-                w.k1 = s == n - 1 ? limit : w.k0 + step;
+                w.table = b0 + row;
+                w.k0 = s * step;
+                w.k1 = s == c.parts - 1 ? limit : w.k0 + step;
                 w.pre = r.pre;
                 w.cnt = r.cnt;
                 w.part = joined ? static_cast<int>(p) + s * a.own_rows : -1;
                 w.wide = a.own_rows == kPgWide;
-                a.p.unit[u + s] = w;
+                write_unit(a.p.unit + u + s, w);
             }
         }
-        parts += part_total;
     }
 }
 
 }  // namespace
 
-// The key axes are split into about 512 workgroups (two a compute unit); a batch whose own rows alone are as many is not
-// split, unless there are prefixes.
+// The key axes are split into about as many workgroups as run at once, two a compute unit, or one where a tile of D = 256 takes
+// most of its LDS (44 rows of 7 tokens behind 800 keys, D = 256: 36 us in 512 of them, 32 in 256); a batch whose own rows alone
+// are as many is not split, unless there are prefixes.
 void paged_plan_sizes(PagedPlanArgs& a) {
     a.own_rows = a.M <= kPgNarrow ? kPgNarrow : kPgWide;
     a.own_tiles = (a.M + a.own_rows - 1) / a.own_rows;
     const long long own = static_cast<long long>(a.B) * a.own_tiles;
-    const long long target = (512 + a.heads - 1) / a.heads;
+    const int workgroups = a.D == 256 ? 256 : 512;
+    const long long target = (workgroups + a.heads - 1) / a.heads;
+    a.shape = 4 * a.heads + 2 * (a.D == 256) + (a.prefix_row ? 1 : 0);
     a.target = a.prefix_row || own < target ? static_cast<int>(target) : 0;
     // a unit more than the split for each job; a run's rows come to one tile more than fit
     const long long rows = static_cast<long long>(a.B) * a.M;

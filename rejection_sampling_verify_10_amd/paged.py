@@ -199,10 +199,10 @@ def paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: tor
 class PagedPlan:
     """How one step's attention is cut up (:func:`paged_plan`): sizes, the tables, and the plan on the GPU."""
 
-    def __init__(self, B, N, q_heads, heads, tables, page_size, with_prefix):
-        self.B, self.N, self.q_heads, self.heads, self.with_prefix = B, N, q_heads, heads, with_prefix
+    def __init__(self, B, N, q_heads, heads, head_dim, tables, page_size, with_prefix):
+        self.B, self.N, self.q_heads, self.heads, self.head_dim, self.with_prefix = B, N, q_heads, heads, head_dim, with_prefix
         self.tables, self.width, self.page_size = tables, tables.shape[1], page_size
-        self.bytes = int(lib().spec_paged_plan_bytes(B, N, q_heads, heads, with_prefix))
+        self.bytes = int(lib().spec_paged_plan_bytes(B, N, q_heads, heads, head_dim, with_prefix))
         self._buffer = torch.empty(self.bytes + 256, dtype=torch.uint8, device=tables.device)
         self._ptr = (self._buffer.data_ptr() + 255) // 256 * 256
 
@@ -235,11 +235,11 @@ def paged_plan(cache: PagedCache, tables: torch.Tensor, lengths: torch.Tensor, N
         raise ValueError("the rows of tables must be contiguous and not overlap")
     with_prefix = prefix_row is not None
     if out is None:
-        out = PagedPlan(B, N, q_heads, cache.heads, tables, cache.page_size, with_prefix)
-    elif ((out.B, out.N, out.q_heads, out.heads, out.with_prefix, out.page_size) !=
-          (B, N, q_heads, cache.heads, with_prefix, cache.page_size) or out.tables is not tables):
+        out = PagedPlan(B, N, q_heads, cache.heads, cache.head_dim, tables, cache.page_size, with_prefix)
+    elif ((out.B, out.N, out.q_heads, out.heads, out.head_dim, out.with_prefix, out.page_size) !=
+          (B, N, q_heads, cache.heads, cache.head_dim, with_prefix, cache.page_size) or out.tables is not tables):
         raise ValueError("out must be a plan of the same sizes and tables")
-    _call(lib().spec_paged_plan, "spec_paged_plan", dev, B, N, q_heads, cache.heads, T, width, cache.page_size,
+    _call(lib().spec_paged_plan, "spec_paged_plan", dev, B, N, q_heads, cache.heads, cache.head_dim, T, width, cache.page_size,
           _tensor(lengths, "lengths", torch.int32, (T,), dev), _optional(counts, "counts", torch.int32, (B,), dev),
           _optional(prefix_row, "prefix_row", torch.int32, (B,), dev), out._ptr, out.bytes)
     return out
@@ -264,7 +264,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, plan: PagedPlan, *, mask
     rq = _rows(q, "q", cache)
     B, N, Hq, D = q.shape
     dev = cache.device
-    if (B, N, Hq, cache.heads, cache.page_size) != (plan.B, plan.N, plan.q_heads, plan.heads, plan.page_size):
+    if (B, N, Hq, cache.heads, D, cache.page_size) != (plan.B, plan.N, plan.q_heads, plan.heads, plan.head_dim, plan.page_size):
         raise ValueError("q and cache must have the plan's sizes")
     if plan.tables.get_device() != dev.index:
         raise ValueError(f"the plan must be on {dev}, got {plan.tables.device}")

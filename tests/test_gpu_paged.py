@@ -379,6 +379,22 @@ def test_long_prefixes(R, B, N, H, G, D, P, shared, tail, dtype):
     check(R, queries(rng, B, N, H * G, D, dtype), cache, tables, lens, B, prefix_row=[B] * B)
 
 
+@pytest.mark.parametrize("B,N", [(1024, 2), (1300, 1), (2500, 3), (1030, 130)])
+def test_many_rows(R, B, N):
+    """More rows than the plan looks at at a time, runs of prefixes across its borders, windows of several tiles among them."""
+    rng = np.random.default_rng(B)
+    H, G, D, P, width = 1, 1, 64, 16, 12
+    lens = rng.integers(0, 40, B).tolist() + [150, 0, 60]
+    pages = 400
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = rng.integers(0, pages, (B + 3, width)).astype(np.int32)
+    prefix = B + (np.arange(B) // 300) % 3
+    prefix[rng.random(B) < 0.01] = -1
+    counts = np.where(rng.random(B) < 0.03, N, rng.integers(0, min(N, 2) + 1, B))
+    counts[[0, B - 1]] = N
+    check(R, queries(rng, B, N, H * G, D, "bf16"), cache, tables, lens, B, counts=counts, prefix_row=prefix)
+
+
 def test_a_plan_of_other_sizes_writes_nothing(R):
     import ctypes
     import torch

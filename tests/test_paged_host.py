@@ -50,7 +50,7 @@ def append(L, **kw):
 
 
 def plan(L, **kw):
-    a = dict(B=2, N=3, Hq=8, H=4, T=3, width=20, P=32, lengths=FAKE, counts=None, prefix=FAKE, plan=FAKE, bytes=1 << 30, stream=None)
+    a = dict(B=2, N=3, Hq=8, H=4, D=128, T=3, width=20, P=32, lengths=FAKE, counts=None, prefix=FAKE, plan=FAKE, bytes=1 << 30, stream=None)
     a.update(kw)
     return L.spec_paged_plan(*a.values())
 
@@ -109,7 +109,7 @@ def test_append_refuses(L, bad, code):
     (dict(B=0), EINVAL), (dict(N=0), EINVAL), (dict(Hq=7), EINVAL), (dict(Hq=0), EINVAL), (dict(H=0), EINVAL), (dict(T=1), EINVAL),
     (dict(width=0), EINVAL), (dict(P=8), EINVAL), (dict(P=33), EINVAL), (dict(lengths=None), EINVAL), (dict(lengths=FAKE + 2), EINVAL),
     (dict(counts=FAKE + 1), EINVAL), (dict(prefix=FAKE + 2), EINVAL), (dict(N=65537), EUNSUPPORTED), (dict(width=1 << 26), EUNSUPPORTED),
-    (dict(B=1 << 20, T=1 << 20, N=1 << 16), EUNSUPPORTED), (dict(plan=None), EWORKSPACE), (dict(plan=FAKE + 4), EWORKSPACE),
+    (dict(D=96), EUNSUPPORTED), (dict(B=1 << 20, T=1 << 20, N=1 << 16), EUNSUPPORTED), (dict(plan=None), EWORKSPACE), (dict(plan=FAKE + 4), EWORKSPACE),
     (dict(bytes=100), EWORKSPACE),
 ])
 def test_plan_refuses(L, bad, code):
@@ -129,8 +129,9 @@ def test_attention_refuses(L, bad, code):
 
 
 def test_sizes_of_plans(L):
-    assert L.spec_paged_plan_bytes(0, 1, 8, 4, 0) == 0 and L.spec_paged_plan_bytes(2, 1, 9, 4, 0) == 0
-    assert 0 < L.spec_paged_plan_bytes(2, 1, 8, 4, 0) <= L.spec_paged_plan_bytes(2, 1, 8, 4, 1)
+    assert L.spec_paged_plan_bytes(0, 1, 8, 4, 64, 0) == 0 and L.spec_paged_plan_bytes(2, 1, 9, 4, 64, 0) == 0
+    assert 0 < L.spec_paged_plan_bytes(2, 1, 8, 4, 64, 0) <= L.spec_paged_plan_bytes(2, 1, 8, 4, 64, 1)
+    assert L.spec_paged_plan_bytes(2, 1, 8, 4, 96, 0) == 0
     assert L.spec_paged_attention_workspace_bytes(2, 1, 8, 4, 96, 1) == 0
     # many rows of their own and no prefix: nothing is split, nothing joined
     assert L.spec_paged_attention_workspace_bytes(4096, 1, 8, 4, 128, 0) == 0
