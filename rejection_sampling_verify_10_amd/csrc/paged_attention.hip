@@ -228,6 +228,10 @@ template <int D, int DT> struct Wave {
     static constexpr int NQ = DT == 1 ? 1 : 3;
     // V's operands are read before the scores' products where there are registers to hold them.
     static constexpr bool kEarlyV = D == 64 || (D == 128 && DT == 1);
+    // K's before the tile's turn, likewise: in a wide unit (bf16 chains of eight, D = 128: 85 us with, 82 without, D = 256: 128 and
+    // 139; float32 ones behind 16384 keys, D = 256: 573 and 324, much of it spilled registers) and in a narrow one, whose buffer
+    // is free sooner with them (64 sequences of one bf16 token: 120 us, 135 without).
+    static constexpr bool kWideK = D == 64 || (D == 256 && DT == 1), kNarrowK = D == 64 || DT == 1;
     u32x4 Q[NQ][D / 16];
     f32x16 O[NT];
     float m, l;
@@ -245,9 +249,12 @@ template <int D, int DT> struct Wave {
     }
     // Chunks are turned by an exclusive or, so that of another chunk is one away: k_at(c, 2s + h2) = ka ^ 32s, and v_at with
     // chunks 4t more is va ^ 64t. Eight keys on is the same turn.
+    __device__ __forceinline__ u32x4 read_k(const Lds<D>& lds, int buf, int s) const {
+        return *reinterpret_cast<const u32x4*>(lds.k[buf] + (ka ^ (32 * s)));
+    }
     __device__ __forceinline__ void read_k(const Lds<D>& lds, int buf) {
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) K[s] = *reinterpret_cast<const u32x4*>(lds.k[buf] + (ka ^ (32 * s)));
+        for (int s = 0; s < D / 16; ++s) K[s] = read_k(lds, buf, s);
     }
     __device__ __forceinline__ void read_v(const Lds<D>& lds, int buf, int s, u32x4 (&out)[NT]) const {
 #pragma unroll
@@ -262,14 +269,16 @@ template <int D, int DT> struct Wave {
 #pragma unroll
         for (int s = 0; s < 2; ++s) read_v(lds, buf, s, V[kEarlyV ? s : 0]);
     }
-    __device__ __forceinline__ f32x16 scores() const {  // of K's tile
+    template <bool READ> __device__ __forceinline__ f32x16 scores(const Lds<D>& lds, int buf) const {     // READ: K's operands are
         f32x16 s;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < D / 16; ++i) {
+            const u32x4 k = READ ? K[i] : read_k(lds, buf, i);
 #pragma unroll
-            for (int p = 0; p < NQ; ++p) s = mfma32(K[i], Q[p][i], s);
+            for (int p = 0; p < NQ; ++p) s = mfma32(k, Q[p][i], s);
+        }
         return s;
     }
     // V's elements that are no numbers would reach queries that give their key no weight: they become zeros in an operand,
@@ -485,7 +494,8 @@ constexpr int kPer = kWindow / 2;                       // tiles of a window of 
 // A unit of up to 128 query rows: wave w has rows 32w .. of it.
 //
 // An iteration: V's operands of its tile are read and the scores formed from K's, read before; then the next tile has
-// arrived, this one's buffer takes the tile four further on, K's operands of the next are read, and the output follows.
+// arrived, this one's buffer takes the tile four further on, K's operands of the next are read, and the output follows. (Where
+// there are no registers to hold K's or V's operands, they are read as the products need them.)
 template <int D, int DT> __device__ __forceinline__ void attend_wide(const PagedAttnArgs& a, const PagedUnit& u, int h, Lds<D>& lds) {
     using W = Wave<D, DT>;
     using L = Loader<D, false>;
@@ -509,14 +519,14 @@ template <int D, int DT> __device__ __forceinline__ void attend_wide(const Paged
     queries_loaded(w);
     wait_loads<0>();
     barrier();
-    if (tiles > 0 && working) w.read_k(lds, 0);
+    if (W::kWideK && tiles > 0 && working) w.read_k(lds, 0);
 
     const auto iterate = [&](auto buffer, int t, bool edge, unsigned none) {
         const int buf = buffer;
         u32x4 P[W::NQ][2];
         if (working) {
             if (W::kEarlyV) w.read_v(lds, buf);
-            f32x16 S = w.scores();
+            f32x16 S = w.template scores<W::kWideK>(lds, buf);
             if (edge) sight.hide(S, u.k0 + t * kTileKeys, w.odd_keys(lds, buf, none));
             w.weigh(S, a.cexp, slack, P);
             if (!W::kEarlyV) w.add(lds, buf, P, edge);
@@ -537,7 +547,7 @@ template <int D, int DT> __device__ __forceinline__ void attend_wide(const Paged
             if (next % kPer == 1 && next > kPer && next + kPer - 1 < tiles) ld.fetch_window(next / kPer + 1);
         }
         if (working) {
-            if (t + 1 < tiles) w.read_k(lds, (buf + 1) % kStages);
+            if (W::kWideK && t + 1 < tiles) w.read_k(lds, (buf + 1) % kStages);
             if (W::kEarlyV) w.add(lds, buf, P, edge);
         }
     };
@@ -586,7 +596,7 @@ template <int D, int DT> __device__ __forceinline__ void attend_narrow(const Pag
         const int first = u.k0 + t * kTileKeys, next = t + kWaves;
         const bool edge = first + kTileKeys > sight.seen || none != 0;
         wait_loads<0>();
-        w.read_k(lds, wave);
+        if (W::kNarrowK) w.read_k(lds, wave);
         if (W::kEarlyV) w.read_v(lds, wave);
         wait_lds();
         if (next < tiles) {
@@ -594,10 +604,14 @@ template <int D, int DT> __device__ __forceinline__ void attend_narrow(const Pag
                 ld.next_window(next / kPer);
                 if ((next / kPer + 1) * kPer < tiles) ld.fetch_window(next / kPer + 1);
             }
-            ld.load_k(next);
+            if (W::kNarrowK) ld.load_k(next);
             if (W::kEarlyV) ld.load_v(next);
         }
-        f32x16 S = w.scores();
+        f32x16 S = w.template scores<W::kNarrowK>(lds, wave);
+        if (!W::kNarrowK && next < tiles) {
+            wait_lds();
+            ld.load_k(next);
+        }
         u32x4 P[W::NQ][2];
         if (edge) sight.hide(S, first, w.odd_keys(lds, wave, none));
         w.weigh(S, a.cexp, slack, P);
