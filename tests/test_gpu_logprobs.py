@@ -229,6 +229,55 @@ def test_captured_and_replayed(R):
             assert torch.equal(a, b)
 
 
+def test_two_graphs_share_a_workspace(R):
+    """Rows in slices, replayed in turns with eager calls of other sizes between."""
+    import torch
+    rng = np.random.default_rng(16)
+    ws = R.new_workspace(R.token_logprobs_workspace_bytes(9, 60000, 20), torch.device("cuda", torch.cuda.current_device()))
+    graphs = []
+    for rows, V, top in ((3, 60000, 20), (9, 32001, 5)):
+        z, tokens = logits(rng, rows, V, "f32")[0], dev(rng.integers(0, V, (rows, 2)).astype(np.int32))
+        call = lambda z=z, tokens=tokens, top=top: R.token_logprobs(z, tokens, 0.9, top, workspace=ws)   # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        graphs.append((graph, out, z, call))
+    for k in range(4):
+        for graph, _, z, _ in graphs:
+            z.copy_(logits(rng, *z.shape, "f32")[0])
+            graph.replay()
+        for _, out, _, call in graphs:
+            for a, b in zip(out, call()):
+                assert torch.equal(a, b)
+    assert not ws.any()
+
+
+def test_offsets_past_32_bits(R):
+    """Rows of a tensor of more than 2^31 elements: what they give in a small one (as many workgroups a row)."""
+    import torch
+    rng = np.random.default_rng(17)
+    V, many = 128256, 17001
+    at = [0, 8000, 16744, many - 1]
+    few, _ = logits(rng, 4, V, "bf16")
+    tok = dev(rng.integers(0, V, (4, 2)).astype(np.int32))
+    got = []
+    for rows, places in ((300, [0, 1, 2, 299]), (many, at)):
+        z = torch.empty(rows, V, dtype=torch.bfloat16, device="cuda")
+        z[places] = few
+        tokens = torch.full((rows, 2), -1, dtype=torch.int32, device="cuda")
+        tokens[places] = tok
+        r = R.token_logprobs(z, tokens, 1.1, 4)
+        g = R.token_logprobs_grad(z, tokens, r.stats, torch.ones(rows, 2, device="cuda"), torch.ones(rows, device="cuda"), 1.1, out=z)
+        got.append([t[places].clone() for t in (*r, g)])
+        for place in set(range(0, rows, 500)) - set(places):
+            assert not g[place].any()
+        del z, g
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_emitted_tokens_of_a_verification(R):
     """The chain's verification and its answer's log probabilities, as a server asks for them."""
     import torch

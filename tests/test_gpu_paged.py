@@ -511,6 +511,39 @@ def test_streams_and_graphs(R):
             assert torch.equal(a, b)
 
 
+def test_calls_at_once(R):
+    """One plan, two streams, each with its own queries and workspace; and two pools at once."""
+    import torch
+    rng = np.random.default_rng(31)
+    B, N, H, G, D, P = 8, 2, 2, 4, 128, 16
+    lens = rng.integers(0, 900, B).tolist() + [3000]
+    width, pages = 200, sum(-(-(n + N) // P) for n in lens)
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = ints(make_tables(rng, pages, P, lens, N, B, width))
+    plan = R.paged_plan(cache, tables, ints(lens), N, H * G, B=B, prefix_row=ints([B] * B))
+    qs = [queries(rng, B, N, H * G, D, "bf16") for _ in range(2)]
+    need = R.paged_attention_workspace_bytes(plan, D) + 256
+    work = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want = [R.paged_attention(q, cache, plan) for q in qs]
+    pools = [R.new_page_pool(64, 30, 700, 16, "cuda") for _ in range(2)]
+    lengths = [ints(rng.integers(0, 100, 64)) for _ in range(2)]
+    alone = [R.page_step(R.new_page_pool(64, 30, 700, 16, "cuda"), n, 40) for n in lengths]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got, steps = [[], []], [None, None]
+    for k in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(R.paged_attention(qs[i], cache, plan, workspace=work[i]))
+                if k == 0:
+                    steps[i] = R.page_step(pools[i], lengths[i], 40)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+        assert torch.equal(steps[i][0], alone[i][0]) and torch.equal(steps[i][1], alone[i][1])
+
+
 def test_a_speculative_run(R):
     """Prompts into the pages, drafts behind them, verification, accepted rows in place, and log probabilities: three
     steps against attention over each sequence's own rows kept apart."""
