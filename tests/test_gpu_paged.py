@@ -366,6 +366,37 @@ def test_pages_that_are_none(R):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,H,G,D,shared,tail", [
+    (1, 1, 8, 8, 128, None, 9000), (1, 1, 1, 1, 64, None, 20000), (4, 8, 2, 1, 256, 3000, 500), (32, 1, 2, 1, 64, 700, 900),
+    (6, 1, 4, 5, 128, 1, 400), (3, 10, 2, 3, 128, None, 1500), (16, 2, 3, 1, 128, 5000, 1),
+])
+def test_small_calls_again_and_again(R, B, N, H, G, D, shared, tail, dtype):
+    """Few rows, cut into many units: layer after layer on one plan the same bits; then other lengths."""
+    import torch
+    rng = np.random.default_rng(B + N + D)
+    P = 16
+    for again in range(2):
+        lens = [tail if b == 0 else int(x) for b, x in enumerate(rng.integers(0, tail + 1, B))] + ([] if shared is None else [shared])
+        width = -(-max(n + N for n in lens) // P)
+        pages = sum(-(-(n + N) // P) for n in lens)
+        cache = make_cache(R, rng, pages, P, H, D)
+        tables = make_tables(rng, pages, P, lens, N, B, width)
+        prefix = None if shared is None else [B if b != 1 else -1 for b in range(B)]
+        counts = rng.integers(0, N + 1, B)
+        counts[0] = N
+        q = queries(rng, B, N, H * G, D, dtype)
+        plan = R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, counts=ints(counts),
+                            prefix_row=None if prefix is None else ints(prefix))
+        first = R.paged_attention(q, cache, plan)
+        check(R, q, cache, tables, lens, B, counts=counts, prefix_row=prefix, got=first)
+        others = [queries(rng, B, N, H * G, D, dtype) for _ in range(3)]
+        for k in range(20):
+            R.paged_attention(others[k % 3], cache, plan)     # (its workspace has held other parts)
+            out, lse = R.paged_attention(q, cache, plan)
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,N,H,G,D,P,shared,tail", [
     (24, 1, 8, 8, 128, 16, 9000, 300), (3, 8, 2, 4, 64, 64, 30011, 100), (1, 1, 1, 1, 128, 16, 70000, 3), (8, 20, 4, 4, 128, 16, 2500, 900),
 ])
@@ -511,11 +542,12 @@ def test_streams_and_graphs(R):
             assert torch.equal(a, b)
 
 
-def test_calls_at_once(R):
+@pytest.mark.parametrize("B,N", [(8, 2), (4, 2), (3, 1)])
+def test_calls_at_once(R, B, N):
     """One plan, two streams, each with its own queries and workspace; and two pools at once."""
     import torch
     rng = np.random.default_rng(31)
-    B, N, H, G, D, P = 8, 2, 2, 4, 128, 16
+    H, G, D, P = 2, 4, 128, 16
     lens = rng.integers(0, 900, B).tolist() + [3000]
     width, pages = 200, sum(-(-(n + N) // P) for n in lens)
     cache = make_cache(R, rng, pages, P, H, D)
