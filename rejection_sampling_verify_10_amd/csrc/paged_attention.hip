@@ -56,6 +56,26 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f
     return c;
 #endif
 }
+// The same with the sums in AGPRs, for good: left to itself the compiler takes them to VGPRs and back in every tile, for the few
+// tiles that rescale them, and spills others (float32 chains of eight behind 16384 keys, D = 256: 318 us, 202 so). It sees no
+// matrix instruction here, so the waits are ours: two states after a VALU write of an operand, four after one of exec; sums_done
+// before anything else reads or writes the sums, sums_set after it has. Products that follow each other on the same sums
+// need none.
+__device__ __forceinline__ void mfma32_sums(const u32x4& a, const u32x4& b, f32x16& c) {
+#if SV_KVQ_DEVICE
+    asm("s_nop 3\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+#endif
+}
+__device__ __forceinline__ void sums_done(f32x16& c) {
+#if SV_KVQ_DEVICE
+    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c));
+#endif
+}
+__device__ __forceinline__ void sums_set(f32x16& c) {
+#if SV_KVQ_DEVICE
+    asm volatile("s_nop 3" : "+a"(c));
+#endif
+}
 // Four 16-bit elements down a column of the 4 x 16 tile that sixteen lanes point at, four elements each.
 __device__ __forceinline__ u32x2 read_transposed(const unsigned char* p) {
 #if SV_KVQ_DEVICE
@@ -234,6 +254,7 @@ __device__ __forceinline__ void load_query(const PagedRows& q, long long off, bo
 template <int D, int DT> struct Wave {
     static constexpr int NT = D / 32;
     static constexpr int NQ = DT == 1 ? 1 : 3;
+    static constexpr bool kSums = D == 256;             // O is in AGPRs
     // V's operands are read before the scores' products where there are registers to hold them.
     static constexpr bool kEarlyV = D == 64 || (D == 128 && DT == 1);
     // K's before the tile's turn, likewise: in a wide unit (bf16 chains of eight, D = 128: 85 us with, 82 without, D = 256: 128 and
@@ -251,6 +272,10 @@ template <int D, int DT> struct Wave {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) O[t][i] = 0.f;
+        if (kSums) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sums_set(O[t]);
+        }
         const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h2 = lane >> 5;
         ka = k_at<D>(c, h2);
         va = v_at<D>(4 * h2 + (lane & 15) / 4, 2 * ((lane >> 4) & 1) + (lane & 3) / 2) + 8 * (lane & 1);
@@ -348,7 +373,11 @@ template <int D, int DT> struct Wave {
             const float al = m == -INFINITY ? 0.f : exp2_fast((m - mn) * cexp);
             l *= al;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) O[t] *= al;
+            for (int t = 0; t < NT; ++t) {
+                if (kSums) sums_done(O[t]);
+                O[t] *= al;
+                if (kSums) sums_set(O[t]);
+            }
             m = mn;
         }
         const float mc = m == -INFINITY ? 0.f : m * cexp;
@@ -371,6 +400,14 @@ template <int D, int DT> struct Wave {
             }
         }
     }
+    // After the last tile: the sum over both halves of the lanes' keys.
+    __device__ __forceinline__ void finish() {
+        l += xshfl(l, 32);
+        if (kSums) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sums_done(O[t]);
+        }
+    }
     // O += V P. V's operands are in registers, or still in the buffer (and perhaps to be cleaned).
     __device__ __forceinline__ void add(const Lds<D>& lds, int buf, const u32x4 (&P)[NQ][2], bool edge) {
 #pragma unroll
@@ -385,7 +422,10 @@ template <int D, int DT> struct Wave {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) O[t] = mfma32(V[kEarlyV ? s : 0][t], P[x][s], O[t]);
+                for (int x = 0; x < NQ; ++x) {
+                    if (kSums) mfma32_sums(V[kEarlyV ? s : 0][t], P[x][s], O[t]);
+                    else O[t] = mfma32(V[kEarlyV ? s : 0][t], P[x][s], O[t]);
+                }
         }
     }
 };
@@ -573,7 +613,7 @@ template <int D, int DT> __device__ __forceinline__ void attend_wide(const Paged
         const unsigned none = static_cast<unsigned>((same ? bad : bad_before) >> (2 * t & (kWindow - 1))) & 3u;
         iterate(t % kStages, t, t >= whole || none != 0, none);
     }
-    w.l += xshfl(w.l, 32);
+    w.finish();
     if (working) write_rows<D, DT, W::NT>(a, u, h, r, 0, true, w.O, w.m, w.l, sight.tok >= 0);
 }
 
@@ -630,7 +670,7 @@ template <int D, int DT> __device__ __forceinline__ void attend_narrow(const Pag
         }
     }
     // join the waves: each leaves its sums, and takes a quarter of the elements (D = 64: two waves a half)
-    w.l += xshfl(w.l, 32);
+    w.finish();
     f32x16(*const sh)[W::NT][kWave] = reinterpret_cast<f32x16(*)[W::NT][kWave]>(&lds);
     static_assert(sizeof(f32x16) * kWaves * W::NT * kWave == offsetof(Lds<D>, page), "the sums take the buffers' place");
     wait_lds();
