@@ -19,10 +19,10 @@
 // float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
 // queries P is the one bf16 of it, which is the output's own rounding.
 //
-// What bounds it (D = 128, 8 heads, bf16): many query rows, the matrix units and the
-// power they draw (64 rows of 8 tokens x 4 heads behind 65536 keys in common: 886-913
-// TFLOP/s, a library product of 8192^3 in the same conditions 1089; matrix units busy
-// half of the time, vector units a sixth); few, HBM (one sequence of 131072 keys:
+// What bounds it (D = 128, 8 heads, bf16): many query rows, the tiles' way through LDS
+// (a wave reads all of a tile for 32 rows: 600 of some 1400 clocks a tile) beside the
+// products (64 rows of 8 tokens x 4 heads behind 65536 keys in common: 886-913 TFLOP/s,
+// matrix units busy half of the time; a library product of 8192^3 1089); few, HBM (one sequence of 131072 keys:
 // 99 us, 5.4 TB/s; the read probe 7.0); in between both (64 sequences of one token
 // behind 32768 keys, ragged tails to 1024: 98-122 us by the clock, 304 MB, 70 GFLOP);
 // short ones, a chain of latencies (4 sequences of one token, 600 keys: 7.4 + 3.5 us).

@@ -10,8 +10,8 @@
 // tail, pages given back behind the tail: no entry is both read and written.
 //
 // Bound by latency: three dependent loads, a sum, a store, and a ticket where it
-// writes in place.  512 sequences of 8 tokens 5.0 us, 16 prompts of 8192 tokens 4.3;
-// a wave a row for the sums of the needs, with 64-bit shuffles, took 10.5 and 9.
+// writes in place.  512 sequences of 8 tokens 5.0 us (10.5 with 64-bit sums by
+// shuffles), 16 prompts of up to 8192 tokens 4.3.
 
 #include <type_traits>
 
