@@ -51,7 +51,6 @@ hipError_t launch_paged_append(const PagedAppendArgs& a, hipStream_t s, Timing t
 
 // ---- attention ----
 
-constexpr int kPgTile = 64;         // keys a workgroup stages at a time
 constexpr int kPgChunk = 128;       // units of the key axes' split
 constexpr int kPgMaskN = 64;         // most new tokens of a call with a mask
 constexpr int kPgWide = 128, kPgNarrow = 32;    // query rows of a workgroup: 32 a wave, or the same 32 for all four
