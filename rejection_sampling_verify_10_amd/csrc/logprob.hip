@@ -72,19 +72,21 @@ constexpr float kSlack = 40.f;                          // 2^40 * 2^20 elements 
 constexpr float kLowest = -1e30f;                       // 0 * kLowest is 0, 0 * -inf is not a number
 constexpr double kLn2 = 0.69314718055994530942;
 
-// x of a logit, mc = m * c.  Where that is no finite float32 (a row of the type's lowest values, or close to its largest)
-// the difference is taken first.
+// x of a logit, mc = m * c, whose rounding is in every x alike.  Where it may pass a power of two (a small temperature, a row of
+// the type's lowest values: 2^x would overflow, or be 0 for all) or mc is infinite, the difference is taken first.
 __device__ __forceinline__ float exponent(float z, float c, float mc) { return fmaxf(__builtin_fmaf(z, c, -mc), kLowest); }
 __device__ __forceinline__ float exponent_wide(float z, float c, float m) { return fmaxf((z - m) * c, kLowest); }
-__device__ __forceinline__ bool is_wide(float m, float c) { return !(fabsf(m * c) <= FLT_MAX); }
+__device__ __forceinline__ bool is_wide(float m, float c) { return !(fabsf(m * c) <= 16777216.f); }
 
-// What the exponents of a slice are relative to: m*c as it was used.
-__device__ __forceinline__ double reference(float m, float c) {
-    return is_wide(m, c) ? static_cast<double>(m) * static_cast<double>(c) : static_cast<double>(m * c);
+// What exponents are relative to: m*c as it was used.
+__device__ __forceinline__ double product(float m, float c, bool wide) {
+    return wide ? static_cast<double>(m) * static_cast<double>(c) : static_cast<double>(m * c);
 }
+__device__ __forceinline__ double reference(float m, float c) { return product(m, c, is_wide(m, c)); }
 
 struct Smem {
-    float red[kWaves], sums[kWaves][3];
+    float red[kWaves], sums[kWaves][2];
+    double base[kWaves];            // what a wave's sums are relative to
     uint32_t lists[2][kWaves][kWave];
     u32x4 stage[kWaves][kStage];
     int32_t stage_i[kWaves][kStage];
@@ -185,45 +187,55 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     const float z_tok = tok >= 0 && !bad ? E::scalar(row, tok) : 0.f;
 
     constexpr int kGroup = 4;                           // vectors between two looks at the reference
-    // sums relative to `ref`, the same in a wave's lanes
-    float tm = -INFINITY, ref = -FLT_MAX, S = 0.f, W = 0.f;
+    // sums relative to ref = mz*c, or (wide) by the differences from mz; the three are the same in a wave's lanes
+    float tm = -INFINITY, mz = -FLT_MAX, ref = mz * a.c, S = 0.f, W = 0.f;
+    bool wide = true, masked = false;                   // masked: a -inf has been met
     const auto add_to = [](float& S, float& W, float x) {
         const float p = exp2_fast(x);
         S += p;
         W = __builtin_fmaf(p, x, W);
     };
-    const auto add = [&](float x) { add_to(S, W, x); };
+    const auto move = [&](float to, bool to_wide) {
+        const float d = static_cast<float>(product(mz, a.c, wide) - product(to, a.c, to_wide)), w = exp2_fast(d);
+        W = w > 0.f ? w * __builtin_fmaf(S, d, W) : 0.f;
+        S = w > 0.f ? S * w : 0.f;
+        mz = to;
+        ref = to * a.c;
+        wide = to_wide;
+    };
     const auto look = [&](float mx) {
         tm = __builtin_elementwise_maximum(tm, mx);
-        if (__ballot(mx * a.c > ref + kSlack) != 0ull) {
-            const float to = fmaxf(ref, wave_max(mx) * a.c), d = ref - to, w = exp2_fast(d);
-            W = w > 0.f ? w * __builtin_fmaf(S, d, W) : 0.f;
-            S *= w;
-            ref = to;
+        if (__ballot((mx - mz) * a.c > kSlack) != 0ull) {
+            const float to = fmaxf(mz, wave_max(mx));
+            move(to, masked || is_wide(to, a.c));
         }
     };
     // A group of vectors, the first of them number `at` of the row, by sums of its own (with 250 additions one after the other
-    // the entropies of 128256 logits were off by 9e-7 of them, and are by 3e-7). -inf makes a NaN of w (0 * -inf), and the group
-    // is taken again with its exponents held above that; what stands for vectors past the end is -inf too, and left out.
+    // the entropies of 128256 logits were off by 9e-7 of them, and are by 3e-7). -inf makes a NaN of w (0 * -inf): that group
+    // and the wave's later ones are taken by differences, held above that (half of 2048 rows of 128256 masked: 101 us, 87 with none, 151 with
+    // such groups taken twice); what stands for vectors past the end is -inf too, and left out.
     const auto sum = [&](const u32x4* v, int at) {
         float s = 0.f, w = 0.f;
+        if (!wide) {
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-            const float before = w;
+            for (int e = 0; e < kGroup; ++e) {
+                const float before = w;
 #pragma unroll
-            for (int i = 0; i < PV; ++i) add_to(s, w, __builtin_fmaf(E::get(v[e], i), a.c, -ref));
-            w = at + e * kLpThreads < last ? w : before;
+                for (int i = 0; i < PV; ++i) add_to(s, w, __builtin_fmaf(E::get(v[e], i), a.c, -ref));
+                w = at + e * kLpThreads < last ? w : before;
+            }
+            if (__ballot(w != w) != 0ull) {
+                masked = true;
+                move(mz, true);
+            }
         }
-        if (__ballot(w != w) != 0ull) {
+        if (wide) {
             s = w = 0.f;
-#pragma unroll 1
-            for (int i = 0; i < PV; ++i) {
+            if (__ballot(tm > -INFINITY) != 0ull) {     // (the wave has met something else)
 #pragma unroll
-                for (int e = 0; e < kGroup; ++e) {
-                    const int at = i / (PV / 4);
-                    const uint32_t x = at == 0 ? v[e][0] : at == 1 ? v[e][1] : at == 2 ? v[e][2] : v[e][3];
-                    add_to(s, w, exponent(DT == 0 ? __uint_as_float(x) : i & 1 ? bf16_hi(x) : bf16_lo(x), a.c, ref));
-                }
+                for (int e = 0; e < kGroup; ++e)
+#pragma unroll
+                    for (int i = 0; i < PV; ++i) add_to(s, w, exponent_wide(E::get(v[e], i), a.c, mz));
             }
         }
         S += s;
@@ -302,7 +314,7 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     }
     if (slice == a.slices - 1) {
         look(z_rest);
-        if (has_rest) add(exponent(z_rest, a.c, ref));
+        if (has_rest) add_to(S, W, wide ? exponent_wide(z_rest, a.c, mz) : exponent(z_rest, a.c, ref));
     }
     {
         const float w = wave_maximum(tm);
@@ -313,18 +325,10 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     float m = sm.red[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = __builtin_elementwise_maximum(m, sm.red[w]);
-    const bool wide = is_wide(m, a.c), some = m > -INFINITY && m < INFINITY;
-    if (some && wide) {
-        // m*c is no finite number: the sums once more, from the differences
-        S = W = 0.f;
-#pragma unroll 1
-        for (int i = first * PV + tid; i < last * PV; i += kLpThreads) add(exponent_wide(E::scalar(row, i), a.c, m));
-        if (has_rest) add(exponent_wide(z_rest, a.c, m));
-        ref = 0.f;
-    }
+    const bool some = m > -INFINITY && m < INFINITY;
     S = wave_sum(S);
     W = wave_sum(W);
-    if (lane == 0) sm.sums[wave][0] = S, sm.sums[wave][1] = W, sm.sums[wave][2] = ref;
+    if (lane == 0) sm.sums[wave][0] = S, sm.sums[wave][1] = W, sm.base[wave] = product(mz, a.c, wide);
 
     pkey_t key = empty_key();
     if (TOP && some) {
@@ -414,14 +418,13 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
         __syncthreads();
     }
     if (wave != 0) return;
-    // the waves' sums, relative to m*c (or to m where that is no finite number)
+    // the waves' sums, relative to the row's (or slice's) largest
     const bool odd = !(m < INFINITY);                   // NaN or +inf; a slice of -inf alone has no sum
-    const float mc = wide ? 0.f : m * a.c;
     Sums s = {0.0, 0.0, 0.0};
     if (some) {
         const int w = lane % kWaves;
-        const float d = lane < kWaves ? sm.sums[w][2] - mc : -INFINITY;
-        const double f = exp2_fast(d), Sw = sm.sums[w][0];      // S*d and W cancel where the reference lies far below the maximum
+        const double d = sm.base[w] - reference(m, a.c);
+        const double f = lane < kWaves ? exp2_fast(static_cast<float>(d)) : 0.f, Sw = sm.sums[w][0];      // S*d and W cancel where the reference lies far below the maximum
         s.S = wave_sum(f > 0.0 ? Sw * f : 0.0);
         s.W = wave_sum(f > 0.0 ? f * (Sw * d + static_cast<double>(sm.sums[w][1])) : 0.0);
     }

@@ -295,3 +295,44 @@ def test_emitted_tokens_of_a_verification(R):
     check(r, want, 3)
     emitted = (torch.arange(K + 1, device="cuda") <= alen.view(-1, 1))
     assert torch.equal(emitted, tokens >= 0) and (r.logprobs[emitted] < 0).all() and (r.logprobs[~emitted] == 0).all()
+
+
+def small(T):
+    """A temperature as the call gets it."""
+    return float(np.float32(T))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1003, 70001])
+@pytest.mark.parametrize("T", [1e-6, 1e-7, 3e-9, 1e-10, 1e-20, 1e-30])
+def test_small_temperatures(R, dtype, V, T):
+    """The product of a logit and log2(e)/T has no binary places left, and rounds by more than a power of two."""
+    rng = np.random.default_rng(int(V - np.log(T)))
+    z, zv = logits(rng, 40, V, dtype, size=6.0)
+    tokens = np.stack([zv.argmax(1), rng.integers(0, V, 40), np.argsort(zv, 1)[:, -2]], 1).astype(np.int32)
+    r = R.token_logprobs(z, dev(tokens), small(T), 4)
+    check(r, ref.forward(zv, tokens, small(T), 4), 4)
+    g = rng.standard_normal((40, 3)).astype(np.float32)
+    check_grad(R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), None, small(T)), *ref.backward(zv, tokens, g, None, small(T), dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1003, 70001])
+@pytest.mark.parametrize("low", [-2e9, -1e10, -1e30])
+def test_rows_far_below_zero(R, dtype, V, low):
+    """Rows masked as a whole by a large negative number, alike or nearly so; some of a row; one token left."""
+    rng = np.random.default_rng(3)
+    base = 3 * rng.standard_normal((5, V)).astype(np.float32)
+    base[0] = low
+    base[1] = low * (1 + 2.0 ** -7 * rng.integers(0, 3, V))
+    base[2, 1:] = low
+    base[3, : V // 2] = low
+    base[4, V // 3:] += low
+    z = dev(base)
+    z = z.bfloat16() if dtype == "bf16" else z
+    zv = z.float().cpu().numpy()
+    tokens = np.stack([np.zeros(5), np.full(5, V - 1), zv.argmax(1)], 1).astype(np.int32)
+    r = R.token_logprobs(z, dev(tokens), 1.0, 5)
+    check(r, ref.forward(zv, tokens, 1.0, 5), 5)
+    g = np.ones((5, 3), np.float32)
+    check_grad(R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g)), *ref.backward(zv, tokens, g, None, 1.0, dtype))
