@@ -549,7 +549,7 @@ __global__ __launch_bounds__(kGradThreads) void logprobs_grad_kernel(LogprobGrad
     const auto at = [&](float z) {
         const float x = (wide ? exponent_wide(z, a.c, m) : exponent(z, a.c, mc)) - l;
         const float p = exp2_fast(x);
-        return ENT ? p * __builtin_fmaf(B, x, A) : p * A;
+        return p == 0.f ? 0.f : p * (ENT ? __builtin_fmaf(B, x, A) : A);      // its factor may be infinite there
     };
 #ifdef __HIP_DEVICE_COMPILE__
     asm volatile("" ::"v"(z_tok));                      // the gradient may take the logits' place: z_tok has arrived

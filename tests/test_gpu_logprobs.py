@@ -336,3 +336,24 @@ def test_rows_far_below_zero(R, dtype, V, low):
     check(r, ref.forward(zv, tokens, 1.0, 5), 5)
     g = np.ones((5, 3), np.float32)
     check_grad(R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g)), *ref.backward(zv, tokens, g, None, 1.0, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,h", [(1e-9, 1.0), (1e-20, -1.0), (1e-30, 1.0), (1.0, 1e10), (1e-37, 0.0)])
+def test_gradient_where_a_factor_is_infinite(R, dtype, T, h):
+    """Tokens of probability 0 get no gradient, however large what multiplies it."""
+    rng = np.random.default_rng(8)
+    z, zv = logits(rng, 9, 5003, dtype)
+    z[1, ::2] = float("-inf")
+    z[2, 1:] = float("-inf")
+    zv = z.float().cpu().numpy()
+    tokens = np.stack([zv.argmax(1), rng.integers(0, 5003, 9), np.full(9, 4)], 1).astype(np.int32)
+    r = R.token_logprobs(z, dev(tokens), small(T))
+    g, gh = np.full((9, 3), 0.5, np.float32), np.full(9, h, np.float32)
+    g[:, 1:] = 0.25 if T > 1e-36 else 3.0                     # the last: (1/T) sum g passes float32
+    got = R.token_logprobs_grad(z, dev(tokens), r.stats, dev(g), dev(gh), small(T)).float().cpu().numpy()
+    want, tol = ref.backward(zv, tokens, g, gh, small(T), dtype)
+    # what is within float32: all but the given tokens' own and the likeliest of the last
+    fits = np.abs(want) + tol < 1e38
+    assert not np.isnan(got).any() and fits.sum() > 9 * 4990
+    assert (np.abs(got - want) <= tol)[fits].all()
