@@ -3,11 +3,15 @@
 //
 // With x_i = log2(e)/T * (z_i - m), m the row's largest logit, S = sum 2^x_i and
 // W = sum 2^x_i x_i:  log p(t) = ln2 * (x_t - log2 S),  H = ln2 * (log2 S - W/S).
-// x is never above 0 but for its rounding, so no exponential overflows.
+// x is never above 0 but for its rounding (of m*log2(e)/T, which is in every x alike).
 //
 // Forward: a workgroup streams a row, or a slice of one where the rows are few.  Each
-// wave takes its vectors as they arrive, against a running reference that moves
-// only where an element passes it by 2^40, so that exponentials overlap the loads.
+// wave takes its vectors as they arrive, against a running reference, a logit that
+// moves only where one passes it by 2^2, so that exponentials overlap the loads.
+// (What is added meanwhile is below 4, and the largest element's exponent so small
+// that its rounding is lost in the sum's: with 2^40 a confident token's log
+// probability was off by 2.4e-6 and the entropy by 9.9e-6, 5e-7 both so. Some 1% of
+// the time.)
 // Of the likeliest: the first eight vectors a thread stay in registers until their
 // threads' maxima say what the rest is measured by.  The n-th largest of them bounds
 // the row's n-th largest element from below, and few elements reach it: the
@@ -68,7 +72,7 @@ __device__ __forceinline__ void stores_done() {
 #endif
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-constexpr float kSlack = 40.f;                          // 2^40 * 2^20 elements * 40 is far from float32's end
+constexpr float kSlack = 2.f;                           // powers of two
 constexpr float kLowest = -1e30f;                       // 0 * kLowest is 0, 0 * -inf is not a number
 constexpr double kLn2 = 0.69314718055994530942;
 
@@ -85,8 +89,8 @@ __device__ __forceinline__ double product(float m, float c, bool wide) {
 __device__ __forceinline__ double reference(float m, float c) { return product(m, c, is_wide(m, c)); }
 
 struct Smem {
-    float red[kWaves], sums[kWaves][2];
-    double base[kWaves];            // what a wave's sums are relative to
+    float red[kWaves];
+    double sums[kWaves][3];         // S, W, and what they are relative to
     uint32_t lists[2][kWaves][kWave];
     u32x4 stage[kWaves][kStage];
     int32_t stage_i[kWaves][kStage];
@@ -210,36 +214,37 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
             move(to, masked || is_wide(to, a.c));
         }
     };
-    // A group of vectors, the first of them number `at` of the row, by sums of its own (with 250 additions one after the other
-    // the entropies of 128256 logits were off by 9e-7 of them, and are by 3e-7). -inf makes a NaN of w (0 * -inf): that group
+    // A group of vectors, the first of them number `at` of the row, by two sums of its own (with 250 additions one after the other
+    // the entropies of 128256 logits were off by 9e-7 of them, by 3e-7 with one a group; peaked rows 7e-7, 5e-7 with two). -inf makes a NaN of w (0 * -inf): that group
     // and the wave's later ones are taken by differences, held above that (half of 2048 rows of 128256 masked: 101 us, 87 with none, 151 with
     // such groups taken twice); what stands for vectors past the end is -inf too, and left out.
     const auto sum = [&](const u32x4* v, int at) {
-        float s = 0.f, w = 0.f;
+        float s[2] = {}, w[2] = {};
         if (!wide) {
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) {
-                const float before = w;
+                const float before = w[e / 2];
 #pragma unroll
-                for (int i = 0; i < PV; ++i) add_to(s, w, __builtin_fmaf(E::get(v[e], i), a.c, -ref));
-                w = at + e * kLpThreads < last ? w : before;
+                for (int i = 0; i < PV; ++i) add_to(s[e / 2], w[e / 2], __builtin_fmaf(E::get(v[e], i), a.c, -ref));
+                w[e / 2] = at + e * kLpThreads < last ? w[e / 2] : before;
             }
-            if (__ballot(w != w) != 0ull) {
+            const float any = w[0] + w[1];
+            if (__ballot(any != any) != 0ull) {
                 masked = true;
                 move(mz, true);
             }
         }
         if (wide) {
-            s = w = 0.f;
+            s[0] = s[1] = w[0] = w[1] = 0.f;
             if (__ballot(tm > -INFINITY) != 0ull) {     // (the wave has met something else)
 #pragma unroll
                 for (int e = 0; e < kGroup; ++e)
 #pragma unroll
-                    for (int i = 0; i < PV; ++i) add_to(s, w, exponent_wide(E::get(v[e], i), a.c, mz));
+                    for (int i = 0; i < PV; ++i) add_to(s[e / 2], w[e / 2], exponent_wide(E::get(v[e], i), a.c, mz));
             }
         }
-        S += s;
-        W += w;
+        S += s[0] + s[1];
+        W += w[0] + w[1];
     };
     // Vectors with an element that reaches tau, to the wave's part of the stage (past its end they are only counted).
     float tau = INFINITY;
@@ -314,7 +319,12 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     }
     if (slice == a.slices - 1) {
         look(z_rest);
-        if (has_rest) add_to(S, W, wide ? exponent_wide(z_rest, a.c, mz) : exponent(z_rest, a.c, ref));
+        if (has_rest) {
+            float s = 0.f, w = 0.f;
+            add_to(s, w, wide ? exponent_wide(z_rest, a.c, mz) : exponent(z_rest, a.c, ref));
+            S += s;
+            W += w;
+        }
     }
     {
         const float w = wave_maximum(tm);
@@ -326,9 +336,8 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = __builtin_elementwise_maximum(m, sm.red[w]);
     const bool some = m > -INFINITY && m < INFINITY;
-    S = wave_sum(S);
-    W = wave_sum(W);
-    if (lane == 0) sm.sums[wave][0] = S, sm.sums[wave][1] = W, sm.base[wave] = product(mz, a.c, wide);
+    const double Sw = wave_sum(static_cast<double>(S)), Ww = wave_sum(static_cast<double>(W));
+    if (lane == 0) sm.sums[wave][0] = Sw, sm.sums[wave][1] = Ww, sm.sums[wave][2] = product(mz, a.c, wide);
 
     pkey_t key = empty_key();
     if (TOP && some) {
@@ -423,13 +432,11 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     Sums s = {0.0, 0.0, 0.0};
     if (some) {
         const int w = lane % kWaves;
-        const double d = sm.base[w] - reference(m, a.c);
-        const double f = lane < kWaves ? exp2_fast(static_cast<float>(d)) : 0.f, Sw = sm.sums[w][0];      // S*d and W cancel where the reference lies far below the maximum
-        s.S = wave_sum(f > 0.0 ? Sw * f : 0.0);
-        s.W = wave_sum(f > 0.0 ? f * (Sw * d + static_cast<double>(sm.sums[w][1])) : 0.0);
+        const double d = sm.sums[w][2] - reference(m, a.c);
+        const double f = lane < kWaves ? exp2(d) : 0.0, Sw = sm.sums[w][0];
+        s.S = wave_sum(Sw * f);
+        s.W = wave_sum(f > 0.0 ? f * (Sw * d + sm.sums[w][1]) : 0.0);
     }
-    S = static_cast<float>(s.S);
-    W = static_cast<float>(s.W);
     if (odd) s.S = __builtin_nan("");
     s.r = reference(m, a.c);
     if (a.slices == 1) {
@@ -442,7 +449,7 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     unsigned long long* rec = a.words + (r * a.slices + slice) * per;
     if (lane == 0) {
         st_agent64(rec, (static_cast<unsigned long long>(__float_as_uint(odd ? __builtin_nanf("") : m)) << 32));
-        st_agent64(rec + 1, (static_cast<unsigned long long>(__float_as_uint(S)) << 32) | __float_as_uint(W));
+        st_agent64(rec + 1, (static_cast<unsigned long long>(__float_as_uint(static_cast<float>(s.S))) << 32) | __float_as_uint(static_cast<float>(s.W)));
     }
     if (TOP && lane < a.top_n) st_agent64(rec + kLpHead + lane, key);
     stores_done();

@@ -357,3 +357,34 @@ def test_gradient_where_a_factor_is_infinite(R, dtype, T, h):
     fits = np.abs(want) + tol < 1e38
     assert not np.isnan(got).any() and fits.sum() > 9 * 4990
     assert (np.abs(got - want) <= tol)[fits].all()
+
+
+def peaked(rng, rows, V, dtype):
+    """Rows of one confident token, 20 to 39 powers of two above the rest, where a wave meets it early, late or last of all."""
+    z = rng.standard_normal((rows, V)).astype(np.float32)
+    r = np.arange(rows)
+    at = np.array([0, 5, V // 3, V // 2, V - 700, V - 2, V - 1])[r % 7]
+    z[r, at] = 4 + np.array([20, 24, 27, 30, 39])[r % 5] * np.log(2)
+    t = dev(z)
+    t = t.bfloat16() if dtype == "bf16" else t
+    return t, t.float().cpu().numpy().astype(np.float64), at
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(8, 20011), (300, 20011), (300, 128256)])
+def test_confident_rows(R, dtype, rows, V):
+    """The sum is 1 and a little. Behind the peak it goes through 15 additions of a group's half, one of the halves, 16 of groups at
+    most, each off by half a step of float32 above 1, which is 2^-24, in either direction: four times the root of the sum of
+    their squares (a third of 2^-48 each); and the peak's own exponential by a step and by its exponent's rounding, 2^-24."""
+    rng = np.random.default_rng(rows + V)
+    z, y, at = peaked(rng, rows, V, dtype)
+    tol = 4 * np.sqrt(32 / 3) * 2.0 ** -24 + 2.0 ** -23 + 2.0 ** -24
+    r = R.token_logprobs(z, dev(at.astype(np.int32)), 1.0, 1)
+    x = y - y[np.arange(rows), at][:, None]
+    e = np.exp(x)
+    e[np.arange(rows), at] = 0.0
+    rest = e.sum(1)
+    lp, h = -np.log1p(rest), np.log1p(rest) - (e * x).sum(1) / (1 + rest)
+    assert np.abs(r.logprobs.double().cpu().numpy() - lp).max() < tol
+    assert (np.abs(r.entropy.double().cpu().numpy() - h) < tol + 8 * 2.0 ** -24 * h).all()
+    assert np.array_equal(r.top_tokens[:, 0].cpu().numpy(), at) and (r.logprobs <= 0).all()
