@@ -809,7 +809,7 @@ int spec_paged_attention(const spec_kvq_rows_t* q, spec_dtype_t dtype, int B, in
  * are negative is not read: log probabilities, entropy and statistics 0, tops -1
  * and -inf; so out_tokens of a verification call can be given as it is.  A row
  * with a NaN, a +inf or only -inf among its logits, or with a token of V or more,
- * answers NaN (and -1).  Sums are float32 over a wave's elements, float64 after.
+ * answers NaN (and -1).  Sums are float32 over a thread's elements, float64 after.
  *   tokens         [R][M] int32, 0 <= M <= SPEC_TOPK_MAX (M 0: NULL, every row is read)
  *   temperature    above 0; log2(e) / temperature a finite float32
  *   top_n          0 <= top_n <= SPEC_TOPK_MAX

@@ -449,7 +449,8 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     unsigned long long* rec = a.words + (r * a.slices + slice) * per;
     if (lane == 0) {
         st_agent64(rec, (static_cast<unsigned long long>(__float_as_uint(odd ? __builtin_nanf("") : m)) << 32));
-        st_agent64(rec + 1, (static_cast<unsigned long long>(__float_as_uint(static_cast<float>(s.S))) << 32) | __float_as_uint(static_cast<float>(s.W)));
+        st_agent64(rec + 1, static_cast<unsigned long long>(__double_as_longlong(s.S)));
+        st_agent64(rec + 2, static_cast<unsigned long long>(__double_as_longlong(s.W)));
     }
     if (TOP && lane < a.top_n) st_agent64(rec + kLpHead + lane, key);
     stores_done();
@@ -461,12 +462,14 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     if (lane == 0) __hip_atomic_store(a.done + r, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // lane l has slice l (at most 64 of them)
     unsigned long long* base = a.words + r * a.slices * per;
-    float ms = -INFINITY, Ss = 0.f, Ws = 0.f;
+    float ms = -INFINITY;
+    double Ss = 0.0, Ws = 0.0;
     if (lane < a.slices) {
-        const unsigned long long w0 = ld_agent64(base + lane * per), w1 = ld_agent64(base + lane * per + 1);
+        const unsigned long long w0 = ld_agent64(base + lane * per), w1 = ld_agent64(base + lane * per + 1),
+                                 w2 = ld_agent64(base + lane * per + 2);
         ms = __uint_as_float(static_cast<uint32_t>(w0 >> 32));
-        Ss = __uint_as_float(static_cast<uint32_t>(w1 >> 32));
-        Ws = __uint_as_float(static_cast<uint32_t>(w1));
+        Ss = __longlong_as_double(static_cast<long long>(w1));
+        Ws = __longlong_as_double(static_cast<long long>(w2));
     }
     if (TOP) {
         // all lists as one: 64 keys at a time, four loads under way
@@ -494,8 +497,8 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     s.r = reference(mr, a.c);
     const double d = ms > -INFINITY ? rs - s.r : 0.0;
     const double w = ms > -INFINITY ? exp2(d) : 0.0;
-    s.S = wave_sum(static_cast<double>(Ss) * w);
-    s.W = wave_sum(w > 0.0 ? w * (static_cast<double>(Ws) + static_cast<double>(Ss) * d) : 0.0);
+    s.S = wave_sum(Ss * w);
+    s.W = wave_sum(w > 0.0 ? w * (Ws + Ss * d) : 0.0);
     if (!(mr < INFINITY)) s.S = __builtin_nan("");
     finish_row(a, r, s, mr, key, tok, z_tok, bad);
 }

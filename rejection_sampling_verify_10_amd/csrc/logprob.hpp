@@ -25,7 +25,7 @@ struct LogprobArgs {
     unsigned long long* words;      // [R][slices][kLpHead + top_n] (slices > 1), zero before and after a call
     unsigned* done;                 // [R] slices that have written theirs, zero before and after a call
 };
-constexpr int kLpHead = 2;          // words of a slice's record before its list
+constexpr int kLpHead = 3;          // words of a slice's record before its list: largest logit, S, W
 
 struct LogprobGradArgs {
     const void* logits;

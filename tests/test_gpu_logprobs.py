@@ -388,3 +388,18 @@ def test_confident_rows(R, dtype, rows, V):
     assert np.abs(r.logprobs.double().cpu().numpy() - lp).max() < tol
     assert (np.abs(r.entropy.double().cpu().numpy() - h) < tol + 8 * 2.0 ** -24 * h).all()
     assert np.array_equal(r.top_tokens[:, 0].cpu().numpy(), at) and (r.logprobs <= 0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 8, 300])
+def test_sums_past_32_bits(R, rows):
+    """A token that is all but certain, whichever way its row is cut up: exponents are whole numbers here (log2(e)/T rounds to 1), so
+    that the sum, 1 + 20010 * 2^-40, is off only by what the peak's own thread had of the rest, 40 elements."""
+    import torch
+    V = 20011
+    for at in (0, 9000, V - 1):
+        z = torch.zeros(rows, V, device="cuda")
+        z[:, at] = 40.0
+        r = R.token_logprobs(z, dev(np.full(rows, at, np.int32)), float(np.float32(np.log2(np.e))))
+        rest = (V - 1) * 2.0 ** -40
+        lp, h = -rest, rest * (1 + 40 * np.log(2))
+        assert (r.logprobs.double() / lp - 1).abs().max() < 41 / V and (r.entropy.double() / h - 1).abs().max() < 41 / V
