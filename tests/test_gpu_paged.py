@@ -640,3 +640,35 @@ def test_a_speculative_run(R):
     free = int(pool.state[1])
     granted, _ = R.page_step(pool, lengths, 1, counts=ints([0, 0, 0, 0]))
     assert granted.tolist() == [0, 0, 0, 0] and pool.held[1] == 0 and int(pool.state[1]) > free
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,n", [(40, 16384), (40, 32768), (1, 32768), (8, 65536)])
+@pytest.mark.parametrize("top", [16.5, 17.375, 18.0])
+def test_one_key_of_weight_one(R, dtype, N, n, top):
+    """And many of 2^-24 to 2^-26, each less than the sum's last place. Units that are not split (as many batch rows as that takes,
+    all on the same pages), of 128 query rows and of 32. Scores are exact here: the queries have one element, the keys too.
+
+    lse: m and the sum's logarithm meet near 25, in base two, off by half a step there (2^-20) and half a step of the product with
+    ln 2 (2^-20); log2(e)/8 is off by 2^-25 of 25; the sum itself by a few 2^-24: 3e-6 in all.  An output of float32 queries: three
+    parts of P, each eight keys' sum rounded to nearest at the output's size: six times the root of the sum of the squares."""
+    import torch
+    rng = np.random.default_rng(n + N)
+    B, H, D, P = 64, 8, 64, 256
+    cache = make_cache(R, rng, n // P + 1, P, H, D)
+    cache.k_pages.zero_()
+    cache.k_pages[0, 3, :, 0] = top
+    tables = np.arange(n // P + 1, dtype=np.int32)[None].repeat(B, 0)
+    q = torch.zeros(B, N, H, D, device="cuda")
+    q[..., 0] = 8.0
+    q = q.bfloat16() if dtype == "bf16" else q
+    out, lse = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints([n] * B), N, H))
+    others = n - 1 + np.arange(1, N + 1)
+    w = np.exp(-top)
+    assert np.abs(f64(lse) - (top + np.log1p(others * w))[None, :, None]).max() < 3e-6
+    if dtype == "f32":
+        v = f64(cache.v_pages).reshape(-1, H, D)
+        rest = np.cumsum(v, 0)[n - 1 + np.arange(1, N + 1)] - v[3]
+        want = (v[3] + w * rest) / (1 + others * w)[:, None, None]
+        tol = 6 * np.sqrt(3 * (n + N) / 8 / 12) * 2.0 ** -22 * np.abs(want) + 2.0 ** -23
+        assert (np.abs(f64(out) - want) < tol).all()
