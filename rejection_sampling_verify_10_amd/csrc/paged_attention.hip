@@ -44,6 +44,7 @@ constexpr int kTileKeys = 32;                           // keys of a tile
 constexpr int kWindow = kWave;                          // 16-key groups whose pages a wave holds, one a lane
 constexpr int kBatch = 8;                               // parts under way in the join
 constexpr float kSlack = 8.f;                           // powers of two a score may pass the running maximum by
+constexpr float kFar = 16777216.f;                      // of a maximum in base two: from here on its rounding passes a power of two
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -264,10 +265,11 @@ template <int D, int DT> struct Wave {
     u32x4 Q[NQ][D / 16];
     f32x16 O[NT];
     float m, l, low;                                    // the sum is l + low
+    bool far;                                           // a maximum of the wave's passes kFar
     u32x4 K[D / 16];                                    // of the tile to come
     u32x4 V[kEarlyV ? 2 : 1][NT];
     unsigned ka, va;                                    // the lane's LDS offsets in a buffer of K and V
-    __device__ __forceinline__ Wave() : m(-INFINITY), l(0.f), low(0.f) {
+    __device__ __forceinline__ Wave() : m(-INFINITY), l(0.f), low(0.f), far(false) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -360,8 +362,8 @@ template <int D, int DT> struct Wave {
         }
         return odd;
     }
-    // P of a tile's scores, and the maximum and sums.
-    __device__ __forceinline__ void weigh(const f32x16& S, float cexp, float slack, u32x4 (&P)[NQ][2]) {
+    // P of a tile's scores (which may be gone then), and the maximum and sums.
+    __device__ __forceinline__ void weigh(f32x16& S, float cexp, float slack, u32x4 (&P)[NQ][2]) {
         float mx = S[0];                                // NaN propagates, and moves no maximum
 #pragma unroll
         for (int i = 1; i < 15; i += 2) mx = maximum3(mx, S[i], S[i + 1]);
@@ -380,8 +382,16 @@ template <int D, int DT> struct Wave {
                 if (kSums) sums_set(O[t]);
             }
             m = mn;
+            far = __ballot(fabsf(m) * cexp >= kFar && m > -INFINITY) != 0ull;
         }
-        const float mc = m == -INFINITY ? 0.f : m * cexp;
+        const float mr = m == -INFINITY ? 0.f : m;
+        float mc = mr * cexp;
+        if (__builtin_expect(far, 0)) {                                      // its rounding would be in every exponent; each query by itself, again
+            const bool mine = fabsf(mr) * cexp >= kFar;
+            mc = mine ? 0.f : mc;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] -= mine ? mr : 0.f;
+        }
         float sum[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {

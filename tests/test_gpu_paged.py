@@ -672,3 +672,29 @@ def test_one_key_of_weight_one(R, dtype, N, n, top):
         want = (v[3] + w * rest) / (1 + others * w)[:, None, None]
         tol = 6 * np.sqrt(3 * (n + N) / 8 / 12) * 2.0 ** -22 * np.abs(want) + 2.0 ** -23
         assert (np.abs(f64(out) - want) < tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("N,n", [(3, 900), (50, 2100)])
+@pytest.mark.parametrize("size", [2.0 ** 26, 2.0 ** 33, 2.0 ** 40, 2.0 ** 110])
+def test_large_scores(R, dtype, D, N, n, size):
+    """Scores whose product with log2(e)*scale rounds by more than a power of two: the largest key alone has weight, or those of the
+    same score share it. Queries of one element, so that scores are exact, negative ones in every second row."""
+    import torch
+    rng = np.random.default_rng(N)
+    B, H, G, P = 2, 2, 1, 16
+    lens = [n, 5, 700]
+    width = -(-(n + N) // P)
+    pages = sum(-(-(x + N) // P) for x in lens)
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    cache.k_pages[..., 1:] = 0
+    cache.k_pages[..., 0] = dev(rng.integers(1, 255, (pages, P, H)).astype(np.float32) / 128).bfloat16()       # ties among them
+    q = torch.zeros(B, N, H * G, D, device="cuda")
+    q[..., 0] = size
+    q[:, 1::2] *= -1
+    q = q.bfloat16() if dtype == "bf16" else q
+    got = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, prefix_row=ints([2, 2])))
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+    check(R, q, cache, tables, lens, B, prefix_row=[2, 2], got=got)
