@@ -185,7 +185,8 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
             if (lane == 0 && (lo | hi)) atomicAdd(&cost, (static_cast<unsigned long long>(hi) << 24) + lo);
         }
         __syncthreads();
-        const int least = static_cast<int>(max((cost + a.target - 1) / a.target, 1ull));
+        // (no job has more than 2^23 chunks)
+        const int least = static_cast<int>(min(max((cost + a.target - 1) / a.target, 1ull), 1ull << 23));
         const auto raised = [](int m) { return m + m / 16 + 1; };
         // two waves a size
         const int step = wave % kSteps;

@@ -698,3 +698,23 @@ def test_large_scores(R, dtype, D, N, n, size):
     got = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, prefix_row=ints([2, 2])))
     assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
     check(R, q, cache, tables, lens, B, prefix_row=[2, 2], got=got)
+
+
+@pytest.mark.parametrize("B,heads,n", [(65536, 8, 2 ** 30 - 1), (65535, 16, 2 ** 30 - 1), (4096, 512, 2 ** 30 - 1), (65536, 8, 2 ** 29 + 77)])
+def test_a_plan_of_the_longest_rows(R, B, heads, n):
+    """More chunks in all than 2^31 a unit of the target: every job is one unit, and nothing is written behind the plan."""
+    import ctypes
+    import torch
+    need = R.lib().spec_paged_plan_bytes(B, 1, heads, heads, 64, 1)
+    plan = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    off = -plan.data_ptr() % 256
+    lengths, prefix = torch.full((B,), n, dtype=torch.int32, device="cuda"), torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    rc = R.lib().spec_paged_plan(B, 1, heads, heads, 64, B, 1 << 20, 1024, lengths.data_ptr(), None, prefix.data_ptr(),
+                                 plan.data_ptr() + off, need, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    words = plan[off:off + need].view(torch.int32)
+    assert words[0].item() == B
+    units = words[64:64 + 12 * B].view(B, 12)                 # behind the sizes, 256 bytes: 48 a unit
+    assert (units[:, 4] == 0).all() and (units[:, 5] == n + 1).all() and (units[:, 8] == -1).all()
+    assert torch.equal(units[:, 0].sort().values, torch.arange(B, dtype=torch.int32, device="cuda"))
+    assert (plan[off + need:] == 0x5a).all() and (plan[:off] == 0x5a).all()
