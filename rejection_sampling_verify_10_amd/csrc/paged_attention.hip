@@ -666,7 +666,10 @@ template <int D, int DT> __device__ __forceinline__ void attend_narrow(const Pag
         if (next < tiles) {
             if (next / kPer != t / kPer) {
                 ld.next_window(next / kPer);
-                if ((next / kPer + 1) * kPer < tiles) ld.fetch_window(next / kPer + 1);
+                if ((next / kPer + 1) * kPer < tiles) {
+                    wait_lds();                         // the window's pages are read before the next ones take their place
+                    ld.fetch_window(next / kPer + 1);
+                }
             }
             if (W::kNarrowK) ld.load_k(next);
             if (W::kEarlyV) ld.load_v(next);
