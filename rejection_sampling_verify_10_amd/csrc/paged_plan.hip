@@ -16,6 +16,8 @@
 // stores: 9-11 us up to 1024 rows.  Units of several sizes are tried at once, two waves
 // a size; reading the rows again for every size in turn took 18-27 us.
 
+#include <algorithm>
+
 #include "paged.hpp"
 
 namespace sv {
@@ -327,11 +329,18 @@ void paged_plan_sizes(PagedPlanArgs& a) {
     const long long target = (workgroups + a.heads - 1) / a.heads;
     a.shape = 4 * a.heads + 2 * (a.D == 256) + (a.prefix_row ? 1 : 0);
     a.target = a.prefix_row || own < target ? static_cast<int>(target) : 0;
-    // a unit more than the split for each job; a run's rows come to one tile more than fit
-    const long long rows = static_cast<long long>(a.B) * a.M;
-    const long long shared = a.prefix_row ? rows / kPgWide + a.B : 0;
-    a.max_units = own + shared + a.target;
-    a.max_parts = a.target ? (own + a.target) * a.own_rows + (a.prefix_row ? (shared + a.target) * kPgWide : 0) : 0;
+    // Every job is a unit, and the split makes fewer than `target` more. The tiles of a run are no more than those of its batch rows by
+    // themselves; their query rows, filled up, are the most for runs of one batch row, or of the fewest that need 128.
+    const bool all_narrow = static_cast<long long>(a.B) * a.M <= kPgNarrow;
+    const long long fewest = a.M <= kPgNarrow ? kPgNarrow / a.M + 1 : 1;
+    long long shared = 0, tile = a.own_rows;
+    if (a.prefix_row) {
+        shared = a.M > kPgNarrow || all_narrow ? own * a.own_rows
+                                               : std::max(own * kPgNarrow, (a.B * static_cast<long long>(kPgWide) + fewest - 1) / fewest);
+        if (!all_narrow) tile = kPgWide;
+    }
+    a.max_units = own + (a.prefix_row ? own : 0) + a.target;
+    a.max_parts = a.target ? own * a.own_rows + shared + a.target * tile : 0;
 }
 
 hipError_t launch_paged_plan(const PagedPlanArgs& a, hipStream_t s, Timing t) {

@@ -718,3 +718,41 @@ def test_a_plan_of_the_longest_rows(R, B, heads, n):
     assert (units[:, 4] == 0).all() and (units[:, 5] == n + 1).all() and (units[:, 8] == -1).all()
     assert torch.equal(units[:, 0].sort().values, torch.arange(B, dtype=torch.int32, device="cuda"))
     assert (plan[off + need:] == 0x5a).all() and (plan[:off] == 0x5a).all()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_plans_stay_within_their_sizes(R, seed):
+    """Units and rows of parts of random batches: all there is room for, no part in two units, every key of every query row once."""
+    import torch
+    rng = np.random.default_rng(seed)
+    for _ in range(12):
+        B, N, G, H = int(rng.choice([1, 2, 3, 7, 30, 64, 500, 1500])), int(rng.choice([1, 2, 7, 27, 70])), int(rng.choice([1, 3, 8])), int(rng.choice([1, 2, 4, 8, 32]))
+        D = int(rng.choice([64, 256]))
+        if B * N > 20000:
+            N = 1
+        runs = int(rng.integers(1, 5))
+        long = int(rng.choice([10, 600, 9000]))
+        lens = np.concatenate((rng.integers(0, int(rng.choice([2, 300, 3000])), B), rng.integers(0, long, runs)))
+        prefix = B + np.sort(rng.integers(0, runs, B))
+        prefix[rng.random(B) < 0.1] = -1
+        if rng.random() < 0.3:
+            prefix = B + np.arange(B) % runs                  # no two neighbours alike
+        P, width = 64, 200
+        cache = make_cache(R, rng, 1, P, H, D)
+        plan = R.paged_plan(cache, torch.zeros(B + runs, width, dtype=torch.int32, device="cuda"), ints(lens), N, H * G, B=B, prefix_row=ints(prefix))
+        words = plan._buffer[plan._ptr - plan._buffer.data_ptr():][:plan.bytes].view(torch.int32).cpu().numpy()
+        n, M = int(words[0]), N * G
+        own_tiles = 1 if M <= 32 else -(-M // 128)
+        target = -(-(256 if D == 256 else 512) // H)
+        assert n <= 2 * B * own_tiles + target
+        u = words[64:64 + 12 * n].reshape(n, 12)
+        rows = (R.paged_attention_workspace_bytes(plan, D)) // (H * (D + 2) * 4)
+        tile = np.where(u[:, 9] != 0, 128, 32)
+        part = u[u[:, 8] >= 0]
+        ends = part[:, 8] + tile[u[:, 8] >= 0]
+        order = np.argsort(part[:, 8])
+        assert ends.max(initial=0) <= rows and (ends[order][:-1] <= part[order][1:, 8]).all()
+        seen = (u[:, 5] - u[:, 4]).astype(np.int64) * np.minimum(tile, u[:, 2] - u[:, 1])
+        shared = np.where(prefix >= 0, lens[np.maximum(prefix, 0)], 0)
+        least = (M * (shared + lens[:B])).sum()
+        assert least <= seen.sum() <= least + M * N * B       # new tokens: those a tile looks at

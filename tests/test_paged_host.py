@@ -159,3 +159,24 @@ def test_reference_attention_by_hand():
     for n in range(2):
         p = np.exp(0.1 * k[:4 + n] @ q[0, n, 0])
         assert np.allclose(out[0, n, 0], p @ v[:4 + n] / p.sum()) and np.isclose(lse[0, n, 0], np.log(p.sum()))
+
+
+@pytest.mark.parametrize("B,N,Hq,H,D,most", [(2048, 1, 64, 8, 128, 600e6), (4, 1, 32, 8, 128, 10e6), (4, 1, 8, 8, 128, 10e6), (32, 8, 32, 8, 128, 62e6)])
+def test_workspaces_hold_what_plans_need(L, B, N, Hq, H, D, most):
+    """Parts of tiles as full as a batch's runs can make them, and of the split: not a tile of 128 rows for each batch row."""
+    assert 0 < L.spec_paged_attention_workspace_bytes(B, N, Hq, H, D, 1) < most
+
+
+def test_rows_of_runs_filled_up():
+    """The bound of paged_plan_sizes on the query rows of runs, each filled up to tiles (32 for up to 32 rows, else 128), against
+    every partition of a batch into runs, by dynamic programming; and of their tiles."""
+    for M in (*range(1, 40), 63, 64, 100, 127, 128, 129, 135, 300):
+        most, tiles = [0], [0]
+        fewest = 32 // M + 1 if M <= 32 else 1
+        for B in range(1, 30):
+            pad = [32 if k * M <= 32 else -(-k * M // 128) * 128 for k in range(B + 1)]
+            most.append(max(pad[k] + most[B - k] for k in range(1, B + 1)))
+            tiles.append(max(max(-(-k * M // 128), 1) + tiles[B - k] for k in range(1, B + 1)))
+            own = B * (1 if M <= 32 else -(-M // 128))
+            bound = own * (32 if M <= 32 else 128) if M > 32 or B * M <= 32 else max(32 * B, -(-B * 128 // fewest))
+            assert most[B] <= bound and tiles[B] <= own, (B, M)
