@@ -10,6 +10,11 @@ Training a draft model on M tokens a position (ids [.., M]) and their gradients 
 
     r = token_logprobs(logits, ids)
     dlogits = token_logprobs_grad(logits, ids, r.stats, g)
+
+or, with logits that require a gradient, through autograd: r.logprobs and r.entropy carry the graph.
+
+    loss = -(weights * token_logprobs(logits, ids).logprobs).sum()
+    loss.backward()
 """
 
 from __future__ import annotations
@@ -17,6 +22,7 @@ from __future__ import annotations
 from typing import Dict, NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import SPEC_TOPK_MAX, lib
 from .kvq import _CODES, _call, _scratch, _tensor
@@ -106,7 +112,15 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], tempera
     M <= 64 a row in a last dimension, or None (every row's entropy and tops alone; logprobs is then empty).  Negative
     tokens are none, and rows without a token are not read: their log probabilities and entropy are 0, their tops -1
     and -inf.  ``workspace`` (:func:`new_workspace`; zero-filled once, calls leave it zero) avoids one a call.
+
+    Where the logits require a gradient, logprobs and entropy pass one on (once: it has none itself); the rest does not.
     """
+    if logits.requires_grad and torch.is_grad_enabled():
+        return TokenLogprobs(*_Logprobs.apply(logits, tokens, temperature, top_n, workspace))
+    return _forward(logits, tokens, temperature, top_n, workspace)
+
+
+def _forward(logits, tokens, temperature, top_n, workspace) -> TokenLogprobs:
     top_n = int(top_n)
     rows, step, M, lead, need = _call_sizes(logits, tokens, top_n)
     V, dev = logits.shape[-1], logits.device
@@ -129,6 +143,30 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], tempera
     return TokenLogprobs(lp, entropy, stats, top, top_lp)
 
 
+class _Logprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature, top_n, workspace):
+        r = _forward(logits, tokens, temperature, top_n, workspace)
+        ctx.save_for_backward(logits, tokens, r.stats)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in r[2:] if t is not None))
+        return tuple(r)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_lp, g_entropy, *_):
+        logits, tokens, stats = ctx.saved_tensors
+        if tokens is None:                      # every row's entropy alone: any token, without a gradient of its own
+            tokens = torch.zeros(logits.shape[:-1], dtype=torch.int32, device=logits.device)
+            g_lp = None
+        if g_lp is None and g_entropy is None:
+            return None, None, None, None, None
+        g_lp = torch.zeros_like(tokens, dtype=torch.float32) if g_lp is None else g_lp.contiguous()
+        g_entropy = None if g_entropy is None else g_entropy.contiguous()
+        return token_logprobs_grad(logits, tokens, stats, g_lp, g_entropy, ctx.temperature), None, None, None, None
+
+
 def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.Tensor, grad_logprobs: torch.Tensor,
                         grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0, *,
                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -148,6 +186,8 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch
         raise ValueError("out must have the logits' shape, type and device")
     else:
         out_step = _logit_rows(out, "out")[1]
+        if not out.is_inference():
+            torch.autograd.graph.increment_version(out)     # a graph that has kept it, as the logits' may, is told
     _call(lib().spec_token_logprobs_grad, "spec_token_logprobs_grad", dev, logits.data_ptr(), _CODES[logits.dtype], step,
           rows, logits.shape[-1], tp, M, _tensor(stats, "stats", torch.float32, lead + (3,), dev),
           _tensor(grad_logprobs, "grad_logprobs", torch.float32, tokens.shape, dev),

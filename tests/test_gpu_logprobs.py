@@ -403,3 +403,90 @@ def test_sums_past_32_bits(R, rows):
         rest = (V - 1) * 2.0 ** -40
         lp, h = -rest, rest * (1 + 40 * np.log(2))
         assert (r.logprobs.double() / lp - 1).abs().max() < 41 / V and (r.entropy.double() / h - 1).abs().max() < 41 / V
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [None, 0, 1, 3])
+def test_autograd(R, dtype, M):
+    """The graph's gradient is the call's, bit for bit; tokens of the leading shape (None), of M a row, or none (0)."""
+    import torch
+    rng = np.random.default_rng(9)
+    z = logits(rng, 12, 5003, dtype, pad=5)[0].view(3, 4, 5003)
+    shape = (3, 4) if M is None else (3, 4, M)
+    tokens = None if M == 0 else dev(rng.integers(-1, 5003, shape).astype(np.int32))
+    g = None if M == 0 else dev(rng.standard_normal(shape).astype(np.float32))
+    gh = dev(rng.standard_normal((3, 4)).astype(np.float32))
+    plain = R.token_logprobs(z, tokens, 0.7, 3)
+    assert not plain.logprobs.requires_grad
+    z.requires_grad_()
+    with torch.no_grad():
+        assert not R.token_logprobs(z, tokens, 0.7).entropy.requires_grad
+    r = R.token_logprobs(z, tokens, 0.7, 3)
+    for a, b in zip(r, plain):
+        assert torch.equal(a, b)
+    assert r.logprobs.requires_grad and r.entropy.requires_grad
+    assert not (r.stats.requires_grad or r.top_tokens.requires_grad or r.top_logprobs.requires_grad)
+    ids = torch.zeros(3, 4, dtype=torch.int32, device="cuda") if M == 0 else tokens
+    none = torch.zeros_like(ids, dtype=torch.float32)
+    zd = z.detach()
+    want = R.token_logprobs_grad(zd, ids, r.stats, none if M == 0 else g, gh, 0.7)
+    loss = (gh * r.entropy).sum() + (0 if M == 0 else (g * r.logprobs).sum())
+    got, = torch.autograd.grad(loss, z, retain_graph=True)
+    assert got.dtype == z.dtype and torch.equal(got, want)
+    got, = torch.autograd.grad(r.entropy.sum(), z, retain_graph=True)     # one of the two alone, a gradient that is expanded
+    assert torch.equal(got, R.token_logprobs_grad(zd, ids, r.stats, none, torch.ones_like(gh), 0.7))
+    if M != 0:
+        got, = torch.autograd.grad(r.logprobs.sum(), z, retain_graph=True)
+        assert torch.equal(got, R.token_logprobs_grad(zd, ids, r.stats, none + 1, None, 0.7))
+    got, = torch.autograd.grad(loss, z, create_graph=True)                # its own gradient is refused
+    with pytest.raises(RuntimeError, match="grad"):
+        got.float().sum().backward()
+    loss = R.token_logprobs(z, tokens, 0.7).entropy.sum()
+    R.token_logprobs_grad(zd, ids, r.stats, none, gh, 0.7, out=zd)        # the logits' memory now holds something else
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_a_draft_models_step(R):
+    """Targets' tokens under a linear head: gradients of its weights and inputs against float64 autograd."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn(2, 9, 64, generator=g, device="cuda", requires_grad=True)
+    w = torch.randn(1003, 64, generator=g, device="cuda", requires_grad=True)
+    ids = torch.randint(0, 1003, (2, 9, 4), generator=g, device="cuda", dtype=torch.int32)
+    p = torch.rand(2, 9, 4, generator=g, device="cuda")
+    r = R.token_logprobs(x @ w.T, ids, 1.3)
+    (-(p * r.logprobs).sum() - 0.1 * r.entropy.sum()).backward()
+    xd, wd = (t.detach().double().requires_grad_() for t in (x, w))
+    lp = ((xd @ wd.T) / 1.3).log_softmax(-1)
+    (-(p * lp.gather(-1, ids.long())).sum() + 0.1 * (lp.exp() * lp).sum()).backward()
+    # sums of 18 and 1003 float32 products, whose terms' roundings do not all point one way
+    for a, b in ((x.grad, xd.grad), (w.grad, wd.grad)):
+        assert (a - b).abs().max() < 64 * 2.0 ** -24 * b.abs().max()
+
+
+def test_a_training_step_captured(R):
+    """Forward and backward captured and replayed on other logits, with eager steps between."""
+    import torch
+    rng = np.random.default_rng(10)
+    x = logits(rng, 4, 40000, "bf16")[0].clone().requires_grad_()
+    tokens = dev(rng.integers(0, 40000, (4, 2)).astype(np.int32))
+
+    def step():
+        r = R.token_logprobs(x, tokens, 0.9)
+        return torch.autograd.grad(r.logprobs.sum() + 0.2 * r.entropy.sum(), x)[0]
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        with torch.no_grad():
+            x.copy_(logits(rng, 4, 40000, "bf16")[0])
+        eager = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
