@@ -437,7 +437,7 @@ bool paged_sizes(PagedPlanArgs& a, int q_heads, int heads, int head_dim, bool wi
     a.prefix_row = with_prefix ? &some : nullptr;       // only whether there is one counts
     paged_plan_sizes(a);
     const double workgroups = static_cast<double>(a.max_units) * heads, rows = static_cast<double>(a.B) * a.N * q_heads;
-    // parts are joined 1024 / D rows a workgroup of 256, at most 16 threads a row each
+    // parts are joined D / 4 threads a row, 64 at most
     return kvq_threads_ok(workgroups, 256) && rows * 64 < 4294967296.0 && a.max_parts < (1ll << 31);
 }
 bool paged_args_ok(int B, int N, int q_heads, int heads) {

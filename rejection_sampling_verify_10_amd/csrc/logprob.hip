@@ -547,7 +547,7 @@ __global__ __launch_bounds__(kGradThreads) void logprobs_grad_kernel(LogprobGrad
     const bool last = slice == a.slices - 1;
     const bool mine = !bad && tok >= first * PV && (last || tok < (first + kGradVecs * kGradThreads) * PV);
     const float z_tok = mine ? E::scalar(row, tok) : 0.f;
-    const float g = a.g_lp && tok >= 0 && lane < a.M ? a.g_lp[r * a.M + lane] : 0.f;
+    const float g = tok >= 0 && lane < a.M ? a.g_lp[r * a.M + lane] : 0.f;
     const float m = a.stats[kLpStats * r], l = bad ? __builtin_nanf("") : a.stats[kLpStats * r + 1];
     const float h = ENT ? a.g_entropy[r] : 0.f, H = ENT ? a.stats[kLpStats * r + 2] : 0.f;
     const float G = wave_sum(g);

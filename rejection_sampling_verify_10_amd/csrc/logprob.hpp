@@ -35,7 +35,7 @@ struct LogprobGradArgs {
     const int32_t* tokens;          // [R][M]
     int M;
     const float* stats;             // [R][kLpStats]
-    const float* g_lp;              // [R][M] or null
+    const float* g_lp;              // [R][M]
     const float* g_entropy;         // [R] or null
     float c, invT;
     int slices;                     // workgroups a row
