@@ -13,6 +13,7 @@
 // writes in place.  512 sequences of 8 tokens 5.0 us (10.5 with 64-bit sums by
 // shuffles), 16 prompts of up to 8192 tokens 4.3.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "paged.hpp"
@@ -23,8 +24,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kPart = 1024;         // tokens of a row that a workgroup finds the slots of
+constexpr int kPart = 1024;         // least tokens of a row that a workgroup finds the slots of, where there are several for it
 constexpr int kRowsMax = 128;       // rows of a workgroup
+constexpr int kMostWorkgroups = 1024;
 
 struct Need {
     int len, cnt, held, need;
@@ -93,7 +95,7 @@ __device__ __forceinline__ int wrap(unsigned x, int pages) {
     return static_cast<int>(x >= static_cast<unsigned>(pages) ? x - pages : x);
 }
 
-__global__ __launch_bounds__(kThreads) void page_step_kernel(PageStepArgs a, int rows_wg, int parts) {
+__global__ __launch_bounds__(kThreads) void page_step_kernel(PageStepArgs a, int rows_wg, int parts, int part_n) {
     __shared__ Pair sh[kWaves];
     __shared__ Served mine[kRowsMax];
     __shared__ unsigned most[kWaves];
@@ -144,8 +146,8 @@ __global__ __launch_bounds__(kThreads) void page_step_kernel(PageStepArgs a, int
             for (int j = s.need + at; j < s.held; j += step)
                 a.ring[wrap(static_cast<unsigned>(s.give) + (j - s.need), a.pages)] = table[j];
         }
-        const int last = min(a.N, (part + 1) * kPart);
-        for (int i = part * kPart + at; i < last; i += step) {
+        const int last = min(a.N, (part + 1) * part_n);
+        for (int i = part * part_n + at; i < last; i += step) {
             int slot = -1;
             if (i < s.cnt) {
                 const int pos = s.len + i, j = pos >> a.page_log2;
@@ -201,11 +203,13 @@ __global__ __launch_bounds__(kThreads) void page_step_kernel(PageStepArgs a, int
 }  // namespace
 
 hipError_t launch_page_step(const PageStepArgs& a, hipStream_t s, Timing t) {
-    // a wave a row, or a workgroup for each 1024 tokens of one
-    const int parts = (a.N + kPart - 1) / kPart;
-    const int rows_wg = parts > 1 ? 1 : a.T <= 512 * kWaves ? kWaves : (a.T + 511) / 512;
+    // A wave a row, or a workgroup for one or for each 1024 tokens of it; about a thousand workgroups at most, since each reads all
+    // rows (4096 rows of 8192 tokens in 32768 of them: 967 us, 52 so).
+    const int parts = std::min((a.N + kPart - 1) / kPart, std::max(1, kMostWorkgroups / a.T));
+    const int rows_wg = a.N > kPart && a.T <= kMostWorkgroups ? 1 : a.T <= 512 * kWaves ? kWaves : (a.T + 511) / 512;
+    const int part_n = (a.N + parts - 1) / parts;
     const dim3 grid(static_cast<unsigned>((a.T + rows_wg - 1) / rows_wg) * parts);
-    launch_timed(t, page_step_kernel, grid, dim3(kThreads), 0, s, a, rows_wg, parts);
+    launch_timed(t, page_step_kernel, grid, dim3(kThreads), 0, s, a, rows_wg, parts, part_n);
     return hipGetLastError();
 }
 

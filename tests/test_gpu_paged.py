@@ -756,3 +756,24 @@ def test_plans_stay_within_their_sizes(R, seed):
         shared = np.where(prefix >= 0, lens[np.maximum(prefix, 0)], 0)
         least = (M * (shared + lens[:B])).sum()
         assert least <= seen.sum() <= least + M * N * B       # new tokens: those a tile looks at
+
+
+@pytest.mark.parametrize("T,N", [(300, 5000), (1024, 1025), (1025, 1500), (9000, 1030)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_prompts_of_many_rows(R, T, N, in_place):
+    """More rows than there are workgroups for each 1024 tokens of them."""
+    import torch
+    rng = np.random.default_rng(T)
+    P, width = 128, -(-(N + 200) // 128)
+    pool = make_pool(R, rng, T, width, P, fill=0.2, spare=int(0.4 * T * width))
+    tables, held, ring, state = pool_arrays(pool)
+    lengths = np.maximum(held * P - rng.integers(0, 2 * P, T), 0).astype(np.int32)
+    lengths[rng.random(T) < 0.1] = -1
+    counts = rng.integers(0, N + 1, T).astype(np.int32)
+    want = ref.page_step(tables, held, ring, state, lengths, counts, N, P)
+    oh, os = (None, None) if in_place else (torch.full_like(pool.held, 77), torch.full_like(pool.state, 77))
+    granted, slots = R.page_step(pool, ints(lengths), N, counts=ints(counts), out_held=oh, out_state=os)
+    got = (granted, slots, pool.tables, pool.held if in_place else oh, pool.ring, pool.state if in_place else os)
+    for name, g, w in zip(("granted", "slots", "tables", "held", "ring", "state"), got, want):
+        assert np.array_equal(g.cpu().numpy(), w), name
+    assert (want[0] > 0).any() and not pool._workspace.any()
