@@ -777,3 +777,84 @@ def test_prompts_of_many_rows(R, T, N, in_place):
     for name, g, w in zip(("granted", "slots", "tables", "held", "ring", "state"), got, want):
         assert np.array_equal(g.cpu().numpy(), w), name
     assert (want[0] > 0).any() and not pool._workspace.any()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "f32"), (128, "f32"), (256, "f32")])
+@pytest.mark.parametrize("N", [1, 3, 40])
+def test_pages_that_are_none_far_along(R, D, dtype, N):
+    """In units that are not split, of 32 query rows and of 128: a bad page in any of the windows of 64 groups of keys that a wave
+    holds the pages of, at their edges, and among the new tokens. Who sees it answers NaN, everyone else the same bits."""
+    import torch
+    rng = np.random.default_rng(D + N)
+    B, H, P, n = 64, 8, 16, 4201
+    width = -(-(n + N) // P)
+    cache = make_cache(R, rng, width + 5, P, H, D)
+    tables = np.stack([rng.permutation(width + 5)[:width] for _ in range(B)]).astype(np.int32)     # pages in common, in any order
+    lens = np.full(B, n)
+    lens[1::4] = 700                                          # one window alone
+    q = queries(rng, B, N, H, D, dtype)
+    first = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints(lens), N, H))
+    few = [0, 1, 2, 3]                                        # (by the definition itself)
+    check(R, q[few], cache, tables[few], lens[few], 4, got=[t[few] for t in first])
+    for page in (0, 1, 31, 32, 43, 63, 64, 65, 127, 128, 191, 192, 255, 256, width - 2, width - 1):
+        broken = tables.copy()
+        hit = rng.random(B) < 0.4
+        broken[hit, page] = rng.choice([-1, width + 5, 2 ** 31 - 1])
+        got = R.paged_attention(q, cache, R.paged_plan(cache, ints(broken), ints(lens), N, H))
+        sees = dev(hit[:, None] & (lens[:, None] + np.arange(N) >= page * P))
+        assert torch.isnan(got[0][sees]).all() and torch.isnan(got[1][sees]).all(), page
+        assert torch.equal(got[0][~sees], first[0][~sees]) and torch.equal(got[1][~sees], first[1][~sees]), page
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f32"), (256, "bf16"), (256, "f32")])
+def test_bad_pages_of_a_prefix(R, D, dtype):
+    """Of several windows, read by tiles of 128 query rows: its own sequences answer NaN, those of the other prefix what they did."""
+    import torch
+    rng = np.random.default_rng(D)
+    B, N, H, G, P, n = 24, 4, 32, 2, 16, 5003                 # 32 heads: 16 units a head, of some 600 keys and more
+    lens = [5] * B + [n, n]
+    width = -(-(n + N) // P)
+    pages = 2 * width + B + 5
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    q = queries(rng, B, N, H * G, D, dtype)
+    prefix = [B] * 12 + [B + 1] * 12
+    first = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, prefix_row=ints(prefix)))
+    for page in (0, 63, 64, 100, 128, 200, width - 1):
+        for row in (0, 1):
+            broken = tables.copy()
+            broken[B + row, page] = -7
+            got = R.paged_attention(q, cache, R.paged_plan(cache, ints(broken), ints(lens), N, H * G, B=B, prefix_row=ints(prefix)))
+            bad, same = (slice(0, 12), slice(12, 24)) if row == 0 else (slice(12, 24), slice(0, 12))
+            if page * P < n:
+                assert torch.isnan(got[0][bad]).all() and torch.isnan(got[1][bad]).all()
+            assert torch.equal(got[0][same], first[0][same]) and torch.equal(got[1][same], first[1][same])
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "f32"), (128, "f32"), (256, "f32")])
+@pytest.mark.parametrize("N,G", [(50, 1), (27, 5), (64, 3)])
+def test_hidden_new_tokens_in_large_windows(R, D, dtype, N, G):
+    """More than 32 query rows: a new token of NaN or infinity reaches only those whose mask shows it."""
+    import torch
+    rng = np.random.default_rng(D + N)
+    B, H, P = 3, 2, 16
+    lens = [37, 1029, 0, 70]
+    width = -(-(max(lens) + N) // P)
+    pages = sum(-(-(x + N) // P) for x in lens)
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    mask = tree_masks(rng, B, N)
+    q = queries(rng, B, N, H * G, D, dtype)
+    plan = R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, prefix_row=ints([3, 3, -1]))
+    first = check(R, q, cache, tables, lens, B, prefix_row=[3, 3, -1], mask=mask)
+    for node in (0, 2, 15, 16, N - 1):
+        for what, bad in (("k", float("inf")), ("v", float("nan")), ("v", -float("inf")), ("k", float("nan"))):
+            t = cache.k_pages if what == "k" else cache.v_pages
+            keep = t.clone()
+            for b in range(B):
+                s = lens[b] + node
+                t[tables[b, s // P], s % P, :, 5] = bad
+            got = R.paged_attention(q, cache, plan, mask=dev(mask))
+            hidden = dev(mask[:, :, node] == 0)
+            assert torch.equal(got[0][hidden], first[0][hidden]) and torch.equal(got[1][hidden], first[1][hidden]), (node, what, bad)
+            t.copy_(keep)
