@@ -858,3 +858,33 @@ def test_hidden_new_tokens_in_large_windows(R, D, dtype, N, G):
             hidden = dev(mask[:, :, node] == 0)
             assert torch.equal(got[0][hidden], first[0][hidden]) and torch.equal(got[1][hidden], first[1][hidden]), (node, what, bad)
             t.copy_(keep)
+
+
+@pytest.mark.parametrize("N,D,n,split", [(2, 64, 9000, True), (2, 128, 65536, True), (40, 128, 20000, True), (2, 64, 65536, False),
+                                         (40, 64, 30000, False), (40, 256, 9000, False)])
+def test_long_sums_of_float32(R, N, D, n, split):
+    """Float32 queries behind many keys, with bounds that do not grow with the keys as a sum that adds them one by one would be off.
+
+    A score goes through D/8 additions of each of three parts, half a step each in either direction: six times the root of the sum
+    of their squares, sqrt(D/8) half steps of its size. The sum of the exponentials keeps what it rounds off, and lies in a few
+    dozen parts; lse has a few roundings of its own. An output's additions, one for eight keys and each of three parts, likewise."""
+    import torch
+    rng = np.random.default_rng(n + N + D)
+    H, P = 8, 64
+    B = 2 if split else 64                                    # (of the same pages)
+    cache = make_cache(R, rng, n // P + 2, P, H, D)
+    tables = np.tile(rng.permutation(n // P + 2).astype(np.int32), (B, 1))
+    q = queries(rng, B, N, H, D, "f32")
+    out, lse = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints([n] * B), N, H))
+    K, V = (t[dev(tables[0].astype(np.int64))].view(-1, H, D)[:n + N].double().transpose(0, 1).contiguous() for t in (cache.k_pages, cache.v_pages))
+    for b in (0, B - 1):
+        s = torch.matmul(q[b].double().transpose(0, 1).contiguous(), K.transpose(1, 2).contiguous()) * D ** -0.5          # [H, N, n + N]
+        size = torch.matmul(q[b].double().abs().transpose(0, 1).contiguous(), K.abs().transpose(1, 2).contiguous()).amax(-1) * D ** -0.5
+        s = s.masked_fill(torch.ones(N, n + N, dtype=torch.bool, device="cuda").tril(n) == 0, float("-inf"))
+        want = s.logsumexp(-1)
+        tol = U * (6 * (D / 8) ** 0.5 * size + 8 * want.abs() + 64)
+        assert ((lse[b].T.double() - want).abs() <= tol).all(), ((lse[b].T.double() - want).abs() / tol).max()
+        p = s.softmax(-1)
+        spread = torch.matmul(p, V.abs())
+        off = (out[b].transpose(0, 1).double() - torch.matmul(p, V)).abs()
+        assert (off <= (2 * tol + 6 * (3 * n / 8 / 3) ** 0.5 * U).unsqueeze(-1) * spread).all()
