@@ -44,7 +44,7 @@ constexpr int kTileKeys = 32;                           // keys of a tile
 constexpr int kWindow = kWave;                          // 16-key groups whose pages a wave holds, one a lane
 constexpr int kBatch = 8;                               // parts under way in the join
 constexpr float kSlack = 8.f;                           // powers of two a score may pass the running maximum by
-constexpr float kFar = 16777216.f;                      // of a maximum in base two: from here on its rounding passes a power of two
+constexpr float kFar = 1024.f;                          // of a maximum in base two: half a step of it is 2^-15 and more from here on
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));

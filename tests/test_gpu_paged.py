@@ -888,3 +888,35 @@ def test_long_sums_of_float32(R, N, D, n, split):
         spread = torch.matmul(p, V.abs())
         off = (out[b].transpose(0, 1).double() - torch.matmul(p, V)).abs()
         assert (off <= (2 * tol + 6 * (3 * n / 8 / 3) ** 0.5 * U).unsqueeze(-1) * spread).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,n", [(3, 900), (50, 2100)])
+@pytest.mark.parametrize("far", [2.0 ** 13, 2.0 ** 20, -2.0 ** 20])
+def test_weights_beside_large_scores(R, dtype, N, n, far):
+    """Scores of one large number and a little, exact both, that rise along the keys: their weights go by the little, also between
+    tiles and units with maxima of their own. Off by the exponents' two roundings (100 powers of two: 2^-17 each) and sums'."""
+    import torch
+    rng = np.random.default_rng(N)
+    B, H, D, P = 2, 2, 64, 16
+    lens = [n, 5, 700]
+    width = -(-(n + N) // P)
+    pages = sum(-(-(x + N) // P) for x in lens)
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    j = np.zeros((pages, P), np.float32)
+    for t, x in enumerate(lens):                              # 0 .. 255 along each row's slots
+        s = np.arange(x + (N if t < B else 0))
+        j[tables[t][s // P], s % P] = s * 256 // (x + N)
+    cache.k_pages.zero_()
+    cache.k_pages[..., 0] = 1.0
+    cache.k_pages[..., 1] = dev(j)[:, :, None].bfloat16()
+    q = torch.zeros(B, N, H, D, device="cuda")
+    q[..., 0], q[..., 1] = far, 1.0
+    q = q.bfloat16() if dtype == "bf16" else q
+    got = R.paged_attention(q, cache, R.paged_plan(cache, ints(tables), ints(lens), N, H, B=B, prefix_row=ints([2, 2])))
+    want, wlse, _, _ = ref.attend(f64(q), f64(cache.k_pages), f64(cache.v_pages), tables, lens, B, None, [2, 2], None, D ** -0.5, 0.0)
+    size = np.abs(f64(cache.v_pages)).max()
+    p = 2.0 ** -8 if dtype == "bf16" else 0.0                 # P, and the output
+    assert np.abs(f64(got[0]) - want).max() < size * (2 * np.log(2) * 2.0 ** -17 + 2.0 ** -18 + 2 * p)
+    assert (np.abs(f64(got[1]) - wlse) < 4 * U * np.abs(wlse) + 2.0 ** -16).all()
