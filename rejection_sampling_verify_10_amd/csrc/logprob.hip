@@ -210,7 +210,7 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     const auto look = [&](float mx) {
         tm = __builtin_elementwise_maximum(tm, mx);
         if (__ballot((mx - mz) * a.c > kSlack) != 0ull) {
-            const float to = fmaxf(mz, wave_max(mx));
+            const float to = bcast(fmaxf(mz, wave_max(mx)), 0);
             move(to, masked || is_wide(to, a.c));
         }
     };
