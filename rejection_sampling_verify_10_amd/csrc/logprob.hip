@@ -22,11 +22,12 @@
 // them joins.
 //
 // What bounds it: 1024 rows of 128256 bf16 logits and more, HBM (2048 rows, no list:
-// 86 us, 6.1 TB/s); 512 rows of which 288 are read, with the 20 likeliest: 27 us,
-// 2.7 TB/s, of which the bytes alone would take 11: a workgroup's row is a chain of
-// first loads, 31 vectors a thread, the list; with one exponential in eight it is
-// still 20 us.  8 rows of 32000: 9 us, latency.  More vectors under way (12, 16) cost
-// occupancy: 27, 29 us.  The gradient is one read and one write of each row at
+// 88-92 us, 5.8 TB/s); 512 rows of which 288 are read, with the 20 likeliest: 28 us,
+// 2.7 TB/s, 22 of them without the list, and 15 by the bytes at a large copy's rate
+// (4.9 TB/s): a workgroup's row is a chain of first loads, 31 vectors a thread, the
+// list; when it took 26, it was still 20 with one exponential in eight, and 27 and 29
+// with more vectors under way (12, 16), which cost occupancy.  Rows with -inf, half of
+// their logits: 33 us, 2048 of them 107.  8 rows of 32000: 9 us, latency.  The gradient is one read and one write of each row at
 // 6.1 TB/s (2048 rows of 128256: 170 us), more than a large copy reaches (4.9).
 
 #include <float.h>
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(kLpThreads, 4) void logprobs_kernel(LogprobArgs a) 
     };
     // A group of vectors, the first of them number `at` of the row, by two sums of its own (with 250 additions one after the other
     // the entropies of 128256 logits were off by 9e-7 of them, by 3e-7 with one a group; peaked rows 7e-7, 5e-7 with two). -inf makes a NaN of w (0 * -inf): that group
-    // and the wave's later ones are taken by differences, held above that (half of 2048 rows of 128256 masked: 101 us, 87 with none, 151 with
+    // and the wave's later ones are taken by differences, held above that (half of 2048 rows of 128256 masked: 107 us, 90 with none, 151 with
     // such groups taken twice); what stands for vectors past the end is -inf too, and left out.
     const auto sum = [&](const u32x4* v, int at) {
         float s[2] = {}, w[2] = {};
@@ -601,7 +602,7 @@ template <int DT> void logprobs(const LogprobArgs& a, hipStream_t s, Timing t) {
 
 }  // namespace
 
-// A workgroup a row where there is a row for each compute unit (512 rows of 128256 bf16 logits: 27 us, two workgroups a row 38);
+// A workgroup a row where there is a row for each compute unit (512 rows of 128256 bf16 logits: 28 us, two workgroups a row 38);
 // fewer rows are cut up, so that their loads spread over the compute units, into slices of four vectors a thread at least.
 void logprob_plan(LogprobArgs& a) {
     const int vecs = a.V / (a.dtype == 1 ? 8 : 4), least = kFewVecs * kLpThreads;

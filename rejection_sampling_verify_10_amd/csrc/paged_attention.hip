@@ -17,14 +17,21 @@
 // permuted in 16-byte chunks so that neither read has bank conflicts.
 //
 // float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
-// queries P is the one bf16 of it, which is the output's own rounding.
+// queries P rounds to the one bf16, beside the output's own rounding: a third more
+// error (0.0022 of the outputs off the 64-bit ones, 0.0017 with the latter alone).  Two
+// parts of P would leave that alone and take 21-35% longer where the matrix products
+// count (64 sequences behind 32768 keys 109 -> 139 us, 32 chains of eight 81 -> 98; one
+// long sequence 97, both); who wants them passes the queries widened to float32.
+//
+// The sum is float32, a tile's added together first, with what it rounds off kept
+// beside it.  An output's is the matrix instruction's: eight keys' products at a time.
 //
 // What bounds it (D = 128, 8 heads, bf16): many query rows, the tiles' way through LDS
 // (a wave reads all of a tile for 32 rows: 600 of some 1400 clocks a tile) beside the
-// products (64 rows of 8 tokens x 4 heads behind 65536 keys in common: 886-913 TFLOP/s,
+// products (64 rows of 8 tokens x 4 heads behind 65536 keys in common: 872-885 TFLOP/s,
 // matrix units busy half of the time; a library product of 8192^3 1089); few, HBM (one sequence of 131072 keys:
 // 99 us, 5.4 TB/s; the read probe 7.0); in between both (64 sequences of one token
-// behind 32768 keys, ragged tails to 1024: 98-122 us by the clock, 304 MB, 70 GFLOP);
+// behind 32768 keys, ragged tails to 1024: 102-125 us by the clock, 304 MB, 70 GFLOP);
 // short ones, a chain of latencies (4 sequences of one token, 600 keys: 7.4 + 3.5 us).
 
 #include <stddef.h>
@@ -58,7 +65,7 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f
 #endif
 }
 // The same with the sums in AGPRs, for good: left to itself the compiler takes them to VGPRs and back in every tile, for the few
-// tiles that rescale them, and spills others (float32 chains of eight behind 16384 keys, D = 256: 318 us, 202 so). It sees no
+// tiles that rescale them, and spills others (float32 chains of eight behind 16384 keys, D = 256: 318 us, 206 so). It sees no
 // matrix instruction here, so the waits are ours: two states after a VALU write of an operand, four after one of exec; sums_done
 // before anything else reads or writes the sums, sums_set after it has. Products that follow each other on the same sums
 // need none.

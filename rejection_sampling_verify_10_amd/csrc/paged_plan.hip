@@ -319,8 +319,11 @@ __global__ __launch_bounds__(kThreads) void paged_plan_kernel(PagedPlanArgs a) {
 }  // namespace
 
 // The key axes are split into about as many workgroups as run at once, two a compute unit, or one where a tile of D = 256 takes
-// most of its LDS (44 rows of 7 tokens behind 800 keys, D = 256: 36 us in 512 of them, 32 in 256); a batch whose own rows alone
-// are as many is not split, unless there are prefixes.
+// most of its LDS (44 rows of 7 tokens behind 800 keys, D = 256: 36 us in 512 of them, 32 in 256). A batch whose own rows alone
+// are as many is not split, unless there are prefixes: no workspace, a plan of 6-9 us and not 9-13, units in no order of length.
+// For rows much alike that is as good (8 heads, D = 128, 8 queries a head, one token: 64 rows of 4096 keys 174 us, 177 split; 256 of
+// 512..2048 233 and 225; 1024 of 256..1024 481 and 485); one much longer than the rest is not (131072 keys among 63 rows of 500: 1358 us,
+// 123 split), and a caller who has such gives prefix rows of -1.
 void paged_plan_sizes(PagedPlanArgs& a) {
     a.own_rows = a.M <= kPgNarrow ? kPgNarrow : kPgWide;
     a.own_tiles = (a.M + a.own_rows - 1) / a.own_rows;

@@ -15,6 +15,8 @@ or, with logits that require a gradient, through autograd: r.logprobs and r.entr
 
     loss = -(weights * token_logprobs(logits, ids).logprobs).sum()
     loss.backward()
+
+(A backward pass that is captured wants no eager graph of the same leaves alive, as any of PyTorch's.)
 """
 
 from __future__ import annotations

@@ -215,7 +215,8 @@ def paged_plan(cache: PagedCache, tables: torch.Tensor, lengths: torch.Tensor, N
     tables [T, width] int32 and lengths [T] int32: a pool's tables and the committed slots of their rows.  The first B
     rows (all by default) are the batch's, with counts [B] new tokens each (N by default).  prefix_row [B] int32: the
     table row whose slots come before batch row b's own, negative for none; neighbouring rows with the same one share
-    the reading of it.  ``out``: a plan of the same sizes and tables to make anew (as a captured graph does).
+    the reading of it.  Without it a large batch's rows are not split over the GPU: where some are much longer than the
+    rest, give -1 for all.  ``out``: a plan of the same sizes and tables to make anew (as a captured graph does).
     """
     if tables.dim() != 2 or 0 in tables.shape:
         raise ValueError("tables must be [T, width]")
@@ -259,7 +260,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, plan: PagedPlan, *, mask
     q [B, N, q_heads, D] bf16 or f32 (strided); the new tokens' rows are in their slots already (:func:`paged_append`).
     mask: None (token n sees new tokens 0..n) or an ancestor mask, [B, N, N] or [N, N] uint8, N <= 64 (what
     :func:`tree_rerank` gives).  scale defaults to D ** -0.5.  Returns (out, of q's type and shape, lse [B, N, q_heads]
-    f32); tokens n >= counts[b] and batch rows out of range give zeros and -inf.
+    f32); tokens n >= counts[b] and batch rows out of range give zeros and -inf.  With bf16 queries the probabilities round
+    to bf16 before they meet V; ``q.float()`` avoids that, for a float32 output and twice the time of many query rows.
     """
     rq = _rows(q, "q", cache)
     B, N, Hq, D = q.shape
