@@ -490,3 +490,42 @@ def test_a_training_step_captured(R):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(3, 4099), (6, 50000), (270, 2003)])
+@pytest.mark.parametrize("T", [1e-12, 1e-3, 0.7, 1e6, 1e30])
+def test_rows_that_move_the_reference(R, dtype, rows, V, T):
+    """Rising, falling, masked in part by -inf and by large numbers, lifted and lowered as a whole, with blocks and peaks."""
+    import torch
+    rng = np.random.default_rng(V + rows)
+    z = 5 * rng.standard_normal((rows, V))
+    for r in range(rows):
+        a, b = np.sort(rng.integers(0, V + 1, 2))
+        how = r % 9 if rows > 9 else (2 * r + V) % 9
+        if how < 2:
+            z[r] = np.sort(z[r])[:: 1 - 2 * how]
+        elif how < 4:
+            z[r, a:b] = -np.inf if how == 2 else rng.choice([-1e4, -1e10, -1e30, -3.3e38])
+        elif how == 4:
+            z[r] += rng.choice([1e5, -1e9, 1e20, -1e30])
+        elif how == 5:
+            z[r, a:b] += rng.choice([50, 1e3, 1e6])
+        elif how == 6:
+            z[r, a:] += 1e4
+        elif how == 7:
+            z[r, rng.random(V) < 0.5] = -np.inf
+    t = dev(z.astype(np.float32))
+    t = t.bfloat16() if dtype == "bf16" else t
+    zv = t.float().cpu().numpy()
+    tokens = np.stack([zv.argmax(1), rng.integers(0, V, rows), np.full(rows, V - 1)], 1).astype(np.int32)
+    r = R.token_logprobs(t, dev(tokens), small(T), 5)
+    want = ref.forward(zv, tokens, small(T), 5)
+    for w in want:                                            # differences past float32's range
+        for k in ("lp", "top_lp"):
+            with np.errstate(over="ignore"):
+                w[k] = np.where(np.isfinite(w[k]), w[k].astype(np.float32), w[k]).astype(np.float64)
+    check(r, want, 5)
+    g, gh = rng.standard_normal((rows, 3)).astype(np.float32), rng.standard_normal(rows).astype(np.float32)
+    got = R.token_logprobs_grad(t, dev(tokens), r.stats, dev(g), dev(gh), small(T))
+    check_grad(got, *ref.backward(zv, tokens, g, gh, small(T), dtype))
