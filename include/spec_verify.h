@@ -775,8 +775,9 @@ int spec_paged_plan(int B, int N, int q_heads, int heads, int head_dim, int T, i
  * of -inf.  What a query does not see never reaches it, whatever its bytes.  One that sees a slot
  * whose K or V holds a NaN or an infinity gives unspecified numbers; one that sees a slot whose
  * page is none of the pool's gives NaN.  Products and sums are float32; with bfloat16
- * queries the probabilities round to bfloat16 before they meet V (the same queries as
- * SPEC_F32 avoid that, and the output is float32).
+ * queries the probabilities round to 16 bits before they meet V, and to bfloat16 where
+ * more than 32 query rows of a head meet the same slots (the same queries as SPEC_F32
+ * avoid that, and the output is float32).
  * workspace: spec_paged_attention_workspace_bytes(...) bytes (may be 0), any contents;
  * left as scratch.
  */

@@ -17,11 +17,13 @@
 // permuted in 16-byte chunks so that neither read has bank conflicts.
 //
 // float32 queries enter as three bf16 parts, and so does P: exact both.  With bf16
-// queries P rounds to the one bf16, beside the output's own rounding: a third more
-// error (0.0022 of the outputs off the 64-bit ones, 0.0017 with the latter alone).  Two
-// parts of P would leave that alone and take 21-35% longer where the matrix products
-// count (64 sequences behind 32768 keys 109 -> 139 us, 32 chains of eight 81 -> 98; one
-// long sequence 97, both); who wants them passes the queries widened to float32.
+// queries P has two parts in units of up to 32 query rows, 2^-17 of it off, which wait
+// for memory (64 sequences of 4096 keys 125.9 us, 126.4 with two; four of 600 12.8 and
+// 13.3).  In those of up to 128 it rounds to one bf16: beside the output's own rounding,
+// a third more error (0.0022 of the outputs off the 64-bit ones, 0.0017 with the latter
+// alone).  A second part takes 21-35% longer there (64 sequences behind 32768 keys 109
+// -> 139 us, 32 chains of eight 81 -> 98); who wants it passes the queries widened to
+// float32.
 //
 // The sum is float32, a tile's added together first, with what it rounds off kept
 // beside it.  An output's is the matrix instruction's: eight keys' products at a time.
@@ -262,6 +264,7 @@ __device__ __forceinline__ void load_query(const PagedRows& q, long long off, bo
 template <int D, int DT> struct Wave {
     static constexpr int NT = D / 32;
     static constexpr int NQ = DT == 1 ? 1 : 3;
+    static constexpr int kWideP = NQ, kNarrowP = DT == 1 ? 2 : 3;       // parts of P, in a wide unit and in a narrow one
     static constexpr bool kSums = D == 256;             // O is in AGPRs
     // V's operands are read before the scores' products where there are registers to hold them.
     static constexpr bool kEarlyV = D == 64 || (D == 128 && DT == 1);
@@ -370,7 +373,7 @@ template <int D, int DT> struct Wave {
         return odd;
     }
     // P of a tile's scores (which may be gone then), and the maximum and sums.
-    __device__ __forceinline__ void weigh(f32x16& S, float cexp, float slack, u32x4 (&P)[NQ][2]) {
+    template <int NP> __device__ __forceinline__ void weigh(f32x16& S, float cexp, float slack, u32x4 (&P)[NP][2]) {
         float mx = S[0];                                // NaN propagates, and moves no maximum
 #pragma unroll
         for (int i = 1; i < 15; i += 2) mx = maximum3(mx, S[i], S[i + 1]);
@@ -407,7 +410,7 @@ template <int D, int DT> struct Wave {
             for (int i = 0; i < 8; ++i) p[i] = exp2_fast(__builtin_fmaf(S[8 * s + i], cexp, -mc));
             sum[s] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
+            for (int x = 0; x < NP; ++x) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     P[x][s][e] = pack_bf16(p[2 * e], p[2 * e + 1]);
@@ -432,7 +435,7 @@ template <int D, int DT> struct Wave {
         }
     }
     // O += V P. V's operands are in registers, or still in the buffer (and perhaps to be cleaned).
-    __device__ __forceinline__ void add(const Lds<D>& lds, int buf, const u32x4 (&P)[NQ][2], bool edge) {
+    template <int NP> __device__ __forceinline__ void add(const Lds<D>& lds, int buf, const u32x4 (&P)[NP][2], bool edge) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (!kEarlyV) {
@@ -445,7 +448,7 @@ template <int D, int DT> struct Wave {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) {
+                for (int x = 0; x < NP; ++x) {
                     if (kSums) mfma32_sums(V[kEarlyV ? s : 0][t], P[x][s], O[t]);
                     else O[t] = mfma32(V[kEarlyV ? s : 0][t], P[x][s], O[t]);
                 }
@@ -594,7 +597,7 @@ template <int D, int DT> __device__ __forceinline__ void attend_wide(const Paged
 
     const auto iterate = [&](auto buffer, int t, bool edge, unsigned none) {
         const int buf = buffer;
-        u32x4 P[W::NQ][2];
+        u32x4 P[W::kWideP][2];
         if (working) {
             if (W::kEarlyV) w.read_v(lds, buf);
             f32x16 S = w.template scores<W::kWideK>(lds, buf);
@@ -686,7 +689,7 @@ template <int D, int DT> __device__ __forceinline__ void attend_narrow(const Pag
             wait_lds();
             ld.load_k(next);
         }
-        u32x4 P[W::NQ][2];
+        u32x4 P[W::kNarrowP][2];
         if (edge) sight.hide(S, first, w.odd_keys(lds, wave, none));
         w.weigh(S, a.cexp, slack, P);
         w.add(lds, wave, P, edge);

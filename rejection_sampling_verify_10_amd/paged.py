@@ -261,7 +261,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, plan: PagedPlan, *, mask
     mask: None (token n sees new tokens 0..n) or an ancestor mask, [B, N, N] or [N, N] uint8, N <= 64 (what
     :func:`tree_rerank` gives).  scale defaults to D ** -0.5.  Returns (out, of q's type and shape, lse [B, N, q_heads]
     f32); tokens n >= counts[b] and batch rows out of range give zeros and -inf.  With bf16 queries the probabilities round
-    to bf16 before they meet V; ``q.float()`` avoids that, for a float32 output and twice the time of many query rows.
+    to bf16 before they meet V where more than 32 query rows of a head see the same slots (a shared prefix's, a large
+    window's); ``q.float()`` avoids that, for a float32 output and twice the time.
     """
     rq = _rows(q, "q", cache)
     B, N, Hq, D = q.shape

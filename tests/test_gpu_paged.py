@@ -920,3 +920,24 @@ def test_weights_beside_large_scores(R, dtype, N, n, far):
     p = 2.0 ** -8 if dtype == "bf16" else 0.0                 # P, and the output
     assert np.abs(f64(got[0]) - want).max() < size * (2 * np.log(2) * 2.0 ** -17 + 2.0 ** -18 + 2 * p)
     assert (np.abs(f64(got[1]) - wlse) < 4 * U * np.abs(wlse) + 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,N,G,shared,tree", [(5, 1, 8, None, False), (3, 8, 4, None, False), (2, 6, 5, None, True), (4, 1, 4, 700, False), (2, 3, 5, 90, False)])
+def test_few_query_rows_round_once(R, D, B, N, G, shared, tree):
+    """bf16 queries, no more than 32 rows that meet the same slots: P is 2^-17 off, and what shows is the output's rounding."""
+    import torch
+    rng = np.random.default_rng(D + B)
+    H, P = 2, 16
+    lens = rng.integers(1, 1500, B).tolist() + ([] if shared is None else [shared])
+    width = -(-(max(lens) + N) // P)
+    pages = sum(-(-(x + N) // P) for x in lens)
+    cache = make_cache(R, rng, pages, P, H, D)
+    tables = make_tables(rng, pages, P, lens, N, B, width)
+    prefix = None if shared is None else [B] * B
+    mask = tree_masks(rng, B, N) if tree else None
+    q = queries(rng, B, N, H * G, D, "bf16")
+    plan = R.paged_plan(cache, ints(tables), ints(lens), N, H * G, B=B, prefix_row=None if prefix is None else ints(prefix))
+    out, _ = R.paged_attention(q, cache, plan, mask=None if mask is None else dev(mask))
+    want, _, tol, _ = ref.attend(f64(q), f64(cache.k_pages), f64(cache.v_pages), tables, lens, B, None, prefix, mask, D ** -0.5, 2.0 ** -16)
+    assert (np.abs(f64(out) - want) <= tol + 2.0 ** -8 * 1.01 * np.abs(want) + 1e-37).all()
